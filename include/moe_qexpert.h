@@ -364,6 +364,133 @@ moe_status moe_unpermute_combine(const void* y_perm, int32_t y_dtype, const int3
                                  const int32_t* n_valid, const float* topk_w, int32_t T, int32_t k, int32_t H,
                                  uint16_t* out, void* stream);
 
+/* ---------------------------------------------------------- scored routing
+ * Top-k expert choice from scores of all experts, with an optional choice bias
+ * and expert groups (moe_route_topk is the expert gate on bare logits).
+ * All scores, sums and comparisons are float64; per token:
+ *     s_e = softmax over the E logits (MOE_SCORE_SOFTMAX) or
+ *           1 / (1 + exp(-logit_e))   (MOE_SCORE_SIGMOID)
+ *     c_e = s_e + bias[e]             (choice score; bias NULL: c_e = s_e)
+ *     n_group > 1: group g holds experts g*E/n_group .. (g+1)*E/n_group - 1 and
+ *           scores the sum of its group_top largest c_e; the topk_group best
+ *           groups stay open, experts of the others are not eligible
+ *     ids = the k eligible experts of largest c_e, descending; ties (experts
+ *           and groups) go to the lower index
+ *     w   = s of the chosen experts (without the bias), divided by their sum if
+ *           renormalize != 0, times scale, rounded once to float32
+ * A logit of -inf or NaN, or a bias of -inf or NaN, bars its expert: its score
+ * is 0 and it is never chosen (+inf counts as FLT_MAX; a group without
+ * eligible experts ranks last).  Slots left over when fewer than k experts are
+ * eligible hold id -1 and weight 0; moe_permute places such pairs after every
+ * valid segment, and the combine adds nothing for them.  A sum of chosen
+ * scores that is 0 gives weights 0.
+ *   logits f32 [T][E]; bias f32 [E] or NULL; topk_ids i32 [T][k]; topk_w f32 [T][k]
+ * 0 <= T, 1 <= k <= E <= 1024, T*k < 2^31, 1 <= n_group <= 64, E % n_group == 0,
+ * 1 <= topk_group <= n_group, group_top 1 or 2, scale finite.  4-byte aligned
+ * pointers.
+ */
+#define MOE_SCORE_SOFTMAX 0
+#define MOE_SCORE_SIGMOID 1
+moe_status moe_route_scored(const float* logits, const float* bias, int32_t T, int32_t E, int32_t k, int32_t score,
+                            int32_t n_group, int32_t topk_group, int32_t group_top, int32_t renormalize, float scale,
+                            int32_t* topk_ids, float* topk_w, void* stream);
+
+/* ------------------------------------------------------- microscaled (MX) rows
+ * Rows of K values in blocks of 32 that share a power-of-two scale (the MX
+ * element formats and e8m0 scale bytes of the OCP Microscaling specification).
+ *   MOE_MX_E4M3  8-bit elements (4 exponent, 3 mantissa bits, largest 448):
+ *                codes u8 [rows][K]
+ *   MOE_MX_E2M1  4-bit elements (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their
+ *                negatives): codes u8 [rows][K/2], even k in the low nibble
+ *   scales u8 [rows][K/32]: byte b stands for 2^(b - 127); 255 for a block that
+ *                is not a number
+ * Quantisation of a block with largest magnitude m, M = 448 or 6: the scale is
+ * the smallest 2^p, p >= -126, with m <= M * 2^p (no element saturates); each
+ * value / 2^p is rounded to the nearest element, ties to even.  A block with an
+ * infinity or NaN gets scale byte 255 and zero codes: all of it reads as NaN.
+ * K % 32 == 0, rows * K < 2^40; 16-byte aligned buffers, except scales.
+ */
+#define MOE_MX_E4M3 1
+#define MOE_MX_E2M1 2
+/* x [rows][K] of x_dtype (MOE_DTYPE_*) -> codes, scales. */
+moe_status moe_quantize_mx(const void* x, int32_t x_dtype, int64_t rows, int32_t K, int32_t fmt, uint8_t* codes,
+                           uint8_t* scales, void* stream);
+/* codes, scales -> the values they stand for, out [rows][K] of out_dtype
+   (MOE_DTYPE_*), rounded once to it (exact in fp32, and in bf16 above its
+   subnormal range). */
+moe_status moe_dequantize_mx(const uint8_t* codes, const uint8_t* scales, int64_t rows, int32_t K, int32_t fmt,
+                             int32_t out_dtype, void* out, void* stream);
+
+/* Residual addition, root-mean-square norm and MX quantisation in one pass:
+ *     v = x + residual, rounded to `dtype`  (residual NULL: v = x)
+ *     n_i = v_i / sqrt(mean_j v_j^2 + eps) * weight_i
+ *     sum = v, y = n rounded to `dtype`, (codes, scales) = MX blocks of n
+ * (n itself is quantised, not its rounding y).  x, residual, sum, y [rows][H]
+ * and weight [H] of `dtype` (MOE_DTYPE_*).  sum (needs residual), y and the MX
+ * output (fmt 0: codes and scales NULL) are each optional; at least one output
+ * is needed.  sum may be x or residual, and y may be x, residual or sum's
+ * place only if that buffer is not written otherwise.  Squares are summed in
+ * fp32 per lane and float64 across lanes; the norm's factor is float64.
+ * rows >= 0, H % 32 == 0, 32 <= H <= 16384, rows * H < 2^40, eps >= 0 and
+ * finite; 16-byte aligned buffers, except scales.
+ */
+moe_status moe_rmsnorm_mx(const void* x, const void* residual, const void* weight, int32_t dtype, int64_t rows,
+                          int32_t H, float eps, void* sum, void* y, int32_t fmt, uint8_t* codes, uint8_t* scales,
+                          void* stream);
+
+/* ------------------------------------------------- MX experts, grouped product
+ * Expert weights as MX rows of 4-bit elements along K:
+ *   MOE_LAYOUT_CANONICAL  codes u8 [E][N][K/2], scales u8 [E][N][K/32]
+ *   MOE_LAYOUT_TILED      (moe_mx_repack) tiles of 32 output channels in the
+ *       operand order of the scaled MFMA: codes [E][N/32][K/64][64 lanes][16 B],
+ *       lane l = channel l % 32, inputs 32*(l/32) .. +31 of the 64; scales
+ *       [E][N/32][ceil(K/256)][64 lanes][4 B], byte s of lane l = the scale of
+ *       channel l % 32, block 2*s + l/32 of the 8 blocks.
+ * N % 32 == 0, K % 128 == 0, E <= 1024, N * K < 2^32.
+ */
+typedef struct moe_mxdesc {
+  int32_t abi_version; /* MOE_ABI_VERSION */
+  int32_t layout;      /* MOE_LAYOUT_* */
+  int32_t E, N, K;
+  int32_t reserved;
+  const uint8_t* codes;
+  const uint8_t* scales;
+} moe_mxdesc;
+
+/* Bytes of MOE_FIELD_CODES or MOE_FIELD_SCALES in w->layout (0: no such field,
+   or an invalid descriptor). */
+size_t moe_mx_field_bytes(const moe_mxdesc* w, int32_t field);
+/* Canonical -> tiled, once, offline; dst's buffers (moe_mx_field_bytes each) are
+   overwritten.  16-byte aligned codes, 4-byte aligned scales. */
+moe_status moe_mx_repack(const moe_mxdesc* src, const moe_mxdesc* dst, void* stream);
+
+/* The grouped product of moe_grouped_qgemm with MX weights and MX activations:
+ * for every segment e of seg_offsets (E segments) and every row i in it,
+ *     a_i = A[gather_pair[i] / k], or A[i] without gather_pair
+ *     y_i = a_i W_e^T
+ * on the values that the blocks stand for; products and sums in the scaled
+ * matrix instructions with fp32 accumulation.  Out, by epilogue:
+ *     MOE_EPI_NONE / _NONE_F32 / _NONE_F16   y_i, bf16 / fp32 / fp16 [M_total][N]
+ *     MOE_EPI_SWIGLU        silu(y_i[:N/2]) * y_i[N/2:], bf16 [M_total][N/2]
+ *     MOE_EPI_SWIGLU_E4M3 / _E2M1   the same as MX rows: out = codes, out_scales
+ *                           u8 [M_total][N/64] (the activations of the next
+ *                           product, quantised from the fp32 values)
+ * A is a_codes, a_scales in a_fmt (MOE_MX_*), [A_rows][K].  The SwiGLU epilogues
+ * need N % 64 == 0.  out_scales is NULL unless the epilogue writes it.  Rows
+ * outside [seg_offsets[0], seg_offsets[E]) are left as they were; offsets are
+ * clamped to 0 .. M_total and gathered rows to A_rows - 1.
+ * kernel: MOE_KERNEL_AUTO, MOE_KERNEL_SMALL (32-row tiles straight from memory:
+ * decode batches) or MOE_KERNEL_TILE64 / _TILE128 (LDS-staged tiles of that many
+ * rows).  No workspace.  a_codes and w: 16-byte aligned, a_scales: 4-byte, out:
+ * 16-byte.  a_codes below 4 GiB.
+ */
+#define MOE_EPI_SWIGLU_E4M3 4
+#define MOE_EPI_SWIGLU_E2M1 5
+moe_status moe_grouped_mxgemm(const moe_mxdesc* w, const uint8_t* a_codes, const uint8_t* a_scales, int32_t a_fmt,
+                              int32_t A_rows, const int32_t* gather_pair, int32_t k, const int32_t* seg_offsets,
+                              int32_t M_total, int32_t epilogue, int32_t kernel, void* out, uint8_t* out_scales,
+                              void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -20,7 +20,10 @@ MOE_ABI_VERSION = 3
 MOE_W_INT4_GROUP, MOE_W_MWQ_2_3_4, MOE_W_DELTA2_SALIENT, MOE_W_INT_PER_EXPERT = 1, 2, 3, 4
 MOE_LAYOUT_CANONICAL, MOE_LAYOUT_TILED = 0, 1
 MOE_EPI_NONE, MOE_EPI_SWIGLU, MOE_EPI_NONE_F32, MOE_EPI_NONE_F16 = 0, 1, 2, 3
+MOE_EPI_SWIGLU_E4M3, MOE_EPI_SWIGLU_E2M1 = 4, 5  # grouped MX product only
 MOE_DTYPE_BF16, MOE_DTYPE_F32, MOE_DTYPE_F16 = 0, 1, 2
+MOE_MX_E4M3, MOE_MX_E2M1 = 1, 2
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
 # plain-epilogue output dtype of each epilogue, and the epilogue that writes a dtype
 _EPI_DTYPE = {MOE_EPI_NONE_F32: torch.float32, MOE_EPI_NONE_F16: torch.float16}
 _DTYPE_EPI = {torch.float32: MOE_EPI_NONE_F32, torch.float16: MOE_EPI_NONE_F16, torch.bfloat16: MOE_EPI_NONE}
@@ -34,6 +37,8 @@ EXPORTED = [
     "moe_permute_workspace_size", "moe_permute", "moe_route_permute", "moe_weight_field_bytes", "moe_repack_weights",
     "moe_grouped_qgemm_workspace_size", "moe_grouped_qgemm", "moe_unpermute_combine",
     "moe_grouped_qgemm_noalloc", "moe_grouped_qgemm_noalloc_scratch_bytes", "moe_copy_rows_async",
+    "moe_route_scored", "moe_quantize_mx", "moe_dequantize_mx", "moe_rmsnorm_mx", "moe_mx_field_bytes",
+    "moe_mx_repack", "moe_grouped_mxgemm",
 ]
 
 
@@ -56,12 +61,20 @@ class WDesc(ctypes.Structure):
     ]
 
 
+class MxDesc(ctypes.Structure):
+    _fields_ = [
+        ("abi_version", ctypes.c_int32), ("layout", ctypes.c_int32), ("E", ctypes.c_int32), ("N", ctypes.c_int32),
+        ("K", ctypes.c_int32), ("reserved", ctypes.c_int32), ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p),
+    ]
+
+
 def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     if not os.path.exists(path):
         raise ImportError(f"{path} is not built; run quantized_moe_expert_top_amd/build.py "
                           "(or __graft_entry__.build()) first")
     lib = ctypes.CDLL(path)
     vp, i32, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
+    i64, f32, mxd = ctypes.c_int64, ctypes.c_float, ctypes.POINTER(MxDesc)
     sig = {
         "moe_status_string": (ctypes.c_char_p, [i32]),
         "moe_last_error_detail": (ctypes.c_char_p, []),
@@ -78,6 +91,13 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "moe_grouped_qgemm_noalloc": (i32, [ctypes.POINTER(WDesc), vp, i32, vp, i32, vp, i32, i32, i32, vp, vp]),
         "moe_grouped_qgemm_noalloc_scratch_bytes": (sz, []),
         "moe_copy_rows_async": (i32, [vp, vp, sz, sz, sz, vp]),
+        "moe_route_scored": (i32, [vp, vp, i32, i32, i32, i32, i32, i32, i32, i32, f32, vp, vp, vp]),
+        "moe_quantize_mx": (i32, [vp, i32, i64, i32, i32, vp, vp, vp]),
+        "moe_dequantize_mx": (i32, [vp, vp, i64, i32, i32, i32, vp, vp]),
+        "moe_rmsnorm_mx": (i32, [vp, vp, vp, i32, i64, i32, f32, vp, vp, i32, vp, vp, vp]),
+        "moe_mx_field_bytes": (sz, [mxd, i32]),
+        "moe_mx_repack": (i32, [mxd, mxd, vp]),
+        "moe_grouped_mxgemm": (i32, [mxd, vp, vp, i32, i32, vp, i32, vp, i32, i32, i32, vp, vp, vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -427,3 +447,9 @@ def moe_layer_forward(x: torch.Tensor, logits: torch.Tensor, k: int, gate_up: Qu
     moe_unpermute_combine(buf.y_perm, buf.perm.pair_pos, buf.w, T, k, out=buf.out, stream=stream,
                           n_valid=buf.perm.seg_offsets[-1:])
     return buf
+
+
+from .mx import (  # noqa: E402  (the MX path builds on the names above)
+    MxExperts, MxLayerBuffers, MxRows, NormOutput, ScoredRouting, alloc_mx_layer, alloc_mx_rows, moe_dequantize_mx,
+    moe_grouped_mxgemm, moe_mx_field_bytes, moe_mx_layer_forward, moe_mx_repack, moe_quantize_mx, moe_rmsnorm_mx,
+    moe_route_scored, mx_experts)

@@ -11,11 +11,14 @@
 #include <string.h>
 
 #include "moe_qexpert.h"
+#include "abi_util.h"
 #include "launch.h"
 
 namespace {
 thread_local char g_detail[512] = "";
+}  // namespace
 
+namespace moe {
 moe_status fail(moe_status s, const char* fmt, ...) {
   va_list ap;
   va_start(ap, fmt);
@@ -31,9 +34,38 @@ moe_status hip_status(int e, const char* what) {
   if (e == 0) return ok();
   return fail(MOE_ERR_HIP, "%s: %s", what, moe::rt_error_string(e));
 }
-// Drops an error left pending by an earlier HIP call of the caller.
-void clear_pending() { (void)moe::rt_take_error(); }
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+
+namespace {
+// Drops an error left pending by an earlier HIP call of the caller.
+void clear_pending() { (void)rt_take_error(); }
+}  // namespace
+
+moe_status check_device() {
+  int dev = 0;
+  int e = rt_current_device(&dev);
+  if (e != 0) return fail(MOE_ERR_HIP, "current device: %s", rt_error_string(e));
+  static thread_local int checked_dev = -1;
+  if (checked_dev != dev) {
+    char arch[64] = "";
+    e = rt_device_arch(dev, arch, sizeof(arch));
+    if (e != 0) return fail(MOE_ERR_HIP, "device properties: %s", rt_error_string(e));
+    if (strncmp(arch, "gfx950", 6) != 0)
+      return fail(MOE_ERR_UNSUPPORTED, "device arch %s; this library is built for gfx950", arch);
+    checked_dev = dev;
+  }
+  clear_pending();
+  return MOE_OK;
+}
+}  // namespace moe
+
+using moe::aligned;
+using moe::check_device;
+using moe::fail;
+using moe::hip_status;
+using moe::ok;
+
+namespace {
 
 // Validates a weight descriptor; `tiled` selects which layout is expected.
 moe_status check_desc(const moe_wdesc* w, int layout, bool need_buffers) {
@@ -111,25 +143,6 @@ moe::QWeights to_q(const moe_wdesc* w) {
   q.sal_val = w->salient_val;
   q.base = w->base;
   return q;
-}
-
-// gfx950 check, once per device and thread, on the first launching call;
-// then any error left pending by the caller's earlier HIP calls is dropped.
-moe_status check_device() {
-  int dev = 0;
-  int e = moe::rt_current_device(&dev);
-  if (e != 0) return fail(MOE_ERR_HIP, "current device: %s", moe::rt_error_string(e));
-  static thread_local int checked_dev = -1;
-  if (checked_dev != dev) {
-    char arch[64] = "";
-    e = moe::rt_device_arch(dev, arch, sizeof(arch));
-    if (e != 0) return fail(MOE_ERR_HIP, "device properties: %s", moe::rt_error_string(e));
-    if (strncmp(arch, "gfx950", 6) != 0)
-      return fail(MOE_ERR_UNSUPPORTED, "device arch %s; this library is built for gfx950", arch);
-    checked_dev = dev;
-  }
-  clear_pending();
-  return MOE_OK;
 }
 }  // namespace
 

@@ -107,4 +107,62 @@ constexpr int kMaxMixedExperts = 256;
 int launch_repack(const QWeights& src, const QWeights& dst, void* stream);
 size_t tiled_salient_bytes(int E, int N, int n_sal);
 
+// ---------------------------------------------------------- scored routing
+struct ScoredArgs {
+  const float* logits;
+  const float* bias;  // or nullptr
+  int T, E, k;
+  int score;  // MOE_SCORE_*
+  int n_group, topk_group, group_top, renorm;
+  float scale;
+  int32_t* ids;
+  float* w;
+};
+int launch_route_scored(const ScoredArgs& a, void* stream);
+
+// ----------------------------------------------------------------- MX rows
+// dtypes MOE_DTYPE_*, fmt MOE_MX_*
+int launch_quantize_mx(const void* x, int x_dtype, int64_t rows, int K, int fmt, uint8_t* codes, uint8_t* scales,
+                       void* stream);
+int launch_dequantize_mx(const uint8_t* codes, const uint8_t* scales, int64_t rows, int K, int fmt, int out_dtype,
+                         void* out, void* stream);
+struct NormArgs {
+  const void* x;
+  const void* residual;  // or nullptr
+  const void* weight;
+  int dtype;
+  int64_t rows;
+  int H;
+  float eps;
+  void* sum;  // or nullptr
+  void* y;    // or nullptr
+  int fmt;    // MOE_MX_*, or 0: no MX output
+  uint8_t* codes;
+  uint8_t* scales;
+};
+constexpr int kNormMaxH = 16384;
+int launch_rmsnorm_mx(const NormArgs& a, void* stream);
+
+// -------------------------------------------------------- MX grouped product
+struct MxGemmArgs {
+  const uint8_t* wcodes;  // tiled
+  const uint8_t* wscales;
+  int E, N, K;
+  const uint8_t* a;
+  const uint8_t* as;
+  int a_fmt;  // MOE_MX_*
+  int A_rows;
+  const int32_t* gather;
+  int k;
+  const int32_t* seg;
+  int M_total;
+  int epilogue;
+  int kernel;  // MOE_KERNEL_*
+  void* out;
+  uint8_t* out_scales;
+};
+int launch_mx_repack(const uint8_t* codes, const uint8_t* scales, int E, int N, int K, uint8_t* tcodes,
+                     uint8_t* tscales, void* stream);
+int launch_mxgemm(const MxGemmArgs& a, void* stream);
+
 }  // namespace moe

@@ -1,0 +1,382 @@
+// MX rows: quantisation, its inverse, and the residual RMS norm that writes
+// them.  All three are one pass over memory; what bounds them is HBM.
+//
+// A block of 32 values belongs to 4 neighbouring lanes with 8 values each (one
+// 16-byte load of a 16-bit type per lane, a wavefront reads 1 KB in a row); its
+// largest magnitude is a maximum over the lane's 8 bit patterns and two DPP
+// quad permutes.  Magnitudes are compared as integers: that orders them like
+// the numbers and keeps infinities and NaN on top, where a float maximum would
+// drop a NaN.
+#include "mx.h"
+
+namespace moe {
+
+namespace {
+constexpr int kThreads = 256;
+constexpr int kUnroll = 4;  // 8-value groups per thread, all loads issued before the first is used
+typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+
+// 8 consecutive values as they are stored: 16 bytes (16-bit types) or 32.
+template <int DT>
+struct Raw8 {
+  u32x4 d[DT == 1 ? 2 : 1];
+};
+template <int DT>
+__device__ __forceinline__ Raw8<DT> load8(const void* x, size_t i8) {
+  Raw8<DT> r;
+  const u32x4* p = static_cast<const u32x4*>(x) + i8 * (DT == 1 ? 2 : 1);
+  r.d[0] = p[0];
+  if constexpr (DT == 1) r.d[1] = p[1];
+  return r;
+}
+template <int DT>
+__device__ __forceinline__ void unpack8(const Raw8<DT>& r, float v[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t w = r.d[0][i];
+    if constexpr (DT == 0) {
+      v[2 * i] = bf16_lo(w);
+      v[2 * i + 1] = bf16_hi(w);
+    } else if constexpr (DT == 2) {
+      v[2 * i] = f16_to_f32((uint16_t)(w & 0xFFFFu));
+      v[2 * i + 1] = f16_to_f32((uint16_t)(w >> 16));
+    } else {
+      const uint32_t w1 = r.d[1][i];
+      v[i] = __builtin_bit_cast(float, w);
+      v[4 + i] = __builtin_bit_cast(float, w1);
+    }
+  }
+}
+__device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
+__device__ __forceinline__ uint32_t pk_umax16(uint32_t a, uint32_t b) {
+  const u16x2 m = __builtin_elementwise_max(__builtin_bit_cast(u16x2, a), __builtin_bit_cast(u16x2, b));
+  return __builtin_bit_cast(uint32_t, m);
+}
+// fp32 bits of the largest magnitude of the lane's 8 values
+template <int DT>
+__device__ __forceinline__ uint32_t absmax8(const Raw8<DT>& r) {
+  if constexpr (DT == 1) {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t a = r.d[0][i], b = r.d[1][i];
+      m = umax(m, umax(a & 0x7FFFFFFFu, b & 0x7FFFFFFFu));
+    }
+    return m;
+  } else {
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t a = r.d[0][i];
+      m = pk_umax16(m, a & 0x7FFF7FFFu);
+    }
+    m = umax(m & 0xFFFFu, m >> 16);
+    return DT == 0 ? m << 16 : __builtin_bit_cast(uint32_t, f16_to_f32((uint16_t)m));
+  }
+}
+__device__ __forceinline__ uint32_t absmax8f(const float v[8]) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const float f = v[i];
+    m = umax(m, __builtin_bit_cast(uint32_t, f) & 0x7FFFFFFFu);
+  }
+  return m;
+}
+
+// Quantises the lane's 8 values (group i8 of the flat array) given its block's
+// largest magnitude; the quad's first lane writes the scale byte.
+template <int FMT>
+__device__ __forceinline__ void store_mx8(const float v[8], uint32_t mbits, size_t i8, uint8_t* __restrict__ codes,
+                                          uint8_t* __restrict__ scales) {
+  const int p = mx_exponent<FMT>(mbits);
+  const bool bad = mx_not_finite(mbits);
+  const float inv = mx_inverse(p);
+  float u[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) u[i] = bad ? 0.0f : v[i] * inv;
+  if constexpr (FMT == kE4M3) {
+    const u32x2 c = {mx_pack4_e4m3(u[0], u[1], u[2], u[3]), mx_pack4_e4m3(u[4], u[5], u[6], u[7])};
+    reinterpret_cast<u32x2*>(codes)[i8] = c;
+  } else {
+    reinterpret_cast<uint32_t*>(codes)[i8] =
+        mx_pack4_e2m1(u[0], u[1], u[2], u[3]) | (mx_pack4_e2m1(u[4], u[5], u[6], u[7]) << 16);
+  }
+  if ((threadIdx.x & 3) == 0) scales[i8 >> 2] = bad ? (uint8_t)255 : (uint8_t)(p + 127);
+}
+
+// n8: 8-value groups (a multiple of 4, so quads are whole).
+template <int DT, int FMT>
+__global__ __launch_bounds__(kThreads) void quantize_mx_kernel(const void* __restrict__ x, size_t n8,
+                                                               uint8_t* __restrict__ codes,
+                                                               uint8_t* __restrict__ scales) {
+  const size_t base = (size_t)blockIdx.x * (kThreads * kUnroll) + threadIdx.x;
+  Raw8<DT> r[kUnroll];
+#pragma unroll
+  for (int j = 0; j < kUnroll; ++j)
+    if (base + j * kThreads < n8) r[j] = load8<DT>(x, base + j * kThreads);
+#pragma unroll
+  for (int j = 0; j < kUnroll; ++j) {
+    const size_t i8 = base + j * kThreads;
+    if (i8 < n8) {
+      float v[8];
+      unpack8<DT>(r[j], v);
+      store_mx8<FMT>(v, quad_umax(absmax8<DT>(r[j])), i8, codes, scales);
+    }
+  }
+}
+
+template <int DT>
+__device__ __forceinline__ void store8(void* out, size_t i8, const float v[8]) {
+  u32x4* p = static_cast<u32x4*>(out) + i8 * (DT == 1 ? 2 : 1);
+  u32x4 o;
+  if constexpr (DT == 1) {
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float f = v[4 * h + i];
+        o[i] = __builtin_bit_cast(uint32_t, f);
+      }
+      p[h] = o;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      o[i] = DT == 0 ? pack_bf16x2(v[2 * i], v[2 * i + 1])
+                     : (uint32_t)f32_to_f16(v[2 * i]) | ((uint32_t)f32_to_f16(v[2 * i + 1]) << 16);
+    p[0] = o;
+  }
+}
+
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+template <int FMT, int DT>
+__global__ __launch_bounds__(kThreads) void dequantize_mx_kernel(const uint8_t* __restrict__ codes,
+                                                                 const uint8_t* __restrict__ scales, size_t n8,
+                                                                 void* __restrict__ out) {
+  const size_t base = (size_t)blockIdx.x * (kThreads * kUnroll) + threadIdx.x;
+  uint32_t lo[kUnroll], hi[kUnroll], sb[kUnroll];
+#pragma unroll
+  for (int j = 0; j < kUnroll; ++j) {
+    const size_t i8 = base + j * kThreads;
+    lo[j] = hi[j] = sb[j] = 0;
+    if (i8 < n8) {
+      if constexpr (FMT == kE4M3) {
+        const u32x2 c = reinterpret_cast<const u32x2*>(codes)[i8];
+        lo[j] = c[0];
+        hi[j] = c[1];
+      } else {
+        lo[j] = reinterpret_cast<const uint32_t*>(codes)[i8];
+      }
+      sb[j] = scales[i8 >> 2];
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < kUnroll; ++j) {
+    const size_t i8 = base + j * kThreads;
+    if (i8 >= n8) continue;
+    f32x2 e[4];
+    if constexpr (FMT == kE4M3) {
+      e[0] = __builtin_amdgcn_cvt_pk_f32_fp8((int)lo[j], false);
+      e[1] = __builtin_amdgcn_cvt_pk_f32_fp8((int)lo[j], true);
+      e[2] = __builtin_amdgcn_cvt_pk_f32_fp8((int)hi[j], false);
+      e[3] = __builtin_amdgcn_cvt_pk_f32_fp8((int)hi[j], true);
+    } else {
+      e[0] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(lo[j], 1.0f, 0);
+      e[1] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(lo[j], 1.0f, 1);
+      e[2] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(lo[j], 1.0f, 2);
+      e[3] = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(lo[j], 1.0f, 3);
+    }
+    // byte 0 is 2^-127 (subnormal), 255 is not a number
+    const uint32_t sbits = sb[j] == 0 ? 0x00400000u : sb[j] == 255 ? 0x7FC00000u : sb[j] << 23;
+    const float s = __builtin_bit_cast(float, sbits);
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = e[i][0] * s;
+      v[2 * i + 1] = e[i][1] * s;
+    }
+    store8<DT>(out, i8, v);
+  }
+}
+
+// ------------------------------------------------------------------- RMS norm
+// TPR threads hold one row in registers (NV groups of 8 values each), so x and
+// residual are read once: v = x + residual rounded to the row's type, the sum
+// of squares (fp32 in the lane, float64 across lanes), then
+// n = (v * weight) * factor.  v * weight of 16-bit values is exact in fp32
+// (8 + 8 or 11 + 11 significant bits) and the factor is a float64 split into two
+// floats, so n is within a hair of half an fp32 ulp: what is quantised next
+// falls on the same side of a rounding border as the exact value.
+template <int DT>
+__device__ __forceinline__ float round_to(float f) {
+  if constexpr (DT == 0) return bf16_to_f32(f32_to_bf16(f));
+  if constexpr (DT == 2) return f16_to_f32(f32_to_f16(f));
+  return f;
+}
+
+template <int DT, int FMT, int TPR, int NV>
+__global__ __launch_bounds__(kThreads) void rmsnorm_mx_kernel(NormArgs a) {
+  constexpr int kRows = kThreads / TPR, kWaves = TPR / 64;
+  __shared__ double part[kThreads / 64];
+  const int sub = threadIdx.x / TPR, t = threadIdx.x % TPR;
+  const size_t row = (size_t)blockIdx.x * kRows + sub;
+  const bool live = row < (size_t)a.rows;
+  const int n8 = a.H >> 3;
+  const size_t r8 = row * n8;
+  float v[NV][8];
+  float ss = 0.0f;
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int c = t + j * TPR;
+    const bool on = live && c < n8;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[j][i] = 0.0f;
+    if (on) {
+      unpack8<DT>(load8<DT>(a.x, r8 + c), v[j]);
+      if (a.residual) {
+        float q[8];
+        unpack8<DT>(load8<DT>(a.residual, r8 + c), q);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) v[j][i] = round_to<DT>(v[j][i] + q[i]);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) ss = __builtin_fmaf(v[j][i], v[j][i], ss);
+  }
+  double sum = (double)ss;
+#pragma unroll
+  for (int off = 32; off > 0; off >>= 1) sum += __shfl_xor(sum, off, 64);
+  if constexpr (kWaves > 1) {
+    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = sum;
+    __syncthreads();
+    sum = 0.0;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) sum += part[sub * kWaves + w];
+  }
+  const double f = 1.0 / sqrt(sum / a.H + (double)a.eps);
+  const float fhi = (float)f, flo = (float)(f - (double)fhi);
+#pragma unroll
+  for (int j = 0; j < NV; ++j) {
+    const int c = t + j * TPR;
+    if (!(live && c < n8)) continue;
+    if (a.sum) store8<DT>(a.sum, r8 + c, v[j]);
+    float w[8];
+    unpack8<DT>(load8<DT>(a.weight, c), w);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float m = v[j][i] * w[i];
+      const float hi = m * fhi;
+      v[j][i] = hi + __builtin_fmaf(m, flo, __builtin_fmaf(m, fhi, -hi));
+    }
+    if (a.y) store8<DT>(a.y, r8 + c, v[j]);
+    if constexpr (FMT != 0) store_mx8<FMT>(v[j], quad_umax(absmax8f(v[j])), r8 + c, a.codes, a.scales);
+  }
+}
+
+// ------------------------------------------------------------------- repack
+// One thread per 16-byte lane record of the tiled codes, resp. per 4-byte lane
+// record of the tiled scales (blocks past K are padded with 2^0).
+__global__ __launch_bounds__(kThreads) void mx_repack_codes_kernel(const uint8_t* __restrict__ src, size_t n, int N, int K,
+                                                                   uint8_t* __restrict__ dst) {
+  const size_t i = (size_t)blockIdx.x * kThreads + threadIdx.x;
+  if (i >= n) return;
+  const int lane = (int)(i & 63);
+  const size_t tk = i >> 6;  // (e, tile, step)
+  const int steps = K >> 6;
+  const size_t row = tk / steps * 32 + (lane & 31);
+  const size_t k0 = tk % steps * 64 + 32 * (lane >> 5);
+  reinterpret_cast<u32x4*>(dst)[i] = *reinterpret_cast<const u32x4*>(src + row * (size_t)(K >> 1) + (k0 >> 1));
+}
+__global__ __launch_bounds__(kThreads) void mx_repack_scales_kernel(const uint8_t* __restrict__ src, size_t n, int K,
+                                                                    uint8_t* __restrict__ dst) {
+  const size_t i = (size_t)blockIdx.x * kThreads + threadIdx.x;
+  if (i >= n) return;
+  const int lane = (int)(i & 63);
+  const int chunks = (K + 255) >> 8, nb = K >> 5;
+  const size_t row = (i >> 6) / chunks * 32 + (lane & 31);
+  const int b0 = (int)((i >> 6) % chunks) * 8 + (lane >> 5);
+  uint32_t v = 0;
+#pragma unroll
+  for (int s = 0; s < 4; ++s) {
+    const int b = b0 + 2 * s;
+    v |= (uint32_t)(b < nb ? src[row * nb + b] : 127) << (8 * s);
+  }
+  reinterpret_cast<uint32_t*>(dst)[i] = v;
+}
+
+inline unsigned blocks_for(size_t n, size_t per) { return (unsigned)((n + per - 1) / per); }
+
+template <int DT, int FMT>
+void norm_rows(const NormArgs& a, hipStream_t s) {
+  // Threads per row: the whole workgroup for a wide row (8 values per thread
+  // and step), one wavefront for narrow ones.
+#define MOE_NORM(TPR, NV)                                                                                    \
+  hipLaunchKernelGGL((rmsnorm_mx_kernel<DT, FMT, TPR, NV>), dim3(blocks_for(a.rows, kThreads / TPR)),        \
+                     dim3(kThreads), 0, s, a)
+  if (a.H <= 512) MOE_NORM(64, 1);
+  else if (a.H <= 2048) MOE_NORM(256, 1);
+  else if (a.H <= 4096) MOE_NORM(256, 2);
+  else if (a.H <= 8192) MOE_NORM(256, 4);
+  else MOE_NORM(256, 8);
+#undef MOE_NORM
+}
+template <int DT>
+void norm_fmt(const NormArgs& a, hipStream_t s) {
+  if (a.fmt == kE4M3) norm_rows<DT, kE4M3>(a, s);
+  else if (a.fmt == kE2M1) norm_rows<DT, kE2M1>(a, s);
+  else norm_rows<DT, 0>(a, s);
+}
+}  // namespace
+
+int launch_quantize_mx(const void* x, int x_dtype, int64_t rows, int K, int fmt, uint8_t* codes, uint8_t* scales,
+                       void* stream) {
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  const size_t n8 = (size_t)rows * K / 8;
+  const dim3 grid(blocks_for(n8, kThreads * kUnroll)), block(kThreads);
+#define MOE_Q(DT)                                                                                              \
+  if (fmt == kE4M3) hipLaunchKernelGGL((quantize_mx_kernel<DT, kE4M3>), grid, block, 0, s, x, n8, codes, scales); \
+  else hipLaunchKernelGGL((quantize_mx_kernel<DT, kE2M1>), grid, block, 0, s, x, n8, codes, scales)
+  if (x_dtype == 0) { MOE_Q(0); }
+  else if (x_dtype == 1) { MOE_Q(1); }
+  else { MOE_Q(2); }
+#undef MOE_Q
+  return (int)hipGetLastError();
+}
+
+int launch_dequantize_mx(const uint8_t* codes, const uint8_t* scales, int64_t rows, int K, int fmt, int out_dtype,
+                         void* out, void* stream) {
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  const size_t n8 = (size_t)rows * K / 8;
+  const dim3 grid(blocks_for(n8, kThreads * kUnroll)), block(kThreads);
+#define MOE_DQ(DT)                                                                                                \
+  if (fmt == kE4M3) hipLaunchKernelGGL((dequantize_mx_kernel<kE4M3, DT>), grid, block, 0, s, codes, scales, n8, out); \
+  else hipLaunchKernelGGL((dequantize_mx_kernel<kE2M1, DT>), grid, block, 0, s, codes, scales, n8, out)
+  if (out_dtype == 0) { MOE_DQ(0); }
+  else if (out_dtype == 1) { MOE_DQ(1); }
+  else { MOE_DQ(2); }
+#undef MOE_DQ
+  return (int)hipGetLastError();
+}
+
+int launch_rmsnorm_mx(const NormArgs& a, void* stream) {
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  if (a.dtype == 0) norm_fmt<0>(a, s);
+  else if (a.dtype == 1) norm_fmt<1>(a, s);
+  else norm_fmt<2>(a, s);
+  return (int)hipGetLastError();
+}
+
+int launch_mx_repack(const uint8_t* codes, const uint8_t* scales, int E, int N, int K, uint8_t* tcodes,
+                     uint8_t* tscales, void* stream) {
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  const size_t tiles = (size_t)E * (N / 32);
+  const size_t nc = tiles * (K / 64) * 64, ns = tiles * ((K + 255) / 256) * 64;
+  hipLaunchKernelGGL(mx_repack_codes_kernel, dim3(blocks_for(nc, kThreads)), dim3(kThreads), 0, s, codes, nc, N, K, tcodes);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return (int)e;
+  hipLaunchKernelGGL(mx_repack_scales_kernel, dim3(blocks_for(ns, kThreads)), dim3(kThreads), 0, s, scales, ns, K, tscales);
+  return (int)hipGetLastError();
+}
+
+}  // namespace moe

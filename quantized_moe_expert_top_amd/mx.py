@@ -1,0 +1,370 @@
+"""Binding of the library's scored routing and of its microscaled (MX) path:
+rows quantised to 8- or 4-bit MX blocks, the residual RMS norm that writes such
+rows, the experts' MX weights, their grouped product and the layer of all.
+
+Argument checks and marshalling only, as in the rest of the binding.  Every
+function runs on the device that holds its tensors, on that device's current
+stream unless `stream` is given; outputs it allocates belong to that stream.
+"""
+from __future__ import annotations
+
+import contextlib
+import ctypes
+from dataclasses import dataclass, field
+from typing import Optional, Union
+
+import torch
+
+from . import (MOE_ABI_VERSION, MOE_DTYPE_BF16, MOE_DTYPE_F16, MOE_DTYPE_F32, MOE_EPI_NONE, MOE_EPI_NONE_F16,
+               MOE_EPI_NONE_F32, MOE_EPI_SWIGLU, MOE_EPI_SWIGLU_E2M1, MOE_EPI_SWIGLU_E4M3, MOE_FIELD_CODES,
+               MOE_FIELD_SCALES, MOE_KERNEL_AUTO, MOE_LAYOUT_CANONICAL, MOE_LAYOUT_TILED, MOE_MX_E2M1, MOE_MX_E4M3,
+               MOE_SCORE_SIGMOID, MOE_SCORE_SOFTMAX, MxDesc, Permutation, _check, _DTYPE_EPI, lib, moe_permute,
+               moe_unpermute_combine)
+
+_DTYPES = {torch.bfloat16: MOE_DTYPE_BF16, torch.float32: MOE_DTYPE_F32, torch.float16: MOE_DTYPE_F16}
+_MX_EPI = {MOE_MX_E4M3: MOE_EPI_SWIGLU_E4M3, MOE_MX_E2M1: MOE_EPI_SWIGLU_E2M1}
+_EPI_FMT = {v: k for k, v in _MX_EPI.items()}
+_EPI_OUT = {MOE_EPI_NONE: torch.bfloat16, MOE_EPI_SWIGLU: torch.bfloat16, MOE_EPI_NONE_F32: torch.float32,
+            MOE_EPI_NONE_F16: torch.float16}
+
+
+# ------------------------------------------------------------------ plumbing
+def _device(*tensors: Optional[torch.Tensor]) -> torch.device:
+    """The one GPU that holds all of `tensors` (None entries aside), which must be contiguous."""
+    dev = None
+    for t in tensors:
+        if t is None:
+            continue
+        if not t.is_cuda:
+            raise ValueError("tensor must live on the GPU")
+        if not t.is_contiguous():
+            raise ValueError("tensor must be contiguous")
+        if dev is None:
+            dev = t.device
+        elif t.device != dev:
+            raise ValueError(f"tensors on {dev} and {t.device}")
+    return dev
+
+
+def _p(t: Optional[torch.Tensor]) -> Optional[int]:
+    return None if t is None else t.data_ptr()
+
+
+def _guard(dev: torch.device, stream):
+    """Makes `dev` current (and `stream`, if given, the stream that allocations belong to)."""
+    if stream is not None:
+        if stream.device != dev:
+            raise ValueError(f"stream of {stream.device} for tensors on {dev}")
+        return torch.cuda.stream(stream)
+    if dev.index != torch.cuda.current_device():
+        return torch.cuda.device(dev)
+    return contextlib.nullcontext()
+
+
+def _call(name: str, *args) -> None:
+    _check(getattr(lib(), name)(*args, torch.cuda.current_stream().cuda_stream), name)
+
+
+def _want(t: torch.Tensor, what: str, dtype: torch.dtype, shape: tuple) -> torch.Tensor:
+    if t.dtype != dtype or tuple(t.shape) != shape:
+        raise ValueError(f"{what} must be {dtype} of shape {shape} (got {t.dtype}, {tuple(t.shape)})")
+    return t
+
+
+# ------------------------------------------------------------ scored routing
+@dataclass
+class ScoredRouting:
+    """How moe_route_scored chooses experts; the defaults are softmax scores, renormalised over the chosen."""
+    score: int = MOE_SCORE_SOFTMAX
+    bias: Optional[torch.Tensor] = None
+    n_group: int = 1
+    topk_group: int = 1
+    group_top: int = 1
+    renormalize: bool = True
+    scale: float = 1.0
+
+
+def moe_route_scored(logits: torch.Tensor, k: int, score: int = MOE_SCORE_SOFTMAX, bias: torch.Tensor = None,
+                     n_group: int = 1, topk_group: int = 1, group_top: int = 1, renormalize: bool = True,
+                     scale: float = 1.0, ids: torch.Tensor = None, w: torch.Tensor = None, stream=None):
+    """Top-k experts by score (MOE_SCORE_*) plus choice bias, within the best expert groups; returns
+    (ids int32 [T][k], w float32 [T][k]).  Slots without an eligible expert hold id -1 and weight 0."""
+    if logits.dtype != torch.float32 or logits.dim() != 2:
+        raise ValueError("logits must be float32 [T][E]")
+    T, E = logits.shape
+    if bias is not None:
+        _want(bias, "bias", torch.float32, (E,))
+    with _guard(_device(logits, bias, ids, w), stream):
+        ids = torch.empty((T, k), dtype=torch.int32, device=logits.device) if ids is None else \
+            _want(ids, "ids", torch.int32, (T, k))
+        w = torch.empty((T, k), dtype=torch.float32, device=logits.device) if w is None else \
+            _want(w, "w", torch.float32, (T, k))
+        _call("moe_route_scored", _p(logits), _p(bias), T, E, k, score, n_group, topk_group, group_top,
+              int(bool(renormalize)), float(scale), _p(ids), _p(w))
+    return ids, w
+
+
+# ------------------------------------------------------------------- MX rows
+@dataclass
+class MxRows:
+    """Rows in MX blocks of 32: codes uint8 [...][K] (MOE_MX_E4M3) or [...][K/2] (MOE_MX_E2M1), scales uint8
+    [...][K/32]."""
+    codes: torch.Tensor
+    scales: torch.Tensor
+    fmt: int
+
+    def __post_init__(self):
+        if self.fmt not in _MX_EPI:
+            raise ValueError(f"unknown MX format {self.fmt}")
+        if self.codes.dtype != torch.uint8 or self.scales.dtype != torch.uint8:
+            raise ValueError("MX codes and scales are uint8")
+        if self.codes.dim() < 1 or tuple(self.codes.shape) != _mx_shape(tuple(self.scales.shape[:-1]) + (self.K,), self.fmt):
+            raise ValueError(f"codes {tuple(self.codes.shape)} and scales {tuple(self.scales.shape)} do not match")
+
+    @property
+    def K(self) -> int:
+        return 32 * self.scales.shape[-1]
+
+    @property
+    def shape(self) -> tuple:
+        return tuple(self.scales.shape[:-1]) + (self.K,)
+
+
+def _mx_shape(shape: tuple, fmt: int) -> tuple:
+    return shape if fmt == MOE_MX_E4M3 else shape[:-1] + (shape[-1] // 2,)
+
+
+def alloc_mx_rows(shape: tuple, fmt: int, device) -> MxRows:
+    """Uninitialised MX rows of `shape` (the last dimension a multiple of 32)."""
+    if not shape or shape[-1] < 32 or shape[-1] % 32:
+        raise ValueError(f"the last dimension of {tuple(shape)} must be a positive multiple of 32")
+    if fmt not in _MX_EPI:
+        raise ValueError(f"unknown MX format {fmt}")
+    return MxRows(torch.empty(_mx_shape(tuple(shape), fmt), dtype=torch.uint8, device=device),
+                  torch.empty(tuple(shape[:-1]) + (shape[-1] // 32,), dtype=torch.uint8, device=device), fmt)
+
+
+def _rows_out(out: Optional[MxRows], shape: tuple, fmt: int, device) -> MxRows:
+    if out is None:
+        return alloc_mx_rows(shape, fmt, device)
+    if out.fmt != fmt or out.shape != shape:
+        raise ValueError(f"out holds MX rows {out.shape} of format {out.fmt}, not {shape} of {fmt}")
+    return out
+
+
+def _count(shape: tuple) -> int:
+    n = 1
+    for v in shape[:-1]:
+        n *= v
+    return n
+
+
+def moe_quantize_mx(x: torch.Tensor, fmt: int = MOE_MX_E4M3, out: MxRows = None, stream=None) -> MxRows:
+    """bf16, fp16 or fp32 [...][K] -> MX rows."""
+    if x.dtype not in _DTYPES or x.dim() < 1:
+        raise ValueError(f"x must be bfloat16, float16 or float32 rows (got {x.dtype}, {tuple(x.shape)})")
+    shape = tuple(x.shape)
+    with _guard(_device(x, *((out.codes, out.scales) if out else ())), stream):
+        out = _rows_out(out, shape, fmt, x.device)
+        _call("moe_quantize_mx", _p(x), _DTYPES[x.dtype], _count(shape), shape[-1], fmt, _p(out.codes), _p(out.scales))
+    return out
+
+
+def moe_dequantize_mx(rows: MxRows, dtype: torch.dtype = torch.bfloat16, out: torch.Tensor = None,
+                      stream=None) -> torch.Tensor:
+    """The values that MX rows stand for."""
+    shape = rows.shape
+    if out is not None:
+        dtype = out.dtype
+    if dtype not in _DTYPES:
+        raise ValueError(f"values in {dtype}: bfloat16, float16 or float32")
+    with _guard(_device(rows.codes, rows.scales, out), stream):
+        out = torch.empty(shape, dtype=dtype, device=rows.codes.device) if out is None else _want(out, "out", dtype, shape)
+        _call("moe_dequantize_mx", _p(rows.codes), _p(rows.scales), _count(shape), shape[-1], rows.fmt, _DTYPES[dtype],
+              _p(out))
+    return out
+
+
+@dataclass
+class NormOutput:
+    sum: Optional[torch.Tensor]  # x + residual (None without residual)
+    y: Optional[torch.Tensor]    # the norm in x's type (None unless wanted)
+    rows: Optional[MxRows]       # the norm as MX rows (None without a format)
+
+
+def moe_rmsnorm_mx(x: torch.Tensor, weight: torch.Tensor, eps: float, residual: torch.Tensor = None,
+                   fmt: Optional[int] = MOE_MX_E4M3, want_y: bool = False, sum: torch.Tensor = None,
+                   y: torch.Tensor = None, out: MxRows = None, stream=None) -> NormOutput:
+    """Root-mean-square norm of x + residual times weight, in one pass: the sum (with a residual; `sum` may be
+    x's or residual's own buffer), the norm in x's type (want_y, or a `y` to write) and the norm as MX rows
+    of `fmt` (None: no MX rows)."""
+    if x.dtype not in _DTYPES or x.dim() < 1:
+        raise ValueError(f"x must be bfloat16, float16 or float32 rows (got {x.dtype}, {tuple(x.shape)})")
+    shape = tuple(x.shape)
+    _want(weight, "weight", x.dtype, shape[-1:])
+    if residual is not None:
+        _want(residual, "residual", x.dtype, shape)
+    elif sum is not None:
+        raise ValueError("sum without residual")
+    if out is not None and fmt is None:
+        raise ValueError("out without an MX format")
+    with _guard(_device(x, weight, residual, sum, y, *((out.codes, out.scales) if out else ())), stream):
+        if residual is not None:
+            sum = torch.empty_like(x) if sum is None else _want(sum, "sum", x.dtype, shape)
+        if y is not None:
+            _want(y, "y", x.dtype, shape)
+        elif want_y:
+            y = torch.empty_like(x)
+        rows = None if fmt is None else _rows_out(out, shape, fmt, x.device)
+        _call("moe_rmsnorm_mx", _p(x), _p(residual), _p(weight), _DTYPES[x.dtype], _count(shape), shape[-1], float(eps),
+              _p(sum), _p(y), fmt or 0, _p(rows.codes) if rows else None, _p(rows.scales) if rows else None)
+    return NormOutput(sum, y, rows)
+
+
+# ---------------------------------------------------------------- MX experts
+@dataclass
+class MxExperts:
+    """MX expert weights in one layout; keeps its tensors alive with the descriptor."""
+    desc: MxDesc
+    tensors: dict = field(default_factory=dict)
+
+    @property
+    def N(self) -> int:
+        return self.desc.N
+
+    @property
+    def K(self) -> int:
+        return self.desc.K
+
+
+def _mx_desc(layout: int, E: int, N: int, K: int, codes=None, scales=None) -> MxExperts:
+    d = MxDesc()
+    d.abi_version, d.layout, d.E, d.N, d.K = MOE_ABI_VERSION, layout, E, N, K
+    d.codes, d.scales = _p(codes), _p(scales)
+    return MxExperts(d, {k: v for k, v in (("codes", codes), ("scales", scales)) if v is not None})
+
+
+def mx_experts(codes: Union[torch.Tensor, MxRows], scales: torch.Tensor = None) -> MxExperts:
+    """Canonical MX expert weights: codes u8 [E][N][K/2] and scales u8 [E][N][K/32], or the MX rows
+    [E][N][K] that moe_quantize_mx gives (MOE_MX_E2M1)."""
+    rows = codes if isinstance(codes, MxRows) else MxRows(codes, scales, MOE_MX_E2M1)
+    if rows.fmt != MOE_MX_E2M1 or len(rows.shape) != 3:
+        raise ValueError(f"expert weights are 4-bit MX rows [E][N][K] (got {rows.shape}, format {rows.fmt})")
+    _device(rows.codes, rows.scales)
+    return _mx_desc(MOE_LAYOUT_CANONICAL, *rows.shape, rows.codes, rows.scales)
+
+
+def moe_mx_field_bytes(w: MxExperts, fld: int) -> int:
+    return lib().moe_mx_field_bytes(ctypes.byref(w.desc), fld)
+
+
+def moe_mx_repack(src: MxExperts, stream=None) -> MxExperts:
+    """Canonical -> tiled copy of MX expert weights (offline; allocates the tiled buffers)."""
+    s = src.desc
+    dev = _device(*src.tensors.values())
+    with _guard(dev, stream):
+        probe = _mx_desc(MOE_LAYOUT_TILED, s.E, s.N, s.K)
+        # (an invalid descriptor has 0 bytes; the call below says why)
+        t = [torch.empty(max(moe_mx_field_bytes(probe, f), 16), dtype=torch.uint8, device=dev)
+             for f in (MOE_FIELD_CODES, MOE_FIELD_SCALES)]
+        dst = _mx_desc(MOE_LAYOUT_TILED, s.E, s.N, s.K, *t)
+        _call("moe_mx_repack", ctypes.byref(s), ctypes.byref(dst.desc))
+    return dst
+
+
+def moe_grouped_mxgemm(w: MxExperts, A: MxRows, seg_offsets: torch.Tensor, M_total: int,
+                       epilogue: int = MOE_EPI_NONE, gather_pair: torch.Tensor = None, k: int = 1,
+                       out: Union[torch.Tensor, MxRows] = None, stream=None, kernel: int = MOE_KERNEL_AUTO):
+    """Grouped product of MX rows A [A_rows][K] with tiled MX experts; `out` (and the result) is a tensor, or MX
+    rows for MOE_EPI_SWIGLU_E4M3 / MOE_EPI_SWIGLU_E2M1."""
+    d = w.desc
+    if len(A.shape) != 2 or A.K != d.K:
+        raise ValueError(f"A must be MX rows [A_rows][{d.K}] (got {A.shape})")
+    if seg_offsets.dtype != torch.int32 or seg_offsets.dim() != 1 or seg_offsets.numel() < d.E + 1:
+        raise ValueError(f"seg_offsets must be int32 with at least {d.E + 1} entries (got {seg_offsets.dtype}, "
+                         f"{tuple(seg_offsets.shape)})")
+    if gather_pair is not None and (gather_pair.dtype != torch.int32 or gather_pair.numel() < M_total):
+        raise ValueError(f"gather_pair must be int32 with at least M_total = {M_total} entries")
+    fmt = _EPI_FMT.get(epilogue)
+    if fmt is None and epilogue not in _EPI_OUT:
+        raise ValueError(f"unknown epilogue {epilogue}")
+    n_out = d.N if epilogue in _DTYPE_EPI.values() else d.N // 2
+    if (isinstance(out, MxRows) if fmt is None else out is not None and not isinstance(out, MxRows)):
+        raise ValueError("out must be MX rows exactly for the MX epilogues")
+    bufs = (out.codes, out.scales) if isinstance(out, MxRows) else (out,)
+    with _guard(_device(A.codes, A.scales, seg_offsets, gather_pair, *w.tensors.values(), *bufs), stream):
+        if fmt is not None:
+            out = _rows_out(out, (M_total, n_out), fmt, A.codes.device)
+            ptrs = _p(out.codes), _p(out.scales)
+        else:
+            out = torch.empty((M_total, n_out), dtype=_EPI_OUT[epilogue], device=A.codes.device) if out is None else \
+                _want(out, "out", _EPI_OUT[epilogue], (M_total, n_out))
+            ptrs = _p(out), None
+        _call("moe_grouped_mxgemm", ctypes.byref(d), _p(A.codes), _p(A.scales), A.fmt, A.shape[0], _p(gather_pair), k,
+              _p(seg_offsets), M_total, epilogue, kernel, *ptrs)
+    return out
+
+
+# --------------------------------------------------------------------- layer
+@dataclass
+class MxLayerBuffers:
+    """Preallocated intermediates of one MX layer forward."""
+    sizes: tuple  # (T, E, k, H, I)
+    ids: torch.Tensor
+    w: torch.Tensor
+    perm: Permutation
+    x: MxRows
+    h: MxRows
+    y_perm: torch.Tensor
+    out: torch.Tensor
+
+
+def alloc_mx_layer(T: int, E: int, k: int, H: int, I: int, device, act: int = MOE_MX_E4M3, h_fmt: int = MOE_MX_E4M3,
+                   y_dtype: torch.dtype = torch.float16) -> MxLayerBuffers:
+    """act: MX format of the layer's input rows; h_fmt: of the SwiGLU activations; y_dtype: the experts' outputs
+    before the combine."""
+    if y_dtype not in _DTYPE_EPI:
+        raise ValueError(f"expert outputs in {y_dtype}: float16, float32 or bfloat16")
+    i32 = dict(dtype=torch.int32, device=device)
+    perm = Permutation(counts=torch.empty(E, **i32), seg_offsets=torch.empty(E + 1, **i32),
+                       sorted_pair=torch.empty(T * k, **i32), pair_pos=torch.empty(T * k, **i32),
+                       workspace=torch.zeros(max(lib().moe_permute_workspace_size(T, k, E, 1), 16), dtype=torch.uint8,
+                                             device=device))
+    return MxLayerBuffers(sizes=(T, E, k, H, I), ids=torch.empty((T, k), **i32),
+                          w=torch.empty((T, k), dtype=torch.float32, device=device), perm=perm,
+                          x=alloc_mx_rows((T, H), act, device), h=alloc_mx_rows((T * k, I), h_fmt, device),
+                          y_perm=torch.empty((T * k, H), dtype=y_dtype, device=device),
+                          out=torch.empty((T, H), dtype=torch.bfloat16, device=device))
+
+
+def moe_mx_layer_forward(x: Union[torch.Tensor, MxRows], logits: torch.Tensor, k: int, gate_up: MxExperts,
+                         down: MxExperts, routing: ScoredRouting = None, buf: MxLayerBuffers = None, stream=None,
+                         kernel: int = MOE_KERNEL_AUTO) -> MxLayerBuffers:
+    """Scored routing -> grouping -> gate_up with SwiGLU, its activations quantised to MX rows -> down -> combine,
+    one stream.  x: bf16, fp16 or fp32 [T][H], quantised to buf.x's format, or MX rows (moe_rmsnorm_mx)."""
+    T, H = x.shape
+    E = logits.shape[1]
+    I = gate_up.N // 2
+    if gate_up.desc.E != E or down.desc.E != E or gate_up.K != H or down.N != H or down.K != I or logits.shape[0] != T:
+        raise ValueError(f"x [{T}][{H}], logits {tuple(logits.shape)}, gate_up [{gate_up.desc.E}][{gate_up.N}]"
+                         f"[{gate_up.K}] and down [{down.desc.E}][{down.N}][{down.K}] do not fit together")
+    rows = x if isinstance(x, MxRows) else None
+    dev = (rows.codes if rows else x).device
+    r = routing or ScoredRouting()
+    with _guard(dev, stream):
+        if buf is None:
+            buf = alloc_mx_layer(T, E, k, H, I, dev, act=rows.fmt if rows else MOE_MX_E4M3)
+        elif buf.sizes != (T, E, k, H, I):
+            raise ValueError(f"buffers of (T, E, k, H, I) = {buf.sizes} for a layer of {(T, E, k, H, I)}")
+        moe_route_scored(logits, k, r.score, r.bias, r.n_group, r.topk_group, r.group_top, r.renormalize, r.scale,
+                         ids=buf.ids, w=buf.w)
+        moe_permute(buf.ids, E, out=buf.perm)
+        if rows is None:
+            rows = moe_quantize_mx(x, buf.x.fmt, out=buf.x)
+        moe_grouped_mxgemm(gate_up, rows, buf.perm.seg_offsets, T * k, _MX_EPI[buf.h.fmt],
+                           gather_pair=buf.perm.sorted_pair, k=k, out=buf.h, kernel=kernel)
+        moe_grouped_mxgemm(down, buf.h, buf.perm.seg_offsets, T * k, _DTYPE_EPI[buf.y_perm.dtype], out=buf.y_perm,
+                           kernel=kernel)
+        moe_unpermute_combine(buf.y_perm, buf.perm.pair_pos, buf.w, T, k, out=buf.out,
+                              n_valid=buf.perm.seg_offsets[-1:])
+    return buf
