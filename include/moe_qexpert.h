@@ -442,11 +442,12 @@ moe_status moe_rmsnorm_mx(const void* x, const void* residual, const void* weigh
  * Expert weights as MX rows of 4-bit elements along K:
  *   MOE_LAYOUT_CANONICAL  codes u8 [E][N][K/2], scales u8 [E][N][K/32]
  *   MOE_LAYOUT_TILED      (moe_mx_repack) tiles of 32 output channels in the
- *       operand order of the scaled MFMA: codes [E][N/32][K/64][64 lanes][16 B],
- *       lane l = channel l % 32, inputs 32*(l/32) .. +31 of the 64; scales
- *       [E][N/32][ceil(K/256)][64 lanes][4 B], byte s of lane l = the scale of
- *       channel l % 32, block 2*s + l/32 of the 8 blocks.
- * N % 32 == 0, K % 128 == 0, E <= 1024, N * K < 2^32.
+ *       operand order of the scaled MFMA, K padded with zeros to C = ceil(K/256)
+ *       chunks of 256: codes [E][N/32][C][4 steps][64 lanes][16 B], lane l =
+ *       channel l % 32, inputs 32*(l/32) .. +31 of the step's 64; scales
+ *       [E][N/32][C][64 lanes][4 B], byte s of lane l = the scale of channel
+ *       l % 32, block 2*s + l/32 of the chunk's 8.
+ * N % 32 == 0, K % 128 == 0, E <= 1024, N * (K + 128) < 2^32.
  */
 typedef struct moe_mxdesc {
   int32_t abi_version; /* MOE_ABI_VERSION */

@@ -35,7 +35,7 @@ moe_status check_mxdesc(const moe_mxdesc* w, int layout, bool need_buffers) {
     return fail(MOE_ERR_BAD_SHAPE, "E=%d N=%d K=%d out of range", w->E, w->N, w->K);
   if (w->N % 32 != 0 || w->K % 128 != 0)
     return fail(MOE_ERR_UNSUPPORTED, "N=%d must be a multiple of 32 and K=%d of 128", w->N, w->K);
-  if ((int64_t)w->N * w->K >= ((int64_t)1 << 32)) return fail(MOE_ERR_BAD_SHAPE, "weights too large");
+  if ((int64_t)w->N * (w->K + 128) >= ((int64_t)1 << 32)) return fail(MOE_ERR_BAD_SHAPE, "weights too large");
   if (!need_buffers) return MOE_OK;
   if (!w->codes || !w->scales) return fail(MOE_ERR_NULL_ARG, "codes or scales is NULL");
   if (!aligned(w->codes, 16)) return fail(MOE_ERR_MISALIGNED, "codes must be 16-byte aligned");
@@ -128,9 +128,9 @@ moe_status moe_rmsnorm_mx(const void* x, const void* residual, const void* weigh
 size_t moe_mx_field_bytes(const moe_mxdesc* w, int32_t field) {
   if (check_mxdesc(w, w ? w->layout : 0, false) != MOE_OK) return 0;
   const size_t EN = (size_t)w->E * w->N;
-  if (field == MOE_FIELD_CODES) return EN * w->K / 2;
-  if (field == MOE_FIELD_SCALES)
-    return w->layout == MOE_LAYOUT_TILED ? EN / 32 * ((w->K + 255) / 256) * 256 : EN * (w->K / 32);
+  const size_t K = w->layout == MOE_LAYOUT_TILED ? ((size_t)w->K + 255) / 256 * 256 : (size_t)w->K;
+  if (field == MOE_FIELD_CODES) return EN * K / 2;
+  if (field == MOE_FIELD_SCALES) return EN * K / 32;
   return 0;
 }
 

@@ -276,17 +276,19 @@ __global__ __launch_bounds__(kThreads) void rmsnorm_mx_kernel(NormArgs a) {
 
 // ------------------------------------------------------------------- repack
 // One thread per 16-byte lane record of the tiled codes, resp. per 4-byte lane
-// record of the tiled scales (blocks past K are padded with 2^0).
-__global__ __launch_bounds__(kThreads) void mx_repack_codes_kernel(const uint8_t* __restrict__ src, size_t n, int N, int K,
+// record of the tiled scales.  K is padded to whole chunks of 256 with zeros
+// under the scale 2^0.
+__global__ __launch_bounds__(kThreads) void mx_repack_codes_kernel(const uint8_t* __restrict__ src, size_t n, int K,
                                                                    uint8_t* __restrict__ dst) {
   const size_t i = (size_t)blockIdx.x * kThreads + threadIdx.x;
   if (i >= n) return;
   const int lane = (int)(i & 63);
   const size_t tk = i >> 6;  // (e, tile, step)
-  const int steps = K >> 6;
+  const int steps = (K + 255) >> 8 << 2;
   const size_t row = tk / steps * 32 + (lane & 31);
   const size_t k0 = tk % steps * 64 + 32 * (lane >> 5);
-  reinterpret_cast<u32x4*>(dst)[i] = *reinterpret_cast<const u32x4*>(src + row * (size_t)(K >> 1) + (k0 >> 1));
+  reinterpret_cast<u32x4*>(dst)[i] =
+      k0 < (size_t)K ? *reinterpret_cast<const u32x4*>(src + row * (size_t)(K >> 1) + (k0 >> 1)) : u32x4{};
 }
 __global__ __launch_bounds__(kThreads) void mx_repack_scales_kernel(const uint8_t* __restrict__ src, size_t n, int K,
                                                                     uint8_t* __restrict__ dst) {
@@ -371,8 +373,8 @@ int launch_mx_repack(const uint8_t* codes, const uint8_t* scales, int E, int N, 
                      uint8_t* tscales, void* stream) {
   const hipStream_t s = static_cast<hipStream_t>(stream);
   const size_t tiles = (size_t)E * (N / 32);
-  const size_t nc = tiles * (K / 64) * 64, ns = tiles * ((K + 255) / 256) * 64;
-  hipLaunchKernelGGL(mx_repack_codes_kernel, dim3(blocks_for(nc, kThreads)), dim3(kThreads), 0, s, codes, nc, N, K, tcodes);
+  const size_t nc = tiles * ((K + 255) / 256) * 256, ns = tiles * ((K + 255) / 256) * 64;
+  hipLaunchKernelGGL(mx_repack_codes_kernel, dim3(blocks_for(nc, kThreads)), dim3(kThreads), 0, s, codes, nc, K, tcodes);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return (int)e;
   hipLaunchKernelGGL(mx_repack_scales_kernel, dim3(blocks_for(ns, kThreads)), dim3(kThreads), 0, s, scales, ns, K, tscales);

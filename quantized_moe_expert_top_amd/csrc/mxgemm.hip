@@ -12,6 +12,8 @@
 //   scale   one byte of a register (op_sel): block h (inputs 32h .. 32h + 31)
 //   result  register r of lane l: channel 8*(r/4) + 4*h + r%4, token l % 32
 // (checked lane by lane against the formula for all four format pairs).
+#include <type_traits>
+
 #include "mx.h"
 
 namespace moe {
@@ -68,6 +70,18 @@ __device__ __forceinline__ int source_row(const MxK& p, int row) {
   const int r = p.gather ? p.gather[row] / p.k : row;
   return min(max(r, 0), p.A_rows - 1);
 }
+// The same for several rows at once (one wait for all of the table's entries).
+template <int N>
+__device__ __forceinline__ void source_rows(const MxK& p, int (&row)[N]) {
+  if (p.gather) {
+#pragma unroll
+    for (int i = 0; i < N; ++i) row[i] = p.gather[row[i]];
+#pragma unroll
+    for (int i = 0; i < N; ++i) row[i] = row[i] / p.k;
+  }
+#pragma unroll
+  for (int i = 0; i < N; ++i) row[i] = min(max(row[i], 0), p.A_rows - 1);
+}
 
 // -------------------------------------------------------- few rows per expert
 // A workgroup takes 64 output channels of one expert (SwiGLU: 32 gate and the
@@ -97,7 +111,7 @@ __global__ __launch_bounds__(64 * NW) void mx_small_kernel(MxK p) {
   const int NT = p.N >> 5, KB = p.K >> 7, KC = (p.K + 255) >> 8;
   const int t0 = is_swiglu(EPI) ? blockIdx.x : 2 * blockIdx.x;
   const int t1 = is_swiglu(EPI) ? NT / 2 + blockIdx.x : min(2 * (int)blockIdx.x + 1, NT - 1);
-  const size_t tile_bytes = (size_t)p.K * 16;  // 32 channels of e2m1
+  const size_t tile_bytes = (size_t)KC * 4096;  // 32 channels of e2m1, K in whole chunks of 256
   const rsrc_t wr0 = make_rsrc(p.wc + ((size_t)e * NT + t0) * tile_bytes, (uint32_t)tile_bytes);
   const rsrc_t wr1 = make_rsrc(p.wc + ((size_t)e * NT + t1) * tile_bytes, (uint32_t)tile_bytes);
   const rsrc_t sr0 = make_rsrc(p.wsc + ((size_t)e * NT + t0) * KC * 256, KC * 256);
@@ -246,6 +260,333 @@ __global__ __launch_bounds__(64 * NW) void mx_small_kernel(MxK p) {
   }
 }
 
+// ------------------------------------------------------- many rows per expert
+// A workgroup of 4 wavefronts takes TM rows of one expert and 8 channel tiles
+// (256 channels; SwiGLU: 128 gate and the matching 128 up channels); a
+// wavefront takes 64 rows and CT of the tiles.  K advances 128 at a time
+// through two LDS stages filled by LDS-DMA: while a stage is multiplied the
+// other one loads.  Two workgroups share a CU, so one multiplies while the
+// other waits at its barrier.
+//
+// Rows in LDS: 16-byte chunks, chunk c of row r at place c ^ swizzle(r), so that
+// the lanes of a fragment read (32 rows, one chunk) fall on different banks,
+// whether 8 or 16 of them are served at once.  A DMA writes 64 chunks in a row,
+// so the lanes fetch them in swizzled order.
+template <int AF>
+__device__ __forceinline__ int swizzle(int row) {
+  return AF == kE4M3 ? ((row & 7) ^ ((row >> 3) & 1)) : (((row >> 1) & 3) ^ ((row >> 3) & 1));
+}
+
+template <int N>
+__device__ __forceinline__ void vm_wait() {
+  __builtin_amdgcn_s_waitcnt(0x0F70 | (N & 15) | ((N >> 4) << 14));  // expcnt, lgkmcnt: no wait
+}
+
+// Which (segment, row tile, channel block) workgroup `id` takes.  Tiles are
+// numbered expert by expert, within an expert in groups of 8 row tiles by
+// channel block, and each XCD (workgroups are dealt to the 8 of them in turn)
+// takes a contiguous range: the weights and rows its CUs share stay in its L2.
+struct TileAt {
+  int e, r0, s1, nb;  // e < 0: nothing to do
+};
+template <int TM>
+__device__ __forceinline__ TileAt find_tile(const MxK& p, int id, int n_nb) {
+  const int lane = threadIdx.x & 63;
+  int total = 0;  // row tiles of all segments
+  for (int e0 = 0; e0 < p.E; e0 += 64) {
+    int s0 = 0, s1 = 0;
+    if (e0 + lane < p.E) segment(p, e0 + lane, s0, s1);
+    int n = (s1 - s0 + TM - 1) / TM;
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) n += __shfl_xor(n, off, 64);
+    total += __builtin_amdgcn_readfirstlane(n);
+  }
+  TileAt t{-1, 0, 0, 0};
+  const int64_t wgs = (int64_t)total * n_nb;
+  const int64_t per = (wgs + 7) >> 3;
+  int64_t idx = (int64_t)(id & 7) * per + (id >> 3);
+  if ((id >> 3) >= per || idx >= wgs) return t;
+  for (int e0 = 0; e0 < p.E; e0 += 64) {
+    int s0 = 0, s1 = 0;
+    if (e0 + lane < p.E) segment(p, e0 + lane, s0, s1);
+    const int n = (s1 - s0 + TM - 1) / TM;
+    int before = n;  // inclusive scan, then exclusive
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+      const int o = __shfl_up(before, off, 64);
+      if (lane >= off) before += o;
+    }
+    const int sum = __builtin_amdgcn_readlane(before, 63);
+    before -= n;
+    if (idx >= (int64_t)sum * n_nb) {
+      idx -= (int64_t)sum * n_nb;
+      continue;
+    }
+    const bool mine = idx >= (int64_t)before * n_nb && idx < (int64_t)(before + n) * n_nb;
+    const int src = __builtin_ctzll(__ballot(mine));
+    const int j = (int)(idx - (int64_t)__builtin_amdgcn_readlane(before, src) * n_nb);
+    const int tiles = __builtin_amdgcn_readlane(n, src);
+    const int g = j / (8 * n_nb), gm = min(8, tiles - 8 * g);
+    const int in = j - g * 8 * n_nb;
+    t.e = e0 + src;
+    t.nb = in / gm;
+    t.r0 = __builtin_amdgcn_readlane(s0, src) + (8 * g + in % gm) * TM;
+    t.s1 = __builtin_amdgcn_readlane(s1, src);
+    break;
+  }
+  return t;
+}
+
+// Exchanges halves of the wavefront: afterwards a holds (a's low half, b's low
+// half) and b (a's high half, b's high half) in lanes (0..31, 32..63).
+__device__ __forceinline__ void swap_halves(uint32_t& a, uint32_t& b) {
+  const auto r = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+  a = r[0];
+  b = r[1];
+}
+
+// One tile of 32 channels x 32 tokens as the accumulator holds it (register
+// 4g + i: channel 8g + 4*half + i) to row `row` of a 16-bit output, 8 channels
+// (16 bytes) per lane and store.
+__device__ __forceinline__ void store_tile16(const uint32_t lohi[8], uint16_t* at, int half, bool on) {
+#pragma unroll
+  for (int g = 0; g < 4; g += 2) {
+    uint32_t a0 = lohi[2 * g], a1 = lohi[2 * g + 1], b0 = lohi[2 * g + 2], b1 = lohi[2 * g + 3];
+    swap_halves(a0, b0);
+    swap_halves(a1, b1);
+    if (on) *reinterpret_cast<u32x4*>(at + 8 * g + 8 * half) = u32x4{a0, a1, b0, b1};
+  }
+}
+
+template <int AF, int EPI, int TM>
+__device__ __forceinline__ void mx_tile_body(const MxK& p, int n_nb, u32x4* x0, u32x4* x1, u32x4* w0, u32x4* w1) {
+  constexpr int XC = AF == kE4M3 ? 8 : 4;              // 16-byte chunks of a row in a K block
+  constexpr int WM = TM / 64, WN = 4 / WM, CT = 8 / WN;  // wavefronts along rows, channels; tiles of one
+  constexpr int XI = TM * XC / 256;                    // row DMAs per wavefront and K block
+  const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int half = lane >> 5, col = lane & 31;
+  const int wm = wv / WN, wn = wv % WN;
+  const TileAt c = find_tile<TM>(p, blockIdx.x, n_nb);
+  if (c.e < 0) return;
+  const int NT = p.N >> 5, KB = p.K >> 7, KC = (p.K + 255) >> 8;
+
+  // the workgroup's tile j (0..7); SwiGLU: 0..3 gate, 4..7 up.  Past the last
+  // channel: tile 0, loaded and never stored.
+  auto wg_tile = [&](int j, bool& valid) {
+    const int t = is_swiglu(EPI) ? 4 * c.nb + (j & 3) : 8 * c.nb + j;
+    valid = t < (is_swiglu(EPI) ? NT / 2 : NT);
+    return (valid ? t : 0) + (is_swiglu(EPI) && j >= 4 ? NT / 2 : 0);
+  };
+  // this wavefront's tile u as the workgroup's: SwiGLU gates first, then their ups
+  auto own_tile = [&](int u) {
+    return is_swiglu(EPI) ? (u < CT / 2 ? wn * (CT / 2) + u : 4 + wn * (CT / 2) + u - CT / 2) : wn * CT + u;
+  };
+
+  const rsrc_t ar = make_rsrc(p.a, p.a_bytes);
+  const rsrc_t asr = make_rsrc(p.as, p.as_bytes);
+  const rsrc_t wr = make_rsrc(p.wc + (size_t)c.e * NT * KC * 4096, (uint32_t)((size_t)NT * KC * 4096));
+  const rsrc_t wsr = make_rsrc(p.wsc + (size_t)c.e * NT * KC * 256, (uint32_t)((size_t)NT * KC * 256));
+  int src[XI + 2];  // source rows of the DMAs' lanes, then of this wavefront's two row tiles
+#pragma unroll
+  for (int i = 0; i < XI; ++i) src[i] = min(c.r0 + ((wv * XI + i) * 64 + lane) / XC, c.s1 - 1);
+#pragma unroll
+  for (int t = 0; t < 2; ++t) src[XI + t] = min(c.r0 + 64 * wm + 32 * t + col, c.s1 - 1);
+  source_rows(p, src);
+  uint32_t xo[XI];
+#pragma unroll
+  for (int i = 0; i < XI; ++i) {
+    const int at = (wv * XI + i) * 64 + lane;
+    xo[i] = (uint32_t)src[i] * (uint32_t)(KB * XC * 16) + 16 * ((at % XC) ^ swizzle<AF>(at / XC));
+  }
+  uint32_t wo[4];  // DMA i: tile wv * 2 + i / 2, step i % 2
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    bool v;
+    wo[i] = (uint32_t)wg_tile(2 * wv + (i >> 1), v) * (uint32_t)(KC * 4096) + 1024 * (i & 1);
+  }
+  uint32_t wso[CT], xso[2];
+#pragma unroll
+  for (int u = 0; u < CT; ++u) {
+    bool v;
+    wso[u] = (uint32_t)wg_tile(own_tile(u), v) * (uint32_t)(KC * 256);
+  }
+#pragma unroll
+  for (int t = 0; t < 2; ++t)
+    xso[t] = (uint32_t)src[XI + t] * (uint32_t)(KB * 4);
+
+  auto issue = [&](u32x4* xs, u32x4* ws, int kb, int kbx) {  // kbx: the rows' block
+#pragma unroll
+    for (int i = 0; i < XI; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(ar, xs + (wv * XI + i) * 64, 16, xo[i], kbx * (XC * 16), 0, 0);
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(wr, ws + (4 * wv + i) * 64, 16, 16 * lane, wo[i] + kb * 2048, 0, 0);
+  };
+  struct Scales {
+    uint32_t w[CT];
+    u32x2 x[2];
+  };
+  auto load_scales = [&](int kc) {  // K blocks 2 kc and 2 kc + 1
+    Scales s;
+#pragma unroll
+    for (int u = 0; u < CT; ++u) s.w[u] = buf_x1(wsr, 4 * lane, wso[u] + kc * 256);
+#pragma unroll
+    for (int t = 0; t < 2; ++t) s.x[t] = buf_x2(asr, xso[t], kc * 8);
+    return s;
+  };
+  f32x16 acc[2][CT] = {};
+  auto ready = [&]() {  // this wavefront's loads have landed; then everyone's
+    __builtin_amdgcn_sched_barrier(0);
+    vm_wait<0>();
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  auto compute = [&](const u32x4* xs, const u32x4* ws, const Scales& sc, auto odd_tag) {
+    constexpr int ODD = decltype(odd_tag)::value;
+    uint32_t xsc[2];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) {
+      const uint32_t v = ODD ? sc.x[t][1] : sc.x[t][0];
+      xsc[t] = v >> (8 * half);
+    }
+    auto step = [&](auto s_tag) {
+      constexpr int S = decltype(s_tag)::value;
+      i32x8 xf[2];
+      u32x4 wf[CT];
+#pragma unroll
+      for (int u = 0; u < CT; ++u) wf[u] = ws[(2 * own_tile(u) + S) * 64 + lane];
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const int row = 64 * wm + 32 * t + col, z = swizzle<AF>(row);
+        if constexpr (AF == kE4M3)
+          xf[t] = operand(xs[row * XC + ((4 * S + half) ^ z)], xs[row * XC + ((4 * S + 2 + half) ^ z)]);
+        else
+          xf[t] = operand(xs[row * XC + ((2 * S + half) ^ z)]);
+      }
+#pragma unroll
+      for (int u = 0; u < CT; ++u)
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+          acc[t][u] = mx_mfma<AF, 2 * ODD + S, 2 * S>(operand(wf[u]), xf[t], acc[t][u], sc.w[u], xsc[t]);
+    };
+    step(std::integral_constant<int, 0>{});
+    step(std::integral_constant<int, 1>{});
+  };
+  const std::integral_constant<int, 0> even{};
+  const std::integral_constant<int, 1> odd{};
+
+  // One loop with no branch in it (a branch around a load makes the compiler
+  // wait for every load in flight, an exit in the middle copies the
+  // accumulators): past the end it fetches blocks again that nothing reads.
+  // The weights are padded with zeros to a whole pair of blocks; the second
+  // block of an odd last pair multiplies them with the first's rows.
+  Scales sc = load_scales(0);
+  issue(x0, w0, 0, 0);
+  for (int kc = 0; kc < KC; ++kc) {
+    const int kn = min(kc + 1, KC - 1);
+    ready();
+    issue(x1, w1, 2 * kc + 1, min(2 * kc + 1, KB - 1));
+    const Scales next = load_scales(kn);
+    compute(x0, w0, sc, even);
+    ready();
+    issue(x0, w0, 2 * kn, 2 * kn);
+    if (2 * kc + 1 == KB) {
+#pragma unroll
+      for (int t = 0; t < 2; ++t) sc.x[t][1] = sc.x[t][0];
+    }
+    compute(x1, w1, sc, odd);
+    sc = next;
+  }
+  vm_wait<0>();  // nothing may land in LDS after the workgroup's end
+
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    const int row = c.r0 + 64 * wm + 32 * t + col;
+    const bool on = row < c.s1;
+    if constexpr (is_swiglu(EPI)) {
+      const int I = p.N / 2;
+#pragma unroll
+      for (int u = 0; u < CT / 2; ++u) {
+        bool valid;
+        const int ht = wg_tile(own_tile(u), valid);
+        float h[16];
+        uint32_t m = 0;
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          h[r] = silu_mul(acc[t][u][r], acc[t][u + CT / 2][r]);
+          const uint32_t b = __builtin_bit_cast(uint32_t, h[r]) & 0x7FFFFFFFu;
+          m = m > b ? m : b;
+        }
+        if constexpr (EPI == kEpiSwiglu) {
+          uint32_t d[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) d[i] = pack_bf16x2(h[2 * i], h[2 * i + 1]);
+          store_tile16(d, static_cast<uint16_t*>(p.out) + (size_t)row * I + 32 * ht, half, on && valid);
+        } else {
+          constexpr int F = EPI == kEpiSwigluE4M3 ? kE4M3 : kE2M1;
+          uint32_t mo = m;
+          swap_halves(m, mo);
+          m = m > mo ? m : mo;
+          const bool bad = mx_not_finite(m);
+          const int pe = mx_exponent<F>(m);
+          const float inv = mx_inverse(pe);
+          uint32_t d[4];
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            float v[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) v[i] = bad ? 0.0f : h[4 * g + i] * inv;
+            d[g] = F == kE4M3 ? mx_pack4_e4m3(v[0], v[1], v[2], v[3]) : mx_pack4_e2m1(v[0], v[1], v[2], v[3]);
+          }
+          // lane half h gets channels 16h .. 16h + 15 of its token
+          swap_halves(d[0], d[2]);
+          swap_halves(d[1], d[3]);
+          if (on && valid) {
+            const size_t o = (size_t)row * I + 32 * ht + 16 * half;
+            if constexpr (F == kE4M3)
+              *reinterpret_cast<u32x4*>(static_cast<uint8_t*>(p.out) + o) = u32x4{d[0], d[2], d[1], d[3]};
+            else
+              *reinterpret_cast<u32x2*>(static_cast<uint8_t*>(p.out) + o / 2) = u32x2{d[0] | (d[2] << 16), d[1] | (d[3] << 16)};
+            if (half == 0) p.out_scales[(size_t)row * (I >> 5) + ht] = bad ? (uint8_t)255 : (uint8_t)(pe + 127);
+          }
+        }
+      }
+    } else {
+#pragma unroll
+      for (int u = 0; u < CT; ++u) {
+        bool valid;
+        const int tile = wg_tile(own_tile(u), valid);
+        const size_t o = (size_t)row * p.N + 32 * tile;
+        if constexpr (EPI == kEpiF32) {
+          if (on && valid) {
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+              *reinterpret_cast<f32x4*>(static_cast<float*>(p.out) + o + 8 * g + 4 * half) =
+                  f32x4{acc[t][u][4 * g], acc[t][u][4 * g + 1], acc[t][u][4 * g + 2], acc[t][u][4 * g + 3]};
+          }
+        } else {
+          uint32_t d[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            d[i] = EPI == kEpiBf16
+                       ? pack_bf16x2(acc[t][u][2 * i], acc[t][u][2 * i + 1])
+                       : (uint32_t)f32_to_f16(acc[t][u][2 * i]) | ((uint32_t)f32_to_f16(acc[t][u][2 * i + 1]) << 16);
+          store_tile16(d, static_cast<uint16_t*>(p.out) + o, half, on && valid);
+        }
+      }
+    }
+  }
+}
+
+// (The LDS stages are declared here: with generic lambdas in the kernel template
+// itself the host's launch stub is not emitted.)
+template <int AF, int EPI, int TM>
+__global__ __launch_bounds__(256, 2) void mx_tile_kernel(MxK p, int n_nb) {
+  constexpr int X = TM * (AF == kE4M3 ? 8 : 4);
+  __shared__ u32x4 x0[X], x1[X], w0[16 * 64], w1[16 * 64];
+  mx_tile_body<AF, EPI, TM>(p, n_nb, x0, x1, w0, w1);
+}
+
 template <int AF, int EPI>
 int launch_small(const MxK& k, hipStream_t s) {
   const int NT = k.N / 32;
@@ -253,15 +594,32 @@ int launch_small(const MxK& k, hipStream_t s) {
   hipLaunchKernelGGL((mx_small_kernel<AF, EPI, 4>), grid, dim3(256), 0, s, k);
   return (int)hipGetLastError();
 }
+template <int AF, int EPI, int TM>
+int launch_tile(const MxK& k, hipStream_t s) {
+  const int NT = k.N / 32;
+  const int n_nb = is_swiglu(EPI) ? (NT / 2 + 3) / 4 : (NT + 7) / 8;
+  // upper bound of the row tiles: one partial tile per segment that has rows
+  const int64_t tiles = (int64_t)k.M_total / TM + (k.E < k.M_total ? k.E : k.M_total);
+  const int64_t wgs = (tiles * n_nb + 7) / 8 * 8;
+  if (wgs >= ((int64_t)1 << 31)) return (int)hipErrorInvalidConfiguration;
+  hipLaunchKernelGGL((mx_tile_kernel<AF, EPI, TM>), dim3((unsigned)wgs), dim3(256), 0, s, k, n_nb);
+  return (int)hipGetLastError();
+}
+template <int AF, int EPI>
+int launch_path(const MxK& k, int path, hipStream_t s) {
+  if (path == 64) return launch_tile<AF, EPI, 64>(k, s);
+  if (path == 128) return launch_tile<AF, EPI, 128>(k, s);
+  return launch_small<AF, EPI>(k, s);
+}
 template <int AF>
-int launch_fmt(const MxK& k, int epi, hipStream_t s) {
+int launch_fmt(const MxK& k, int epi, int path, hipStream_t s) {
   switch (epi) {
-    case kEpiBf16: return launch_small<AF, kEpiBf16>(k, s);
-    case kEpiSwiglu: return launch_small<AF, kEpiSwiglu>(k, s);
-    case kEpiF32: return launch_small<AF, kEpiF32>(k, s);
-    case kEpiF16: return launch_small<AF, kEpiF16>(k, s);
-    case kEpiSwigluE4M3: return launch_small<AF, kEpiSwigluE4M3>(k, s);
-    default: return launch_small<AF, kEpiSwigluE2M1>(k, s);
+    case kEpiBf16: return launch_path<AF, kEpiBf16>(k, path, s);
+    case kEpiSwiglu: return launch_path<AF, kEpiSwiglu>(k, path, s);
+    case kEpiF32: return launch_path<AF, kEpiF32>(k, path, s);
+    case kEpiF16: return launch_path<AF, kEpiF16>(k, path, s);
+    case kEpiSwigluE4M3: return launch_path<AF, kEpiSwigluE4M3>(k, path, s);
+    default: return launch_path<AF, kEpiSwigluE2M1>(k, path, s);
   }
 }
 }  // namespace
@@ -272,7 +630,8 @@ int launch_mxgemm(const MxGemmArgs& a, void* stream) {
   const MxK k{a.wcodes, a.wscales, a.N, a.K, a.a, a.as, (uint32_t)(a.A_rows * row_codes),
               (uint32_t)((size_t)a.A_rows * (a.K / 32)), a.A_rows, a.gather, a.gather ? a.k : 1, a.seg, a.E, a.M_total,
               a.out, a.out_scales};
-  return a.a_fmt == kE4M3 ? launch_fmt<kE4M3>(k, a.epilogue, s) : launch_fmt<kE2M1>(k, a.epilogue, s);
+  const int path = mxgemm_path(a.M_total, a.E, a.kernel);
+  return a.a_fmt == kE4M3 ? launch_fmt<kE4M3>(k, a.epilogue, path, s) : launch_fmt<kE2M1>(k, a.epilogue, path, s);
 }
 
 }  // namespace moe

@@ -128,4 +128,14 @@ size_t qgemm_workspace_bytes(const QWeights& w, int A_rows, int M_total, int ker
   return need;
 }
 
+// Grouped MX product: 0 = 32-row tiles straight from memory, 64 / 128 =
+// LDS-staged tiles of that many rows, from the mean rows per segment.
+int mxgemm_path(int M_total, int E, int kernel) {
+  if (kernel == 1) return 0;
+  if (kernel == 4) return 64;
+  if (kernel == 5) return 128;
+  const double avg = (double)M_total / E;
+  return avg < 32.0 ? 0 : avg < 96.0 ? 64 : 128;
+}
+
 }  // namespace moe

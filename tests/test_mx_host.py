@@ -120,6 +120,7 @@ def test_mx_weights_validation_and_sizes(lib):
         assert fb(mxdesc(layout), q.MOE_FIELD_SCALES) == 4 * 128 * 256 // 32
         assert fb(mxdesc(layout), q.MOE_FIELD_BASE) == 0
     assert fb(mxdesc(canon, K=384), q.MOE_FIELD_SCALES) == 4 * 128 * 12
+    assert fb(mxdesc(tiled, K=384), q.MOE_FIELD_CODES) == 4 * 128 * 512 // 2
     assert fb(mxdesc(tiled, K=384), q.MOE_FIELD_SCALES) == 4 * 4 * 2 * 256   # padded to whole chunks of 256 inputs
     assert fb(mxdesc(N=48), q.MOE_FIELD_CODES) == fb(mxdesc(K=192), q.MOE_FIELD_CODES) == 0
     rep = lambda a, b: lib.moe_mx_repack(ctypes.byref(a), ctypes.byref(b), None)  # noqa: E731
