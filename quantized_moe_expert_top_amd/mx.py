@@ -8,7 +8,6 @@ stream unless `stream` is given; outputs it allocates belong to that stream.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 from dataclasses import dataclass, field
 from typing import Optional, Union
@@ -29,6 +28,14 @@ _EPI_OUT = {MOE_EPI_NONE: torch.bfloat16, MOE_EPI_SWIGLU: torch.bfloat16, MOE_EP
 
 
 # ------------------------------------------------------------------ plumbing
+# Small calls are bound by the host: these helpers read raw handles instead of
+# building Stream and device objects, and outputs made here skip the checks of
+# caller-made ones.
+_current_device = torch._C._cuda_getDevice
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_fns: dict = {}
+
+
 def _device(*tensors: Optional[torch.Tensor]) -> torch.device:
     """The one GPU that holds all of `tensors` (None entries aside), which must be contiguous."""
     dev = None
@@ -46,28 +53,36 @@ def _device(*tensors: Optional[torch.Tensor]) -> torch.device:
     return dev
 
 
+def _elsewhere(dev: torch.device, stream) -> bool:
+    """Whether a call has to change the current device or stream first."""
+    return stream is not None or dev.index != _current_device()
+
+
+def _guard(dev: torch.device, stream):
+    """Makes `dev` current, and `stream` (if given) the stream that work and allocations belong to."""
+    if stream is None:
+        return torch.cuda.device(dev)
+    if stream.device != dev:
+        raise ValueError(f"stream of {stream.device} for tensors on {dev}")
+    return torch.cuda.stream(stream)
+
+
 def _p(t: Optional[torch.Tensor]) -> Optional[int]:
     return None if t is None else t.data_ptr()
 
 
-def _guard(dev: torch.device, stream):
-    """Makes `dev` current (and `stream`, if given, the stream that allocations belong to)."""
-    if stream is not None:
-        if stream.device != dev:
-            raise ValueError(f"stream of {stream.device} for tensors on {dev}")
-        return torch.cuda.stream(stream)
-    if dev.index != torch.cuda.current_device():
-        return torch.cuda.device(dev)
-    return contextlib.nullcontext()
-
-
-def _call(name: str, *args) -> None:
-    _check(getattr(lib(), name)(*args, torch.cuda.current_stream().cuda_stream), name)
+def _call(name: str, dev: torch.device, *args) -> None:
+    fn = _fns.get(name)
+    if fn is None:
+        fn = _fns[name] = getattr(lib(), name)
+    status = fn(*args, _raw_stream(dev.index))
+    if status:
+        _check(status, name)
 
 
 def _want(t: torch.Tensor, what: str, dtype: torch.dtype, shape: tuple) -> torch.Tensor:
-    if t.dtype != dtype or tuple(t.shape) != shape:
-        raise ValueError(f"{what} must be {dtype} of shape {shape} (got {t.dtype}, {tuple(t.shape)})")
+    if t.dtype != dtype or t.shape != shape:
+        raise ValueError(f"{what} must be {dtype} of shape {tuple(shape)} (got {t.dtype}, {tuple(t.shape)})")
     return t
 
 
@@ -94,13 +109,14 @@ def moe_route_scored(logits: torch.Tensor, k: int, score: int = MOE_SCORE_SOFTMA
     T, E = logits.shape
     if bias is not None:
         _want(bias, "bias", torch.float32, (E,))
-    with _guard(_device(logits, bias, ids, w), stream):
-        ids = torch.empty((T, k), dtype=torch.int32, device=logits.device) if ids is None else \
-            _want(ids, "ids", torch.int32, (T, k))
-        w = torch.empty((T, k), dtype=torch.float32, device=logits.device) if w is None else \
-            _want(w, "w", torch.float32, (T, k))
-        _call("moe_route_scored", _p(logits), _p(bias), T, E, k, score, n_group, topk_group, group_top,
-              int(bool(renormalize)), float(scale), _p(ids), _p(w))
+    dev = _device(logits, bias, ids, w)
+    if _elsewhere(dev, stream):
+        with _guard(dev, stream):
+            return moe_route_scored(logits, k, score, bias, n_group, topk_group, group_top, renormalize, scale, ids, w)
+    ids = logits.new_empty((T, k), dtype=torch.int32) if ids is None else _want(ids, "ids", torch.int32, (T, k))
+    w = logits.new_empty((T, k)) if w is None else _want(w, "w", torch.float32, (T, k))
+    _call("moe_route_scored", dev, _p(logits), _p(bias), T, E, k, score, n_group, topk_group, group_top,
+          1 if renormalize else 0, scale, _p(ids), _p(w))
     return ids, w
 
 
@@ -118,7 +134,7 @@ class MxRows:
             raise ValueError(f"unknown MX format {self.fmt}")
         if self.codes.dtype != torch.uint8 or self.scales.dtype != torch.uint8:
             raise ValueError("MX codes and scales are uint8")
-        if self.codes.dim() < 1 or tuple(self.codes.shape) != _mx_shape(tuple(self.scales.shape[:-1]) + (self.K,), self.fmt):
+        if self.codes.dim() < 1 or self.codes.shape != _mx_shape(self.shape, self.fmt):
             raise ValueError(f"codes {tuple(self.codes.shape)} and scales {tuple(self.scales.shape)} do not match")
 
     @property
@@ -134,6 +150,14 @@ def _mx_shape(shape: tuple, fmt: int) -> tuple:
     return shape if fmt == MOE_MX_E4M3 else shape[:-1] + (shape[-1] // 2,)
 
 
+def _new_rows(like: torch.Tensor, shape: tuple, fmt: int) -> MxRows:
+    rows = object.__new__(MxRows)
+    rows.codes = like.new_empty(_mx_shape(shape, fmt), dtype=torch.uint8)
+    rows.scales = like.new_empty(shape[:-1] + (shape[-1] // 32,), dtype=torch.uint8)
+    rows.fmt = fmt
+    return rows
+
+
 def alloc_mx_rows(shape: tuple, fmt: int, device) -> MxRows:
     """Uninitialised MX rows of `shape` (the last dimension a multiple of 32)."""
     if not shape or shape[-1] < 32 or shape[-1] % 32:
@@ -144,9 +168,11 @@ def alloc_mx_rows(shape: tuple, fmt: int, device) -> MxRows:
                   torch.empty(tuple(shape[:-1]) + (shape[-1] // 32,), dtype=torch.uint8, device=device), fmt)
 
 
-def _rows_out(out: Optional[MxRows], shape: tuple, fmt: int, device) -> MxRows:
+def _rows_out(out: Optional[MxRows], like: torch.Tensor, shape: tuple, fmt: int) -> MxRows:
     if out is None:
-        return alloc_mx_rows(shape, fmt, device)
+        if shape[-1] < 32 or shape[-1] % 32 or fmt not in _MX_EPI:
+            return alloc_mx_rows(shape, fmt, like.device)  # says what is wrong
+        return _new_rows(like, shape, fmt)
     if out.fmt != fmt or out.shape != shape:
         raise ValueError(f"out holds MX rows {out.shape} of format {out.fmt}, not {shape} of {fmt}")
     return out
@@ -163,10 +189,13 @@ def moe_quantize_mx(x: torch.Tensor, fmt: int = MOE_MX_E4M3, out: MxRows = None,
     """bf16, fp16 or fp32 [...][K] -> MX rows."""
     if x.dtype not in _DTYPES or x.dim() < 1:
         raise ValueError(f"x must be bfloat16, float16 or float32 rows (got {x.dtype}, {tuple(x.shape)})")
+    dev = _device(x) if out is None else _device(x, out.codes, out.scales)
+    if _elsewhere(dev, stream):
+        with _guard(dev, stream):
+            return moe_quantize_mx(x, fmt, out)
     shape = tuple(x.shape)
-    with _guard(_device(x, *((out.codes, out.scales) if out else ())), stream):
-        out = _rows_out(out, shape, fmt, x.device)
-        _call("moe_quantize_mx", _p(x), _DTYPES[x.dtype], _count(shape), shape[-1], fmt, _p(out.codes), _p(out.scales))
+    out = _rows_out(out, x, shape, fmt)
+    _call("moe_quantize_mx", dev, _p(x), _DTYPES[x.dtype], _count(shape), shape[-1], fmt, _p(out.codes), _p(out.scales))
     return out
 
 
@@ -178,10 +207,13 @@ def moe_dequantize_mx(rows: MxRows, dtype: torch.dtype = torch.bfloat16, out: to
         dtype = out.dtype
     if dtype not in _DTYPES:
         raise ValueError(f"values in {dtype}: bfloat16, float16 or float32")
-    with _guard(_device(rows.codes, rows.scales, out), stream):
-        out = torch.empty(shape, dtype=dtype, device=rows.codes.device) if out is None else _want(out, "out", dtype, shape)
-        _call("moe_dequantize_mx", _p(rows.codes), _p(rows.scales), _count(shape), shape[-1], rows.fmt, _DTYPES[dtype],
-              _p(out))
+    dev = _device(rows.codes, rows.scales, out)
+    if _elsewhere(dev, stream):
+        with _guard(dev, stream):
+            return moe_dequantize_mx(rows, dtype, out)
+    out = rows.codes.new_empty(shape, dtype=dtype) if out is None else _want(out, "out", dtype, shape)
+    _call("moe_dequantize_mx", dev, _p(rows.codes), _p(rows.scales), _count(shape), shape[-1], rows.fmt, _DTYPES[dtype],
+          _p(out))
     return out
 
 
@@ -208,16 +240,21 @@ def moe_rmsnorm_mx(x: torch.Tensor, weight: torch.Tensor, eps: float, residual: 
         raise ValueError("sum without residual")
     if out is not None and fmt is None:
         raise ValueError("out without an MX format")
-    with _guard(_device(x, weight, residual, sum, y, *((out.codes, out.scales) if out else ())), stream):
-        if residual is not None:
-            sum = torch.empty_like(x) if sum is None else _want(sum, "sum", x.dtype, shape)
-        if y is not None:
-            _want(y, "y", x.dtype, shape)
-        elif want_y:
-            y = torch.empty_like(x)
-        rows = None if fmt is None else _rows_out(out, shape, fmt, x.device)
-        _call("moe_rmsnorm_mx", _p(x), _p(residual), _p(weight), _DTYPES[x.dtype], _count(shape), shape[-1], float(eps),
-              _p(sum), _p(y), fmt or 0, _p(rows.codes) if rows else None, _p(rows.scales) if rows else None)
+    dev = _device(x, weight, residual, sum, y)
+    if out is not None:
+        _device(x, out.codes, out.scales)
+    if _elsewhere(dev, stream):
+        with _guard(dev, stream):
+            return moe_rmsnorm_mx(x, weight, eps, residual, fmt, want_y, sum, y, out)
+    if residual is not None:
+        sum = torch.empty_like(x) if sum is None else _want(sum, "sum", x.dtype, shape)
+    if y is not None:
+        _want(y, "y", x.dtype, shape)
+    elif want_y:
+        y = torch.empty_like(x)
+    rows = None if fmt is None else _rows_out(out, x, shape, fmt)
+    _call("moe_rmsnorm_mx", dev, _p(x), _p(residual), _p(weight), _DTYPES[x.dtype], _count(shape), shape[-1], eps,
+          _p(sum), _p(y), fmt or 0, rows and rows.codes.data_ptr(), rows and rows.scales.data_ptr())
     return NormOutput(sum, y, rows)
 
 
@@ -268,7 +305,7 @@ def moe_mx_repack(src: MxExperts, stream=None) -> MxExperts:
         t = [torch.empty(max(moe_mx_field_bytes(probe, f), 16), dtype=torch.uint8, device=dev)
              for f in (MOE_FIELD_CODES, MOE_FIELD_SCALES)]
         dst = _mx_desc(MOE_LAYOUT_TILED, s.E, s.N, s.K, *t)
-        _call("moe_mx_repack", ctypes.byref(s), ctypes.byref(dst.desc))
+        _call("moe_mx_repack", dev, ctypes.byref(s), ctypes.byref(dst.desc))
     return dst
 
 
@@ -292,16 +329,19 @@ def moe_grouped_mxgemm(w: MxExperts, A: MxRows, seg_offsets: torch.Tensor, M_tot
     if (isinstance(out, MxRows) if fmt is None else out is not None and not isinstance(out, MxRows)):
         raise ValueError("out must be MX rows exactly for the MX epilogues")
     bufs = (out.codes, out.scales) if isinstance(out, MxRows) else (out,)
-    with _guard(_device(A.codes, A.scales, seg_offsets, gather_pair, *w.tensors.values(), *bufs), stream):
-        if fmt is not None:
-            out = _rows_out(out, (M_total, n_out), fmt, A.codes.device)
-            ptrs = _p(out.codes), _p(out.scales)
-        else:
-            out = torch.empty((M_total, n_out), dtype=_EPI_OUT[epilogue], device=A.codes.device) if out is None else \
-                _want(out, "out", _EPI_OUT[epilogue], (M_total, n_out))
-            ptrs = _p(out), None
-        _call("moe_grouped_mxgemm", ctypes.byref(d), _p(A.codes), _p(A.scales), A.fmt, A.shape[0], _p(gather_pair), k,
-              _p(seg_offsets), M_total, epilogue, kernel, *ptrs)
+    dev = _device(A.codes, A.scales, seg_offsets, gather_pair, *w.tensors.values(), *bufs)
+    if _elsewhere(dev, stream):
+        with _guard(dev, stream):
+            return moe_grouped_mxgemm(w, A, seg_offsets, M_total, epilogue, gather_pair, k, out, None, kernel)
+    if fmt is not None:
+        out = _rows_out(out, A.codes, (M_total, n_out), fmt)
+        o, osc = _p(out.codes), _p(out.scales)
+    else:
+        dt = _EPI_OUT[epilogue]
+        out = A.codes.new_empty((M_total, n_out), dtype=dt) if out is None else _want(out, "out", dt, (M_total, n_out))
+        o, osc = _p(out), None
+    _call("moe_grouped_mxgemm", dev, ctypes.byref(d), _p(A.codes), _p(A.scales), A.fmt, A.shape[0], _p(gather_pair), k,
+          _p(seg_offsets), M_total, epilogue, kernel, o, osc)
     return out
 
 
@@ -351,20 +391,23 @@ def moe_mx_layer_forward(x: Union[torch.Tensor, MxRows], logits: torch.Tensor, k
     rows = x if isinstance(x, MxRows) else None
     dev = (rows.codes if rows else x).device
     r = routing or ScoredRouting()
-    with _guard(dev, stream):
-        if buf is None:
-            buf = alloc_mx_layer(T, E, k, H, I, dev, act=rows.fmt if rows else MOE_MX_E4M3)
-        elif buf.sizes != (T, E, k, H, I):
-            raise ValueError(f"buffers of (T, E, k, H, I) = {buf.sizes} for a layer of {(T, E, k, H, I)}")
-        moe_route_scored(logits, k, r.score, r.bias, r.n_group, r.topk_group, r.group_top, r.renormalize, r.scale,
-                         ids=buf.ids, w=buf.w)
-        moe_permute(buf.ids, E, out=buf.perm)
-        if rows is None:
-            rows = moe_quantize_mx(x, buf.x.fmt, out=buf.x)
-        moe_grouped_mxgemm(gate_up, rows, buf.perm.seg_offsets, T * k, _MX_EPI[buf.h.fmt],
-                           gather_pair=buf.perm.sorted_pair, k=k, out=buf.h, kernel=kernel)
-        moe_grouped_mxgemm(down, buf.h, buf.perm.seg_offsets, T * k, _DTYPE_EPI[buf.y_perm.dtype], out=buf.y_perm,
-                           kernel=kernel)
-        moe_unpermute_combine(buf.y_perm, buf.perm.pair_pos, buf.w, T, k, out=buf.out,
-                              n_valid=buf.perm.seg_offsets[-1:])
+    if dev.type != "cuda":
+        raise ValueError("tensor must live on the GPU")
+    if _elsewhere(dev, stream):
+        with _guard(dev, stream):
+            return moe_mx_layer_forward(x, logits, k, gate_up, down, routing, buf, None, kernel)
+    if buf is None:
+        buf = alloc_mx_layer(T, E, k, H, I, dev, act=rows.fmt if rows else MOE_MX_E4M3)
+    elif buf.sizes != (T, E, k, H, I):
+        raise ValueError(f"buffers of (T, E, k, H, I) = {buf.sizes} for a layer of {(T, E, k, H, I)}")
+    moe_route_scored(logits, k, r.score, r.bias, r.n_group, r.topk_group, r.group_top, r.renormalize, r.scale,
+                     buf.ids, buf.w)
+    moe_permute(buf.ids, E, out=buf.perm)
+    if rows is None:
+        rows = moe_quantize_mx(x, buf.x.fmt, buf.x)
+    moe_grouped_mxgemm(gate_up, rows, buf.perm.seg_offsets, T * k, _MX_EPI[buf.h.fmt], buf.perm.sorted_pair, k, buf.h,
+                       None, kernel)
+    moe_grouped_mxgemm(down, buf.h, buf.perm.seg_offsets, T * k, _DTYPE_EPI[buf.y_perm.dtype], None, 1, buf.y_perm,
+                       None, kernel)
+    moe_unpermute_combine(buf.y_perm, buf.perm.pair_pos, buf.w, T, k, out=buf.out, n_valid=buf.perm.seg_offsets[-1:])
     return buf
