@@ -2,11 +2,20 @@
 // expert groups, top-k, renormalised and scaled weights.
 //
 // One wavefront per token; lane l owns experts l, l + 64, ... (NS per lane).
-// Scores are float64: the choice depends on scores next to each other, and
-// float64 makes it the same however they are summed.  Groups are contiguous, so
-// their bests come from the wavefront's LDS copy of the choice scores, one lane
-// per group; the group ranks are a count of better groups.  Then k wave-wide
-// arg-max rounds over (score, -index).
+// The choice is defined on float64 scores, but float64 exponentials of all
+// experts and 64-bit arg-max rounds through LDS shuffles took 18 us for 8192
+// tokens of 64 experts and 47 us for 16384 of 256 (0.5 and 3.6 us of memory
+// traffic).  So the choice is prepared in fp32 and settled in float64:
+//   1. fp32 keys, each within a margin of the choice score;
+//   2. a key that at least k experts reach and few more do, by bisection (one
+//      compare and ballot per 64 experts and step); every expert within the
+//      margins of it can be among the first k and becomes a candidate;
+//   3. candidate i in lane i, in index order: its float64 score, its rank among
+//      the candidates, the weights of the first k.
+// Groups are chosen from the keys too, or from float64 scores where two group
+// scores at the border are within the margins.  Where the candidates exceed the
+// 64 lanes (many equal scores) the token takes float64 rounds over all experts.
+// Every way gives the same result.
 #include <float.h>
 
 #include "common.h"
@@ -15,7 +24,6 @@ namespace moe {
 
 namespace {
 constexpr int kWavesPerBlock = 4;
-constexpr int kMaxE = 1024;
 
 __device__ __forceinline__ void wave_fence() {
   __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
@@ -24,30 +32,22 @@ __device__ __forceinline__ void wave_fence() {
 }
 __device__ __forceinline__ double neg_inf() { return -__builtin_inf(); }
 
+// float64 scores and choice scores of the lane's experts, by the definition.
+// top: the largest logit (softmax).  Reads the logits again, so that no register
+// of the usual path is kept for it.
 template <int NS>
-__global__ __launch_bounds__(64 * kWavesPerBlock) void route_scored_kernel(ScoredArgs a) {
-  __shared__ double lds[kWavesPerBlock][64 * NS];
-  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6;
-  const int t = blockIdx.x * kWavesPerBlock + wv;
-  if (t >= a.T) return;
-  double* const buf = lds[wv];
+__device__ __forceinline__ void exact_scores(const ScoredArgs& a, int t, float top, double (&score)[NS], double (&c)[NS]) {
+  const int lane = threadIdx.x & 63;
   const float* row = a.logits + (size_t)t * a.E;
-
   float x[NS], b[NS];
-  float top = -__builtin_inff();
 #pragma unroll
   for (int s = 0; s < NS; ++s) {
     const int e = lane + 64 * s;
-    float v = e < a.E ? row[e] : -__builtin_inff();
+    const float v = e < a.E ? row[e] : -__builtin_inff();
+    x[s] = v != v ? -__builtin_inff() : fminf(v, FLT_MAX);
     b[s] = (a.bias && e < a.E) ? a.bias[e] : 0.0f;
-    v = v != v ? -__builtin_inff() : fminf(v, FLT_MAX);
-    x[s] = v;
-    top = fmaxf(top, v);
   }
-  double score[NS], c[NS];
   if (a.score == 0) {
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1) top = fmaxf(top, __shfl_xor(top, off, 64));
     double sum = 0.0;
 #pragma unroll
     for (int s = 0; s < NS; ++s) {
@@ -67,34 +67,55 @@ __global__ __launch_bounds__(64 * kWavesPerBlock) void route_scored_kernel(Score
     const double v = score[s] + (double)b[s];
     c[s] = (x[s] == -__builtin_inff() || v != v) ? neg_inf() : v;
   }
+}
 
-  if (a.n_group > 1) {
-    const int size = a.E / a.n_group;
+// The open groups (bit g) by float64 sums; buf: the wavefront's LDS.
+template <int NS>
+__device__ __forceinline__ uint64_t exact_groups(const ScoredArgs& a, const double (&c)[NS], double* buf) {
+  const int lane = threadIdx.x & 63;
+  const int size = a.E / a.n_group;
 #pragma unroll
-    for (int s = 0; s < NS; ++s) buf[lane + 64 * s] = c[s];
-    wave_fence();
-    double best = neg_inf(), second = neg_inf();
-    if (lane < a.n_group)
-      for (int i = 0; i < size; ++i) {
-        const double v = buf[lane * size + i];
-        if (v > best) {
-          second = best;
-          best = v;
-        } else if (v > second) {
-          second = v;
-        }
-      }
-    if (a.group_top == 2 && second > neg_inf()) best += second;
-    int before = 0;
-    for (int g = 0; g < a.n_group; ++g) {
-      const double v = __shfl(best, g, 64);
-      before += (v > best || (v == best && g < lane)) ? 1 : 0;
+  for (int s = 0; s < NS; ++s) buf[lane + 64 * s] = c[s];
+  wave_fence();
+  const int sh = 31 - __builtin_clz(64 / a.n_group), P = 1 << sh, g = lane >> sh;
+  double best = neg_inf(), second = neg_inf();
+  if (g < a.n_group)
+    for (int i = lane & (P - 1); i < size; i += P) {
+      const double v = buf[g * size + i];
+      second = v > best ? best : (v > second ? v : second);
+      best = v > best ? v : best;
     }
-    const uint64_t open = __ballot(lane < a.n_group && before < a.topk_group);
+  for (int off = 1; off < P; off <<= 1) {
+    const double ob = __shfl_xor(best, off, 64), os = __shfl_xor(second, off, 64);
+    const double low = best < ob ? best : ob, hi2 = second > os ? second : os;
+    best = best > ob ? best : ob;
+    second = low > hi2 ? low : hi2;
+  }
+  if (a.group_top == 2 && second > neg_inf()) best += second;
+  int before = 0;
+  for (int j = 0; j < a.n_group; ++j) {
+    const double v = __shfl(best, j << sh, 64);
+    before += (v > best || (v == best && j < g)) ? 1 : 0;
+  }
+  const uint64_t by_lane = __ballot(g < a.n_group && before < a.topk_group && (lane & (P - 1)) == 0);
+  wave_fence();
+  uint64_t open = 0;
+  for (int j = 0; j < a.n_group; ++j) open |= ((by_lane >> (j << sh)) & 1) << j;
+  return open;
+}
+
+// float64 over all experts: the definition, step by step.
+template <int NS>
+__device__ __forceinline__ void route_exact(const ScoredArgs& a, int t, float top, double* buf) {
+  const int lane = threadIdx.x & 63;
+  double score[NS], c[NS];
+  exact_scores<NS>(a, t, top, score, c);
+  if (a.n_group > 1) {
+    const uint64_t open = exact_groups<NS>(a, c, buf);
+    const int size = a.E / a.n_group;
 #pragma unroll
     for (int s = 0; s < NS; ++s)
       if (lane + 64 * s < a.E && !((open >> ((lane + 64 * s) / size)) & 1)) c[s] = neg_inf();
-    wave_fence();
   }
 
   // k rounds; slot j's score goes to the wavefront's buffer
@@ -138,16 +159,269 @@ __global__ __launch_bounds__(64 * kWavesPerBlock) void route_scored_kernel(Score
   for (int j = lane; j < a.k; j += 64)
     a.w[o + j] = sum > 0.0 ? (float)(buf[j] / sum * (double)a.scale) : 0.0f;
 }
+
+// Signed integer that orders like the float (NaN-free).
+__device__ __forceinline__ int order_key(float f) {
+  const int i = __builtin_bit_cast(int, f);
+  return i ^ ((i >> 31) & 0x7FFFFFFF);
+}
+__device__ __forceinline__ float key_value(int k) {
+  return __builtin_bit_cast(float, k ^ ((k >> 31) & 0x7FFFFFFF));
+}
+// Maximum over the wavefront (rows of 16 by shifts, then row broadcasts; the
+// last lane has it).
+__device__ __forceinline__ int wave_imax(int v) {
+#define MOE_STEP(CTRL, RMASK)                                                                  \
+  {                                                                                            \
+    const int o = __builtin_amdgcn_update_dpp((int)0x80000000, v, CTRL, RMASK, 0xF, false);    \
+    v = v > o ? v : o;                                                                         \
+  }
+  MOE_STEP(0x111, 0xF) MOE_STEP(0x112, 0xF) MOE_STEP(0x114, 0xF) MOE_STEP(0x118, 0xF)
+  MOE_STEP(0x142, 0xA) MOE_STEP(0x143, 0xC)
+#undef MOE_STEP
+  return __builtin_amdgcn_readlane(v, 63);
+}
+__device__ __forceinline__ double readlane_f64(double v, int l) {
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)u, l);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(u >> 32), l);
+  return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+
+// Keys and how far they are from what orders the experts:
+//   float64 softmax scores plus bias, rounded (SOFT_ALL): 2^-24 relative;
+//   without a bias, where no scores are added up: the logit itself, which the
+//   scores ascend with (float64 scores of logits closer than the margin may
+//   tie; where the scores reach 0 or 1 in float64 they tie over wider
+//   distances, so the keys end 700 below the largest logit, or at -700 and 20);
+//   else the fp32 sigmoid plus bias: 1.9 * 2^-23 (the exponent's rounding, 2^-24
+//   times s (1 - s) |x| <= 0.23; one ulp of the exponential times s (1 - s); half
+//   an ulp of the sum and one of the reciprocal) and 2^-24 relative.
+// kMargin * (1 + |key|), or kMargin * |key| with SOFT_ALL, is above all of these.
+constexpr float kMargin = 0x1p-22f;
+constexpr int kSpare = 6;  // candidates beyond k that cost less than another step of the bisection
+
+// SOFT_ALL: the softmax denominator is needed (a bias, weights that are not
+// renormalised, sums of two scores per group): float64 exponentials of all
+// experts give it and the keys.
+template <int NS, bool SOFT_ALL>
+__global__ __launch_bounds__(64 * kWavesPerBlock) void route_scored_kernel(ScoredArgs a) {
+  __shared__ double lds[kWavesPerBlock][64 * NS];
+  const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int t = blockIdx.x * kWavesPerBlock + wv;
+  if (t >= a.T) return;
+  double* const buf = lds[wv];
+  const float* row = a.logits + (size_t)t * a.E;
+
+  float x[NS], b[NS];
+#pragma unroll
+  for (int s = 0; s < NS; ++s) x[s] = row[min(lane + 64 * s, a.E - 1)];  // no branch between the loads
+  if (a.bias) {
+#pragma unroll
+    for (int s = 0; s < NS; ++s) b[s] = a.bias[min(lane + 64 * s, a.E - 1)];
+  } else {
+#pragma unroll
+    for (int s = 0; s < NS; ++s) b[s] = 0.0f;
+  }
+  float top = -__builtin_inff();
+#pragma unroll
+  for (int s = 0; s < NS; ++s) {
+    x[s] = (x[s] != x[s] || lane + 64 * s >= a.E) ? -__builtin_inff() : fminf(x[s], FLT_MAX);
+    top = fmaxf(top, x[s]);
+  }
+  double soft_sum = 0.0;
+  float key[NS];
+  if (a.score == 0) top = key_value(wave_imax(order_key(top)));
+  if constexpr (SOFT_ALL) {
+    double ex[NS];
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+      ex[s] = x[s] == -__builtin_inff() ? 0.0 : exp((double)x[s] - (double)top);
+      soft_sum += ex[s];
+    }
+#pragma unroll
+    for (int off = 32; off > 0; off >>= 1) soft_sum += __shfl_xor(soft_sum, off, 64);
+    const double inv = soft_sum > 0.0 ? 1.0 / soft_sum : 0.0;
+#pragma unroll
+    for (int s = 0; s < NS; ++s) key[s] = (float)(ex[s] * inv + (double)b[s]);
+  } else if (a.score == 0) {
+#pragma unroll
+    for (int s = 0; s < NS; ++s) key[s] = fmaxf(x[s], top - 700.0f);
+  } else if (!a.bias && (a.n_group == 1 || a.group_top == 1)) {
+#pragma unroll
+    for (int s = 0; s < NS; ++s) key[s] = fmaxf(fminf(x[s], 20.0f), -700.0f);
+  } else {
+#pragma unroll
+    for (int s = 0; s < NS; ++s) key[s] = __builtin_amdgcn_rcpf(1.0f + __expf(-x[s])) + b[s];
+  }
+  constexpr float kBase = SOFT_ALL ? 0.0f : 1.0f;
+#pragma unroll
+  for (int s = 0; s < NS; ++s)
+    if (x[s] == -__builtin_inff() || key[s] != key[s]) key[s] = -__builtin_inff();
+
+  if (a.n_group > 1) {
+    // Best one or two keys of each group: P lanes per group stride over the
+    // group's keys in LDS and merge.
+    const int size = a.E / a.n_group;
+    float* const fk = reinterpret_cast<float*>(buf);
+#pragma unroll
+    for (int s = 0; s < NS; ++s) fk[lane + 64 * s] = key[s];
+    wave_fence();
+    const int sh = 31 - __builtin_clz(64 / a.n_group), P = 1 << sh;
+    const int g = lane >> sh;
+    float best = -__builtin_inff(), second = -__builtin_inff();
+    if (g < a.n_group)
+      for (int i = lane & (P - 1); i < size; i += P) {
+        const float v = fk[g * size + i];
+        second = fmaxf(second, fminf(best, v));
+        best = fmaxf(best, v);
+      }
+    for (int off = 1; off < P; off <<= 1) {
+      const float ob = __shfl_xor(best, off, 64), os = __shfl_xor(second, off, 64);
+      second = fmaxf(fmaxf(second, os), fminf(best, ob));
+      best = fmaxf(best, ob);
+    }
+    float mag = fabsf(best);  // of what the group's score was made from
+    if (a.group_top == 2 && second > -__builtin_inff()) {
+      mag += fabsf(second);
+      best += second;
+    }
+    // certainly and possibly better groups; one bound of the errors for all
+    const bool some = g < a.n_group && best > -__builtin_inff();
+    const float err = 2.0f * kMargin * (2.0f * kBase + __builtin_bit_cast(float, wave_imax(some ? __builtin_bit_cast(int, mag) : 0)));
+    int sure = 0, maybe = -1;  // (a group is possibly as good as itself)
+    for (int j = 0; j < a.n_group; ++j) {
+      const float v = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, best), j << sh));
+      sure += v > best + err ? 1 : 0;
+      maybe += v >= best - err ? 1 : 0;
+    }
+    const bool mine = g < a.n_group;
+    // bit g: group g is open
+    uint64_t open = 0;
+    if (__ballot(mine && sure < a.topk_group && maybe >= a.topk_group)) {
+      double score[NS], c[NS];
+      wave_fence();
+      exact_scores<NS>(a, t, top, score, c);
+      open = exact_groups<NS>(a, c, buf);
+    } else {
+      const uint64_t by_lane = __ballot(mine && maybe < a.topk_group);
+      for (int j = 0; j < a.n_group; ++j) open |= ((by_lane >> (j << sh)) & 1) << j;
+    }
+    // e / size in fp32: (e + 0.5) / size is at least 1 / 2048 away from a whole number
+    const float inv = 1.0f / (float)size;
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+      const int e = lane + 64 * s;
+      const int ge = (int)(((float)e + 0.5f) * inv);
+      if (e < a.E && !((open >> ge) & 1)) key[s] = -__builtin_inff();
+    }
+    wave_fence();
+  }
+
+  // How many keys reach `from`
+  auto reach = [&](float from) {
+    int c = 0;
+#pragma unroll
+    for (int s = 0; s < NS; ++s) c += __popcll(__ballot(key[s] >= from));
+    return c;
+  };
+  float kmax = key[0], kmin = key[0];
+#pragma unroll
+  for (int s = 1; s < NS; ++s) kmax = fmaxf(kmax, key[s]);
+  kmax = key_value(wave_imax(order_key(kmax)));
+  kmin = __builtin_inff();
+#pragma unroll
+  for (int s = 0; s < NS; ++s) kmin = key[s] == -__builtin_inff() ? kmin : fminf(kmin, key[s]);
+  kmin = key_value(~wave_imax(~order_key(kmin)));
+  // at least min(k, eligible) keys reach `lo`; fewer than k reach `hi`
+  float lo = kmin, hi = kmax;
+  int n = kmax == -__builtin_inff() ? 0 : reach(kmin);
+  for (int i = 0; n > a.k + kSpare && i < 40; ++i) {
+    const float mid = 0.5f * lo + 0.5f * hi;
+    if (!(mid > lo && mid < hi)) break;
+    const int c = reach(mid);
+    if (c >= a.k) {
+      lo = mid;
+      n = c;
+    } else {
+      hi = mid;
+    }
+  }
+  if (n >= a.k) {
+    lo = fmaxf(lo - 4.0f * kMargin * (kBase + fabsf(lo)), -FLT_MAX);
+    n = reach(lo);
+  }
+  const bool exact = n > 64;  // many (nearly) equal keys
+  int cand = -1;
+  if (!exact) {
+    int* const list = reinterpret_cast<int*>(buf);
+    int base = 0;
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+      const bool in = n > 0 && key[s] >= lo;
+      const uint64_t m = __ballot(in);
+      if (in) list[base + __builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0))] = lane + 64 * s;
+      base += __popcll(m);
+    }
+    wave_fence();
+    if (lane < n) cand = list[lane];
+  }
+  if (exact) {
+    wave_fence();
+    route_exact<NS>(a, t, top, buf);
+    return;
+  }
+
+  // float64 scores of the candidates, their ranks, the weights of the first k
+  double score = 0.0, c = neg_inf();
+  if (cand >= 0) {
+    const double xv = (double)fminf(row[cand], FLT_MAX);
+    const double bv = a.bias ? (double)a.bias[cand] : 0.0;
+    if (a.score == 0) {
+      score = exp(xv - (double)top);
+      if constexpr (SOFT_ALL) score = score / soft_sum;
+    } else {
+      score = 1.0 / (1.0 + exp(-xv));
+    }
+    c = score + bv;
+  }
+  int rank = 0;
+  for (int j = 0; j < n; ++j) {
+    const double cj = readlane_f64(c, j);
+    rank += (cj > c || (cj == c && j < lane)) ? 1 : 0;
+  }
+  const bool chosen = cand >= 0 && rank < a.k;
+  double sum = 1.0;
+  if (a.renorm) {
+    sum = 0.0;
+    for (uint64_t left = __ballot(chosen); left; left &= left - 1) sum += readlane_f64(score, __builtin_ctzll(left));
+  }
+  const size_t o = (size_t)t * a.k;
+  if (chosen) {
+    a.ids[o + rank] = cand;
+    a.w[o + rank] = sum > 0.0 ? (float)(score / sum * (double)a.scale) : 0.0f;
+  }
+  for (int j = n + lane; j < a.k; j += 64) {  // fewer eligible experts than slots
+    a.ids[o + j] = -1;
+    a.w[o + j] = 0.0f;
+  }
+}
 }  // namespace
+
+template <int NS>
+static void launch_ns(const ScoredArgs& a, hipStream_t s) {
+  const dim3 grid((a.T + kWavesPerBlock - 1) / kWavesPerBlock), block(64 * kWavesPerBlock);
+  if (a.score == 0 && (a.bias || !a.renorm || (a.n_group > 1 && a.group_top == 2))) hipLaunchKernelGGL((route_scored_kernel<NS, true>), grid, block, 0, s, a);
+  else hipLaunchKernelGGL((route_scored_kernel<NS, false>), grid, block, 0, s, a);
+}
 
 int launch_route_scored(const ScoredArgs& a, void* stream) {
   const hipStream_t s = static_cast<hipStream_t>(stream);
-  const dim3 grid((a.T + kWavesPerBlock - 1) / kWavesPerBlock), block(64 * kWavesPerBlock);
-  if (a.E <= 64) hipLaunchKernelGGL(route_scored_kernel<1>, grid, block, 0, s, a);
-  else if (a.E <= 128) hipLaunchKernelGGL(route_scored_kernel<2>, grid, block, 0, s, a);
-  else if (a.E <= 256) hipLaunchKernelGGL(route_scored_kernel<4>, grid, block, 0, s, a);
-  else if (a.E <= 512) hipLaunchKernelGGL(route_scored_kernel<8>, grid, block, 0, s, a);
-  else hipLaunchKernelGGL(route_scored_kernel<16>, grid, block, 0, s, a);
+  if (a.E <= 64) launch_ns<1>(a, s);
+  else if (a.E <= 128) launch_ns<2>(a, s);
+  else if (a.E <= 256) launch_ns<4>(a, s);
+  else if (a.E <= 512) launch_ns<8>(a, s);
+  else launch_ns<16>(a, s);
   return (int)hipGetLastError();
 }
 

@@ -226,6 +226,21 @@ def test_route_scored_ties(E):
 
 
 @pytest.mark.parametrize("sigmoid", [False, True])
+@pytest.mark.parametrize("E,G,gt", [(48, 1, 1), (64, 4, 1), (64, 4, 2), (256, 8, 2), (1000, 10, 1)])
+def test_route_scored_near_ties(sigmoid, E, G, gt):
+    """Scores closer than fp32 tells apart: single fp32 steps of equal logits, differences of 1e-6, saturated scores."""
+    rng = np.random.default_rng(E + G + gt)
+    logits = (1.5 + 1e-6 * rng.standard_normal((24, E))).astype(np.float32)
+    if gt == 1:
+        logits[:8] = np.float32(1.5) + rng.integers(0, 6, (8, E)).astype(np.float32) * np.float32(2.0 ** -23)
+        logits[8:12] += 21  # sigmoid: 1 - 2e-10, steps of 1e-16
+    bias = (1e-6 * rng.standard_normal(E)).astype(np.float32)
+    for b in (None, bias):
+        check_route(logits, 7, sigmoid=sigmoid, bias=b, n_group=G, topk_group=max(1, G // 2), group_top=gt)
+    check_route(logits, 7, sigmoid=sigmoid, n_group=G, topk_group=max(1, G // 2), group_top=gt, renorm=False)
+
+
+@pytest.mark.parametrize("sigmoid", [False, True])
 @pytest.mark.parametrize("E,G", [(16, 1), (16, 4), (96, 8), (256, 16)])
 def test_route_scored_barred_experts(sigmoid, E, G):
     """-inf and NaN logits and biases bar experts; rows with too few, one and no expert left; +inf counts as FLT_MAX."""
