@@ -34,7 +34,8 @@ struct MxK {  // kernel arguments
   uint32_t a_bytes, as_bytes;
   int A_rows;
   const int32_t* gather;
-  int k;
+  uint32_t k_mul;  // pair / k = (pair * k_mul) >> (31 + k_shift), 0 <= pair < 2^31
+  int k_shift;
   const int32_t* seg;
   int E, M_total;
   void* out;
@@ -66,21 +67,12 @@ __device__ __forceinline__ void segment(const MxK& p, int e, int& s0, int& s1) {
   s0 = min(max(p.seg[e], 0), p.M_total);
   s1 = min(max(p.seg[e + 1], s0), p.M_total);
 }
-__device__ __forceinline__ int source_row(const MxK& p, int row) {
-  const int r = p.gather ? p.gather[row] / p.k : row;
-  return min(max(r, 0), p.A_rows - 1);
+__device__ __forceinline__ int pair_token(const MxK& p, int pair) {
+  return (int)(((uint64_t)(uint32_t)pair * p.k_mul) >> (31 + p.k_shift));
 }
-// The same for several rows at once (one wait for all of the table's entries).
-template <int N>
-__device__ __forceinline__ void source_rows(const MxK& p, int (&row)[N]) {
-  if (p.gather) {
-#pragma unroll
-    for (int i = 0; i < N; ++i) row[i] = p.gather[row[i]];
-#pragma unroll
-    for (int i = 0; i < N; ++i) row[i] = row[i] / p.k;
-  }
-#pragma unroll
-  for (int i = 0; i < N; ++i) row[i] = min(max(row[i], 0), p.A_rows - 1);
+__device__ __forceinline__ int source_row(const MxK& p, int row) {
+  const int r = p.gather ? pair_token(p, p.gather[row]) : row;
+  return min(max(r, 0), p.A_rows - 1);
 }
 
 // -------------------------------------------------------- few rows per expert
@@ -262,11 +254,15 @@ __global__ __launch_bounds__(64 * NW) void mx_small_kernel(MxK p) {
 
 // ------------------------------------------------------- many rows per expert
 // A workgroup of 4 wavefronts takes TM rows of one expert and 8 channel tiles
-// (256 channels; SwiGLU: 128 gate and the matching 128 up channels); a
-// wavefront takes 64 rows and CT of the tiles.  K advances 128 at a time
-// through two LDS stages filled by LDS-DMA: while a stage is multiplied the
-// other one loads.  Two workgroups share a CU, so one multiplies while the
-// other waits at its barrier.
+// (256 channels; SwiGLU: 128 gate and the matching 128 up channels), a
+// wavefront all TM rows and 2 of the tiles (a gate and its up tile).  K advances
+// 128 at a time: rows and their scales through two LDS stages filled by
+// LDS-DMA, shared by the wavefronts; weights, which only one wavefront uses,
+// straight into its registers.  Workgroups share a CU (2 of 128 rows, 3 of 64),
+// so one multiplies while another waits at its barrier.
+//
+// Each XCD (workgroups are dealt to the 8 of them in turn) takes a contiguous
+// range of tiles, so that the weights and rows its CUs share stay in its L2.
 //
 // Rows in LDS: 16-byte chunks, chunk c of row r at place c ^ swizzle(r), so that
 // the lanes of a fragment read (32 rows, one chunk) fall on different banks,
@@ -277,55 +273,49 @@ __device__ __forceinline__ int swizzle(int row) {
   return AF == kE4M3 ? ((row & 7) ^ ((row >> 3) & 1)) : (((row >> 1) & 3) ^ ((row >> 3) & 1));
 }
 
-template <int N>
-__device__ __forceinline__ void vm_wait() {
-  __builtin_amdgcn_s_waitcnt(0x0F70 | (N & 15) | ((N >> 4) << 14));  // expcnt, lgkmcnt: no wait
-}
-
-// Which (segment, row tile, channel block) workgroup `id` takes.  Tiles are
-// numbered expert by expert, within an expert in groups of 8 row tiles by
-// channel block, and each XCD (workgroups are dealt to the 8 of them in turn)
-// takes a contiguous range: the weights and rows its CUs share stay in its L2.
-struct TileAt {
-  int e, r0, s1, nb;  // e < 0: nothing to do
+// Tiles (row tile, channel block) are numbered expert by expert, within an
+// expert in groups of 8 row tiles by channel block.
+struct Tile {
+  int e, r0, s1, nb;
 };
+// Inclusive sum over the wavefront's lanes (DPP: shifts within rows of 16, then
+// row broadcasts).
+__device__ __forceinline__ int wave_scan(int v) {
+#define MOE_STEP(CTRL, RMASK) v += __builtin_amdgcn_update_dpp(0, v, CTRL, RMASK, 0xF, false);
+  MOE_STEP(0x111, 0xF) MOE_STEP(0x112, 0xF) MOE_STEP(0x114, 0xF) MOE_STEP(0x118, 0xF)
+  MOE_STEP(0x142, 0xA) MOE_STEP(0x143, 0xC)
+#undef MOE_STEP
+  return v;
+}
 template <int TM>
-__device__ __forceinline__ TileAt find_tile(const MxK& p, int id, int n_nb) {
-  const int lane = threadIdx.x & 63;
-  int total = 0;  // row tiles of all segments
+__device__ __forceinline__ int row_tiles(const MxK& p, int e, int& s0, int& s1) {
+  s0 = s1 = 0;
+  if (e < p.E) segment(p, e, s0, s1);
+  return (s1 - s0 + TM - 1) / TM;
+}
+template <int TM>
+__device__ __forceinline__ int count_tiles(const MxK& p, int n_nb) {
+  int total = 0, s0, s1;
+  for (int e0 = 0; e0 < p.E; e0 += 64)
+    total += __builtin_amdgcn_readlane(wave_scan(row_tiles<TM>(p, e0 + (threadIdx.x & 63), s0, s1)), 63);
+  return total * n_nb;
+}
+// Tile `idx`, which exists.
+template <int TM>
+__device__ __forceinline__ Tile find_tile(const MxK& p, int idx, int n_nb) {
+  Tile t{0, 0, 0, 0};
   for (int e0 = 0; e0 < p.E; e0 += 64) {
-    int s0 = 0, s1 = 0;
-    if (e0 + lane < p.E) segment(p, e0 + lane, s0, s1);
-    int n = (s1 - s0 + TM - 1) / TM;
-#pragma unroll
-    for (int off = 32; off > 0; off >>= 1) n += __shfl_xor(n, off, 64);
-    total += __builtin_amdgcn_readfirstlane(n);
-  }
-  TileAt t{-1, 0, 0, 0};
-  const int64_t wgs = (int64_t)total * n_nb;
-  const int64_t per = (wgs + 7) >> 3;
-  int64_t idx = (int64_t)(id & 7) * per + (id >> 3);
-  if ((id >> 3) >= per || idx >= wgs) return t;
-  for (int e0 = 0; e0 < p.E; e0 += 64) {
-    int s0 = 0, s1 = 0;
-    if (e0 + lane < p.E) segment(p, e0 + lane, s0, s1);
-    const int n = (s1 - s0 + TM - 1) / TM;
-    int before = n;  // inclusive scan, then exclusive
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-      const int o = __shfl_up(before, off, 64);
-      if (lane >= off) before += o;
-    }
-    const int sum = __builtin_amdgcn_readlane(before, 63);
-    before -= n;
-    if (idx >= (int64_t)sum * n_nb) {
-      idx -= (int64_t)sum * n_nb;
+    int s0, s1;
+    const int n = row_tiles<TM>(p, e0 + (threadIdx.x & 63), s0, s1);
+    const int end = wave_scan(n);
+    const int sum = __builtin_amdgcn_readlane(end, 63);
+    if (idx >= sum * n_nb) {
+      idx -= sum * n_nb;
       continue;
     }
-    const bool mine = idx >= (int64_t)before * n_nb && idx < (int64_t)(before + n) * n_nb;
-    const int src = __builtin_ctzll(__ballot(mine));
-    const int j = (int)(idx - (int64_t)__builtin_amdgcn_readlane(before, src) * n_nb);
+    const int src = __builtin_ctzll(__ballot(idx < end * n_nb));
     const int tiles = __builtin_amdgcn_readlane(n, src);
+    const int j = idx - (__builtin_amdgcn_readlane(end, src) - tiles) * n_nb;
     const int g = j / (8 * n_nb), gm = min(8, tiles - 8 * g);
     const int in = j - g * 8 * n_nb;
     t.e = e0 + src;
@@ -359,161 +349,197 @@ __device__ __forceinline__ void store_tile16(const uint32_t lohi[8], uint16_t* a
 }
 
 template <int AF, int EPI, int TM>
-__device__ __forceinline__ void mx_tile_body(const MxK& p, int n_nb, u32x4* x0, u32x4* x1, u32x4* w0, u32x4* w1) {
-  constexpr int XC = AF == kE4M3 ? 8 : 4;              // 16-byte chunks of a row in a K block
-  constexpr int WM = TM / 64, WN = 4 / WM, CT = 8 / WN;  // wavefronts along rows, channels; tiles of one
-  constexpr int XI = TM * XC / 256;                    // row DMAs per wavefront and K block
+__device__ __forceinline__ void mx_tile_body(const MxK& p, int n_nb, u32x4* x0, u32x4* x1, uint32_t* s0, uint32_t* s1) {
+  constexpr int XC = AF == kE4M3 ? 8 : 4;  // 16-byte chunks of a row in a K block
+  constexpr int RT = TM / 32;              // row tiles
+  constexpr int XI = TM * XC / 256;        // row DMAs per wavefront and K block
+  constexpr int RW = TM / 4;               // rows whose scales a wavefront fetches
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int half = lane >> 5, col = lane & 31;
-  const int wm = wv / WN, wn = wv % WN;
-  const TileAt c = find_tile<TM>(p, blockIdx.x, n_nb);
-  if (c.e < 0) return;
+  const int wgs = count_tiles<TM>(p, n_nb), per = (wgs + 7) >> 3;
+  const int idx = ((int)blockIdx.x & 7) * per + ((int)blockIdx.x >> 3);
+  if (((int)blockIdx.x >> 3) >= per || idx >= wgs) return;
+  const Tile c = find_tile<TM>(p, idx, n_nb);
   const int NT = p.N >> 5, KB = p.K >> 7, KC = (p.K + 255) >> 8;
 
-  // the workgroup's tile j (0..7); SwiGLU: 0..3 gate, 4..7 up.  Past the last
-  // channel: tile 0, loaded and never stored.
-  auto wg_tile = [&](int j, bool& valid) {
-    const int t = is_swiglu(EPI) ? 4 * c.nb + (j & 3) : 8 * c.nb + j;
-    valid = t < (is_swiglu(EPI) ? NT / 2 : NT);
-    return (valid ? t : 0) + (is_swiglu(EPI) && j >= 4 ? NT / 2 : 0);
-  };
-  // this wavefront's tile u as the workgroup's: SwiGLU gates first, then their ups
-  auto own_tile = [&](int u) {
-    return is_swiglu(EPI) ? (u < CT / 2 ? wn * (CT / 2) + u : 4 + wn * (CT / 2) + u - CT / 2) : wn * CT + u;
-  };
-
+  // this wavefront's tiles; past the last channel: tile 0, loaded and never stored
+  bool valid[2];
+  int tile[2];
+#pragma unroll
+  for (int u = 0; u < 2; ++u) {
+    const int t = is_swiglu(EPI) ? 4 * c.nb + wv : 8 * c.nb + 2 * wv + u;
+    valid[u] = t < (is_swiglu(EPI) ? NT / 2 : NT);
+    tile[u] = (valid[u] ? t : 0) + (is_swiglu(EPI) && u ? NT / 2 : 0);
+  }
   const rsrc_t ar = make_rsrc(p.a, p.a_bytes);
   const rsrc_t asr = make_rsrc(p.as, p.as_bytes);
   const rsrc_t wr = make_rsrc(p.wc + (size_t)c.e * NT * KC * 4096, (uint32_t)((size_t)NT * KC * 4096));
   const rsrc_t wsr = make_rsrc(p.wsc + (size_t)c.e * NT * KC * 256, (uint32_t)((size_t)NT * KC * 256));
-  int src[XI + 2];  // source rows of the DMAs' lanes, then of this wavefront's two row tiles
+  // grouped rows of this lane's DMAs, then the row whose scales it fetches; past
+  // the segment's end the last row again (its column is never stored)
+  int src[XI + 1];
 #pragma unroll
   for (int i = 0; i < XI; ++i) src[i] = min(c.r0 + ((wv * XI + i) * 64 + lane) / XC, c.s1 - 1);
+  src[XI] = min(c.r0 + RW * wv + (lane & (RW - 1)), c.s1 - 1);
+  if (p.gather) {
 #pragma unroll
-  for (int t = 0; t < 2; ++t) src[XI + t] = min(c.r0 + 64 * wm + 32 * t + col, c.s1 - 1);
-  source_rows(p, src);
+    for (int i = 0; i < XI + 1; ++i) src[i] = p.gather[src[i]];
+#pragma unroll
+    for (int i = 0; i < XI + 1; ++i) src[i] = pair_token(p, src[i]);
+  }
+#pragma unroll
+  for (int i = 0; i < XI + 1; ++i) src[i] = min(max(src[i], 0), p.A_rows - 1);
   uint32_t xo[XI];
 #pragma unroll
   for (int i = 0; i < XI; ++i) {
     const int at = (wv * XI + i) * 64 + lane;
     xo[i] = (uint32_t)src[i] * (uint32_t)(KB * XC * 16) + 16 * ((at % XC) ^ swizzle<AF>(at / XC));
   }
-  uint32_t wo[4];  // DMA i: tile wv * 2 + i / 2, step i % 2
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    bool v;
-    wo[i] = (uint32_t)wg_tile(2 * wv + (i >> 1), v) * (uint32_t)(KC * 4096) + 1024 * (i & 1);
-  }
-  uint32_t wso[CT], xso[2];
-#pragma unroll
-  for (int u = 0; u < CT; ++u) {
-    bool v;
-    wso[u] = (uint32_t)wg_tile(own_tile(u), v) * (uint32_t)(KC * 256);
-  }
-#pragma unroll
-  for (int t = 0; t < 2; ++t)
-    xso[t] = (uint32_t)src[XI + t] * (uint32_t)(KB * 4);
+  const uint32_t xso = (uint32_t)src[XI] * (uint32_t)(KB * 4);
+  const uint32_t wo[2] = {(uint32_t)tile[0] * (uint32_t)(KC * 4096), (uint32_t)tile[1] * (uint32_t)(KC * 4096)};
 
-  auto issue = [&](u32x4* xs, u32x4* ws, int kb, int kbx) {  // kbx: the rows' block
+  // XI + 1 loads of K block kb's rows and scales into a stage
+  auto issue = [&](u32x4* xs, uint32_t* ss, int kb) {
 #pragma unroll
     for (int i = 0; i < XI; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(ar, xs + (wv * XI + i) * 64, 16, xo[i], kbx * (XC * 16), 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(ar, xs + (wv * XI + i) * 64, 16, xo[i], kb * (XC * 16), 0, 0);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(asr, ss + wv * 64, 4, xso, kb * 4, 0, 0);
+  };
+  struct Weights {  // of a K block: [tile][step]
+    u32x4 w[2][2];
+  };
+  auto load_weights = [&](int kb) {  // 4 loads
+    Weights b;
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(wr, ws + (4 * wv + i) * 64, 16, 16 * lane, wo[i] + kb * 2048, 0, 0);
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int s = 0; s < 2; ++s) b.w[u][s] = buf_x4(wr, 16 * lane, wo[u] + kb * 2048 + 1024 * s);
+    return b;
   };
-  struct Scales {
-    uint32_t w[CT];
-    u32x2 x[2];
+  struct Scales {  // of the weights in two K blocks
+    uint32_t w[2];
   };
-  auto load_scales = [&](int kc) {  // K blocks 2 kc and 2 kc + 1
+  auto load_scales = [&](int kc) {
     Scales s;
 #pragma unroll
-    for (int u = 0; u < CT; ++u) s.w[u] = buf_x1(wsr, 4 * lane, wso[u] + kc * 256);
-#pragma unroll
-    for (int t = 0; t < 2; ++t) s.x[t] = buf_x2(asr, xso[t], kc * 8);
+    for (int u = 0; u < 2; ++u) s.w[u] = buf_x1(wsr, 4 * lane, wo[u] / 16 + kc * 256);
     return s;
   };
-  f32x16 acc[2][CT] = {};
-  auto ready = [&]() {  // this wavefront's loads have landed; then everyone's
+  struct Frag {  // 32 rows' values in a step (64 inputs)
+    u32x4 x[AF == kE4M3 ? 2 : 1];
+  };
+  auto read = [&](const u32x4* xs, int S, int t) {
+    Frag f;
+    const int row = 32 * t + col, z = swizzle<AF>(row);
+    if constexpr (AF == kE4M3) {
+      f.x[0] = xs[row * XC + ((4 * S + half) ^ z)];
+      f.x[1] = xs[row * XC + ((4 * S + 2 + half) ^ z)];
+    } else {
+      f.x[0] = xs[row * XC + ((2 * S + half) ^ z)];
+    }
+    return f;
+  };
+  struct RowScales {
+    uint32_t x[RT];
+  };
+  auto read_scales = [&](const uint32_t* ss) {
+    RowScales s;
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+      const int row = 32 * t + col;
+      s.x[t] = ss[row / RW * 64 + row % RW] >> (8 * half);
+    }
+    return s;
+  };
+  f32x16 acc[RT][2];
+  Frag f[RT];
+  // One step: multiplies f and replaces it, row tile by row tile, with the next
+  // step's fragments (stage xs, step S_NEXT; not after the last).
+  auto step = [&](const Weights& w, const Scales& sc, const RowScales& xsc, auto odd_tag, auto s_tag, auto first_tag,
+                  const u32x4* xs, auto next_tag) {
+    constexpr int ODD = decltype(odd_tag)::value, S = decltype(s_tag)::value;
+#pragma unroll
+    for (int t = 0; t < RT; ++t) {
+      i32x8 xf;
+      if constexpr (AF == kE4M3) xf = operand(f[t].x[0], f[t].x[1]);
+      else xf = operand(f[t].x[0]);
+#pragma unroll
+      for (int u = 0; u < 2; ++u) {
+        const f32x16 c0 = decltype(first_tag)::value ? f32x16{} : acc[t][u];
+        acc[t][u] = mx_mfma<AF, 2 * ODD + S, 2 * S>(operand(w.w[u][S]), xf, c0, sc.w[u], xsc.x[t]);
+      }
+      if constexpr (decltype(next_tag)::value) f[t] = read(xs, 1 - S, t);
+    }
+  };
+  const std::integral_constant<int, 0> zero{};
+  const std::integral_constant<int, 1> one{};
+  // Everyone's fragments of the current block have arrived, and the next block's
+  // rows.  Loads complete in order: `left` newer ones, the weights loaded since
+  // those rows were issued (at least that many; the scheduling barriers keep them
+  // between the two), may be on their way.  Waiting for them too cost 3 to 30 %.
+  auto ready = [&](auto left_tag) {
     __builtin_amdgcn_sched_barrier(0);
-    vm_wait<0>();
+    __builtin_amdgcn_s_waitcnt(0x0070 | decltype(left_tag)::value);  // vmcnt `left`, lgkmcnt 0
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
   };
-  auto compute = [&](const u32x4* xs, const u32x4* ws, const Scales& sc, auto odd_tag) {
-    constexpr int ODD = decltype(odd_tag)::value;
-    uint32_t xsc[2];
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      const uint32_t v = ODD ? sc.x[t][1] : sc.x[t][0];
-      xsc[t] = v >> (8 * half);
-    }
-    auto step = [&](auto s_tag) {
-      constexpr int S = decltype(s_tag)::value;
-      i32x8 xf[2];
-      u32x4 wf[CT];
-#pragma unroll
-      for (int u = 0; u < CT; ++u) wf[u] = ws[(2 * own_tile(u) + S) * 64 + lane];
-#pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        const int row = 64 * wm + 32 * t + col, z = swizzle<AF>(row);
-        if constexpr (AF == kE4M3)
-          xf[t] = operand(xs[row * XC + ((4 * S + half) ^ z)], xs[row * XC + ((4 * S + 2 + half) ^ z)]);
-        else
-          xf[t] = operand(xs[row * XC + ((2 * S + half) ^ z)]);
-      }
-#pragma unroll
-      for (int u = 0; u < CT; ++u)
-#pragma unroll
-        for (int t = 0; t < 2; ++t)
-          acc[t][u] = mx_mfma<AF, 2 * ODD + S, 2 * S>(operand(wf[u]), xf[t], acc[t][u], sc.w[u], xsc[t]);
-    };
-    step(std::integral_constant<int, 0>{});
-    step(std::integral_constant<int, 1>{});
-  };
-  const std::integral_constant<int, 0> even{};
-  const std::integral_constant<int, 1> odd{};
+  const std::integral_constant<int, 4> weights_may_fly{};
 
-  // One loop with no branch in it (a branch around a load makes the compiler
-  // wait for every load in flight, an exit in the middle copies the
-  // accumulators): past the end it fetches blocks again that nothing reads.
-  // The weights are padded with zeros to a whole pair of blocks; the second
-  // block of an odd last pair multiplies them with the first's rows.
+  // At block i's barrier nobody reads its stage any more and block i + 1's rows
+  // have landed: block i + 2's are issued into the free stage, then block i's
+  // second step and block i + 1's first multiply.  No branch in the loop (a
+  // branch around a load makes the compiler wait for every load in flight, an
+  // exit in the middle copies the accumulators): the weights are padded with
+  // zeros to a whole pair of blocks, the second block of an odd last pair
+  // multiplies them with the first's rows.
   Scales sc = load_scales(0);
-  issue(x0, w0, 0, 0);
-  for (int kc = 0; kc < KC; ++kc) {
-    const int kn = min(kc + 1, KC - 1);
-    ready();
-    issue(x1, w1, 2 * kc + 1, min(2 * kc + 1, KB - 1));
-    const Scales next = load_scales(kn);
-    compute(x0, w0, sc, even);
-    ready();
-    issue(x0, w0, 2 * kn, 2 * kn);
-    if (2 * kc + 1 == KB) {
+  Weights wa = load_weights(0);
+  issue(x0, s0, 0);
+  ready(zero);
+  issue(x1, s1, min(1, KB - 1));
+  __builtin_amdgcn_sched_barrier(0);
+  Weights wb = load_weights(1);
 #pragma unroll
-      for (int t = 0; t < 2; ++t) sc.x[t][1] = sc.x[t][0];
-    }
-    compute(x1, w1, sc, odd);
+  for (int t = 0; t < RT; ++t) f[t] = read(x0, 0, t);
+  RowScales xa = read_scales(s0), xb;
+  step(wa, sc, xa, zero, zero, one, x0, one);
+  for (int kc = 0; kc + 1 < KC; ++kc) {
+    ready(weights_may_fly);
+    issue(x0, s0, 2 * kc + 2);
+    const Scales next = load_scales(kc + 1);
+    xb = read_scales(s1);
+    __builtin_amdgcn_sched_barrier(0);
+    step(wa, sc, xa, zero, one, zero, x1, one);
+    wa = load_weights(2 * kc + 2);
+    step(wb, sc, xb, one, zero, zero, x1, one);
+    ready(weights_may_fly);
+    issue(x1, s1, min(2 * kc + 3, KB - 1));
+    xa = read_scales(s0);
+    __builtin_amdgcn_sched_barrier(0);
+    step(wb, sc, xb, one, one, zero, x0, one);
+    wb = load_weights(2 * kc + 3);
     sc = next;
+    step(wa, sc, xa, zero, zero, zero, x0, one);
   }
-  vm_wait<0>();  // nothing may land in LDS after the workgroup's end
+  ready(zero);
+  xb = read_scales(s1);
+  step(wa, sc, xa, zero, one, zero, x1, one);
+  step(wb, sc, xb, one, zero, zero, x1, one);
+  step(wb, sc, xb, one, one, zero, x1, zero);
 
 #pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    const int row = c.r0 + 64 * wm + 32 * t + col;
+  for (int t = 0; t < RT; ++t) {
+    const int row = c.r0 + 32 * t + col;
     const bool on = row < c.s1;
     if constexpr (is_swiglu(EPI)) {
       const int I = p.N / 2;
-#pragma unroll
-      for (int u = 0; u < CT / 2; ++u) {
-        bool valid;
-        const int ht = wg_tile(own_tile(u), valid);
+      {
+        const int ht = tile[0];
         float h[16];
         uint32_t m = 0;
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
-          h[r] = silu_mul(acc[t][u][r], acc[t][u + CT / 2][r]);
+          h[r] = silu_mul(acc[t][0][r], acc[t][1][r]);
           const uint32_t b = __builtin_bit_cast(uint32_t, h[r]) & 0x7FFFFFFFu;
           m = m > b ? m : b;
         }
@@ -521,7 +547,7 @@ __device__ __forceinline__ void mx_tile_body(const MxK& p, int n_nb, u32x4* x0, 
           uint32_t d[8];
 #pragma unroll
           for (int i = 0; i < 8; ++i) d[i] = pack_bf16x2(h[2 * i], h[2 * i + 1]);
-          store_tile16(d, static_cast<uint16_t*>(p.out) + (size_t)row * I + 32 * ht, half, on && valid);
+          store_tile16(d, static_cast<uint16_t*>(p.out) + (size_t)row * I + 32 * ht, half, on && valid[0]);
         } else {
           constexpr int F = EPI == kEpiSwigluE4M3 ? kE4M3 : kE2M1;
           uint32_t mo = m;
@@ -541,7 +567,7 @@ __device__ __forceinline__ void mx_tile_body(const MxK& p, int n_nb, u32x4* x0, 
           // lane half h gets channels 16h .. 16h + 15 of its token
           swap_halves(d[0], d[2]);
           swap_halves(d[1], d[3]);
-          if (on && valid) {
+          if (on && valid[0]) {
             const size_t o = (size_t)row * I + 32 * ht + 16 * half;
             if constexpr (F == kE4M3)
               *reinterpret_cast<u32x4*>(static_cast<uint8_t*>(p.out) + o) = u32x4{d[0], d[2], d[1], d[3]};
@@ -553,12 +579,14 @@ __device__ __forceinline__ void mx_tile_body(const MxK& p, int n_nb, u32x4* x0, 
       }
     } else {
 #pragma unroll
-      for (int u = 0; u < CT; ++u) {
-        bool valid;
-        const int tile = wg_tile(own_tile(u), valid);
-        const size_t o = (size_t)row * p.N + 32 * tile;
+      for (int u = 0; u < 2; ++u) {
+        const size_t o = (size_t)row * p.N + 32 * tile[u];
         if constexpr (EPI == kEpiF32) {
-          if (on && valid) {
+          // A use of the sums outside the branch (no instruction): without it the
+          // compiler moves the last matrix instructions, which take operands
+          // from all lanes, into the branch that only lanes with a row enter.
+          asm volatile("" : "+v"(acc[t][u]));
+          if (on && valid[u]) {
 #pragma unroll
             for (int g = 0; g < 4; ++g)
               *reinterpret_cast<f32x4*>(static_cast<float*>(p.out) + o + 8 * g + 4 * half) =
@@ -571,7 +599,7 @@ __device__ __forceinline__ void mx_tile_body(const MxK& p, int n_nb, u32x4* x0, 
             d[i] = EPI == kEpiBf16
                        ? pack_bf16x2(acc[t][u][2 * i], acc[t][u][2 * i + 1])
                        : (uint32_t)f32_to_f16(acc[t][u][2 * i]) | ((uint32_t)f32_to_f16(acc[t][u][2 * i + 1]) << 16);
-          store_tile16(d, static_cast<uint16_t*>(p.out) + o, half, on && valid);
+          store_tile16(d, static_cast<uint16_t*>(p.out) + o, half, on && valid[u]);
         }
       }
     }
@@ -581,10 +609,11 @@ __device__ __forceinline__ void mx_tile_body(const MxK& p, int n_nb, u32x4* x0, 
 // (The LDS stages are declared here: with generic lambdas in the kernel template
 // itself the host's launch stub is not emitted.)
 template <int AF, int EPI, int TM>
-__global__ __launch_bounds__(256, 2) void mx_tile_kernel(MxK p, int n_nb) {
+__global__ __launch_bounds__(256, TM == 128 ? 2 : 3) void mx_tile_kernel(MxK p, int n_nb) {
   constexpr int X = TM * (AF == kE4M3 ? 8 : 4);
-  __shared__ u32x4 x0[X], x1[X], w0[16 * 64], w1[16 * 64];
-  mx_tile_body<AF, EPI, TM>(p, n_nb, x0, x1, w0, w1);
+  __shared__ u32x4 x0[X], x1[X];
+  __shared__ uint32_t s0[256], s1[256];
+  mx_tile_body<AF, EPI, TM>(p, n_nb, x0, x1, s0, s1);
 }
 
 template <int AF, int EPI>
@@ -627,8 +656,11 @@ int launch_fmt(const MxK& k, int epi, int path, hipStream_t s) {
 int launch_mxgemm(const MxGemmArgs& a, void* stream) {
   const hipStream_t s = static_cast<hipStream_t>(stream);
   const size_t row_codes = a.a_fmt == kE4M3 ? a.K : a.K / 2;
+  const int div = a.gather ? a.k : 1;
+  int sh = 0;
+  while (((int64_t)1 << sh) < div) ++sh;
   const MxK k{a.wcodes, a.wscales, a.N, a.K, a.a, a.as, (uint32_t)(a.A_rows * row_codes),
-              (uint32_t)((size_t)a.A_rows * (a.K / 32)), a.A_rows, a.gather, a.gather ? a.k : 1, a.seg, a.E, a.M_total,
+              (uint32_t)((size_t)a.A_rows * (a.K / 32)), a.A_rows, a.gather, (uint32_t)((((uint64_t)1 << (31 + sh)) + div - 1) / div), sh, a.seg, a.E, a.M_total,
               a.out, a.out_scales};
   const int path = mxgemm_path(a.M_total, a.E, a.kernel);
   return a.a_fmt == kE4M3 ? launch_fmt<kE4M3>(k, a.epilogue, path, s) : launch_fmt<kE2M1>(k, a.epilogue, path, s);
