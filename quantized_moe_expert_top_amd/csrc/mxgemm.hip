@@ -77,8 +77,8 @@ __device__ __forceinline__ int source_row(const MxK& p, int row) {
 
 // -------------------------------------------------------- few rows per expert
 // A workgroup takes 64 output channels of one expert (SwiGLU: 32 gate and the
-// matching 32 up channels) and the expert's rows, 32 at a time; its NW
-// wavefronts split K and add their sums through LDS.  Weights and activations
+// matching 32 up channels) and 32 of the expert's rows (every gridDim.z-th
+// group of 32); its NW wavefronts split K and add their sums through LDS.  Weights and activations
 // go from memory straight to the operand registers: each weight byte is read
 // once per 32 rows.
 template <int AF>
@@ -88,9 +88,10 @@ struct SmallBlock {  // operands of one K block of 128
   uint32_t ws[2], as;
 };
 
-template <int AF, int EPI, int NW>
-__global__ __launch_bounds__(64 * NW) void mx_small_kernel(MxK p) {
-  constexpr int D = 2;  // K blocks in flight
+template <int AF, int EPI>
+__global__ __launch_bounds__(256, 3) void mx_small_kernel(MxK p) {
+  constexpr int NW = 4;  // 8 wavefronts were slower where the chip has work (8 experts, 64 rows, 2048 x 2048: 15 for 12 us)
+  constexpr int D = 2;   // K blocks in flight
   __shared__ float red[NW][2][16][64];
   __shared__ uint32_t amx[4][32];
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
@@ -98,7 +99,7 @@ __global__ __launch_bounds__(64 * NW) void mx_small_kernel(MxK p) {
   const int e = blockIdx.y;
   int s0, s1;
   segment(p, e, s0, s1);
-  if (s0 >= s1) return;
+  if (s0 + 32 * (int)blockIdx.z >= s1) return;
 
   const int NT = p.N >> 5, KB = p.K >> 7, KC = (p.K + 255) >> 8;
   const int t0 = is_swiglu(EPI) ? blockIdx.x : 2 * blockIdx.x;
@@ -113,7 +114,7 @@ __global__ __launch_bounds__(64 * NW) void mx_small_kernel(MxK p) {
   const int kb0 = KB * wv / NW, kb1 = KB * (wv + 1) / NW;
   constexpr int kXB = AF == kE4M3 ? 128 : 64;  // activation bytes of a K block
 
-  for (int r0 = s0; r0 < s1; r0 += 32) {
+  for (int r0 = s0 + 32 * (int)blockIdx.z; r0 < s1; r0 += 32 * (int)gridDim.z) {
     // a lane without a row loads the last one's: its column is never stored
     const int src = source_row(p, min(r0 + col, s1 - 1));
     const uint32_t x_off = (uint32_t)src * (uint32_t)(KB * kXB) + 16 * half;
@@ -145,8 +146,7 @@ __global__ __launch_bounds__(64 * NW) void mx_small_kernel(MxK p) {
 #pragma unroll
       for (int i = 0; i < D; ++i) {
         if (kb + i < kb1) {
-          const SmallBlock<AF> b = q[i];
-          if (kb + i + D < kb1) q[i] = load(kb + i + D);
+          const SmallBlock<AF>& b = q[i];
           i32x8 x0, x1;
           if constexpr (AF == kE4M3) {
             x0 = operand(b.x[0][0], b.x[0][1]);
@@ -160,6 +160,7 @@ __global__ __launch_bounds__(64 * NW) void mx_small_kernel(MxK p) {
             acc[t] = mx_mfma<AF, 0, 0>(operand(b.w[t][0]), x0, acc[t], b.ws[t], b.as);
             acc[t] = mx_mfma<AF, 1, 2>(operand(b.w[t][1]), x1, acc[t], b.ws[t], b.as);
           }
+          if (kb + i + D < kb1) q[i] = load(kb + i + D);
         }
       }
     }
@@ -173,7 +174,7 @@ __global__ __launch_bounds__(64 * NW) void mx_small_kernel(MxK p) {
     __syncthreads();
     const int row = r0 + col;
     float v[2][4];
-    if (wv < 4) {
+    {
 #pragma unroll
       for (int t = 0; t < 2; ++t)
 #pragma unroll
@@ -228,7 +229,7 @@ __global__ __launch_bounds__(64 * NW) void mx_small_kernel(MxK p) {
     }
     __syncthreads();
     if constexpr (EPI == kEpiSwigluE4M3 || EPI == kEpiSwigluE2M1) {
-      if (wv < 4 && row < s1) {
+      if (row < s1) {
         constexpr int F = EPI == kEpiSwigluE4M3 ? kE4M3 : kE2M1;
         const int I = p.N / 2, ch = 8 * wv + 4 * half;
         uint32_t m = amx[0][col];
@@ -619,8 +620,11 @@ __global__ __launch_bounds__(256, TM == 128 ? 2 : 3) void mx_tile_kernel(MxK p, 
 template <int AF, int EPI>
 int launch_small(const MxK& k, hipStream_t s) {
   const int NT = k.N / 32;
-  const dim3 grid(is_swiglu(EPI) ? NT / 2 : (NT + 1) / 2, k.E);
-  hipLaunchKernelGGL((mx_small_kernel<AF, EPI, 4>), grid, dim3(256), 0, s, k);
+  // one workgroup per 32 rows up to twice the mean rows of an expert; fuller
+  // experts' workgroups go round
+  const int gz = (2 * (k.M_total / k.E) + 31) / 32;
+  const dim3 grid(is_swiglu(EPI) ? NT / 2 : (NT + 1) / 2, k.E, gz < 1 ? 1 : gz > 64 ? 64 : gz);
+  hipLaunchKernelGGL((mx_small_kernel<AF, EPI>), grid, dim3(256), 0, s, k);
   return (int)hipGetLastError();
 }
 template <int AF, int EPI, int TM>
@@ -662,7 +666,7 @@ int launch_mxgemm(const MxGemmArgs& a, void* stream) {
   const MxK k{a.wcodes, a.wscales, a.N, a.K, a.a, a.as, (uint32_t)(a.A_rows * row_codes),
               (uint32_t)((size_t)a.A_rows * (a.K / 32)), a.A_rows, a.gather, (uint32_t)((((uint64_t)1 << (31 + sh)) + div - 1) / div), sh, a.seg, a.E, a.M_total,
               a.out, a.out_scales};
-  const int path = mxgemm_path(a.M_total, a.E, a.kernel);
+  const int path = mxgemm_path(a.M_total, a.E, a.N, a.K, a.kernel);
   return a.a_fmt == kE4M3 ? launch_fmt<kE4M3>(k, a.epilogue, path, s) : launch_fmt<kE2M1>(k, a.epilogue, path, s);
 }
 
