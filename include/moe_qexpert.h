@@ -492,6 +492,49 @@ moe_status moe_grouped_mxgemm(const moe_mxdesc* w, const uint8_t* a_codes, const
                               int32_t M_total, int32_t epilogue, int32_t kernel, void* out, uint8_t* out_scales,
                               void* stream);
 
+/* One MX layer in one call: moe_route_scored, moe_permute, moe_quantize_mx (if x
+ * is given), the two products (SwiGLU to MX rows in h, then down to y) and
+ * moe_unpermute_combine with the grouping's number of valid rows, with the same
+ * results bit for bit and fewer launches where the batch is small.  E, H and I
+ * are gate_up's and down's: gate_up [E][2I][H], down [E][H][I], I % 128 == 0.
+ *   x       [T][H] of x_dtype, quantised to x_codes / x_scales in x_fmt; or NULL:
+ *           x_codes / x_scales already hold the rows (moe_rmsnorm_mx)
+ *   routing as for moe_route_scored; grouping buffers as for moe_permute (S = 1),
+ *           workspace at least moe_permute_workspace_size(T, k, E, 1) bytes
+ *   h       MX rows [T*k][I] in h_fmt; y [T*k][H] of y_dtype (MOE_DTYPE_*)
+ *   out     bf16 [T][H]
+ * Alignment as for those calls.  Every argument is checked before anything is
+ * launched; T == 0 writes nothing.  T * k < 2^31, k <= E.
+ */
+typedef struct moe_mxlayer {
+  int32_t abi_version; /* MOE_ABI_VERSION */
+  int32_t T, k;
+  int32_t x_dtype, x_fmt, h_fmt, y_dtype;
+  int32_t kernel; /* of both products, as for moe_grouped_mxgemm */
+  int32_t score, n_group, topk_group, group_top, renormalize;
+  float scale;
+  const moe_mxdesc* gate_up; /* host pointers, tiled */
+  const moe_mxdesc* down;
+  const void* x;
+  const float* logits;
+  const float* bias;
+  int32_t* topk_ids;
+  float* topk_w;
+  int32_t* expert_counts;
+  int32_t* seg_offsets;
+  int32_t* sorted_pair;
+  int32_t* pair_pos;
+  void* workspace;
+  size_t workspace_bytes;
+  uint8_t* x_codes;
+  uint8_t* x_scales;
+  uint8_t* h_codes;
+  uint8_t* h_scales;
+  void* y;
+  uint16_t* out;
+} moe_mxlayer;
+moe_status moe_mx_layer(const moe_mxlayer* layer, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -38,7 +38,7 @@ EXPORTED = [
     "moe_grouped_qgemm_workspace_size", "moe_grouped_qgemm", "moe_unpermute_combine",
     "moe_grouped_qgemm_noalloc", "moe_grouped_qgemm_noalloc_scratch_bytes", "moe_copy_rows_async",
     "moe_route_scored", "moe_quantize_mx", "moe_dequantize_mx", "moe_rmsnorm_mx", "moe_mx_field_bytes",
-    "moe_mx_repack", "moe_grouped_mxgemm",
+    "moe_mx_repack", "moe_grouped_mxgemm", "moe_mx_layer",
 ]
 
 
@@ -66,6 +66,16 @@ class MxDesc(ctypes.Structure):
         ("abi_version", ctypes.c_int32), ("layout", ctypes.c_int32), ("E", ctypes.c_int32), ("N", ctypes.c_int32),
         ("K", ctypes.c_int32), ("reserved", ctypes.c_int32), ("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p),
     ]
+
+
+class MxLayer(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("abi_version", "T", "k", "x_dtype", "x_fmt", "h_fmt", "y_dtype", "kernel",
+                                              "score", "n_group", "topk_group", "group_top", "renormalize")] + [
+        ("scale", ctypes.c_float), ("gate_up", ctypes.POINTER(MxDesc)), ("down", ctypes.POINTER(MxDesc))] + [
+        (n, ctypes.c_void_p) for n in ("x", "logits", "bias", "topk_ids", "topk_w", "expert_counts", "seg_offsets",
+                                       "sorted_pair", "pair_pos", "workspace")] + [
+        ("workspace_bytes", ctypes.c_size_t)] + [
+        (n, ctypes.c_void_p) for n in ("x_codes", "x_scales", "h_codes", "h_scales", "y", "out")]
 
 
 def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
@@ -98,6 +108,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "moe_mx_field_bytes": (sz, [mxd, i32]),
         "moe_mx_repack": (i32, [mxd, mxd, vp]),
         "moe_grouped_mxgemm": (i32, [mxd, vp, vp, i32, i32, vp, i32, vp, i32, i32, i32, vp, vp, vp]),
+        "moe_mx_layer": (i32, [ctypes.POINTER(MxLayer), vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)

@@ -42,13 +42,9 @@ moe_status check_mxdesc(const moe_mxdesc* w, int layout, bool need_buffers) {
   if (!aligned(w->scales, 4)) return fail(MOE_ERR_MISALIGNED, "scales must be 4-byte aligned");
   return MOE_OK;
 }
-}  // namespace
-
-extern "C" {
-
-moe_status moe_route_scored(const float* logits, const float* bias, int32_t T, int32_t E, int32_t k, int32_t score,
-                            int32_t n_group, int32_t topk_group, int32_t group_top, int32_t renormalize, float scale,
-                            int32_t* topk_ids, float* topk_w, void* stream) {
+moe_status check_route(const float* logits, const float* bias, int32_t T, int32_t E, int32_t k, int32_t score,
+                       int32_t n_group, int32_t topk_group, int32_t group_top, float scale, const int32_t* topk_ids,
+                       const float* topk_w) {
   if (T < 0) return fail(MOE_ERR_BAD_SHAPE, "T=%d < 0", T);
   if (E < 1 || E > 1024) return fail(MOE_ERR_BAD_SHAPE, "E=%d outside 1..1024", E);
   if (k < 1 || k > E) return fail(MOE_ERR_BAD_SHAPE, "k=%d outside 1..E (E=%d)", k, E);
@@ -60,11 +56,39 @@ moe_status moe_route_scored(const float* logits, const float* bias, int32_t T, i
     return fail(MOE_ERR_BAD_SHAPE, "topk_group=%d outside 1..n_group (%d)", topk_group, n_group);
   if (group_top != 1 && group_top != 2) return fail(MOE_ERR_BAD_SHAPE, "group_top=%d (1 or 2)", group_top);
   if (!isfinite(scale)) return fail(MOE_ERR_BAD_SHAPE, "scale must be finite");
-  if (T == 0) return ok();
+  if (T == 0) return MOE_OK;
   if (!logits || !topk_ids || !topk_w) return fail(MOE_ERR_NULL_ARG, "logits, topk_ids and topk_w are required");
   if (!aligned(logits, 4) || !aligned(bias, 4) || !aligned(topk_ids, 4) || !aligned(topk_w, 4))
     return fail(MOE_ERR_MISALIGNED, "route buffers must be 4-byte aligned");
-  const moe_status st = check_device();
+  return MOE_OK;
+}
+
+moe_status check_kernel(int32_t kernel) {
+  if (kernel < MOE_KERNEL_AUTO || kernel > MOE_KERNEL_LDS_DMA_PER_WIDTH)
+    return fail(MOE_ERR_BAD_FORMAT, "unknown kernel choice %d", kernel);
+  if (kernel != MOE_KERNEL_AUTO && kernel != MOE_KERNEL_SMALL && kernel != MOE_KERNEL_TILE64 &&
+      kernel != MOE_KERNEL_TILE128)
+    return fail(MOE_ERR_UNSUPPORTED, "kernel choice %d does not run MX weights", kernel);
+  return MOE_OK;
+}
+
+moe_status check_code_bytes(int64_t rows, int32_t K, int32_t fmt) {
+  const int64_t n = rows * (fmt == MOE_MX_E4M3 ? K : K / 2);
+  if (n >= ((int64_t)1 << 32))
+    return fail(MOE_ERR_UNSUPPORTED, "activation codes of %lld bytes (4 GiB or more)", (long long)n);
+  return MOE_OK;
+}
+}  // namespace
+
+extern "C" {
+
+moe_status moe_route_scored(const float* logits, const float* bias, int32_t T, int32_t E, int32_t k, int32_t score,
+                            int32_t n_group, int32_t topk_group, int32_t group_top, int32_t renormalize, float scale,
+                            int32_t* topk_ids, float* topk_w, void* stream) {
+  moe_status st = check_route(logits, bias, T, E, k, score, n_group, topk_group, group_top, scale, topk_ids, topk_w);
+  if (st != MOE_OK) return st;
+  if (T == 0) return ok();
+  st = check_device();
   if (st != MOE_OK) return st;
   const moe::ScoredArgs a{logits, bias, T, E, k, score, n_group, topk_group, group_top, renormalize != 0, scale,
                           topk_ids, topk_w};
@@ -162,11 +186,8 @@ moe_status moe_grouped_mxgemm(const moe_mxdesc* w, const uint8_t* a_codes, const
   const bool mx_out = epilogue == MOE_EPI_SWIGLU_E4M3 || epilogue == MOE_EPI_SWIGLU_E2M1;
   if ((epilogue == MOE_EPI_SWIGLU || mx_out) && w->N % 64 != 0)
     return fail(MOE_ERR_UNSUPPORTED, "N=%d must be a multiple of 64 with a SwiGLU epilogue", w->N);
-  if (kernel < MOE_KERNEL_AUTO || kernel > MOE_KERNEL_LDS_DMA_PER_WIDTH)
-    return fail(MOE_ERR_BAD_FORMAT, "unknown kernel choice %d", kernel);
-  if (kernel != MOE_KERNEL_AUTO && kernel != MOE_KERNEL_SMALL && kernel != MOE_KERNEL_TILE64 &&
-      kernel != MOE_KERNEL_TILE128)
-    return fail(MOE_ERR_UNSUPPORTED, "kernel choice %d does not run MX weights", kernel);
+  st = check_kernel(kernel);
+  if (st != MOE_OK) return st;
   if (gather_pair) {
     if (k < 1) return fail(MOE_ERR_BAD_SHAPE, "k=%d with gather_pair", k);
     if ((int64_t)A_rows * k < M_total) return fail(MOE_ERR_BAD_SHAPE, "A_rows*k < M_total");
@@ -180,14 +201,84 @@ moe_status moe_grouped_mxgemm(const moe_mxdesc* w, const uint8_t* a_codes, const
   if (!aligned(a_codes, 16) || !aligned(out, 16)) return fail(MOE_ERR_MISALIGNED, "a_codes and out must be 16-byte aligned");
   if (!aligned(a_scales, 4) || !aligned(seg_offsets, 4) || !aligned(gather_pair, 4))
     return fail(MOE_ERR_MISALIGNED, "a_scales, seg_offsets and gather_pair must be 4-byte aligned");
-  const int64_t a_bytes = (int64_t)A_rows * (a_fmt == MOE_MX_E4M3 ? w->K : w->K / 2);
-  if (a_bytes >= ((int64_t)1 << 32))
-    return fail(MOE_ERR_UNSUPPORTED, "activation codes of %lld bytes (4 GiB or more)", (long long)a_bytes);
+  st = check_code_bytes(A_rows, w->K, a_fmt);
+  if (st != MOE_OK) return st;
   st = check_device();
   if (st != MOE_OK) return st;
   const moe::MxGemmArgs a{w->codes, w->scales, w->E, w->N, w->K, a_codes, a_scales, a_fmt, A_rows, gather_pair, k,
                           seg_offsets, M_total, epilogue, kernel, out, out_scales};
   return hip_status(moe::launch_mxgemm(a, stream), "grouped_mxgemm launch");
+}
+
+moe_status moe_mx_layer(const moe_mxlayer* l, void* stream) {
+  if (!l) return fail(MOE_ERR_NULL_ARG, "layer is NULL");
+  if (l->abi_version != MOE_ABI_VERSION)
+    return fail(MOE_ERR_BAD_FORMAT, "layer abi_version %d, library %d", l->abi_version, MOE_ABI_VERSION);
+  moe_status st = check_mxdesc(l->gate_up, MOE_LAYOUT_TILED, true);
+  if (st != MOE_OK) return st;
+  st = check_mxdesc(l->down, MOE_LAYOUT_TILED, true);
+  if (st != MOE_OK) return st;
+  const moe_mxdesc &gu = *l->gate_up, &dn = *l->down;
+  const int32_t E = gu.E, H = gu.K, I = dn.K, T = l->T, k = l->k;
+  if (dn.E != E || dn.N != H || gu.N != 2 * I)
+    return fail(MOE_ERR_BAD_SHAPE, "gate_up [%d][%d][%d] and down [%d][%d][%d] do not fit together", E, gu.N, H, dn.E, dn.N, I);
+  st = check_route(l->logits, l->bias, T, E, k, l->score, l->n_group, l->topk_group, l->group_top, l->scale,
+                   l->topk_ids, l->topk_w);
+  if (st != MOE_OK) return st;
+  if (l->x && !known_dtype(l->x_dtype)) return fail(MOE_ERR_BAD_FORMAT, "x_dtype %d", l->x_dtype);
+  if (!known_fmt(l->x_fmt) || !known_fmt(l->h_fmt))
+    return fail(MOE_ERR_BAD_FORMAT, "unknown MX format (x %d, h %d)", l->x_fmt, l->h_fmt);
+  if (!known_dtype(l->y_dtype)) return fail(MOE_ERR_BAD_FORMAT, "y_dtype %d", l->y_dtype);
+  st = check_kernel(l->kernel);
+  if (st != MOE_OK) return st;
+  st = check_code_bytes(T, H, l->x_fmt);
+  if (st != MOE_OK) return st;
+  st = check_code_bytes((int64_t)T * k, I, l->h_fmt);
+  if (st != MOE_OK) return st;
+  if (T == 0) return ok();
+  if (!l->expert_counts || !l->seg_offsets || !l->sorted_pair || !l->pair_pos || !l->workspace)
+    return fail(MOE_ERR_NULL_ARG, "the grouping's buffers are required");
+  if (!l->x_codes || !l->x_scales || !l->h_codes || !l->h_scales || !l->y || !l->out)
+    return fail(MOE_ERR_NULL_ARG, "x, h, y and out buffers are required");
+  const size_t need = moe::permute_workspace_bytes(T * k, E, 1);
+  if (l->workspace_bytes < need)
+    return fail(MOE_ERR_WORKSPACE_TOO_SMALL, "workspace %zu bytes, %zu needed", l->workspace_bytes, need);
+  if (!aligned(l->x, 16) || !aligned(l->x_codes, 16) || !aligned(l->h_codes, 16) || !aligned(l->y, 16) ||
+      !aligned(l->out, 16) || !aligned(l->workspace, 16))
+    return fail(MOE_ERR_MISALIGNED, "x, codes, y, out and workspace must be 16-byte aligned");
+  if (!aligned(l->x_scales, 4) || !aligned(l->h_scales, 4) || !aligned(l->expert_counts, 4) ||
+      !aligned(l->seg_offsets, 4) || !aligned(l->sorted_pair, 4) || !aligned(l->pair_pos, 4))
+    return fail(MOE_ERR_MISALIGNED, "scales and grouping buffers must be 4-byte aligned");
+  st = check_device();
+  if (st != MOE_OK) return st;
+
+  const moe::ScoredArgs route{l->logits, l->bias, T, E, k, l->score, l->n_group, l->topk_group, l->group_top,
+                              l->renormalize != 0, l->scale, l->topk_ids, l->topk_w};
+  const moe::FrontRows rows{l->x, l->x_dtype, l->x_fmt, l->x ? (size_t)T * H / 8 : 0, l->x_codes, l->x_scales};
+  const moe::FrontGroups groups{l->expert_counts, l->seg_offsets, l->sorted_pair, l->pair_pos,
+                                static_cast<uint32_t*>(l->workspace)};
+  bool grouped = false;
+  int e = moe::launch_mx_front(route, rows, groups, &grouped, stream);
+  if (e == 0 && !grouped) {
+    const moe::PermuteArgs p{l->topk_ids, nullptr, T * k, k, E, 1, l->expert_counts, l->seg_offsets, l->sorted_pair,
+                             l->pair_pos, nullptr, 0, nullptr, l->workspace};
+    e = moe::launch_permute(p, stream);
+  }
+  if (e == 0) {
+    const moe::MxGemmArgs g{gu.codes, gu.scales, E, gu.N, H, l->x_codes, l->x_scales, l->x_fmt, T, l->sorted_pair, k,
+                            l->seg_offsets, T * k, l->h_fmt == MOE_MX_E4M3 ? MOE_EPI_SWIGLU_E4M3 : MOE_EPI_SWIGLU_E2M1,
+                            l->kernel, l->h_codes, l->h_scales};
+    e = moe::launch_mxgemm(g, stream);
+  }
+  if (e == 0) {
+    const int epi = l->y_dtype == MOE_DTYPE_F32 ? MOE_EPI_NONE_F32 : l->y_dtype == MOE_DTYPE_F16 ? MOE_EPI_NONE_F16 : MOE_EPI_NONE;
+    const moe::MxGemmArgs g{dn.codes, dn.scales, E, H, I, l->h_codes, l->h_scales, l->h_fmt, T * k, nullptr, 1,
+                            l->seg_offsets, T * k, epi, l->kernel, l->y, nullptr};
+    e = moe::launch_mxgemm(g, stream);
+  }
+  if (e == 0)
+    e = moe::launch_combine(l->y, l->y_dtype, l->pair_pos, l->seg_offsets + E, l->topk_w, T, k, H, l->out, stream);
+  return hip_status(e, "mx_layer launch");
 }
 
 }  // extern "C"

@@ -119,6 +119,24 @@ struct ScoredArgs {
   float* w;
 };
 int launch_route_scored(const ScoredArgs& a, void* stream);
+// The start of a layer's call in one launch: routing, the quantisation of n8
+// 8-value groups (0: none), and for few tokens the grouping of the pairs too
+// (*grouped says whether).
+struct FrontRows {
+  const void* x;
+  int dtype, fmt;  // MOE_DTYPE_*, MOE_MX_*
+  size_t n8;
+  uint8_t* codes;
+  uint8_t* scales;
+};
+struct FrontGroups {
+  int32_t* counts;
+  int32_t* seg_offsets;
+  int32_t* sorted_pair;
+  int32_t* pair_pos;
+  uint32_t* flag;
+};
+int launch_mx_front(const ScoredArgs& a, const FrontRows& q, const FrontGroups& g, bool* grouped, void* stream);
 
 // ----------------------------------------------------------------- MX rows
 // dtypes MOE_DTYPE_*, fmt MOE_MX_*

@@ -13,117 +13,12 @@ namespace moe {
 
 namespace {
 constexpr int kThreads = 256;
-constexpr int kUnroll = 4;  // 8-value groups per thread, all loads issued before the first is used
-typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
-
-// 8 consecutive values as they are stored: 16 bytes (16-bit types) or 32.
-template <int DT>
-struct Raw8 {
-  u32x4 d[DT == 1 ? 2 : 1];
-};
-template <int DT>
-__device__ __forceinline__ Raw8<DT> load8(const void* x, size_t i8) {
-  Raw8<DT> r;
-  const u32x4* p = static_cast<const u32x4*>(x) + i8 * (DT == 1 ? 2 : 1);
-  r.d[0] = p[0];
-  if constexpr (DT == 1) r.d[1] = p[1];
-  return r;
-}
-template <int DT>
-__device__ __forceinline__ void unpack8(const Raw8<DT>& r, float v[8]) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t w = r.d[0][i];
-    if constexpr (DT == 0) {
-      v[2 * i] = bf16_lo(w);
-      v[2 * i + 1] = bf16_hi(w);
-    } else if constexpr (DT == 2) {
-      v[2 * i] = f16_to_f32((uint16_t)(w & 0xFFFFu));
-      v[2 * i + 1] = f16_to_f32((uint16_t)(w >> 16));
-    } else {
-      const uint32_t w1 = r.d[1][i];
-      v[i] = __builtin_bit_cast(float, w);
-      v[4 + i] = __builtin_bit_cast(float, w1);
-    }
-  }
-}
-__device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b ? a : b; }
-__device__ __forceinline__ uint32_t pk_umax16(uint32_t a, uint32_t b) {
-  const u16x2 m = __builtin_elementwise_max(__builtin_bit_cast(u16x2, a), __builtin_bit_cast(u16x2, b));
-  return __builtin_bit_cast(uint32_t, m);
-}
-// fp32 bits of the largest magnitude of the lane's 8 values
-template <int DT>
-__device__ __forceinline__ uint32_t absmax8(const Raw8<DT>& r) {
-  if constexpr (DT == 1) {
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t a = r.d[0][i], b = r.d[1][i];
-      m = umax(m, umax(a & 0x7FFFFFFFu, b & 0x7FFFFFFFu));
-    }
-    return m;
-  } else {
-    uint32_t m = 0;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const uint32_t a = r.d[0][i];
-      m = pk_umax16(m, a & 0x7FFF7FFFu);
-    }
-    m = umax(m & 0xFFFFu, m >> 16);
-    return DT == 0 ? m << 16 : __builtin_bit_cast(uint32_t, f16_to_f32((uint16_t)m));
-  }
-}
-__device__ __forceinline__ uint32_t absmax8f(const float v[8]) {
-  uint32_t m = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float f = v[i];
-    m = umax(m, __builtin_bit_cast(uint32_t, f) & 0x7FFFFFFFu);
-  }
-  return m;
-}
-
-// Quantises the lane's 8 values (group i8 of the flat array) given its block's
-// largest magnitude; the quad's first lane writes the scale byte.
-template <int FMT>
-__device__ __forceinline__ void store_mx8(const float v[8], uint32_t mbits, size_t i8, uint8_t* __restrict__ codes,
-                                          uint8_t* __restrict__ scales) {
-  const int p = mx_exponent<FMT>(mbits);
-  const bool bad = mx_not_finite(mbits);
-  const float inv = mx_inverse(p);
-  float u[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) u[i] = bad ? 0.0f : v[i] * inv;
-  if constexpr (FMT == kE4M3) {
-    const u32x2 c = {mx_pack4_e4m3(u[0], u[1], u[2], u[3]), mx_pack4_e4m3(u[4], u[5], u[6], u[7])};
-    reinterpret_cast<u32x2*>(codes)[i8] = c;
-  } else {
-    reinterpret_cast<uint32_t*>(codes)[i8] =
-        mx_pack4_e2m1(u[0], u[1], u[2], u[3]) | (mx_pack4_e2m1(u[4], u[5], u[6], u[7]) << 16);
-  }
-  if ((threadIdx.x & 3) == 0) scales[i8 >> 2] = bad ? (uint8_t)255 : (uint8_t)(p + 127);
-}
-
-// n8: 8-value groups (a multiple of 4, so quads are whole).
+constexpr int kUnroll = kQuantUnroll;
 template <int DT, int FMT>
 __global__ __launch_bounds__(kThreads) void quantize_mx_kernel(const void* __restrict__ x, size_t n8,
                                                                uint8_t* __restrict__ codes,
                                                                uint8_t* __restrict__ scales) {
-  const size_t base = (size_t)blockIdx.x * (kThreads * kUnroll) + threadIdx.x;
-  Raw8<DT> r[kUnroll];
-#pragma unroll
-  for (int j = 0; j < kUnroll; ++j)
-    if (base + j * kThreads < n8) r[j] = load8<DT>(x, base + j * kThreads);
-#pragma unroll
-  for (int j = 0; j < kUnroll; ++j) {
-    const size_t i8 = base + j * kThreads;
-    if (i8 < n8) {
-      float v[8];
-      unpack8<DT>(r[j], v);
-      store_mx8<FMT>(v, quad_umax(absmax8<DT>(r[j])), i8, codes, scales);
-    }
-  }
+  quantize_block<DT, FMT, kThreads>(x, n8, codes, scales, blockIdx.x);
 }
 
 template <int DT>

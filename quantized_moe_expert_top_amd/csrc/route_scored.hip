@@ -18,7 +18,8 @@
 // Every way gives the same result.
 #include <float.h>
 
-#include "common.h"
+#include "mx.h"
+#include "permute_dev.h"
 
 namespace moe {
 
@@ -204,13 +205,10 @@ constexpr int kSpare = 6;  // candidates beyond k that cost less than another st
 // SOFT_ALL: the softmax denominator is needed (a bias, weights that are not
 // renormalised, sums of two scores per group): float64 exponentials of all
 // experts give it and the keys.
+// Token t by this wavefront; buf: 64 * NS doubles of LDS of its own.
 template <int NS, bool SOFT_ALL>
-__global__ __launch_bounds__(64 * kWavesPerBlock) void route_scored_kernel(ScoredArgs a) {
-  __shared__ double lds[kWavesPerBlock][64 * NS];
-  const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  const int t = blockIdx.x * kWavesPerBlock + wv;
-  if (t >= a.T) return;
-  double* const buf = lds[wv];
+__device__ __forceinline__ void route_token(const ScoredArgs& a, int t, double* buf) {
+  const int lane = threadIdx.x & 63;
   const float* row = a.logits + (size_t)t * a.E;
 
   float x[NS], b[NS];
@@ -406,13 +404,107 @@ __global__ __launch_bounds__(64 * kWavesPerBlock) void route_scored_kernel(Score
     a.w[o + j] = 0.0f;
   }
 }
+template <int NS, bool SOFT_ALL>
+__global__ __launch_bounds__(64 * kWavesPerBlock) void route_scored_kernel(ScoredArgs a) {
+  __shared__ double lds[kWavesPerBlock][64 * NS];
+  const int wv = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int t = blockIdx.x * kWavesPerBlock + wv;
+  if (t < a.T) route_token<NS, SOFT_ALL>(a, t, lds[wv]);
+}
+
+// ------------------------------------------------- the start of a layer's call
+// Routing and the quantisation of the layer's rows do not depend on each other:
+// one launch has workgroups for both.  Up to kFrontTokens tokens are routed by
+// one workgroup, a wavefront each, which then groups the pairs as well.
+template <int NT>
+__device__ __forceinline__ void quantize_any(const FrontRows& q, size_t block) {
+  const size_t n8 = q.n8;
+#define MOE_Q(DT)                                                                        \
+  if (q.fmt == kE4M3) quantize_block<DT, kE4M3, NT>(q.x, n8, q.codes, q.scales, block);  \
+  else quantize_block<DT, kE2M1, NT>(q.x, n8, q.codes, q.scales, block)
+  if (q.dtype == 0) { MOE_Q(0); }
+  else if (q.dtype == 1) { MOE_Q(1); }
+  else { MOE_Q(2); }
+#undef MOE_Q
+}
+
+template <int NS, bool SOFT_ALL>
+__global__ __launch_bounds__(64 * kWavesPerBlock) void mx_front_kernel(ScoredArgs a, FrontRows q, int n_route) {
+  __shared__ double lds[kWavesPerBlock][64 * NS];
+  if ((int)blockIdx.x >= n_route) {
+    quantize_any<64 * kWavesPerBlock>(q, blockIdx.x - n_route);
+    return;
+  }
+  const int wv = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int t = blockIdx.x * kWavesPerBlock + wv;
+  if (t < a.T) route_token<NS, SOFT_ALL>(a, t, lds[wv]);
+}
+
+constexpr int kFrontTokens = 16, kFrontThreads = 64 * kFrontTokens;
+template <int NS, bool SOFT_ALL>
+__global__ __launch_bounds__(kFrontThreads) void mx_front_small_kernel(ScoredArgs a, FrontRows q, FrontGroups g) {
+  __shared__ double lds[kFrontTokens][64 * NS];
+  __shared__ int hist[64 * NS + 1], tags[kFrontTokens * (64 * NS + 1)], scratch[kFrontTokens + 1];
+  __shared__ uint32_t bad;
+  if (blockIdx.x > 0) {
+    quantize_any<kFrontThreads>(q, blockIdx.x - 1);
+    return;
+  }
+  const int wv = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  if (wv < a.T) route_token<NS, SOFT_ALL>(a, wv, lds[wv]);
+  __syncthreads();  // the ids, read back by the whole workgroup
+  const Keyer kr{a.ids, nullptr, a.E, 1, a.E};
+  permute_block<kFrontThreads>(kr, a.T * a.k, g.counts, g.seg_offsets, g.sorted_pair, g.pair_pos, g.flag, hist, tags,
+                               scratch, &bad);
+}
+
+inline bool soft_all(const ScoredArgs& a) {
+  return a.score == 0 && (a.bias || !a.renorm || (a.n_group > 1 && a.group_top == 2));
+}
+template <int NS>
+void launch_ns(const ScoredArgs& a, hipStream_t s) {
+  const dim3 grid((a.T + kWavesPerBlock - 1) / kWavesPerBlock), block(64 * kWavesPerBlock);
+  if (soft_all(a)) hipLaunchKernelGGL((route_scored_kernel<NS, true>), grid, block, 0, s, a);
+  else hipLaunchKernelGGL((route_scored_kernel<NS, false>), grid, block, 0, s, a);
+}
+inline unsigned quant_blocks(const FrontRows& q, int threads) {
+  const size_t per = (size_t)threads * kQuantUnroll;
+  return (unsigned)((q.n8 + per - 1) / per);
+}
+template <int NS>
+void launch_front_ns(const ScoredArgs& a, const FrontRows& q, hipStream_t s) {
+  const int n_route = (a.T + kWavesPerBlock - 1) / kWavesPerBlock;
+  const dim3 grid(n_route + quant_blocks(q, 64 * kWavesPerBlock)), block(64 * kWavesPerBlock);
+  if (soft_all(a)) hipLaunchKernelGGL((mx_front_kernel<NS, true>), grid, block, 0, s, a, q, n_route);
+  else hipLaunchKernelGGL((mx_front_kernel<NS, false>), grid, block, 0, s, a, q, n_route);
+}
+template <int NS>
+void launch_front_small_ns(const ScoredArgs& a, const FrontRows& q, const FrontGroups& g, hipStream_t s) {
+  const dim3 grid(1 + quant_blocks(q, kFrontThreads)), block(kFrontThreads);
+  if (soft_all(a)) hipLaunchKernelGGL((mx_front_small_kernel<NS, true>), grid, block, 0, s, a, q, g);
+  else hipLaunchKernelGGL((mx_front_small_kernel<NS, false>), grid, block, 0, s, a, q, g);
+}
 }  // namespace
 
-template <int NS>
-static void launch_ns(const ScoredArgs& a, hipStream_t s) {
-  const dim3 grid((a.T + kWavesPerBlock - 1) / kWavesPerBlock), block(64 * kWavesPerBlock);
-  if (a.score == 0 && (a.bias || !a.renorm || (a.n_group > 1 && a.group_top == 2))) hipLaunchKernelGGL((route_scored_kernel<NS, true>), grid, block, 0, s, a);
-  else hipLaunchKernelGGL((route_scored_kernel<NS, false>), grid, block, 0, s, a);
+int launch_mx_front(const ScoredArgs& a, const FrontRows& q, const FrontGroups& g, bool* grouped, void* stream) {
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  *grouped = a.T <= kFrontTokens && a.E <= 256;
+  if (*grouped) {
+    if (a.E <= 64) launch_front_small_ns<1>(a, q, g, s);
+    else if (a.E <= 128) launch_front_small_ns<2>(a, q, g, s);
+    else launch_front_small_ns<4>(a, q, g, s);
+  } else if (a.E <= 64) {
+    launch_front_ns<1>(a, q, s);
+  } else if (a.E <= 128) {
+    launch_front_ns<2>(a, q, s);
+  } else if (a.E <= 256) {
+    launch_front_ns<4>(a, q, s);
+  } else if (a.E <= 512) {
+    launch_front_ns<8>(a, q, s);
+  } else {
+    launch_front_ns<16>(a, q, s);
+  }
+  return (int)hipGetLastError();
 }
 
 int launch_route_scored(const ScoredArgs& a, void* stream) {

@@ -17,8 +17,7 @@ import torch
 from . import (MOE_ABI_VERSION, MOE_DTYPE_BF16, MOE_DTYPE_F16, MOE_DTYPE_F32, MOE_EPI_NONE, MOE_EPI_NONE_F16,
                MOE_EPI_NONE_F32, MOE_EPI_SWIGLU, MOE_EPI_SWIGLU_E2M1, MOE_EPI_SWIGLU_E4M3, MOE_FIELD_CODES,
                MOE_FIELD_SCALES, MOE_KERNEL_AUTO, MOE_LAYOUT_CANONICAL, MOE_LAYOUT_TILED, MOE_MX_E2M1, MOE_MX_E4M3,
-               MOE_SCORE_SIGMOID, MOE_SCORE_SOFTMAX, MxDesc, Permutation, _check, _DTYPE_EPI, lib, moe_permute,
-               moe_unpermute_combine)
+               MOE_SCORE_SIGMOID, MOE_SCORE_SOFTMAX, MxDesc, MxLayer, Permutation, _check, _DTYPE_EPI, lib)
 
 _DTYPES = {torch.bfloat16: MOE_DTYPE_BF16, torch.float32: MOE_DTYPE_F32, torch.float16: MOE_DTYPE_F16}
 _MX_EPI = {MOE_MX_E4M3: MOE_EPI_SWIGLU_E4M3, MOE_MX_E2M1: MOE_EPI_SWIGLU_E2M1}
@@ -400,14 +399,33 @@ def moe_mx_layer_forward(x: Union[torch.Tensor, MxRows], logits: torch.Tensor, k
         buf = alloc_mx_layer(T, E, k, H, I, dev, act=rows.fmt if rows else MOE_MX_E4M3)
     elif buf.sizes != (T, E, k, H, I):
         raise ValueError(f"buffers of (T, E, k, H, I) = {buf.sizes} for a layer of {(T, E, k, H, I)}")
-    moe_route_scored(logits, k, r.score, r.bias, r.n_group, r.topk_group, r.group_top, r.renormalize, r.scale,
-                     buf.ids, buf.w)
-    moe_permute(buf.ids, E, out=buf.perm)
     if rows is None:
-        rows = moe_quantize_mx(x, buf.x.fmt, buf.x)
-    moe_grouped_mxgemm(gate_up, rows, buf.perm.seg_offsets, T * k, _MX_EPI[buf.h.fmt], buf.perm.sorted_pair, k, buf.h,
-                       None, kernel)
-    moe_grouped_mxgemm(down, buf.h, buf.perm.seg_offsets, T * k, _DTYPE_EPI[buf.y_perm.dtype], None, 1, buf.y_perm,
-                       None, kernel)
-    moe_unpermute_combine(buf.y_perm, buf.perm.pair_pos, buf.w, T, k, out=buf.out, n_valid=buf.perm.seg_offsets[-1:])
+        if x.dtype not in _DTYPES:
+            raise ValueError(f"x must be bfloat16, float16, float32 or MX rows (got {x.dtype})")
+        q = buf.x
+    else:
+        q = rows
+    if logits.dtype != torch.float32:
+        raise ValueError(f"logits must be float32 (got {logits.dtype})")
+    if r.bias is not None:
+        _want(r.bias, "bias", torch.float32, (E,))
+    p = buf.perm
+    P = T * k
+    if (q.shape != (T, H) or buf.h.shape != (P, I) or buf.y_perm.shape != (P, H) or buf.y_perm.dtype not in _DTYPES
+            or buf.ids.nbytes != 4 * P or buf.w.nbytes != 4 * P or buf.out.nbytes != 2 * T * H
+            or p.counts.nbytes < 4 * E or p.seg_offsets.nbytes < 4 * E + 4 or p.sorted_pair.nbytes < 4 * P
+            or p.pair_pos.nbytes < 4 * P):
+        raise ValueError("a layer buffer was replaced by one of another size")
+    if _device(logits, r.bias, q.codes, q.scales, buf.ids, buf.w, p.counts, p.seg_offsets, p.sorted_pair, p.pair_pos,
+               p.workspace, buf.h.codes, buf.h.scales, buf.y_perm, buf.out, *gate_up.tensors.values(),
+               *down.tensors.values()) != dev or (rows is None and not x.is_contiguous()):
+        raise ValueError(f"x (contiguous, on {dev}) and the layer's tensors must be on one GPU")
+    args = MxLayer(MOE_ABI_VERSION, T, k, MOE_DTYPE_BF16 if rows else _DTYPES[x.dtype], q.fmt, buf.h.fmt,
+                   _DTYPES[buf.y_perm.dtype], kernel, r.score, r.n_group, r.topk_group, r.group_top,
+                   1 if r.renormalize else 0, r.scale, ctypes.pointer(gate_up.desc), ctypes.pointer(down.desc),
+                   None if rows else x.data_ptr(), logits.data_ptr(), _p(r.bias), buf.ids.data_ptr(), buf.w.data_ptr(),
+                   p.counts.data_ptr(), p.seg_offsets.data_ptr(), p.sorted_pair.data_ptr(), p.pair_pos.data_ptr(),
+                   p.workspace.data_ptr(), p.workspace.numel(), q.codes.data_ptr(), q.scales.data_ptr(),
+                   buf.h.codes.data_ptr(), buf.h.scales.data_ptr(), buf.y_perm.data_ptr(), buf.out.data_ptr())
+    _call("moe_mx_layer", dev, ctypes.byref(args))
     return buf

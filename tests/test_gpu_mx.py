@@ -485,6 +485,45 @@ def test_layer_quantises_bf16_input_and_checks_sizes():
     assert q.moe_mx_layer_forward(x[:0], logits[:0], k, gu, dn).out.shape == (0, H)
 
 
+@pytest.mark.parametrize("T,E,k,given", [(1, 4, 1, False), (16, 256, 8, False), (16, 64, 6, True), (17, 64, 6, False),
+                                         (9, 300, 5, False), (3, 100, 33, False), (700, 40, 8, True), (1200, 130, 4, False)])
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+def test_layer_call_equals_its_parts(T, E, k, given, dt):
+    """The layer's one call (fused starts for few tokens, separate launches for many) against routing, grouping,
+    quantisation, products and combine called one by one: every buffer bit for bit."""
+    H, I = 128, 128
+    g = torch.Generator(device=DEV).manual_seed(T + E)
+    r = lambda *s: torch.randn(*s, device=DEV, generator=g)  # noqa: E731
+    gu = q.moe_mx_repack(q.mx_experts(q.moe_quantize_mx(r(E, 2 * I, H), q.MOE_MX_E2M1)))
+    dn = q.moe_mx_repack(q.mx_experts(q.moe_quantize_mx(r(E, H, I), q.MOE_MX_E2M1)))
+    x, logits, bias = r(T, H).to(DT[dt]), r(T, E), 0.1 * r(E)
+    if T > 2:
+        logits[1] = -float("inf")
+        logits[2, 1:] = float("nan")
+    show("layer parts", T, E, k, given, dt)
+    for routing in (q.ScoredRouting(), q.ScoredRouting(score=q.MOE_SCORE_SIGMOID, bias=bias, renormalize=False, scale=2.5),
+                    q.ScoredRouting(bias=bias, n_group=4 if E % 4 == 0 else 1, topk_group=2 if E % 4 == 0 else 1, group_top=2)):
+        rows = q.moe_quantize_mx(x, q.MOE_MX_E2M1)
+        buf = q.alloc_mx_layer(T, E, k, H, I, DEV, act=q.MOE_MX_E2M1)
+        for t in (buf.out, buf.y_perm, buf.w):
+            t.fill_(7)
+        q.moe_mx_layer_forward(rows if given else x, logits, k, gu, dn, routing=routing, buf=buf)
+        ids, w = q.moe_route_scored(logits, k, routing.score, routing.bias, routing.n_group, routing.topk_group,
+                                    routing.group_top, routing.renormalize, routing.scale)
+        p = q.moe_permute(ids, E)
+        h = q.moe_grouped_mxgemm(gu, rows, p.seg_offsets, T * k, q.MOE_EPI_SWIGLU_E4M3, gather_pair=p.sorted_pair, k=k)
+        y = q.moe_grouped_mxgemm(dn, h, p.seg_offsets, T * k, q.MOE_EPI_NONE_F16)
+        out = q.moe_unpermute_combine(y, p.pair_pos, w, T, k, n_valid=p.seg_offsets[-1:])
+        n = int(p.seg_offsets[-1])
+        assert torch.equal(buf.ids, ids) and torch.equal(buf.w, w) and torch.equal(buf.out, out)
+        for a, b in ((buf.perm.counts, p.counts), (buf.perm.seg_offsets, p.seg_offsets),
+                     (buf.perm.sorted_pair, p.sorted_pair), (buf.perm.pair_pos, p.pair_pos),
+                     (buf.h.codes[:n], h.codes[:n]), (buf.h.scales[:n], h.scales[:n]), (buf.y_perm[:n], y[:n])):
+            assert torch.equal(a, b)
+        if not given:
+            assert torch.equal(buf.x.codes, rows.codes) and torch.equal(buf.x.scales, rows.scales)
+
+
 def test_layer_captured_and_on_other_streams():
     """The run of operators captured into a graph, replayed on new inputs with eager work between the replays, and
     issued on a side stream: the eager bits each time."""

@@ -150,6 +150,37 @@ def test_grouped_mxgemm_validation(lib):
     assert gemm(M=0, a=None, s=None, seg=None, out=None) == OK
 
 
+def test_mx_layer_validation(lib):
+    def call(**kw):
+        gu = mxdesc(E=4, N=2 * kw.pop("I", 256), K=kw.get("H", 128))
+        dn = mxdesc(E=kw.pop("E_down", 4), N=kw.pop("N_down", kw.pop("H", 128)), K=256)
+        f = dict(abi_version=q.MOE_ABI_VERSION, T=3, k=2, x_dtype=q.MOE_DTYPE_BF16, x_fmt=1, h_fmt=1, y_dtype=q.MOE_DTYPE_F16,
+                 kernel=0, score=0, n_group=1, topk_group=1, group_top=1, renormalize=1, scale=1.0, bias=None,
+                 workspace_bytes=256, gate_up=ctypes.pointer(gu), down=ctypes.pointer(dn))
+        for n in ("x", "logits", "topk_ids", "topk_w", "expert_counts", "seg_offsets", "sorted_pair", "pair_pos", "workspace",
+                  "x_codes", "x_scales", "h_codes", "h_scales", "y", "out"):
+            f[n] = 0x1000
+        f.update(kw)
+        layer = q.MxLayer()
+        for n, v in f.items():
+            setattr(layer, n, v)
+        return lib.moe_mx_layer(ctypes.byref(layer), None)
+    assert lib.moe_mx_layer(None, None) == NULL_ARG
+    assert call(abi_version=2) == call(x_dtype=5) == call(x_fmt=0) == call(h_fmt=3) == call(y_dtype=3) == BAD_FORMAT
+    assert call(score=2) == call(kernel=9) == BAD_FORMAT and call(kernel=6) == UNSUPPORTED
+    assert call(I=320) == call(E_down=5) == call(N_down=256) == BAD_SHAPE            # the two products do not fit
+    assert call(T=-1) == call(k=5) == call(n_group=3) == call(scale=float("nan")) == BAD_SHAPE
+    for n in ("logits", "topk_ids", "topk_w", "expert_counts", "seg_offsets", "sorted_pair", "pair_pos", "workspace",
+              "x_codes", "x_scales", "h_codes", "h_scales", "y", "out"):
+        assert call(**{n: None}) == NULL_ARG, n
+    assert call(workspace_bytes=255) == WS_SMALL
+    for n in ("x", "x_codes", "h_codes", "y", "out", "workspace"):
+        assert call(**{n: 0x1008}) == MISALIGNED, n
+    for n in ("x_scales", "h_scales", "logits", "bias", "seg_offsets", "sorted_pair", "pair_pos", "expert_counts"):
+        assert call(**{n: 0x1002}) == MISALIGNED, n
+    assert call(T=0, logits=None, x=None, out=None) == OK
+
+
 # ------------------------------------------------------------ the binding's checks
 def test_mx_rows_object():
     u8 = dict(dtype=torch.uint8)
