@@ -19,22 +19,45 @@ __device__ __forceinline__ int mx_exponent(uint32_t mbits) {
   return p < -126 ? -126 : p;
 }
 __device__ __forceinline__ bool mx_not_finite(uint32_t mbits) { return mbits >= 0x7F800000u; }
-// 2^-p for -126 <= p <= 126
-__device__ __forceinline__ float mx_inverse(int p) { return __builtin_bit_cast(float, (uint32_t)(127 - p) << 23); }
+// 2^p for -126 <= p <= 126
+__device__ __forceinline__ float mx_scale(int p) { return __builtin_bit_cast(float, (uint32_t)(p + 127) << 23); }
 
-// Four values, already divided by the scale, to their codes: 4 bytes of e4m3,
-// or 2 bytes of e2m1 (the first value in the low nibble).  The conversions
+// Four values over the scale (a power of two: exact) to their codes: 4 bytes of
+// e4m3, or 2 bytes of e2m1 (the first value in the low nibble).  The conversions
 // round to nearest even; with mx_exponent's scale nothing exceeds the largest
 // element, so their saturation is never reached.
-__device__ __forceinline__ uint32_t mx_pack4_e4m3(float a, float b, float c, float d) {
-  int v = __builtin_amdgcn_cvt_pk_fp8_f32(a, b, 0, false);
-  v = __builtin_amdgcn_cvt_pk_fp8_f32(c, d, v, true);
-  return (uint32_t)v;
+template <int FMT>
+__device__ __forceinline__ uint32_t mx_pack4(float a, float b, float c, float d, float scale) {
+  if constexpr (FMT == kE4M3) {
+    typedef short s16x2 __attribute__((ext_vector_type(2)));
+    s16x2 v = {0, 0};
+    v = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(v, a, b, scale, false);
+    v = __builtin_amdgcn_cvt_scalef32_pk_fp8_f32(v, c, d, scale, true);
+    return __builtin_bit_cast(uint32_t, v);
+  } else {
+    uint32_t v = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0u, a, b, scale, 0);
+    return __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(v, c, d, scale, 1);
+  }
 }
-__device__ __forceinline__ uint32_t mx_pack4_e2m1(float a, float b, float c, float d) {
-  uint32_t v = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(0u, a, b, 1.0f, 0);
-  v = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(v, c, d, 1.0f, 1);
-  return v;
+
+// Bits of the largest magnitude of n values; a NaN among them stays (IEEE
+// maximum, two values per instruction).
+template <int N>
+__device__ __forceinline__ uint32_t absmax_bits(const float (&v)[N]) {
+  float m = __builtin_fabsf(v[0]);
+#pragma unroll
+  for (int i = 1; i + 1 < N; i += 2)
+    m = __builtin_elementwise_maximum(__builtin_elementwise_maximum(__builtin_fabsf(v[i]), __builtin_fabsf(v[i + 1])), m);
+  if (N % 2 == 0) m = __builtin_elementwise_maximum(__builtin_fabsf(v[N - 1]), m);
+  return __builtin_bit_cast(uint32_t, m) & 0x7FFFFFFFu;
+}
+
+// fp16 pair, rounded to nearest even
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+  typedef float f32x2_t __attribute__((ext_vector_type(2)));
+  typedef _Float16 f16x2_t __attribute__((ext_vector_type(2)));
+  const f32x2_t v = {lo, hi};
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(v, f16x2_t));
 }
 
 // max over the 4 lanes of a quad (DPP quad permutes: no LDS traffic)
@@ -106,34 +129,19 @@ __device__ __forceinline__ uint32_t absmax8(const Raw8<DT>& r) {
     return DT == 0 ? m << 16 : __builtin_bit_cast(uint32_t, f16_to_f32((uint16_t)m));
   }
 }
-__device__ __forceinline__ uint32_t absmax8f(const float v[8]) {
-  uint32_t m = 0;
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float f = v[i];
-    m = umax(m, __builtin_bit_cast(uint32_t, f) & 0x7FFFFFFFu);
-  }
-  return m;
-}
-
 // Quantises the lane's 8 values (group i8 of the flat array) given its block's
 // largest magnitude; the quad's first lane writes the scale byte.
 template <int FMT>
-__device__ __forceinline__ void store_mx8(const float v[8], uint32_t mbits, size_t i8, uint8_t* __restrict__ codes,
+__device__ __forceinline__ void store_mx8(const float (&v)[8], uint32_t mbits, size_t i8, uint8_t* __restrict__ codes,
                                           uint8_t* __restrict__ scales) {
   const int p = mx_exponent<FMT>(mbits);
   const bool bad = mx_not_finite(mbits);
-  const float inv = mx_inverse(p);
-  float u[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) u[i] = bad ? 0.0f : v[i] * inv;
-  if constexpr (FMT == kE4M3) {
-    const u32x2 c = {mx_pack4_e4m3(u[0], u[1], u[2], u[3]), mx_pack4_e4m3(u[4], u[5], u[6], u[7])};
-    reinterpret_cast<u32x2*>(codes)[i8] = c;
-  } else {
-    reinterpret_cast<uint32_t*>(codes)[i8] =
-        mx_pack4_e2m1(u[0], u[1], u[2], u[3]) | (mx_pack4_e2m1(u[4], u[5], u[6], u[7]) << 16);
-  }
+  const float scale = mx_scale(p);
+  const uint32_t lo = mx_pack4<FMT>(v[0], v[1], v[2], v[3], scale), hi = mx_pack4<FMT>(v[4], v[5], v[6], v[7], scale);
+  if constexpr (FMT == kE4M3)
+    reinterpret_cast<u32x2*>(codes)[i8] = u32x2{bad ? 0u : lo, bad ? 0u : hi};
+  else
+    reinterpret_cast<uint32_t*>(codes)[i8] = bad ? 0u : lo | (hi << 16);
   if ((threadIdx.x & 3) == 0) scales[i8 >> 2] = bad ? (uint8_t)255 : (uint8_t)(p + 127);
 }
 

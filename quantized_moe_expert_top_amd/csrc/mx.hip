@@ -39,7 +39,7 @@ __device__ __forceinline__ void store8(void* out, size_t i8, const float v[8]) {
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       o[i] = DT == 0 ? pack_bf16x2(v[2 * i], v[2 * i + 1])
-                     : (uint32_t)f32_to_f16(v[2 * i]) | ((uint32_t)f32_to_f16(v[2 * i + 1]) << 16);
+                     : pack_f16x2(v[2 * i], v[2 * i + 1]);
     p[0] = o;
   }
 }
@@ -165,7 +165,7 @@ __global__ __launch_bounds__(kThreads) void rmsnorm_mx_kernel(NormArgs a) {
       v[j][i] = hi + __builtin_fmaf(m, flo, __builtin_fmaf(m, fhi, -hi));
     }
     if (a.y) store8<DT>(a.y, r8 + c, v[j]);
-    if constexpr (FMT != 0) store_mx8<FMT>(v[j], quad_umax(absmax8f(v[j])), r8 + c, a.codes, a.scales);
+    if constexpr (FMT != 0) store_mx8<FMT>(v[j], quad_umax(absmax_bits(v[j])), r8 + c, a.codes, a.scales);
   }
 }
 

@@ -196,12 +196,7 @@ __global__ __launch_bounds__(256, 3) void mx_small_kernel(MxK p) {
             *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(p.out) + (size_t)row * I + 32 * t0 + ch) = o;
           }
         } else {
-          uint32_t m = 0;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const uint32_t b = __builtin_bit_cast(uint32_t, h[i]) & 0x7FFFFFFFu;
-            m = m > b ? m : b;
-          }
+          const uint32_t m = absmax_bits(h);
           const uint32_t o = __shfl_xor(m, 32, 64);
           if (half == 0) amx[wv][col] = m > o ? m : o;
         }
@@ -220,7 +215,7 @@ __global__ __launch_bounds__(256, 3) void mx_small_kernel(MxK p) {
 #pragma unroll
               for (int i = 0; i < 2; ++i)
                 b[i] = EPI == kEpiBf16 ? pack_bf16x2(v[t][2 * i], v[t][2 * i + 1])
-                                       : (uint32_t)f32_to_f16(v[t][2 * i]) | ((uint32_t)f32_to_f16(v[t][2 * i + 1]) << 16);
+                                       : pack_f16x2(v[t][2 * i], v[t][2 * i + 1]);
               *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(p.out) + o) = b;
             }
           }
@@ -237,15 +232,12 @@ __global__ __launch_bounds__(256, 3) void mx_small_kernel(MxK p) {
         for (int w = 1; w < 4; ++w) m = m > amx[w][col] ? m : amx[w][col];
         const bool bad = mx_not_finite(m);
         const int pe = mx_exponent<F>(m);
-        const float inv = mx_inverse(pe);
-        float u[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) u[i] = bad ? 0.0f : v[0][i] * inv;
+        const uint32_t d = bad ? 0u : mx_pack4<F>(v[0][0], v[0][1], v[0][2], v[0][3], mx_scale(pe));
         const size_t o = (size_t)row * I + 32 * t0 + ch;
         if constexpr (F == kE4M3)
-          *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.out) + o) = mx_pack4_e4m3(u[0], u[1], u[2], u[3]);
+          *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(p.out) + o) = d;
         else
-          *reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(p.out) + o / 2) = (uint16_t)mx_pack4_e2m1(u[0], u[1], u[2], u[3]);
+          *reinterpret_cast<uint16_t*>(static_cast<uint8_t*>(p.out) + o / 2) = (uint16_t)d;
         if (wv == 0 && half == 0) p.out_scales[(size_t)row * (I >> 5) + t0] = bad ? (uint8_t)255 : (uint8_t)(pe + 127);
       }
       __syncthreads();  // amx is written again for the next rows
@@ -294,38 +286,40 @@ __device__ __forceinline__ int row_tiles(const MxK& p, int e, int& s0, int& s1) 
   if (e < p.E) segment(p, e, s0, s1);
   return (s1 - s0 + TM - 1) / TM;
 }
+// This workgroup's tile (false: none).  64 segments at a time, one per lane; with
+// more the first pass counts the tiles and a second one finds it.
 template <int TM>
-__device__ __forceinline__ int count_tiles(const MxK& p, int n_nb) {
-  int total = 0, s0, s1;
-  for (int e0 = 0; e0 < p.E; e0 += 64)
-    total += __builtin_amdgcn_readlane(wave_scan(row_tiles<TM>(p, e0 + (threadIdx.x & 63), s0, s1)), 63);
-  return total * n_nb;
-}
-// Tile `idx`, which exists.
-template <int TM>
-__device__ __forceinline__ Tile find_tile(const MxK& p, int idx, int n_nb) {
-  Tile t{0, 0, 0, 0};
-  for (int e0 = 0; e0 < p.E; e0 += 64) {
-    int s0, s1;
-    const int n = row_tiles<TM>(p, e0 + (threadIdx.x & 63), s0, s1);
-    const int end = wave_scan(n);
-    const int sum = __builtin_amdgcn_readlane(end, 63);
-    if (idx >= sum * n_nb) {
-      idx -= sum * n_nb;
-      continue;
-    }
-    const int src = __builtin_ctzll(__ballot(idx < end * n_nb));
-    const int tiles = __builtin_amdgcn_readlane(n, src);
-    const int j = idx - (__builtin_amdgcn_readlane(end, src) - tiles) * n_nb;
-    const int g = j / (8 * n_nb), gm = min(8, tiles - 8 * g);
-    const int in = j - g * 8 * n_nb;
-    t.e = e0 + src;
-    t.nb = in / gm;
-    t.r0 = __builtin_amdgcn_readlane(s0, src) + (8 * g + in % gm) * TM;
-    t.s1 = __builtin_amdgcn_readlane(s1, src);
-    break;
+__device__ __forceinline__ bool own_tile(const MxK& p, int n_nb, Tile& t) {
+  const int lane = threadIdx.x & 63;
+  int s0, s1;
+  int n = row_tiles<TM>(p, lane, s0, s1);
+  int end = wave_scan(n), total = __builtin_amdgcn_readlane(end, 63);
+  for (int e0 = 64; e0 < p.E; e0 += 64) {
+    int a, b;
+    total += __builtin_amdgcn_readlane(wave_scan(row_tiles<TM>(p, e0 + lane, a, b)), 63);
   }
-  return t;
+  const int wgs = total * n_nb, per = (wgs + 7) >> 3;
+  int idx = ((int)blockIdx.x & 7) * per + ((int)blockIdx.x >> 3);
+  if (((int)blockIdx.x >> 3) >= per || idx >= wgs) return false;
+  int e0 = 0;
+  while (true) {
+    const int sum = __builtin_amdgcn_readlane(end, 63) * n_nb;
+    if (idx < sum || e0 + 64 >= p.E) break;
+    idx -= sum;
+    e0 += 64;
+    n = row_tiles<TM>(p, e0 + lane, s0, s1);
+    end = wave_scan(n);
+  }
+  const int src = __builtin_ctzll(__ballot(idx < end * n_nb));
+  const int tiles = __builtin_amdgcn_readlane(n, src);
+  const int j = idx - (__builtin_amdgcn_readlane(end, src) - tiles) * n_nb;
+  const int g = j / (8 * n_nb), gm = min(8, tiles - 8 * g);
+  const int in = j - g * 8 * n_nb;
+  t.e = e0 + src;
+  t.nb = in / gm;
+  t.r0 = __builtin_amdgcn_readlane(s0, src) + (8 * g + in % gm) * TM;
+  t.s1 = __builtin_amdgcn_readlane(s1, src);
+  return true;
 }
 
 // Exchanges halves of the wavefront: afterwards a holds (a's low half, b's low
@@ -357,10 +351,8 @@ __device__ __forceinline__ void mx_tile_body(const MxK& p, int n_nb, u32x4* x0, 
   constexpr int RW = TM / 4;               // rows whose scales a wavefront fetches
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int half = lane >> 5, col = lane & 31;
-  const int wgs = count_tiles<TM>(p, n_nb), per = (wgs + 7) >> 3;
-  const int idx = ((int)blockIdx.x & 7) * per + ((int)blockIdx.x >> 3);
-  if (((int)blockIdx.x >> 3) >= per || idx >= wgs) return;
-  const Tile c = find_tile<TM>(p, idx, n_nb);
+  Tile c;
+  if (!own_tile<TM>(p, n_nb, c)) return;
   const int NT = p.N >> 5, KB = p.K >> 7, KC = (p.K + 255) >> 8;
 
   // this wavefront's tiles; past the last channel: tile 0, loaded and never stored
@@ -376,6 +368,30 @@ __device__ __forceinline__ void mx_tile_body(const MxK& p, int n_nb, u32x4* x0, 
   const rsrc_t asr = make_rsrc(p.as, p.as_bytes);
   const rsrc_t wr = make_rsrc(p.wc + (size_t)c.e * NT * KC * 4096, (uint32_t)((size_t)NT * KC * 4096));
   const rsrc_t wsr = make_rsrc(p.wsc + (size_t)c.e * NT * KC * 256, (uint32_t)((size_t)NT * KC * 256));
+  const uint32_t wo[2] = {(uint32_t)tile[0] * (uint32_t)(KC * 4096), (uint32_t)tile[1] * (uint32_t)(KC * 4096)};
+  struct Weights {  // of a K block: [tile][step]
+    u32x4 w[2][2];
+  };
+  auto load_weights = [&](int kb) {  // 4 loads
+    Weights b;
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+#pragma unroll
+      for (int s = 0; s < 2; ++s) b.w[u][s] = buf_x4(wr, 16 * lane, wo[u] + kb * 2048 + 1024 * s);
+    return b;
+  };
+  struct Scales {  // of the weights in two K blocks
+    uint32_t w[2];
+  };
+  auto load_scales = [&](int kc) {
+    Scales s;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) s.w[u] = buf_x1(wsr, 4 * lane, wo[u] / 16 + kc * 256);
+    return s;
+  };
+  // the weights' way does not wait for the rows' addresses
+  Scales sc = load_scales(0);
+  Weights wa = load_weights(0);
   // grouped rows of this lane's DMAs, then the row whose scales it fetches; past
   // the segment's end the last row again (its column is never stored)
   int src[XI + 1];
@@ -397,7 +413,6 @@ __device__ __forceinline__ void mx_tile_body(const MxK& p, int n_nb, u32x4* x0, 
     xo[i] = (uint32_t)src[i] * (uint32_t)(KB * XC * 16) + 16 * ((at % XC) ^ swizzle<AF>(at / XC));
   }
   const uint32_t xso = (uint32_t)src[XI] * (uint32_t)(KB * 4);
-  const uint32_t wo[2] = {(uint32_t)tile[0] * (uint32_t)(KC * 4096), (uint32_t)tile[1] * (uint32_t)(KC * 4096)};
 
   // XI + 1 loads of K block kb's rows and scales into a stage
   auto issue = [&](u32x4* xs, uint32_t* ss, int kb) {
@@ -405,26 +420,6 @@ __device__ __forceinline__ void mx_tile_body(const MxK& p, int n_nb, u32x4* x0, 
     for (int i = 0; i < XI; ++i)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(ar, xs + (wv * XI + i) * 64, 16, xo[i], kb * (XC * 16), 0, 0);
     __builtin_amdgcn_raw_ptr_buffer_load_lds(asr, ss + wv * 64, 4, xso, kb * 4, 0, 0);
-  };
-  struct Weights {  // of a K block: [tile][step]
-    u32x4 w[2][2];
-  };
-  auto load_weights = [&](int kb) {  // 4 loads
-    Weights b;
-#pragma unroll
-    for (int u = 0; u < 2; ++u)
-#pragma unroll
-      for (int s = 0; s < 2; ++s) b.w[u][s] = buf_x4(wr, 16 * lane, wo[u] + kb * 2048 + 1024 * s);
-    return b;
-  };
-  struct Scales {  // of the weights in two K blocks
-    uint32_t w[2];
-  };
-  auto load_scales = [&](int kc) {
-    Scales s;
-#pragma unroll
-    for (int u = 0; u < 2; ++u) s.w[u] = buf_x1(wsr, 4 * lane, wo[u] / 16 + kc * 256);
-    return s;
   };
   struct Frag {  // 32 rows' values in a step (64 inputs)
     u32x4 x[AF == kE4M3 ? 2 : 1];
@@ -493,8 +488,6 @@ __device__ __forceinline__ void mx_tile_body(const MxK& p, int n_nb, u32x4* x0, 
   // exit in the middle copies the accumulators): the weights are padded with
   // zeros to a whole pair of blocks, the second block of an odd last pair
   // multiplies them with the first's rows.
-  Scales sc = load_scales(0);
-  Weights wa = load_weights(0);
   issue(x0, s0, 0);
   ready(zero);
   issue(x1, s1, min(1, KB - 1));
@@ -537,13 +530,8 @@ __device__ __forceinline__ void mx_tile_body(const MxK& p, int n_nb, u32x4* x0, 
       {
         const int ht = tile[0];
         float h[16];
-        uint32_t m = 0;
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          h[r] = silu_mul(acc[t][0][r], acc[t][1][r]);
-          const uint32_t b = __builtin_bit_cast(uint32_t, h[r]) & 0x7FFFFFFFu;
-          m = m > b ? m : b;
-        }
+        for (int r = 0; r < 16; ++r) h[r] = silu_mul(acc[t][0][r], acc[t][1][r]);
         if constexpr (EPI == kEpiSwiglu) {
           uint32_t d[8];
 #pragma unroll
@@ -551,20 +539,16 @@ __device__ __forceinline__ void mx_tile_body(const MxK& p, int n_nb, u32x4* x0, 
           store_tile16(d, static_cast<uint16_t*>(p.out) + (size_t)row * I + 32 * ht, half, on && valid[0]);
         } else {
           constexpr int F = EPI == kEpiSwigluE4M3 ? kE4M3 : kE2M1;
-          uint32_t mo = m;
+          uint32_t m = absmax_bits(h), mo = m;
           swap_halves(m, mo);
           m = m > mo ? m : mo;
           const bool bad = mx_not_finite(m);
           const int pe = mx_exponent<F>(m);
-          const float inv = mx_inverse(pe);
+          const float scale = mx_scale(pe);
           uint32_t d[4];
 #pragma unroll
-          for (int g = 0; g < 4; ++g) {
-            float v[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) v[i] = bad ? 0.0f : h[4 * g + i] * inv;
-            d[g] = F == kE4M3 ? mx_pack4_e4m3(v[0], v[1], v[2], v[3]) : mx_pack4_e2m1(v[0], v[1], v[2], v[3]);
-          }
+          for (int g = 0; g < 4; ++g)
+            d[g] = bad ? 0u : mx_pack4<F>(h[4 * g], h[4 * g + 1], h[4 * g + 2], h[4 * g + 3], scale);
           // lane half h gets channels 16h .. 16h + 15 of its token
           swap_halves(d[0], d[2]);
           swap_halves(d[1], d[3]);
@@ -599,7 +583,7 @@ __device__ __forceinline__ void mx_tile_body(const MxK& p, int n_nb, u32x4* x0, 
           for (int i = 0; i < 8; ++i)
             d[i] = EPI == kEpiBf16
                        ? pack_bf16x2(acc[t][u][2 * i], acc[t][u][2 * i + 1])
-                       : (uint32_t)f32_to_f16(acc[t][u][2 * i]) | ((uint32_t)f32_to_f16(acc[t][u][2 * i + 1]) << 16);
+                       : pack_f16x2(acc[t][u][2 * i], acc[t][u][2 * i + 1]);
           store_tile16(d, static_cast<uint16_t*>(p.out) + o, half, on && valid[u]);
         }
       }
