@@ -428,9 +428,9 @@ moe_status moe_dequantize_mx(const uint8_t* codes, const uint8_t* scales, int64_
  * (n itself is quantised, not its rounding y).  x, residual, sum, y [rows][H]
  * and weight [H] of `dtype` (MOE_DTYPE_*).  sum (needs residual), y and the MX
  * output (fmt 0: codes and scales NULL) are each optional; at least one output
- * is needed.  sum may be x or residual, and y may be x, residual or sum's
- * place only if that buffer is not written otherwise.  Squares are summed in
- * fp32 per lane and float64 across lanes; the norm's factor is float64.
+ * is needed.  sum and y may each be x's or residual's own buffer, not the same
+ * one; no other buffers may overlap.  The sum of squares
+ * and the norm's factor are float64.
  * rows >= 0, H % 32 == 0, 32 <= H <= 16384, rows * H < 2^40, eps >= 0 and
  * finite; 16-byte aligned buffers, except scales.
  */

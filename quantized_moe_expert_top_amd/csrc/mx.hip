@@ -98,11 +98,14 @@ __global__ __launch_bounds__(kThreads) void dequantize_mx_kernel(const uint8_t* 
 // ------------------------------------------------------------------- RMS norm
 // TPR threads hold one row in registers (NV groups of 8 values each), so x and
 // residual are read once: v = x + residual rounded to the row's type, the sum
-// of squares (fp32 in the lane, float64 across lanes), then
-// n = (v * weight) * factor.  v * weight of 16-bit values is exact in fp32
+// of squares in float64 (hidden behind the loads; it cannot overflow either),
+// then n = (v * weight) * factor.  v * weight of 16-bit values is exact in fp32
 // (8 + 8 or 11 + 11 significant bits) and the factor is a float64 split into two
-// floats, so n is within a hair of half an fp32 ulp: what is quantised next
-// falls on the same side of a rounding border as the exact value.
+// floats.  n is rounded to nearest for an fp32 y; what is rounded again, to 16
+// bits or to an MX element, is rounded to odd first (an inexact n gets an odd
+// last bit), so that the second rounding is that of the exact value and not of
+// an fp32 number on the border.  8192 rows of
+// 4096 bf16 with residual, sum, y and 8-bit blocks: 61 us, 5.0 TB/s.
 template <int DT>
 __device__ __forceinline__ float round_to(float f) {
   if constexpr (DT == 0) return bf16_to_f32(f32_to_bf16(f));
@@ -112,6 +115,7 @@ __device__ __forceinline__ float round_to(float f) {
 
 template <int DT, int FMT, int TPR, int NV>
 __global__ __launch_bounds__(kThreads) void rmsnorm_mx_kernel(NormArgs a) {
+#pragma clang fp contract(off)  // hi + lo below must not become m * fhi + lo
   constexpr int kRows = kThreads / TPR, kWaves = TPR / 64;
   __shared__ double part[kThreads / 64];
   const int sub = threadIdx.x / TPR, t = threadIdx.x % TPR;
@@ -120,7 +124,7 @@ __global__ __launch_bounds__(kThreads) void rmsnorm_mx_kernel(NormArgs a) {
   const int n8 = a.H >> 3;
   const size_t r8 = row * n8;
   float v[NV][8];
-  float ss = 0.0f;
+  double sum = 0.0;
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     const int c = t + j * TPR;
@@ -137,9 +141,8 @@ __global__ __launch_bounds__(kThreads) void rmsnorm_mx_kernel(NormArgs a) {
       }
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) ss = __builtin_fmaf(v[j][i], v[j][i], ss);
+    for (int i = 0; i < 8; ++i) sum = __builtin_fma((double)v[j][i], (double)v[j][i], sum);
   }
-  double sum = (double)ss;
 #pragma unroll
   for (int off = 32; off > 0; off >>= 1) sum += __shfl_xor(sum, off, 64);
   if constexpr (kWaves > 1) {
@@ -156,15 +159,23 @@ __global__ __launch_bounds__(kThreads) void rmsnorm_mx_kernel(NormArgs a) {
     const int c = t + j * TPR;
     if (!(live && c < n8)) continue;
     if (a.sum) store8<DT>(a.sum, r8 + c, v[j]);
-    float w[8];
+    float w[8], nearest[8];
     unpack8<DT>(load8<DT>(a.weight, c), w);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float m = v[j][i] * w[i];
       const float hi = m * fhi;
-      v[j][i] = hi + __builtin_fmaf(m, flo, __builtin_fmaf(m, fhi, -hi));
+      float lo = __builtin_fmaf(m, flo, __builtin_fmaf(m, fhi, -hi));
+      if constexpr (DT == 1) lo = __builtin_fmaf(__builtin_fmaf(v[j][i], w[i], -m), fhi, lo);
+      const float n = hi + lo;
+      const float rest = lo - (n - hi);
+      nearest[i] = n;
+      const int b = __builtin_bit_cast(int, n);
+      // the neighbour on the side of the rest (NaN: not greater, stays)
+      const int odd = b + ((rest > 0.0f) == (b > 0) ? 1 : -1);
+      v[j][i] = (__builtin_fabsf(rest) > 0.0f && !(b & 1)) ? __builtin_bit_cast(float, odd) : n;
     }
-    if (a.y) store8<DT>(a.y, r8 + c, v[j]);
+    if (a.y) store8<DT>(a.y, r8 + c, DT == 1 ? nearest : v[j]);
     if constexpr (FMT != 0) store_mx8<FMT>(v[j], quad_umax(absmax_bits(v[j])), r8 + c, a.codes, a.scales);
   }
 }
