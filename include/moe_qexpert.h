@@ -500,7 +500,8 @@ moe_status moe_grouped_mxgemm(const moe_mxdesc* w, const uint8_t* a_codes, const
  *   x       [T][H] of x_dtype, quantised to x_codes / x_scales in x_fmt; or NULL:
  *           x_codes / x_scales already hold the rows (moe_rmsnorm_mx)
  *   routing as for moe_route_scored; grouping buffers as for moe_permute (S = 1),
- *           workspace at least moe_permute_workspace_size(T, k, E, 1) bytes
+ *           workspace at least moe_mx_layer_workspace_size(T, k, E) bytes; its
+ *           contents need not start at zero; calls that share one must be ordered
  *   h       MX rows [T*k][I] in h_fmt; y [T*k][H] of y_dtype (MOE_DTYPE_*)
  *   out     bf16 [T][H]
  * Alignment as for those calls.  Every argument is checked before anything is
@@ -533,6 +534,7 @@ typedef struct moe_mxlayer {
   void* y;
   uint16_t* out;
 } moe_mxlayer;
+size_t moe_mx_layer_workspace_size(int32_t T, int32_t k, int32_t E);
 moe_status moe_mx_layer(const moe_mxlayer* layer, void* stream);
 
 #ifdef __cplusplus

@@ -38,7 +38,7 @@ EXPORTED = [
     "moe_grouped_qgemm_workspace_size", "moe_grouped_qgemm", "moe_unpermute_combine",
     "moe_grouped_qgemm_noalloc", "moe_grouped_qgemm_noalloc_scratch_bytes", "moe_copy_rows_async",
     "moe_route_scored", "moe_quantize_mx", "moe_dequantize_mx", "moe_rmsnorm_mx", "moe_mx_field_bytes",
-    "moe_mx_repack", "moe_grouped_mxgemm", "moe_mx_layer",
+    "moe_mx_repack", "moe_grouped_mxgemm", "moe_mx_layer", "moe_mx_layer_workspace_size",
 ]
 
 
@@ -108,6 +108,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "moe_mx_field_bytes": (sz, [mxd, i32]),
         "moe_mx_repack": (i32, [mxd, mxd, vp]),
         "moe_grouped_mxgemm": (i32, [mxd, vp, vp, i32, i32, vp, i32, vp, i32, i32, i32, vp, vp, vp]),
+        "moe_mx_layer_workspace_size": (sz, [i32, i32, i32]),
         "moe_mx_layer": (i32, [ctypes.POINTER(MxLayer), vp]),
     }
     for name, (res, args) in sig.items():

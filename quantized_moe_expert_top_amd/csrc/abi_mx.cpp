@@ -210,6 +210,11 @@ moe_status moe_grouped_mxgemm(const moe_mxdesc* w, const uint8_t* a_codes, const
   return hip_status(moe::launch_mxgemm(a, stream), "grouped_mxgemm launch");
 }
 
+size_t moe_mx_layer_workspace_size(int32_t T, int32_t k, int32_t E) {
+  if (T < 0 || k < 1 || E < 1 || E > 1024 || (int64_t)T * k >= ((int64_t)1 << 31)) return 0;
+  return moe::mx_layer_workspace_bytes(T, k, E);
+}
+
 moe_status moe_mx_layer(const moe_mxlayer* l, void* stream) {
   if (!l) return fail(MOE_ERR_NULL_ARG, "layer is NULL");
   if (l->abi_version != MOE_ABI_VERSION)
@@ -240,7 +245,7 @@ moe_status moe_mx_layer(const moe_mxlayer* l, void* stream) {
     return fail(MOE_ERR_NULL_ARG, "the grouping's buffers are required");
   if (!l->x_codes || !l->x_scales || !l->h_codes || !l->h_scales || !l->y || !l->out)
     return fail(MOE_ERR_NULL_ARG, "x, h, y and out buffers are required");
-  const size_t need = moe::permute_workspace_bytes(T * k, E, 1);
+  const size_t need = moe::mx_layer_workspace_bytes(T, k, E);
   if (l->workspace_bytes < need)
     return fail(MOE_ERR_WORKSPACE_TOO_SMALL, "workspace %zu bytes, %zu needed", l->workspace_bytes, need);
   if (!aligned(l->x, 16) || !aligned(l->x_codes, 16) || !aligned(l->h_codes, 16) || !aligned(l->y, 16) ||
@@ -256,7 +261,8 @@ moe_status moe_mx_layer(const moe_mxlayer* l, void* stream) {
                               l->renormalize != 0, l->scale, l->topk_ids, l->topk_w};
   const moe::FrontRows rows{l->x, l->x_dtype, l->x_fmt, l->x ? (size_t)T * H / 8 : 0, l->x_codes, l->x_scales};
   const moe::FrontGroups groups{l->expert_counts, l->seg_offsets, l->sorted_pair, l->pair_pos,
-                                static_cast<uint32_t*>(l->workspace)};
+                                static_cast<uint32_t*>(l->workspace),
+                                reinterpret_cast<int*>(static_cast<uint8_t*>(l->workspace) + 256)};
   bool grouped = false;
   int e = moe::launch_mx_front(route, rows, groups, &grouped, stream);
   if (e == 0 && !grouped) {

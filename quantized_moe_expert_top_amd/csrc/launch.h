@@ -135,7 +135,12 @@ struct FrontGroups {
   int32_t* sorted_pair;
   int32_t* pair_pos;
   uint32_t* flag;
+  int* chunk_hist;  // mx_layer_workspace_bytes behind the flag's 256 bytes
 };
+// Tokens that a wavefront of the layer's start routes one after another where it
+// also counts the pairs (0: it does not), and the workspace for those counts.
+int front_tokens_per_wave(int T, int E);
+size_t mx_layer_workspace_bytes(int T, int k, int E);
 int launch_mx_front(const ScoredArgs& a, const FrontRows& q, const FrontGroups& g, bool* grouped, void* stream);
 
 // ----------------------------------------------------------------- MX rows

@@ -128,6 +128,27 @@ size_t qgemm_workspace_bytes(const QWeights& w, int A_rows, int M_total, int ker
   return need;
 }
 
+// The start of an MX layer: chunks of 8 wavefronts' tokens, whose counts (E + 1
+// per chunk) every workgroup of the second launch reads in full: at most 256
+// chunks and 32768 counters.  A wavefront routes at most 4 tokens one after
+// another (2.5 us each); beyond that routing gets a launch to itself.
+namespace {
+constexpr int kChunks = 256, kChunkInts = 32768, kChunkTokens = 8;
+}  // namespace
+int front_tokens_per_wave(int T, int E) {
+  const int most = kChunkInts / (E + 1) < kChunks ? kChunkInts / (E + 1) : kChunks;
+  const int per = (T + kChunkTokens * most - 1) / (kChunkTokens * most);
+  return per <= 4 ? per : 0;
+}
+size_t mx_layer_workspace_bytes(int T, int k, int E) {
+  const size_t sort = permute_workspace_bytes(T * k, E, 1);
+  const int per = front_tokens_per_wave(T, E);
+  if (per == 0) return sort;
+  const size_t chunks = (size_t)(T + kChunkTokens * per - 1) / (kChunkTokens * per);
+  const size_t counts = 256 + align256(chunks * (E + 1) * 4);
+  return counts > sort ? counts : sort;
+}
+
 // Grouped MX product: 0 = 32-row tiles straight from memory, 64 / 128 =
 // LDS-staged tiles of that many rows.  AUTO takes the least of three estimates
 //     a + K * max(b, c * (workgroups / 256 + d))      (microseconds)

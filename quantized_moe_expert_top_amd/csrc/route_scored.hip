@@ -107,7 +107,7 @@ __device__ __forceinline__ uint64_t exact_groups(const ScoredArgs& a, const doub
 
 // float64 over all experts: the definition, step by step.
 template <int NS>
-__device__ __forceinline__ void route_exact(const ScoredArgs& a, int t, float top, double* buf) {
+__device__ __forceinline__ void route_exact(const ScoredArgs& a, int t, float top, double* buf, int* hist) {
   const int lane = threadIdx.x & 63;
   double score[NS], c[NS];
   exact_scores<NS>(a, t, top, score, c);
@@ -148,6 +148,7 @@ __device__ __forceinline__ void route_exact(const ScoredArgs& a, int t, float to
       }
     if (lane == 0) {
       a.ids[o + j] = none ? -1 : bi;
+      if (hist) atomicAdd(&hist[none ? a.E : bi], 1);
       if (none) buf[j] = 0.0;
     }
   }
@@ -205,9 +206,10 @@ constexpr int kSpare = 6;  // candidates beyond k that cost less than another st
 // SOFT_ALL: the softmax denominator is needed (a bias, weights that are not
 // renormalised, sums of two scores per group): float64 exponentials of all
 // experts give it and the keys.
-// Token t by this wavefront; buf: 64 * NS doubles of LDS of its own.
+// Token t by this wavefront; buf: 64 * NS doubles of LDS of its own; hist: E + 1
+// counters in LDS that its pairs' experts (E: none) are added to, or nullptr.
 template <int NS, bool SOFT_ALL>
-__device__ __forceinline__ void route_token(const ScoredArgs& a, int t, double* buf) {
+__device__ __forceinline__ void route_token(const ScoredArgs& a, int t, double* buf, int* hist = nullptr) {
   const int lane = threadIdx.x & 63;
   const float* row = a.logits + (size_t)t * a.E;
 
@@ -366,7 +368,7 @@ __device__ __forceinline__ void route_token(const ScoredArgs& a, int t, double* 
   }
   if (exact) {
     wave_fence();
-    route_exact<NS>(a, t, top, buf);
+    route_exact<NS>(a, t, top, buf, hist);
     return;
   }
 
@@ -398,7 +400,9 @@ __device__ __forceinline__ void route_token(const ScoredArgs& a, int t, double* 
   if (chosen) {
     a.ids[o + rank] = cand;
     a.w[o + rank] = sum > 0.0 ? (float)(score / sum * (double)a.scale) : 0.0f;
+    if (hist) atomicAdd(&hist[cand], 1);
   }
+  if (hist && n < a.k && lane == 0) atomicAdd(&hist[a.E], a.k - n);
   for (int j = n + lane; j < a.k; j += 64) {  // fewer eligible experts than slots
     a.ids[o + j] = -1;
     a.w[o + j] = 0.0f;
@@ -458,6 +462,72 @@ __global__ __launch_bounds__(kFrontThreads) void mx_front_small_kernel(ScoredArg
                                scratch, &bad);
 }
 
+// More tokens: chunks of 8 wavefronts' tokens, whose workgroups also count their
+// pairs per expert (order-free LDS counters), and a second launch in which every
+// workgroup sums the chunks' counts for itself (they fit L2: at most
+// kChunkInts) and places its chunk's pairs.  Two launches where counting,
+// scanning and scattering alone were three (23 us for 65536 pairs).
+constexpr int kChunkWaves = 8, kChunkThreads = 64 * kChunkWaves;
+template <int NS, bool SOFT_ALL>
+__global__ __launch_bounds__(kChunkThreads) void mx_front_chunk_kernel(ScoredArgs a, FrontRows q, int n_chunks, int per_wave,
+                                                                       int* __restrict__ chunk_hist) {
+  __shared__ double lds[kChunkWaves][64 * NS];
+  __shared__ int hist[64 * NS + 1];
+  if ((int)blockIdx.x >= n_chunks) {
+    quantize_any<kChunkThreads>(q, blockIdx.x - n_chunks);
+    return;
+  }
+  for (int i = threadIdx.x; i <= a.E; i += kChunkThreads) hist[i] = 0;
+  __syncthreads();
+  const int wv = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int t0 = (blockIdx.x * kChunkWaves + wv) * per_wave;
+  for (int t = t0; t < min(t0 + per_wave, a.T); ++t) {
+    wave_fence();  // the last token's reads of the wavefront's buffer are done
+    route_token<NS, SOFT_ALL>(a, t, lds[wv], hist);
+  }
+  __syncthreads();
+  for (int i = threadIdx.x; i <= a.E; i += kChunkThreads) chunk_hist[(size_t)blockIdx.x * (a.E + 1) + i] = hist[i];
+}
+
+constexpr int kPlaceThreads = 256;
+__global__ __launch_bounds__(kPlaceThreads) void mx_place_kernel(Keyer kr, int P, int chunk_pairs, int n_chunks,
+                                                                 const int* __restrict__ chunk_hist, FrontGroups g) {
+  __shared__ int base[1025], before[1025], tags[(kPlaceThreads / 64) * 1025], scratch[kPlaceThreads / 64 + 1];
+  const int tid = threadIdx.x, nk1 = kr.NK + 1, b = blockIdx.x;
+  for (int i = tid; i < nk1; i += kPlaceThreads) base[i] = before[i] = 0;
+  for (int i = tid; i < (kPlaceThreads / 64) * nk1; i += kPlaceThreads) tags[i] = -1;
+  __syncthreads();
+  // a lane per key, the wavefronts share the chunks
+  for (int k0 = 0; k0 < nk1; k0 += 64) {
+    const int key = k0 + (tid & 63);
+    if (key < nk1) {
+      int all = 0, prior = 0;
+#pragma unroll 8
+      for (int c = tid >> 6; c < n_chunks; c += kPlaceThreads / 64) {
+        const int n = chunk_hist[(size_t)c * nk1 + key];
+        all += n;
+        prior += c < b ? n : 0;
+      }
+      atomicAdd(&base[key], all);
+      atomicAdd(&before[key], prior);
+    }
+  }
+  __syncthreads();
+  if (b == 0) {
+    for (int e = tid; e < kr.E; e += kPlaceThreads) g.counts[e] = base[e];
+    if (tid == 0) g.flag[0] = base[kr.E] != 0;
+    __syncthreads();
+  }
+  block_exclusive_scan<kPlaceThreads>(base, nk1, scratch);
+  if (b == 0)
+    for (int i = tid; i < nk1; i += kPlaceThreads) g.seg_offsets[i] = base[i];
+  __syncthreads();
+  for (int i = tid; i < nk1; i += kPlaceThreads) base[i] += before[i];
+  __syncthreads();
+  const int p0 = b * chunk_pairs;
+  scatter_chunk<kPlaceThreads>(kr, p0, min(P, p0 + chunk_pairs), base, tags, g.sorted_pair, g.pair_pos);
+}
+
 inline bool soft_all(const ScoredArgs& a) {
   return a.score == 0 && (a.bias || !a.renorm || (a.n_group > 1 && a.group_top == 2));
 }
@@ -479,6 +549,12 @@ void launch_front_ns(const ScoredArgs& a, const FrontRows& q, hipStream_t s) {
   else hipLaunchKernelGGL((mx_front_kernel<NS, false>), grid, block, 0, s, a, q, n_route);
 }
 template <int NS>
+void launch_front_chunk_ns(const ScoredArgs& a, const FrontRows& q, int n_chunks, int per_wave, int* hist, hipStream_t s) {
+  const dim3 grid(n_chunks + quant_blocks(q, kChunkThreads)), block(kChunkThreads);
+  if (soft_all(a)) hipLaunchKernelGGL((mx_front_chunk_kernel<NS, true>), grid, block, 0, s, a, q, n_chunks, per_wave, hist);
+  else hipLaunchKernelGGL((mx_front_chunk_kernel<NS, false>), grid, block, 0, s, a, q, n_chunks, per_wave, hist);
+}
+template <int NS>
 void launch_front_small_ns(const ScoredArgs& a, const FrontRows& q, const FrontGroups& g, hipStream_t s) {
   const dim3 grid(1 + quant_blocks(q, kFrontThreads)), block(kFrontThreads);
   if (soft_all(a)) hipLaunchKernelGGL((mx_front_small_kernel<NS, true>), grid, block, 0, s, a, q, g);
@@ -488,11 +564,24 @@ void launch_front_small_ns(const ScoredArgs& a, const FrontRows& q, const FrontG
 
 int launch_mx_front(const ScoredArgs& a, const FrontRows& q, const FrontGroups& g, bool* grouped, void* stream) {
   const hipStream_t s = static_cast<hipStream_t>(stream);
-  *grouped = a.T <= kFrontTokens && a.E <= 256;
-  if (*grouped) {
+  const int per_wave = front_tokens_per_wave(a.T, a.E);
+  *grouped = (a.T <= kFrontTokens && a.E <= 256) || per_wave > 0;
+  if (a.T <= kFrontTokens && a.E <= 256) {
     if (a.E <= 64) launch_front_small_ns<1>(a, q, g, s);
     else if (a.E <= 128) launch_front_small_ns<2>(a, q, g, s);
     else launch_front_small_ns<4>(a, q, g, s);
+  } else if (per_wave > 0) {
+    const int tokens = kChunkWaves * per_wave, n_chunks = (a.T + tokens - 1) / tokens;
+    if (a.E <= 64) launch_front_chunk_ns<1>(a, q, n_chunks, per_wave, g.chunk_hist, s);
+    else if (a.E <= 128) launch_front_chunk_ns<2>(a, q, n_chunks, per_wave, g.chunk_hist, s);
+    else if (a.E <= 256) launch_front_chunk_ns<4>(a, q, n_chunks, per_wave, g.chunk_hist, s);
+    else if (a.E <= 512) launch_front_chunk_ns<8>(a, q, n_chunks, per_wave, g.chunk_hist, s);
+    else launch_front_chunk_ns<16>(a, q, n_chunks, per_wave, g.chunk_hist, s);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return (int)e;
+    const Keyer kr{a.ids, nullptr, a.E, 1, a.E};
+    hipLaunchKernelGGL(mx_place_kernel, dim3(n_chunks), dim3(kPlaceThreads), 0, s, kr, a.T * a.k, tokens * a.k, n_chunks,
+                       g.chunk_hist, g);
   } else if (a.E <= 64) {
     launch_front_ns<1>(a, q, s);
   } else if (a.E <= 128) {

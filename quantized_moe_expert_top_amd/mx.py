@@ -367,7 +367,7 @@ def alloc_mx_layer(T: int, E: int, k: int, H: int, I: int, device, act: int = MO
     i32 = dict(dtype=torch.int32, device=device)
     perm = Permutation(counts=torch.empty(E, **i32), seg_offsets=torch.empty(E + 1, **i32),
                        sorted_pair=torch.empty(T * k, **i32), pair_pos=torch.empty(T * k, **i32),
-                       workspace=torch.zeros(max(lib().moe_permute_workspace_size(T, k, E, 1), 16), dtype=torch.uint8,
+                       workspace=torch.zeros(max(lib().moe_mx_layer_workspace_size(T, k, E), 16), dtype=torch.uint8,
                                              device=device))
     return MxLayerBuffers(sizes=(T, E, k, H, I), ids=torch.empty((T, k), **i32),
                           w=torch.empty((T, k), dtype=torch.float32, device=device), perm=perm,

@@ -156,7 +156,7 @@ def test_mx_layer_validation(lib):
         dn = mxdesc(E=kw.pop("E_down", 4), N=kw.pop("N_down", kw.pop("H", 128)), K=256)
         f = dict(abi_version=q.MOE_ABI_VERSION, T=3, k=2, x_dtype=q.MOE_DTYPE_BF16, x_fmt=1, h_fmt=1, y_dtype=q.MOE_DTYPE_F16,
                  kernel=0, score=0, n_group=1, topk_group=1, group_top=1, renormalize=1, scale=1.0, bias=None,
-                 workspace_bytes=256, gate_up=ctypes.pointer(gu), down=ctypes.pointer(dn))
+                 workspace_bytes=512, gate_up=ctypes.pointer(gu), down=ctypes.pointer(dn))
         for n in ("x", "logits", "topk_ids", "topk_w", "expert_counts", "seg_offsets", "sorted_pair", "pair_pos", "workspace",
                   "x_codes", "x_scales", "h_codes", "h_scales", "y", "out"):
             f[n] = 0x1000
@@ -173,7 +173,12 @@ def test_mx_layer_validation(lib):
     for n in ("logits", "topk_ids", "topk_w", "expert_counts", "seg_offsets", "sorted_pair", "pair_pos", "workspace",
               "x_codes", "x_scales", "h_codes", "h_scales", "y", "out"):
         assert call(**{n: None}) == NULL_ARG, n
-    assert call(workspace_bytes=255) == WS_SMALL
+    assert call(workspace_bytes=511) == WS_SMALL
+    size = lib.moe_mx_layer_workspace_size
+    assert size(3, 2, 4) == 256 + 256                       # the flag words; one chunk of 8 tokens, 5 counters
+    assert size(8192, 8, 64) == 256 + 256 * 65 * 4          # 256 chunks of 32 tokens
+    assert size(8193, 8, 64) == lib.moe_permute_workspace_size(8193, 8, 64, 1)
+    assert size(-1, 2, 4) == size(3, 0, 4) == size(3, 2, 1025) == size(1 << 28, 16, 64) == 0
     for n in ("x", "x_codes", "h_codes", "y", "out", "workspace"):
         assert call(**{n: 0x1008}) == MISALIGNED, n
     for n in ("x_scales", "h_scales", "logits", "bias", "seg_offsets", "sorted_pair", "pair_pos", "expert_counts"):
