@@ -385,7 +385,7 @@ moe_status moe_unpermute_combine(const void* y_perm, int32_t y_dtype, const int3
  * valid segment, and the combine adds nothing for them.  A sum of chosen
  * scores that is 0 gives weights 0.
  *   logits f32 [T][E]; bias f32 [E] or NULL; topk_ids i32 [T][k]; topk_w f32 [T][k]
- * 0 <= T, 1 <= k <= E <= 1024, T*k < 2^31, 1 <= n_group <= 64, E % n_group == 0,
+ * 0 <= T < 2^25, 1 <= k <= E <= 1024, T*k < 2^31, 1 <= n_group <= 64, E % n_group == 0,
  * 1 <= topk_group <= n_group, group_top 1 or 2, scale finite.  4-byte aligned
  * pointers.
  */
@@ -408,7 +408,8 @@ moe_status moe_route_scored(const float* logits, const float* bias, int32_t T, i
  * the smallest 2^p, p >= -126, with m <= M * 2^p (no element saturates); each
  * value / 2^p is rounded to the nearest element, ties to even.  A block with an
  * infinity or NaN gets scale byte 255 and zero codes: all of it reads as NaN.
- * K % 32 == 0, rows * K < 2^40; 16-byte aligned buffers, except scales.
+ * K % 32 == 0, rows * K < 2^34; 16-byte aligned buffers, except scales; no two
+ * may overlap.
  */
 #define MOE_MX_E4M3 1
 #define MOE_MX_E2M1 2
@@ -431,7 +432,7 @@ moe_status moe_dequantize_mx(const uint8_t* codes, const uint8_t* scales, int64_
  * is needed.  sum and y may each be x's or residual's own buffer, not the same
  * one; no other buffers may overlap.  The sum of squares
  * and the norm's factor are float64.
- * rows >= 0, H % 32 == 0, 32 <= H <= 16384, rows * H < 2^40, eps >= 0 and
+ * 0 <= rows < 2^24, H % 32 == 0, 32 <= H <= 16384, rows * H < 2^34, eps >= 0 and
  * finite; 16-byte aligned buffers, except scales.
  */
 moe_status moe_rmsnorm_mx(const void* x, const void* residual, const void* weight, int32_t dtype, int64_t rows,
@@ -462,7 +463,8 @@ typedef struct moe_mxdesc {
    or an invalid descriptor). */
 size_t moe_mx_field_bytes(const moe_mxdesc* w, int32_t field);
 /* Canonical -> tiled, once, offline; dst's buffers (moe_mx_field_bytes each) are
-   overwritten.  16-byte aligned codes, 4-byte aligned scales. */
+   overwritten.  E * N * K < 2^36, K rounded up to 256 (more: experts in parts).
+   16-byte aligned codes, 4-byte aligned scales. */
 moe_status moe_mx_repack(const moe_mxdesc* src, const moe_mxdesc* dst, void* stream);
 
 /* The grouped product of moe_grouped_qgemm with MX weights and MX activations:
@@ -482,7 +484,7 @@ moe_status moe_mx_repack(const moe_mxdesc* src, const moe_mxdesc* dst, void* str
  * clamped to 0 .. M_total and gathered rows to A_rows - 1.
  * kernel: MOE_KERNEL_AUTO, MOE_KERNEL_SMALL (32-row tiles straight from memory:
  * decode batches) or MOE_KERNEL_TILE64 / _TILE128 (LDS-staged tiles of that many
- * rows).  No workspace.  a_codes and w: 16-byte aligned, a_scales: 4-byte, out:
+ * rows).  No workspace; out overlaps no input.  a_codes and w: 16-byte aligned, a_scales: 4-byte, out:
  * 16-byte.  a_codes below 4 GiB.
  */
 #define MOE_EPI_SWIGLU_E4M3 4

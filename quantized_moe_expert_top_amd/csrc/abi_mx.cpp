@@ -20,7 +20,8 @@ bool known_fmt(int f) { return f == MOE_MX_E4M3 || f == MOE_MX_E2M1; }
 moe_status check_rows(int64_t rows, int32_t K) {
   if (rows < 0) return fail(MOE_ERR_BAD_SHAPE, "rows=%lld < 0", (long long)rows);
   if (K < 32 || K % 32 != 0) return fail(MOE_ERR_BAD_SHAPE, "row width %d must be a positive multiple of 32", K);
-  if (rows >= ((int64_t)1 << 40) / K) return fail(MOE_ERR_BAD_SHAPE, "rows * width too large");
+  // (a launch of one thread per 8 or 16 values has fewer than 2^32 threads)
+  if (rows >= ((int64_t)1 << 34) / K) return fail(MOE_ERR_BAD_SHAPE, "rows * width too large");
   return MOE_OK;
 }
 
@@ -48,7 +49,7 @@ moe_status check_route(const float* logits, const float* bias, int32_t T, int32_
   if (T < 0) return fail(MOE_ERR_BAD_SHAPE, "T=%d < 0", T);
   if (E < 1 || E > 1024) return fail(MOE_ERR_BAD_SHAPE, "E=%d outside 1..1024", E);
   if (k < 1 || k > E) return fail(MOE_ERR_BAD_SHAPE, "k=%d outside 1..E (E=%d)", k, E);
-  if ((int64_t)T * k >= ((int64_t)1 << 31)) return fail(MOE_ERR_BAD_SHAPE, "T*k too large");
+  if ((int64_t)T * k >= ((int64_t)1 << 31) || T >= 1 << 25) return fail(MOE_ERR_BAD_SHAPE, "T=%d, T*k too large", T);
   if (score != MOE_SCORE_SOFTMAX && score != MOE_SCORE_SIGMOID) return fail(MOE_ERR_BAD_FORMAT, "unknown score %d", score);
   if (n_group < 1 || n_group > 64 || E % n_group != 0)
     return fail(MOE_ERR_BAD_SHAPE, "n_group=%d must be in 1..64 and divide E=%d", n_group, E);
@@ -104,6 +105,7 @@ moe_status moe_quantize_mx(const void* x, int32_t x_dtype, int64_t rows, int32_t
   if (rows == 0) return ok();
   if (!x || !codes || !scales) return fail(MOE_ERR_NULL_ARG, "x, codes and scales are required");
   if (!aligned(x, 16) || !aligned(codes, 16)) return fail(MOE_ERR_MISALIGNED, "x and codes must be 16-byte aligned");
+  if (x == codes) return fail(MOE_ERR_BAD_SHAPE, "quantisation cannot run in place");
   st = check_device();
   if (st != MOE_OK) return st;
   return hip_status(moe::launch_quantize_mx(x, x_dtype, rows, K, fmt, codes, scales, stream), "quantize_mx launch");
@@ -118,6 +120,7 @@ moe_status moe_dequantize_mx(const uint8_t* codes, const uint8_t* scales, int64_
   if (rows == 0) return ok();
   if (!out || !codes || !scales) return fail(MOE_ERR_NULL_ARG, "codes, scales and out are required");
   if (!aligned(out, 16) || !aligned(codes, 16)) return fail(MOE_ERR_MISALIGNED, "out and codes must be 16-byte aligned");
+  if (out == codes) return fail(MOE_ERR_BAD_SHAPE, "dequantisation cannot run in place");
   st = check_device();
   if (st != MOE_OK) return st;
   return hip_status(moe::launch_dequantize_mx(codes, scales, rows, K, fmt, out_dtype, out, stream),
@@ -132,6 +135,7 @@ moe_status moe_rmsnorm_mx(const void* x, const void* residual, const void* weigh
   moe_status st = check_rows(rows, H);
   if (st != MOE_OK) return st;
   if (H > moe::kNormMaxH) return fail(MOE_ERR_UNSUPPORTED, "H=%d (at most %d)", H, moe::kNormMaxH);
+  if (rows >= 1 << 24) return fail(MOE_ERR_BAD_SHAPE, "rows=%lld (fewer than 2^24)", (long long)rows);
   if (!(eps >= 0.0f) || !isfinite(eps)) return fail(MOE_ERR_BAD_SHAPE, "eps must be finite and not negative");
   if (rows == 0) return ok();
   if (!x || !weight) return fail(MOE_ERR_NULL_ARG, "x and weight are required");
@@ -140,6 +144,8 @@ moe_status moe_rmsnorm_mx(const void* x, const void* residual, const void* weigh
     return fail(MOE_ERR_NULL_ARG, "codes and scales go with an MX format (fmt %d)", fmt);
   if (!sum && !y && fmt == 0) return fail(MOE_ERR_NULL_ARG, "no output requested");
   if (y && y == sum) return fail(MOE_ERR_BAD_SHAPE, "sum and y share a buffer");
+  if (codes && (codes == x || codes == residual || codes == sum || codes == y))
+    return fail(MOE_ERR_BAD_SHAPE, "codes share a buffer with rows of values");
   if (!aligned(x, 16) || !aligned(residual, 16) || !aligned(weight, 16) || !aligned(sum, 16) || !aligned(y, 16) ||
       !aligned(codes, 16))
     return fail(MOE_ERR_MISALIGNED, "norm buffers must be 16-byte aligned");
@@ -165,6 +171,8 @@ moe_status moe_mx_repack(const moe_mxdesc* src, const moe_mxdesc* dst, void* str
   if (st != MOE_OK) return st;
   if (src->E != dst->E || src->N != dst->N || src->K != dst->K)
     return fail(MOE_ERR_BAD_SHAPE, "source and destination descriptors disagree");
+  if ((int64_t)src->E * src->N * ((src->K + 255) / 256 * 256) >= (int64_t)1 << 36)
+    return fail(MOE_ERR_BAD_SHAPE, "2^36 weights or more: repack the experts in parts");
   if (src->codes == dst->codes || src->scales == dst->scales) return fail(MOE_ERR_BAD_SHAPE, "repack cannot run in place");
   st = check_device();
   if (st != MOE_OK) return st;
@@ -197,6 +205,7 @@ moe_status moe_grouped_mxgemm(const moe_mxdesc* w, const uint8_t* a_codes, const
   if (M_total == 0) return ok();
   if (!a_codes || !a_scales || !seg_offsets || !out)
     return fail(MOE_ERR_NULL_ARG, "a_codes, a_scales, seg_offsets and out are required");
+  if (out == a_codes || out == a_scales) return fail(MOE_ERR_BAD_SHAPE, "the product cannot run in place");
   if (mx_out != (out_scales != nullptr)) return fail(MOE_ERR_NULL_ARG, "out_scales goes with an MX epilogue (%d)", epilogue);
   if (!aligned(a_codes, 16) || !aligned(out, 16)) return fail(MOE_ERR_MISALIGNED, "a_codes and out must be 16-byte aligned");
   if (!aligned(a_scales, 4) || !aligned(seg_offsets, 4) || !aligned(gather_pair, 4))
@@ -211,7 +220,7 @@ moe_status moe_grouped_mxgemm(const moe_mxdesc* w, const uint8_t* a_codes, const
 }
 
 size_t moe_mx_layer_workspace_size(int32_t T, int32_t k, int32_t E) {
-  if (T < 0 || k < 1 || E < 1 || E > 1024 || (int64_t)T * k >= ((int64_t)1 << 31)) return 0;
+  if (T < 0 || k < 1 || E < 1 || E > 1024 || T >= 1 << 25 || (int64_t)T * k >= ((int64_t)1 << 31)) return 0;
   return moe::mx_layer_workspace_bytes(T, k, E);
 }
 
@@ -245,6 +254,8 @@ moe_status moe_mx_layer(const moe_mxlayer* l, void* stream) {
     return fail(MOE_ERR_NULL_ARG, "the grouping's buffers are required");
   if (!l->x_codes || !l->x_scales || !l->h_codes || !l->h_scales || !l->y || !l->out)
     return fail(MOE_ERR_NULL_ARG, "x, h, y and out buffers are required");
+  if (l->x == l->x_codes || l->x_codes == l->h_codes || l->h_codes == l->y || l->x_codes == l->y || l->y == l->out)
+    return fail(MOE_ERR_BAD_SHAPE, "x, x_codes, h_codes, y and out share a buffer");
   const size_t need = moe::mx_layer_workspace_bytes(T, k, E);
   if (l->workspace_bytes < need)
     return fail(MOE_ERR_WORKSPACE_TOO_SMALL, "workspace %zu bytes, %zu needed", l->workspace_bytes, need);

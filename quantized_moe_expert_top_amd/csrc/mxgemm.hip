@@ -696,7 +696,7 @@ int launch_tile(const MxK& k, hipStream_t s) {
   // upper bound of the row tiles: one partial tile per segment that has rows
   const int64_t tiles = (int64_t)k.M_total / TM + (k.E < k.M_total ? k.E : k.M_total);
   const int64_t wgs = (tiles * n_nb + 7) / 8 * 8;
-  if (wgs >= ((int64_t)1 << 31)) return (int)hipErrorInvalidConfiguration;
+  if (wgs >= ((int64_t)1 << 24)) return (int)hipErrorInvalidConfiguration;
   hipLaunchKernelGGL((mx_tile_kernel<AF, EPI, TM>), dim3((unsigned)wgs), dim3(256), 0, s, k, n_nb);
   return (int)hipGetLastError();
 }

@@ -138,6 +138,54 @@ def test_quantize_beside_every_border(fmt, shift):
     assert np.array_equal(decoded(r), mx.values(codes, scales, F))
 
 
+def test_offsets_past_32_bits():
+    """Rows behind the 4 GiB and 2^31 element marks against the same rows on their own (bit for bit)."""
+    def tail(t, n=96):
+        return t[-n:].clone()
+    g = torch.Generator(device=DEV).manual_seed(5)
+    big = torch.empty(70001, 32768, device=DEV, dtype=torch.float16)   # 2.3e9 values
+    big[-96:] = torch.randn(96, 32768, device=DEV, generator=g)
+    big[:-96] = 1.0
+    for fmt in (q.MOE_MX_E4M3, q.MOE_MX_E2M1):
+        show("past 32 bits: quantise", fmt)
+        r = q.moe_quantize_mx(big, fmt)
+        one = q.moe_quantize_mx(tail(big), fmt)
+        assert torch.equal(r.codes[-96:], one.codes) and torch.equal(r.scales[-96:], one.scales)
+        show("past 32 bits: dequantise", fmt)
+        back = q.moe_dequantize_mx(r)
+        assert torch.equal(back[-96:], q.moe_dequantize_mx(one))
+        assert (back[:3] == 1).all()
+        del r, back
+    x = big.view(-1, 8192)                                              # 280004 rows
+    wn = torch.randn(8192, device=DEV, generator=g).half()
+    show("past 32 bits: norm")
+    a = q.moe_rmsnorm_mx(x, wn, 1e-5, residual=x, fmt=q.MOE_MX_E4M3, want_y=True)
+    b = q.moe_rmsnorm_mx(tail(x), wn, 1e-5, residual=tail(x), fmt=q.MOE_MX_E4M3, want_y=True)
+    assert torch.equal(a.sum[-96:], b.sum) and torch.equal(a.y[-96:], b.y) and torch.equal(a.rows.codes[-96:], b.rows.codes)
+    del a, x, big
+    show("past 32 bits: routing")
+    logits = torch.zeros(2200000, 1024, device=DEV)
+    logits[-96:] = torch.randn(96, 1024, device=DEV, generator=g)
+    logits[:-96, 7] = 1.0
+    ids, w = q.moe_route_scored(logits, 2, q.MOE_SCORE_SIGMOID)
+    i1, w1 = q.moe_route_scored(tail(logits), 2, q.MOE_SCORE_SIGMOID)
+    assert torch.equal(ids[-96:], i1) and torch.equal(w[-96:], w1) and (ids[:-96, 0] == 7).all()
+    del logits
+    # product: 4.6 GB of fp32 outputs, 2.1 GB of rows
+    M, N, K = 140000, 8192, 16384
+    codes = torch.full((M, K), 0x38, device=DEV, dtype=torch.uint8)    # 1.0
+    codes[-96:] = q.moe_quantize_mx(torch.randn(96, K, device=DEV, generator=g)).codes
+    A = q.MxRows(codes, torch.full((M, K // 32), 120, device=DEV, dtype=torch.uint8), q.MOE_MX_E4M3)
+    wt = q.moe_mx_repack(q.mx_experts(q.moe_quantize_mx(torch.randn(1, N, K, device=DEV, generator=g), q.MOE_MX_E2M1)))
+    seg = torch.tensor([0, M], device=DEV, dtype=torch.int32)
+    for kernel in (q.MOE_KERNEL_TILE64, q.MOE_KERNEL_TILE128):
+        show("past 32 bits: product", kernel)
+        y = q.moe_grouped_mxgemm(wt, A, seg, M, q.MOE_EPI_NONE_F32, kernel=kernel)
+        y1 = q.moe_grouped_mxgemm(wt, q.MxRows(tail(A.codes), tail(A.scales), A.fmt), torch.tensor([0, 96], device=DEV, dtype=torch.int32),
+                                  96, q.MOE_EPI_NONE_F32, kernel=kernel)
+        assert torch.equal(y[-96:], y1) and torch.equal(y[5], y[-97])
+
+
 def test_quantize_leading_dims_out_and_empty():
     x = torch.randn(3, 5, 64, device=DEV)
     r = q.moe_quantize_mx(x, q.MOE_MX_E2M1)

@@ -64,7 +64,7 @@ def test_route_scored_validation(lib):
     def call(logits=A, bias=None, T=4, E=8, k=2, score=0, ng=1, tg=1, gt=1, scale=1.0, ids=A, w=A):
         return lib.moe_route_scored(logits, bias, T, E, k, score, ng, tg, gt, 1, scale, ids, w, None)
     assert call(T=-1) == call(E=0) == call(E=1025) == call(k=0) == call(k=9) == BAD_SHAPE
-    assert call(T=1 << 28, E=1024, k=16) == BAD_SHAPE
+    assert call(T=1 << 28, E=1024, k=16) == call(T=1 << 25, k=1) == BAD_SHAPE
     assert call(score=2) == call(score=-1) == BAD_FORMAT
     assert call(ng=0) == call(ng=3) == call(E=1024, ng=128) == BAD_SHAPE
     assert call(ng=4, tg=5) == call(ng=4, tg=0) == call(gt=0) == call(gt=3) == BAD_SHAPE
@@ -75,10 +75,12 @@ def test_route_scored_validation(lib):
 
 
 def test_mx_rows_validation(lib):
-    def quant(x=A, dt=0, rows=4, K=64, fmt=1, c=A, s=A):
+    B = ctypes.c_void_p(0x2000)
+
+    def quant(x=B, dt=0, rows=4, K=64, fmt=1, c=A, s=A):
         return lib.moe_quantize_mx(x, dt, rows, K, fmt, c, s, None)
 
-    def dequant(c=A, s=A, rows=4, K=64, fmt=1, dt=0, out=A):
+    def dequant(c=A, s=A, rows=4, K=64, fmt=1, dt=0, out=B):
         return lib.moe_dequantize_mx(c, s, rows, K, fmt, dt, out, None)
     for f in (quant, dequant):
         assert f(dt=3) == f(fmt=0) == f(fmt=3) == BAD_FORMAT
@@ -86,14 +88,15 @@ def test_mx_rows_validation(lib):
         assert f(c=None) == f(s=None) == NULL_ARG
         assert f(c=ctypes.c_void_p(0x1008)) == MISALIGNED
         assert f(rows=0, c=None, s=None) == OK
+        assert f(c=B) == f(rows=(1 << 29), K=32) == BAD_SHAPE  # in place; 2^34 values
     assert quant(x=None) == dequant(out=None) == NULL_ARG
     assert quant(x=ctypes.c_void_p(0x1008)) == dequant(out=ctypes.c_void_p(0x1008)) == MISALIGNED
 
 
 def test_rmsnorm_validation(lib):
-    B, C, D = (ctypes.c_void_p(v) for v in (0x2000, 0x3000, 0x4000))
+    B, C, D, F = (ctypes.c_void_p(v) for v in (0x2000, 0x3000, 0x4000, 0x5000))
 
-    def norm(x=A, r=B, w=C, dt=0, rows=4, H=64, eps=1e-5, sum=B, y=D, fmt=1, c=A, s=A):
+    def norm(x=A, r=B, w=C, dt=0, rows=4, H=64, eps=1e-5, sum=B, y=D, fmt=1, c=F, s=A):
         return lib.moe_rmsnorm_mx(x, r, w, dt, rows, H, eps, sum, y, fmt, c, s, None)
     assert norm(dt=3) == norm(fmt=3) == BAD_FORMAT
     assert norm(rows=-1) == norm(H=40) == norm(eps=-1.0) == norm(eps=float("nan")) == norm(eps=float("inf")) == BAD_SHAPE
@@ -102,6 +105,7 @@ def test_rmsnorm_validation(lib):
     assert norm(c=None) == norm(s=None) == norm(fmt=0) == NULL_ARG             # codes exactly with a format
     assert norm(sum=None, y=None, fmt=0, c=None, s=None) == NULL_ARG           # no output
     assert norm(y=B) == BAD_SHAPE                                              # sum and y in one buffer
+    assert norm(c=A) == norm(c=B) == norm(c=D) == norm(rows=1 << 24, H=32) == BAD_SHAPE     # codes over values; many rows
     assert norm(x=ctypes.c_void_p(0x1008)) == norm(w=ctypes.c_void_p(0x3008)) == norm(y=ctypes.c_void_p(8)) == MISALIGNED
     assert norm(rows=0, x=None, w=None) == OK
 
@@ -131,10 +135,13 @@ def test_mx_weights_validation_and_sizes(lib):
     assert rep(mxdesc(canon, codes=0), dst) == NULL_ARG
     assert rep(mxdesc(canon, codes=0x10008), dst) == rep(mxdesc(canon, scales=0x20002), dst) == MISALIGNED
     assert rep(mxdesc(canon, E=1025), mxdesc(E=1025)) == rep(mxdesc(canon, N=1 << 17, K=1 << 17), dst) == BAD_SHAPE
+    big = dict(E=1024, N=1 << 13, K=1 << 14)  # 2^37 weights
+    assert rep(mxdesc(canon, codes=0x30000, scales=0x40000, **big), mxdesc(**big)) == BAD_SHAPE
 
 
 def test_grouped_mxgemm_validation(lib):
-    def gemm(d=None, a=A, s=A, fmt=1, rows=64, gather=A, k=2, seg=A, M=128, epi=q.MOE_EPI_NONE, kernel=0, out=A, osc=None):
+    def gemm(d=None, a=A, s=A, fmt=1, rows=64, gather=A, k=2, seg=A, M=128, epi=q.MOE_EPI_NONE, kernel=0, out=ctypes.c_void_p(0x2000),
+             osc=None):
         d = d or mxdesc()
         return lib.moe_grouped_mxgemm(ctypes.byref(d), a, s, fmt, rows, gather, k, seg, M, epi, kernel, out, osc, None)
     assert gemm(mxdesc(q.MOE_LAYOUT_CANONICAL)) == gemm(mxdesc(version=2)) == gemm(fmt=0) == gemm(epi=6) == BAD_FORMAT
@@ -142,6 +149,7 @@ def test_grouped_mxgemm_validation(lib):
     assert gemm(kernel=q.MOE_KERNEL_LDS_DMA) == gemm(kernel=q.MOE_KERNEL_SMALL_PER_WIDTH) == UNSUPPORTED
     assert gemm(mxdesc(N=96), epi=q.MOE_EPI_SWIGLU) == gemm(mxdesc(N=48)) == gemm(mxdesc(K=160)) == UNSUPPORTED
     assert gemm(M=-1) == gemm(rows=-1) == gemm(k=0) == gemm(rows=63) == gemm(gather=None, rows=127) == BAD_SHAPE
+    assert gemm(out=A) == BAD_SHAPE                                             # in place
     assert gemm(a=None) == gemm(s=None) == gemm(seg=None) == gemm(out=None) == NULL_ARG
     assert gemm(osc=A) == gemm(epi=q.MOE_EPI_SWIGLU_E4M3) == NULL_ARG           # scales exactly with an MX epilogue
     assert gemm(a=ctypes.c_void_p(0x1008)) == gemm(out=ctypes.c_void_p(0x1008)) == MISALIGNED
@@ -157,9 +165,9 @@ def test_mx_layer_validation(lib):
         f = dict(abi_version=q.MOE_ABI_VERSION, T=3, k=2, x_dtype=q.MOE_DTYPE_BF16, x_fmt=1, h_fmt=1, y_dtype=q.MOE_DTYPE_F16,
                  kernel=0, score=0, n_group=1, topk_group=1, group_top=1, renormalize=1, scale=1.0, bias=None,
                  workspace_bytes=512, gate_up=ctypes.pointer(gu), down=ctypes.pointer(dn))
-        for n in ("x", "logits", "topk_ids", "topk_w", "expert_counts", "seg_offsets", "sorted_pair", "pair_pos", "workspace",
-                  "x_codes", "x_scales", "h_codes", "h_scales", "y", "out"):
-            f[n] = 0x1000
+        for i, n in enumerate(("x", "logits", "topk_ids", "topk_w", "expert_counts", "seg_offsets", "sorted_pair", "pair_pos", "workspace",
+                  "x_codes", "x_scales", "h_codes", "h_scales", "y", "out")):
+            f[n] = 0x1000 * (i + 1)
         f.update(kw)
         layer = q.MxLayer()
         for n, v in f.items():
@@ -174,6 +182,8 @@ def test_mx_layer_validation(lib):
               "x_codes", "x_scales", "h_codes", "h_scales", "y", "out"):
         assert call(**{n: None}) == NULL_ARG, n
     assert call(workspace_bytes=511) == WS_SMALL
+    for a, b in (("x", "x_codes"), ("x_codes", "h_codes"), ("h_codes", "y"), ("y", "out")):
+        assert call(**{a: 0x100000, b: 0x100000}) == BAD_SHAPE, (a, b)
     size = lib.moe_mx_layer_workspace_size
     assert size(3, 2, 4) == 256 + 256                       # the flag words; one chunk of 8 tokens, 5 counters
     assert size(8192, 8, 64) == 256 + 256 * 65 * 4          # 256 chunks of 32 tokens
