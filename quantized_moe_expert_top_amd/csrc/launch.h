@@ -137,9 +137,11 @@ struct FrontGroups {
   uint32_t* flag;
   int* chunk_hist;  // mx_layer_workspace_bytes behind the flag's 256 bytes
 };
-// Tokens that a wavefront of the layer's start routes one after another where it
-// also counts the pairs (0: it does not), and the workspace for those counts.
-int front_tokens_per_wave(int T, int E);
+// Tokens per workgroup of the layer's start where it also counts the pairs (ns:
+// experts per lane; the registers of 9 and more allow half), front_chunk_tokens:
+// the same for E experts, or 0 where it does not count; the workspace.
+constexpr int chunk_tokens(int ns) { return ns <= 8 ? 16 : 8; }
+int front_chunk_tokens(int T, int E);
 size_t mx_layer_workspace_bytes(int T, int k, int E);
 int launch_mx_front(const ScoredArgs& a, const FrontRows& q, const FrontGroups& g, bool* grouped, void* stream);
 

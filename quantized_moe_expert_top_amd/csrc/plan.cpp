@@ -128,24 +128,19 @@ size_t qgemm_workspace_bytes(const QWeights& w, int A_rows, int M_total, int ker
   return need;
 }
 
-// The start of an MX layer: chunks of 8 wavefronts' tokens, whose counts (E + 1
-// per chunk) every workgroup of the second launch reads in full: at most 256
-// chunks and 32768 counters.  A wavefront routes at most 4 tokens one after
-// another (2.5 us each); beyond that routing gets a launch to itself.
-namespace {
-constexpr int kChunks = 256, kChunkInts = 32768, kChunkTokens = 8;
-}  // namespace
-int front_tokens_per_wave(int T, int E) {
-  const int most = kChunkInts / (E + 1) < kChunks ? kChunkInts / (E + 1) : kChunks;
-  const int per = (T + kChunkTokens * most - 1) / (kChunkTokens * most);
-  return per <= 4 ? per : 0;
+// The start of an MX layer: the counts (E + 1 per chunk of a workgroup's tokens)
+// that every workgroup of the second launch reads in full are at most 68 K (270
+// KB, about 2 us); with more, grouping is a call of its own.
+int front_chunk_tokens(int T, int E) {
+  const int tokens = chunk_tokens((E + 63) / 64);
+  const int64_t chunks = ((int64_t)T + tokens - 1) / tokens;
+  return chunks * (E + 1) <= 68 * 1024 ? tokens : 0;
 }
 size_t mx_layer_workspace_bytes(int T, int k, int E) {
   const size_t sort = permute_workspace_bytes(T * k, E, 1);
-  const int per = front_tokens_per_wave(T, E);
-  if (per == 0) return sort;
-  const size_t chunks = (size_t)(T + kChunkTokens * per - 1) / (kChunkTokens * per);
-  const size_t counts = 256 + align256(chunks * (E + 1) * 4);
+  const int tokens = front_chunk_tokens(T, E);
+  if (tokens == 0) return sort;
+  const size_t counts = 256 + align256((size_t)(T + tokens - 1) / tokens * (E + 1) * 4);
   return counts > sort ? counts : sort;
 }
 

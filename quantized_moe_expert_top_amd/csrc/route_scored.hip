@@ -18,6 +18,8 @@
 // Every way gives the same result.
 #include <float.h>
 
+#include <utility>
+
 #include "mx.h"
 #include "permute_dev.h"
 
@@ -206,10 +208,14 @@ constexpr int kSpare = 6;  // candidates beyond k that cost less than another st
 // SOFT_ALL: the softmax denominator is needed (a bias, weights that are not
 // renormalised, sums of two scores per group): float64 exponentials of all
 // experts give it and the keys.
-// Token t by this wavefront; buf: 64 * NS doubles of LDS of its own; hist: E + 1
-// counters in LDS that its pairs' experts (E: none) are added to, or nullptr.
+// The first two steps for token t by this wavefront: the number of candidates,
+// listed at the start of buf (64 * NS doubles of LDS of the wavefront's own); or
+// -1 where they exceed the lanes and the token was settled over all experts.
+// hist: E + 1 counters in LDS that its pairs' experts (E: none) are added to, or
+// nullptr.
 template <int NS, bool SOFT_ALL>
-__device__ __forceinline__ void route_token(const ScoredArgs& a, int t, double* buf, int* hist = nullptr) {
+__device__ __forceinline__ int route_candidates(const ScoredArgs& a, int t, double* buf, int* hist, float& top,
+                                                double& soft_sum) {
   const int lane = threadIdx.x & 63;
   const float* row = a.logits + (size_t)t * a.E;
 
@@ -223,13 +229,13 @@ __device__ __forceinline__ void route_token(const ScoredArgs& a, int t, double* 
 #pragma unroll
     for (int s = 0; s < NS; ++s) b[s] = 0.0f;
   }
-  float top = -__builtin_inff();
+  top = -__builtin_inff();
 #pragma unroll
   for (int s = 0; s < NS; ++s) {
     x[s] = (x[s] != x[s] || lane + 64 * s >= a.E) ? -__builtin_inff() : fminf(x[s], FLT_MAX);
     top = fmaxf(top, x[s]);
   }
-  double soft_sum = 0.0;
+  soft_sum = 0.0;
   float key[NS];
   if (a.score == 0) top = key_value(wave_imax(order_key(top)));
   if constexpr (SOFT_ALL) {
@@ -351,69 +357,151 @@ __device__ __forceinline__ void route_token(const ScoredArgs& a, int t, double* 
     lo = fmaxf(lo - 4.0f * kMargin * (kBase + fabsf(lo)), -FLT_MAX);
     n = reach(lo);
   }
-  const bool exact = n > 64;  // many (nearly) equal keys
-  int cand = -1;
-  if (!exact) {
-    int* const list = reinterpret_cast<int*>(buf);
-    int base = 0;
-#pragma unroll
-    for (int s = 0; s < NS; ++s) {
-      const bool in = n > 0 && key[s] >= lo;
-      const uint64_t m = __ballot(in);
-      if (in) list[base + __builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0))] = lane + 64 * s;
-      base += __popcll(m);
-    }
-    wave_fence();
-    if (lane < n) cand = list[lane];
-  }
-  if (exact) {
+  if (n > 64) {  // many (nearly) equal keys
     wave_fence();
     route_exact<NS>(a, t, top, buf, hist);
-    return;
+    return -1;
   }
+  int* const list = reinterpret_cast<int*>(buf);
+  int base = 0;
+#pragma unroll
+  for (int s = 0; s < NS; ++s) {
+    const bool in = n > 0 && key[s] >= lo;
+    const uint64_t m = __ballot(in);
+    if (in) list[base + __builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0))] = lane + 64 * s;
+    base += __popcll(m);
+  }
+  wave_fence();
+  return n;
+}
 
-  // float64 scores of the candidates, their ranks, the weights of the first k
-  double score = 0.0, c = neg_inf();
-  if (cand >= 0) {
-    const double xv = (double)fminf(row[cand], FLT_MAX);
-    const double bv = a.bias ? (double)a.bias[cand] : 0.0;
-    if (a.score == 0) {
-      score = exp(xv - (double)top);
-      if constexpr (SOFT_ALL) score = score / soft_sum;
-    } else {
-      score = 1.0 / (1.0 + exp(-xv));
-    }
-    c = score + bv;
+// float64 score and choice score of candidate cand of token t.
+template <bool SOFT_ALL>
+__device__ __forceinline__ void candidate_score(const ScoredArgs& a, int t, int cand, float top, double soft_sum,
+                                                double& score, double& c) {
+  score = 0.0;
+  c = neg_inf();
+  if (cand < 0) return;
+  const double xv = (double)fminf(a.logits[(size_t)t * a.E + cand], FLT_MAX);
+  const double bv = a.bias ? (double)a.bias[cand] : 0.0;
+  if (a.score == 0) {
+    score = exp(xv - (double)top);
+    if constexpr (SOFT_ALL) score = score / soft_sum;
+  } else {
+    score = 1.0 / (1.0 + exp(-xv));
   }
+  c = score + bv;
+}
+// The results of a token, by W lanes (i: this one) that hold its n candidates.
+template <int W>
+__device__ __forceinline__ void store_token(const ScoredArgs& a, int t, int i, int n, int cand, int rank, double score,
+                                            double sum, int* hist) {
+  const size_t o = (size_t)t * a.k;
+  if (cand >= 0 && rank < a.k) {
+    a.ids[o + rank] = cand;
+    a.w[o + rank] = sum > 0.0 ? (float)(score / sum * (double)a.scale) : 0.0f;
+    if (hist) atomicAdd(&hist[cand], 1);
+  }
+  if (hist && n < a.k && i == 0) atomicAdd(&hist[a.E], a.k - n);
+  for (int j = n + i; j < a.k; j += W) {  // fewer eligible experts than slots
+    a.ids[o + j] = -1;
+    a.w[o + j] = 0.0f;
+  }
+}
+
+// The third step for one token: candidates' ranks, the sum over the chosen in
+// index order.
+template <bool SOFT_ALL>
+__device__ __forceinline__ void settle_one(const ScoredArgs& a, int t, int cand, int n, float top, double soft_sum, int* hist) {
+  const int lane = threadIdx.x & 63;
+  double score, c;
+  candidate_score<SOFT_ALL>(a, t, cand, top, soft_sum, score, c);
   int rank = 0;
   for (int j = 0; j < n; ++j) {
     const double cj = readlane_f64(c, j);
     rank += (cj > c || (cj == c && j < lane)) ? 1 : 0;
   }
-  const bool chosen = cand >= 0 && rank < a.k;
   double sum = 1.0;
   if (a.renorm) {
     sum = 0.0;
-    for (uint64_t left = __ballot(chosen); left; left &= left - 1) sum += readlane_f64(score, __builtin_ctzll(left));
+    for (uint64_t left = __ballot(cand >= 0 && rank < a.k); left; left &= left - 1)
+      sum += readlane_f64(score, __builtin_ctzll(left));
   }
-  const size_t o = (size_t)t * a.k;
-  if (chosen) {
-    a.ids[o + rank] = cand;
-    a.w[o + rank] = sum > 0.0 ? (float)(score / sum * (double)a.scale) : 0.0f;
-    if (hist) atomicAdd(&hist[cand], 1);
+  store_token<64>(a, t, lane, n, cand, rank, score, sum, hist);
+}
+
+// The same for four tokens at once, a row of 16 lanes each (n < 0: nothing left
+// to do for the row's token).
+template <int J>
+__device__ __forceinline__ double row_value(double v) {  // of lane J of the row
+  const uint64_t u = __builtin_bit_cast(uint64_t, v);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, 0x150 + J, 0xF, 0xF, true);
+  const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), 0x150 + J, 0xF, 0xF, true);
+  return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+template <int... J>
+__device__ __forceinline__ int row_rank(std::integer_sequence<int, J...>, double c, int i) {
+  int rank = 0;
+  ((rank += (row_value<J>(c) > c || (row_value<J>(c) == c && J < i)) ? 1 : 0), ...);
+  return rank;
+}
+template <int... J>
+__device__ __forceinline__ double row_sum(std::integer_sequence<int, J...>, double v) {
+  double sum = 0.0;
+  ((sum += row_value<J>(v)), ...);
+  return sum;
+}
+constexpr int kRow = 16;
+template <bool SOFT_ALL>
+__device__ __forceinline__ void settle_rows(const ScoredArgs& a, int t, int cand, int n, float top, double soft_sum, int* hist) {
+  const int i = threadIdx.x & (kRow - 1);
+  double score, c;
+  candidate_score<SOFT_ALL>(a, t, cand, top, soft_sum, score, c);
+  const std::make_integer_sequence<int, kRow> lanes{};
+  const int rank = row_rank(lanes, c, i);
+  const double sum = a.renorm ? row_sum(lanes, cand >= 0 && rank < a.k ? score : 0.0) : 1.0;
+  if (n >= 0) store_token<kRow>(a, t, i, n, cand, rank, score, sum, hist);
+}
+
+// Token t0 + w by wavefront w of a workgroup of W; the third step of four tokens
+// at a time by one of the first W / 4 wavefronts (a lane per candidate of one
+// token would leave three quarters of the lanes idle, over the float64
+// exponentials and divisions), but for tokens whose candidates exceed a row.
+// (One wavefront with a loop over four tokens needs 50 registers more, for what
+// the compiler moves out of the loop, and was slower from 128 experts up.)
+struct RowToken {
+  double soft_sum;
+  float top;
+  int n;
+};
+template <int W, int NS, bool SOFT_ALL>
+__device__ __forceinline__ void route_block(const ScoredArgs& a, int t0, double (*buf)[64 * NS], RowToken* rows, int* hist) {
+  const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  float top = 0.0f;
+  double soft_sum = 1.0;
+  int n = -1;
+  if (t0 + wv < a.T) {
+    n = route_candidates<NS, SOFT_ALL>(a, t0 + wv, buf[wv], hist, top, soft_sum);
+    if (n > kRow) {
+      const int* const list = reinterpret_cast<const int*>(buf[wv]);
+      settle_one<SOFT_ALL>(a, t0 + wv, lane < n ? list[lane] : -1, n, top, soft_sum, hist);
+      n = -1;
+    }
   }
-  if (hist && n < a.k && lane == 0) atomicAdd(&hist[a.E], a.k - n);
-  for (int j = n + lane; j < a.k; j += 64) {  // fewer eligible experts than slots
-    a.ids[o + j] = -1;
-    a.w[o + j] = 0.0f;
+  if (lane == 0) rows[wv] = RowToken{soft_sum, top, n};
+  __syncthreads();
+  if (wv < W / 4) {
+    const int r = 4 * wv + lane / kRow, i = lane % kRow;
+    const RowToken m = rows[r];
+    const int cand = i < m.n ? reinterpret_cast<const int*>(buf[r])[i] : -1;
+    settle_rows<SOFT_ALL>(a, t0 + r, cand, m.n, m.top, m.soft_sum, hist);
   }
 }
 template <int NS, bool SOFT_ALL>
 __global__ __launch_bounds__(64 * kWavesPerBlock) void route_scored_kernel(ScoredArgs a) {
   __shared__ double lds[kWavesPerBlock][64 * NS];
-  const int wv = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  const int t = blockIdx.x * kWavesPerBlock + wv;
-  if (t < a.T) route_token<NS, SOFT_ALL>(a, t, lds[wv]);
+  __shared__ RowToken rows[kWavesPerBlock];
+  route_block<kWavesPerBlock, NS, SOFT_ALL>(a, blockIdx.x * kWavesPerBlock, lds, rows, nullptr);
 }
 
 // ------------------------------------------------- the start of a layer's call
@@ -435,82 +523,76 @@ __device__ __forceinline__ void quantize_any(const FrontRows& q, size_t block) {
 template <int NS, bool SOFT_ALL>
 __global__ __launch_bounds__(64 * kWavesPerBlock) void mx_front_kernel(ScoredArgs a, FrontRows q, int n_route) {
   __shared__ double lds[kWavesPerBlock][64 * NS];
+  __shared__ RowToken rows[kWavesPerBlock];
   if ((int)blockIdx.x >= n_route) {
     quantize_any<64 * kWavesPerBlock>(q, blockIdx.x - n_route);
     return;
   }
-  const int wv = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  const int t = blockIdx.x * kWavesPerBlock + wv;
-  if (t < a.T) route_token<NS, SOFT_ALL>(a, t, lds[wv]);
+  route_block<kWavesPerBlock, NS, SOFT_ALL>(a, blockIdx.x * kWavesPerBlock, lds, rows, nullptr);
 }
 
 constexpr int kFrontTokens = 16, kFrontThreads = 64 * kFrontTokens;
 template <int NS, bool SOFT_ALL>
 __global__ __launch_bounds__(kFrontThreads) void mx_front_small_kernel(ScoredArgs a, FrontRows q, FrontGroups g) {
   __shared__ double lds[kFrontTokens][64 * NS];
+  __shared__ RowToken rows[kFrontTokens];
   __shared__ int hist[64 * NS + 1], tags[kFrontTokens * (64 * NS + 1)], scratch[kFrontTokens + 1];
   __shared__ uint32_t bad;
   if (blockIdx.x > 0) {
     quantize_any<kFrontThreads>(q, blockIdx.x - 1);
     return;
   }
-  const int wv = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  if (wv < a.T) route_token<NS, SOFT_ALL>(a, wv, lds[wv]);
+  route_block<kFrontTokens, NS, SOFT_ALL>(a, 0, lds, rows, nullptr);
   __syncthreads();  // the ids, read back by the whole workgroup
   const Keyer kr{a.ids, nullptr, a.E, 1, a.E};
   permute_block<kFrontThreads>(kr, a.T * a.k, g.counts, g.seg_offsets, g.sorted_pair, g.pair_pos, g.flag, hist, tags,
                                scratch, &bad);
 }
 
-// More tokens: chunks of 8 wavefronts' tokens, whose workgroups also count their
+// More tokens: chunks of a workgroup's tokens, whose workgroups also count their
 // pairs per expert (order-free LDS counters), and a second launch in which every
-// workgroup sums the chunks' counts for itself (they fit L2: at most
-// kChunkInts) and places its chunk's pairs.  Two launches where counting,
-// scanning and scattering alone were three (23 us for 65536 pairs).
-constexpr int kChunkWaves = 8, kChunkThreads = 64 * kChunkWaves;
+// workgroup sums the chunks' counts for itself (they fit L2) and places the pairs
+// of some chunks.  Two launches, 24 us for 8192 tokens x 8 of 64 experts with the
+// quantisation of 2048 bf16 each; routing and quantising in one and counting,
+// scanning and scattering in three more took 38 us.
 template <int NS, bool SOFT_ALL>
-__global__ __launch_bounds__(kChunkThreads) void mx_front_chunk_kernel(ScoredArgs a, FrontRows q, int n_chunks, int per_wave,
-                                                                       int* __restrict__ chunk_hist) {
-  __shared__ double lds[kChunkWaves][64 * NS];
+__global__ __launch_bounds__(64 * chunk_tokens(NS)) void mx_front_chunk_kernel(ScoredArgs a, FrontRows q, int n_chunks,
+                                                                               int* __restrict__ chunk_hist) {
+  constexpr int W = chunk_tokens(NS), kThreads = 64 * W;
+  __shared__ double lds[W][64 * NS];
+  __shared__ RowToken rows[W];
   __shared__ int hist[64 * NS + 1];
   if ((int)blockIdx.x >= n_chunks) {
-    quantize_any<kChunkThreads>(q, blockIdx.x - n_chunks);
+    quantize_any<kThreads>(q, blockIdx.x - n_chunks);
     return;
   }
-  for (int i = threadIdx.x; i <= a.E; i += kChunkThreads) hist[i] = 0;
+  for (int i = threadIdx.x; i <= a.E; i += kThreads) hist[i] = 0;
   __syncthreads();
-  const int wv = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  const int t0 = (blockIdx.x * kChunkWaves + wv) * per_wave;
-  for (int t = t0; t < min(t0 + per_wave, a.T); ++t) {
-    wave_fence();  // the last token's reads of the wavefront's buffer are done
-    route_token<NS, SOFT_ALL>(a, t, lds[wv], hist);
-  }
+  route_block<W, NS, SOFT_ALL>(a, blockIdx.x * W, lds, rows, hist);
   __syncthreads();
-  for (int i = threadIdx.x; i <= a.E; i += kChunkThreads) chunk_hist[(size_t)blockIdx.x * (a.E + 1) + i] = hist[i];
+  for (int i = threadIdx.x; i <= a.E; i += kThreads) chunk_hist[(size_t)blockIdx.x * (a.E + 1) + i] = hist[i];
 }
 
-constexpr int kPlaceThreads = 256;
-__global__ __launch_bounds__(kPlaceThreads) void mx_place_kernel(Keyer kr, int P, int chunk_pairs, int n_chunks,
-                                                                 const int* __restrict__ chunk_hist, FrontGroups g) {
+constexpr int kPlaceThreads = 1024;
+__global__ __launch_bounds__(kPlaceThreads) void mx_place_kernel(Keyer kr, int P, int chunk_pairs, int per_block,
+                                                                 int n_chunks, const int* __restrict__ chunk_hist, FrontGroups g) {
   __shared__ int base[1025], before[1025], tags[(kPlaceThreads / 64) * 1025], scratch[kPlaceThreads / 64 + 1];
-  const int tid = threadIdx.x, nk1 = kr.NK + 1, b = blockIdx.x;
+  const int tid = threadIdx.x, nk1 = kr.NK + 1, b = blockIdx.x * per_block;  // b: its first chunk
   for (int i = tid; i < nk1; i += kPlaceThreads) base[i] = before[i] = 0;
   for (int i = tid; i < (kPlaceThreads / 64) * nk1; i += kPlaceThreads) tags[i] = -1;
   __syncthreads();
-  // a lane per key, the wavefronts share the chunks
-  for (int k0 = 0; k0 < nk1; k0 += 64) {
-    const int key = k0 + (tid & 63);
-    if (key < nk1) {
-      int all = 0, prior = 0;
+  // a thread per key and slice of the chunks (a few loads one after another each)
+  const int slices = max(kPlaceThreads / nk1, 1), slice = tid / nk1;
+  for (int key = tid - slice * nk1; key < nk1 && slice < slices; key += kPlaceThreads) {
+    int all = 0, prior = 0;
 #pragma unroll 8
-      for (int c = tid >> 6; c < n_chunks; c += kPlaceThreads / 64) {
-        const int n = chunk_hist[(size_t)c * nk1 + key];
-        all += n;
-        prior += c < b ? n : 0;
-      }
-      atomicAdd(&base[key], all);
-      atomicAdd(&before[key], prior);
+    for (int c = slice; c < n_chunks; c += slices) {
+      const int n = chunk_hist[(size_t)c * nk1 + key];
+      all += n;
+      prior += c < b ? n : 0;
     }
+    atomicAdd(&base[key], all);
+    atomicAdd(&before[key], prior);
   }
   __syncthreads();
   if (b == 0) {
@@ -525,7 +607,7 @@ __global__ __launch_bounds__(kPlaceThreads) void mx_place_kernel(Keyer kr, int P
   for (int i = tid; i < nk1; i += kPlaceThreads) base[i] += before[i];
   __syncthreads();
   const int p0 = b * chunk_pairs;
-  scatter_chunk<kPlaceThreads>(kr, p0, min(P, p0 + chunk_pairs), base, tags, g.sorted_pair, g.pair_pos);
+  scatter_chunk<kPlaceThreads>(kr, p0, min((int64_t)P, p0 + (int64_t)per_block * chunk_pairs), base, tags, g.sorted_pair, g.pair_pos);
 }
 
 inline bool soft_all(const ScoredArgs& a) {
@@ -549,10 +631,12 @@ void launch_front_ns(const ScoredArgs& a, const FrontRows& q, hipStream_t s) {
   else hipLaunchKernelGGL((mx_front_kernel<NS, false>), grid, block, 0, s, a, q, n_route);
 }
 template <int NS>
-void launch_front_chunk_ns(const ScoredArgs& a, const FrontRows& q, int n_chunks, int per_wave, int* hist, hipStream_t s) {
-  const dim3 grid(n_chunks + quant_blocks(q, kChunkThreads)), block(kChunkThreads);
-  if (soft_all(a)) hipLaunchKernelGGL((mx_front_chunk_kernel<NS, true>), grid, block, 0, s, a, q, n_chunks, per_wave, hist);
-  else hipLaunchKernelGGL((mx_front_chunk_kernel<NS, false>), grid, block, 0, s, a, q, n_chunks, per_wave, hist);
+void launch_front_chunk_ns(const ScoredArgs& a, const FrontRows& q, int* hist, hipStream_t s) {
+  constexpr int W = chunk_tokens(NS), kThreads = 64 * W;
+  const int n_chunks = (a.T + W - 1) / W;
+  const dim3 grid(n_chunks + quant_blocks(q, kThreads)), block(kThreads);
+  if (soft_all(a)) hipLaunchKernelGGL((mx_front_chunk_kernel<NS, true>), grid, block, 0, s, a, q, n_chunks, hist);
+  else hipLaunchKernelGGL((mx_front_chunk_kernel<NS, false>), grid, block, 0, s, a, q, n_chunks, hist);
 }
 template <int NS>
 void launch_front_small_ns(const ScoredArgs& a, const FrontRows& q, const FrontGroups& g, hipStream_t s) {
@@ -564,24 +648,24 @@ void launch_front_small_ns(const ScoredArgs& a, const FrontRows& q, const FrontG
 
 int launch_mx_front(const ScoredArgs& a, const FrontRows& q, const FrontGroups& g, bool* grouped, void* stream) {
   const hipStream_t s = static_cast<hipStream_t>(stream);
-  const int per_wave = front_tokens_per_wave(a.T, a.E);
-  *grouped = (a.T <= kFrontTokens && a.E <= 256) || per_wave > 0;
+  const int tokens = front_chunk_tokens(a.T, a.E);
+  *grouped = (a.T <= kFrontTokens && a.E <= 256) || tokens > 0;
   if (a.T <= kFrontTokens && a.E <= 256) {
     if (a.E <= 64) launch_front_small_ns<1>(a, q, g, s);
     else if (a.E <= 128) launch_front_small_ns<2>(a, q, g, s);
     else launch_front_small_ns<4>(a, q, g, s);
-  } else if (per_wave > 0) {
-    const int tokens = kChunkWaves * per_wave, n_chunks = (a.T + tokens - 1) / tokens;
-    if (a.E <= 64) launch_front_chunk_ns<1>(a, q, n_chunks, per_wave, g.chunk_hist, s);
-    else if (a.E <= 128) launch_front_chunk_ns<2>(a, q, n_chunks, per_wave, g.chunk_hist, s);
-    else if (a.E <= 256) launch_front_chunk_ns<4>(a, q, n_chunks, per_wave, g.chunk_hist, s);
-    else if (a.E <= 512) launch_front_chunk_ns<8>(a, q, n_chunks, per_wave, g.chunk_hist, s);
-    else launch_front_chunk_ns<16>(a, q, n_chunks, per_wave, g.chunk_hist, s);
+  } else if (tokens > 0) {
+    if (a.E <= 64) launch_front_chunk_ns<1>(a, q, g.chunk_hist, s);
+    else if (a.E <= 128) launch_front_chunk_ns<2>(a, q, g.chunk_hist, s);
+    else if (a.E <= 256) launch_front_chunk_ns<4>(a, q, g.chunk_hist, s);
+    else if (a.E <= 512) launch_front_chunk_ns<8>(a, q, g.chunk_hist, s);
+    else launch_front_chunk_ns<16>(a, q, g.chunk_hist, s);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return (int)e;
     const Keyer kr{a.ids, nullptr, a.E, 1, a.E};
-    hipLaunchKernelGGL(mx_place_kernel, dim3(n_chunks), dim3(kPlaceThreads), 0, s, kr, a.T * a.k, tokens * a.k, n_chunks,
-                       g.chunk_hist, g);
+    const int n_chunks = (a.T + tokens - 1) / tokens, per_block = (n_chunks + 255) / 256;
+    hipLaunchKernelGGL(mx_place_kernel, dim3((n_chunks + per_block - 1) / per_block), dim3(kPlaceThreads), 0, s, kr,
+                       a.T * a.k, tokens * a.k, per_block, n_chunks, g.chunk_hist, g);
   } else if (a.E <= 64) {
     launch_front_ns<1>(a, q, s);
   } else if (a.E <= 128) {

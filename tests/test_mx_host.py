@@ -185,9 +185,9 @@ def test_mx_layer_validation(lib):
     for a, b in (("x", "x_codes"), ("x_codes", "h_codes"), ("h_codes", "y"), ("y", "out")):
         assert call(**{a: 0x100000, b: 0x100000}) == BAD_SHAPE, (a, b)
     size = lib.moe_mx_layer_workspace_size
-    assert size(3, 2, 4) == 256 + 256                       # the flag words; one chunk of 8 tokens, 5 counters
-    assert size(8192, 8, 64) == 256 + 256 * 65 * 4          # 256 chunks of 32 tokens
-    assert size(8193, 8, 64) == lib.moe_permute_workspace_size(8193, 8, 64, 1)
+    assert size(3, 2, 4) == 256 + 256                       # the flag words; one chunk of 16 tokens, 5 counters
+    assert size(16384, 8, 64) == 256 + 1024 * 65 * 4        # 1024 chunks
+    assert size(20000, 8, 64) == lib.moe_permute_workspace_size(20000, 8, 64, 1)
     assert size(-1, 2, 4) == size(3, 0, 4) == size(3, 2, 1025) == size(1 << 28, 16, 64) == 0
     for n in ("x", "x_codes", "h_codes", "y", "out", "workspace"):
         assert call(**{n: 0x1008}) == MISALIGNED, n
