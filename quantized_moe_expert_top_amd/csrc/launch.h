@@ -141,7 +141,7 @@ struct FrontGroups {
 // experts per lane; the registers of 9 and more allow half), front_chunk_tokens:
 // the same for E experts, or 0 where it does not count; the workspace.
 constexpr int chunk_tokens(int ns) { return ns <= 8 ? 16 : 8; }
-int front_chunk_tokens(int T, int E);
+int front_chunk_tokens(int T, int k, int E);
 size_t mx_layer_workspace_bytes(int T, int k, int E);
 int launch_mx_front(const ScoredArgs& a, const FrontRows& q, const FrontGroups& g, bool* grouped, void* stream);
 

@@ -128,17 +128,22 @@ size_t qgemm_workspace_bytes(const QWeights& w, int A_rows, int M_total, int ker
   return need;
 }
 
-// The start of an MX layer: the counts (E + 1 per chunk of a workgroup's tokens)
-// that every workgroup of the second launch reads in full are at most 68 K (270
-// KB, about 2 us); with more, grouping is a call of its own.
-int front_chunk_tokens(int T, int E) {
+// The start of an MX layer counts its pairs while every workgroup of the second
+// launch can read all counts (E + 1 per chunk of a workgroup's tokens): up to
+// 256 K of them, or 3 per pair and 1.1 M; with more, grouping is a call of its
+// own.  Layers of 128 x 128 experts, us so / apart: 64 experts 74 / 87 (16384
+// tokens x 8, 67 K counts), 502 / 611 (131072, 532 K); 256 experts 362 / 383
+// (65536 x 8, 1.05 M); 1000 experts 48 / 65 (1000 x 4, 125 K), 66 / 67 (2048,
+// 256 K), 91 / 79 (4096, 512 K).
+int front_chunk_tokens(int T, int k, int E) {
   const int tokens = chunk_tokens((E + 63) / 64);
-  const int64_t chunks = ((int64_t)T + tokens - 1) / tokens;
-  return chunks * (E + 1) <= 68 * 1024 ? tokens : 0;
+  const int64_t counts = ((int64_t)T + tokens - 1) / tokens * (E + 1);
+  const int64_t by_pairs = 3 * (int64_t)T * k < 1100 * 1024 ? 3 * (int64_t)T * k : 1100 * 1024;
+  return counts <= 256 * 1024 || counts <= by_pairs ? tokens : 0;
 }
 size_t mx_layer_workspace_bytes(int T, int k, int E) {
   const size_t sort = permute_workspace_bytes(T * k, E, 1);
-  const int tokens = front_chunk_tokens(T, E);
+  const int tokens = front_chunk_tokens(T, k, E);
   if (tokens == 0) return sort;
   const size_t counts = 256 + align256((size_t)(T + tokens - 1) / tokens * (E + 1) * 4);
   return counts > sort ? counts : sort;

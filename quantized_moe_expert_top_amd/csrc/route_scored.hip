@@ -648,7 +648,7 @@ void launch_front_small_ns(const ScoredArgs& a, const FrontRows& q, const FrontG
 
 int launch_mx_front(const ScoredArgs& a, const FrontRows& q, const FrontGroups& g, bool* grouped, void* stream) {
   const hipStream_t s = static_cast<hipStream_t>(stream);
-  const int tokens = front_chunk_tokens(a.T, a.E);
+  const int tokens = front_chunk_tokens(a.T, a.k, a.E);
   *grouped = (a.T <= kFrontTokens && a.E <= 256) || tokens > 0;
   if (a.T <= kFrontTokens && a.E <= 256) {
     if (a.E <= 64) launch_front_small_ns<1>(a, q, g, s);

@@ -555,7 +555,8 @@ def test_layer_quantises_bf16_input_and_checks_sizes():
 @pytest.mark.parametrize("T,E,k,given", [(1, 4, 1, False), (16, 256, 8, False), (16, 64, 6, True), (17, 64, 6, False),
                                          (9, 300, 5, False), (3, 100, 33, False), (700, 40, 8, True), (1200, 130, 4, False),
                                          (300, 1000, 2, False), (8192, 12, 2, False), (8200, 5, 1, False),
-                                         (17409, 63, 1, False), (9000, 128, 2, True), (2000, 520, 2, False)])
+                                         (17409, 63, 1, False), (9000, 128, 2, True), (2000, 520, 2, False),
+                                         (3000, 1000, 2, False), (70000, 63, 1, False), (33000, 200, 1, False)])
 @pytest.mark.parametrize("dt", ["bf16", "fp32"])
 def test_layer_call_equals_its_parts(T, E, k, given, dt):
     """The layer's one call (fused starts for few tokens, separate launches for many) against routing, grouping,

@@ -187,7 +187,8 @@ def test_mx_layer_validation(lib):
     size = lib.moe_mx_layer_workspace_size
     assert size(3, 2, 4) == 256 + 256                       # the flag words; one chunk of 16 tokens, 5 counters
     assert size(16384, 8, 64) == 256 + 1024 * 65 * 4        # 1024 chunks
-    assert size(20000, 8, 64) == lib.moe_permute_workspace_size(20000, 8, 64, 1)
+    assert size(131072, 8, 64) == 256 + 8192 * 65 * 4       # not more than 3 counters per pair
+    assert size(131072, 1, 64) == lib.moe_permute_workspace_size(131072, 1, 64, 1)
     assert size(-1, 2, 4) == size(3, 0, 4) == size(3, 2, 1025) == size(1 << 28, 16, 64) == 0
     for n in ("x", "x_codes", "h_codes", "y", "out", "workspace"):
         assert call(**{n: 0x1008}) == MISALIGNED, n
