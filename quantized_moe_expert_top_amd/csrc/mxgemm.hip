@@ -354,18 +354,27 @@ __device__ __forceinline__ void store_tile16(const uint32_t lohi[8], uint16_t* a
   }
 }
 
-template <int AF, int EPI, int TM>
-__device__ __forceinline__ void mx_tile_body(const MxK& p, int n_nb, u32x4* x0, u32x4* x1, uint32_t* s0, uint32_t* s1) {
+template <int AF, int EPI, int TM, int KS>
+__device__ __forceinline__ void mx_tile_body(const MxK& p, int n_nb, u32x4* x0, u32x4* x1, uint32_t* s0, uint32_t* s1,
+                                             f32x4* red) {
   constexpr int XC = 8;                      // 16-byte chunks of a row in a stage
   constexpr int SS = AF == kE4M3 ? 2 : 4;    // steps of 64 inputs in a stage
   constexpr int RT = TM / 32;                // row tiles
   constexpr int XI = TM * XC / 256;          // row DMAs per wavefront and stage
   constexpr int RW = TM / 4;                 // rows whose scales a wavefront fetches
-  const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63, all = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int wv = all & 3, grp = KS == 1 ? 0 : all >> 2;
   const int half = lane >> 5, col = lane & 31;
   Tile c;
   if (!own_tile<TM>(p, n_nb, c)) return;
   const int NT = p.N >> 5, KB = p.K >> 7, KC = (p.K + 255) >> 8;
+
+  // this group's chunks of 256 inputs
+  const int per_group = (KC + KS - 1) / KS, c0 = grp * per_group, n = KS == 1 ? KC : min(per_group, KC - c0);
+  x0 += grp * (TM * XC);
+  x1 += grp * (TM * XC);
+  s0 += grp * 256;
+  s1 += grp * 256;
 
   // this wavefront's tiles; past the last channel: tile 0, loaded and never stored
   bool valid[2];
@@ -386,7 +395,7 @@ __device__ __forceinline__ void mx_tile_body(const MxK& p, int n_nb, u32x4* x0, 
   u32x4 w[2][4];
   auto load_weights = [&](int kc, int j) {
 #pragma unroll
-    for (int u = 0; u < 2; ++u) w[u][j] = buf_x4(wr, 16 * lane, wo[u] + kc * 4096 + 1024 * j);
+    for (int u = 0; u < 2; ++u) w[u][j] = buf_x4(wr, 16 * lane, wo[u] + (c0 + kc) * 4096 + 1024 * j);
   };
   struct Scales {  // of a chunk's weights
     uint32_t w[2];
@@ -394,7 +403,7 @@ __device__ __forceinline__ void mx_tile_body(const MxK& p, int n_nb, u32x4* x0, 
   auto load_scales = [&](int kc) {
     Scales s;
 #pragma unroll
-    for (int u = 0; u < 2; ++u) s.w[u] = buf_x1(wsr, 4 * lane, wo[u] / 16 + kc * 256);
+    for (int u = 0; u < 2; ++u) s.w[u] = buf_x1(wsr, 4 * lane, wo[u] / 16 + (c0 + kc) * 256);
     return s;
   };
   // the weights' way does not wait for the rows' addresses
@@ -427,8 +436,10 @@ __device__ __forceinline__ void mx_tile_body(const MxK& p, int n_nb, u32x4* x0, 
   const bool high = ((lane % XC) ^ swizzle(lane / XC)) >= 4, high_s = (lane / RW) & 1;
   if (AF == kE2M1 && high_s) xso += 4;
 
-  // XI + 1 loads of a stage's rows and scales
-  auto issue = [&](u32x4* xs, uint32_t* ss, int st) {
+  // XI + 1 loads of the group's stage st, rows and scales
+  const int st0 = AF == kE4M3 ? 2 * c0 : c0, last = (AF == kE4M3 ? KB : KC) - 1;
+  auto issue = [&](u32x4* xs, uint32_t* ss, int rel) {
+    const int st = min(st0 + rel, last);
     const bool half_stage = AF == kE2M1 && 2 * st + 1 == KB;
     const uint32_t back = half_stage && high ? 64 : 0, back_s = half_stage && high_s ? 4 : 0;
 #pragma unroll
@@ -507,7 +518,7 @@ __device__ __forceinline__ void mx_tile_body(const MxK& p, int n_nb, u32x4* x0, 
   issue(x0, s0, 0);
   ready(zero);
   if constexpr (AF == kE4M3) {  // two stages in a chunk
-    issue(x1, s1, min(1, KB - 1));
+    issue(x1, s1, 1);
     __builtin_amdgcn_sched_barrier(0);
     load_weights(0, 2);
     load_weights(0, 3);
@@ -516,7 +527,7 @@ __device__ __forceinline__ void mx_tile_body(const MxK& p, int n_nb, u32x4* x0, 
     RowScales xa = read_scales(s0), xb;
     step(zero, sc, xa, one, x0, one);
     int kc = 0;
-    for (; kc + 1 < KC; ++kc) {
+    for (; kc + 1 < n; ++kc) {
       load_weights(kc + 1, 0);
       ready(weights_may_fly);
       issue(x0, s0, 2 * kc + 2);
@@ -528,7 +539,7 @@ __device__ __forceinline__ void mx_tile_body(const MxK& p, int n_nb, u32x4* x0, 
       step(two, sc, xb, zero, x1, one);
       load_weights(kc + 1, 2);
       ready(weights_may_fly);
-      issue(x1, s1, min(2 * kc + 3, KB - 1));
+      issue(x1, s1, 2 * kc + 3);
       xa = read_scales(s0);
       __builtin_amdgcn_sched_barrier(0);
       step(three, sc, xb, zero, x0, one);
@@ -542,13 +553,13 @@ __device__ __forceinline__ void mx_tile_body(const MxK& p, int n_nb, u32x4* x0, 
     step(two, sc, xb, zero, x1, one);
     step(three, sc, xb, zero, x1, zero);
   } else {  // one
-    issue(x1, s1, min(1, KC - 1));
-    Scales next = load_scales(min(1, KC - 1));
+    const int k1 = min(1, n - 1);
+    issue(x1, s1, k1);
+    Scales next = load_scales(k1);
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int t = 0; t < RT; ++t) f[t] = read(x0, 0, t);
     RowScales xa = read_scales(s0), xb;
-    const int k1 = min(1, KC - 1);
     step(zero, sc, xa, one, x0, one);
     load_weights(k1, 0);
     step(one, sc, xa, zero, x0, one);
@@ -556,7 +567,7 @@ __device__ __forceinline__ void mx_tile_body(const MxK& p, int n_nb, u32x4* x0, 
     step(two, sc, xa, zero, x0, one);
     load_weights(k1, 2);
     int kc = 0;
-    for (; kc + 2 < KC; kc += 2) {
+    for (; kc + 2 < n; kc += 2) {
       ready(weights_may_fly);
       issue(x0, s0, kc + 2);
       xb = read_scales(s1);
@@ -572,13 +583,13 @@ __device__ __forceinline__ void mx_tile_body(const MxK& p, int n_nb, u32x4* x0, 
       step(two, sc, xb, zero, x1, one);
       load_weights(kc + 2, 2);
       ready(weights_may_fly);
-      issue(x1, s1, min(kc + 3, KC - 1));
+      const int k3 = min(kc + 3, n - 1);
+      issue(x1, s1, k3);
       xa = read_scales(s0);
       __builtin_amdgcn_sched_barrier(0);
       step(three, sc, xb, zero, x0, one);
       load_weights(kc + 2, 3);
       sc = next;
-      const int k3 = min(kc + 3, KC - 1);
       next = load_scales(k3);
       step(zero, sc, xa, zero, x0, one);
       load_weights(k3, 0);
@@ -590,7 +601,7 @@ __device__ __forceinline__ void mx_tile_body(const MxK& p, int n_nb, u32x4* x0, 
     ready(zero);
     xb = read_scales(s1);
     step(three, sc, xa, zero, x1, one);
-    if (kc + 1 < KC) {
+    if (kc + 1 < n) {
       load_weights(kc + 1, 3);
       step(zero, next, xb, zero, x1, one);
       step(one, next, xb, zero, x1, one);
@@ -599,9 +610,42 @@ __device__ __forceinline__ void mx_tile_body(const MxK& p, int n_nb, u32x4* x0, 
     }
   }
 
+  int first = 0;  // the row tile of acc[0]
+  if constexpr (KS == 2) {
+    // A group with a chunk less waits at as many barriers (A8: 2 a chunk; A4: one,
+    // rounded up to even); then the groups exchange sums, each keeps half the rows.
+    auto barriers = [](int chunks) { return AF == kE4M3 ? 2 * chunks : (chunks + 1) / 2 * 2; };
+    for (int i = barriers(n); i < barriers(per_group); ++i) __builtin_amdgcn_s_barrier();
+    constexpr int Q = RT / 2 * 2 * 4;  // 16-byte quarters of the sums that a lane gives away
+    f32x4* const out = red + (size_t)all * Q * 64 + lane;
+    const f32x4* const in = red + (size_t)(all ^ 4) * Q * 64 + lane;
 #pragma unroll
-  for (int t = 0; t < RT; ++t) {
-    const int row = c.r0 + 32 * t + col;
+    for (int t = 0; t < RT / 2; ++t)
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          f32x4 v;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) v[i] = grp ? acc[t][u][4 * g + i] : acc[RT / 2 + t][u][4 * g + i];
+          out[((t * 2 + u) * 4 + g) * 64] = v;
+        }
+    __syncthreads();
+#pragma unroll
+    for (int t = 0; t < RT / 2; ++t)
+#pragma unroll
+      for (int u = 0; u < 2; ++u)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const f32x4 v = in[((t * 2 + u) * 4 + g) * 64];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) acc[t][u][4 * g + i] = (grp ? acc[RT / 2 + t][u][4 * g + i] : acc[t][u][4 * g + i]) + v[i];
+        }
+    first = grp * (RT / 2);
+  }
+#pragma unroll
+  for (int t = 0; t < RT / KS; ++t) {
+    const int row = c.r0 + 32 * (first + t) + col;
     const bool on = row < c.s1;
     if constexpr (is_swiglu(EPI)) {
       const int I = p.N / 2;
@@ -676,7 +720,16 @@ __global__ __launch_bounds__(256, TM == 128 ? 2 : 3) void mx_tile_kernel(MxK p, 
   constexpr int X = TM * 8;
   __shared__ u32x4 x0[X], x1[X];
   __shared__ uint32_t s0[256], s1[256];
-  mx_tile_body<AF, EPI, TM>(p, n_nb, x0, x1, s0, s1);
+  mx_tile_body<AF, EPI, TM, 1>(p, n_nb, x0, x1, s0, s1, nullptr);
+}
+// Two groups of four wavefronts, each with stages of its own, take half of K each
+// (K > 256): alone on its CU, a workgroup waits for loads most of the time.
+template <int AF, int EPI>
+__global__ __launch_bounds__(512, 2) void mx_tile_split_kernel(MxK p, int n_nb) {
+  __shared__ u32x4 x0[2 * 64 * 8], x1[2 * 64 * 8];
+  __shared__ uint32_t s0[512], s1[512];
+  __shared__ f32x4 red[8 * 8 * 64];
+  mx_tile_body<AF, EPI, 64, 2>(p, n_nb, x0, x1, s0, s1, red);
 }
 
 template <int AF, int EPI>
@@ -690,20 +743,26 @@ int launch_small(const MxK& k, hipStream_t s) {
   return (int)hipGetLastError();
 }
 template <int AF, int EPI, int TM>
-int launch_tile(const MxK& k, hipStream_t s) {
+int launch_tile(const MxK& k, bool split, hipStream_t s) {
   const int NT = k.N / 32;
   const int n_nb = is_swiglu(EPI) ? (NT / 2 + 3) / 4 : (NT + 7) / 8;
   // upper bound of the row tiles: one partial tile per segment that has rows
   const int64_t tiles = (int64_t)k.M_total / TM + (k.E < k.M_total ? k.E : k.M_total);
   const int64_t wgs = (tiles * n_nb + 7) / 8 * 8;
   if (wgs >= ((int64_t)1 << 24)) return (int)hipErrorInvalidConfiguration;
+  if constexpr (TM == 64) {
+    if (split) {
+      hipLaunchKernelGGL((mx_tile_split_kernel<AF, EPI>), dim3((unsigned)wgs), dim3(512), 0, s, k, n_nb);
+      return (int)hipGetLastError();
+    }
+  }
   hipLaunchKernelGGL((mx_tile_kernel<AF, EPI, TM>), dim3((unsigned)wgs), dim3(256), 0, s, k, n_nb);
   return (int)hipGetLastError();
 }
 template <int AF, int EPI>
 int launch_path(const MxK& k, int path, hipStream_t s) {
-  if (path == 64) return launch_tile<AF, EPI, 64>(k, s);
-  if (path == 128) return launch_tile<AF, EPI, 128>(k, s);
+  if (path == 64 || path == kMxSplit) return launch_tile<AF, EPI, 64>(k, path == kMxSplit, s);
+  if (path == 128) return launch_tile<AF, EPI, 128>(k, false, s);
   return launch_small<AF, EPI>(k, s);
 }
 template <int AF>

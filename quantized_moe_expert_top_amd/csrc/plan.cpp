@@ -159,15 +159,22 @@ size_t mx_layer_workspace_bytes(int T, int k, int E) {
 // are that close either is taken.  E.g. 8 experts of 2048 x 2048, us for
 // 32-row / 64-row / 128-row tiles: 6.5 / 9.8 / 14.1 at 16 rows per expert,
 // 17.9 / 11.2 / 14.6 at 128; 64 experts at 512 rows: 450 / 148 / 131.
+// 64-row tiles split K over two groups of wavefronts where K is long and every
+// workgroup has a CU of its own: 8 experts of 4096 x 14336, 32 rows each 52 -> 43
+// us, 16 of 448 x 4096, 256 rows 19.7 -> 17.3, 8 of 2048 x 2048, 192 rows 11.5 ->
+// 11.0; with 288 workgroups 15.9 -> 20.2, with K = 1024 6.8 -> 7.5.
 int mxgemm_path(int M_total, int E, int N, int K, int kernel) {
   if (kernel == 1) return 0;
-  if (kernel == 4) return 64;
-  if (kernel == 5) return 128;
   const double active = M_total < E ? M_total : E;  // experts that can have rows
   const double nt = N / 32.0;
+  const double blocks64 = (double)(int64_t)((nt + 7.0) / 8.0) * (M_total / 64.0 + 0.5 * active);
+  const int path64 = K >= 2048 && blocks64 <= 256.0 ? kMxSplit : 64;
+  if (kernel == 4) return 64;
+  if (kernel == 8) return kMxSplit;
+  if (kernel == 5) return 128;
   int best = 0;
   double least = 0.0;
-  const int rows[3] = {32, 64, 128}, path[3] = {0, 64, 128};
+  const int rows[3] = {32, 64, 128}, path[3] = {0, path64, 128};
   const double a[3] = {2.6, 2.7, 3.8}, b[3] = {1.2e-3, 3.0e-3, 4.8e-3}, c[3] = {1.71e-3, 4.0e-3, 6.9e-3},
                d[3] = {0.5, 0.5, 0.25};
   for (int i = 0; i < 3; ++i) {
