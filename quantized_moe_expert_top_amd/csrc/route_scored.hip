@@ -11,11 +11,14 @@
 //      compare and ballot per 64 experts and step); every expert within the
 //      margins of it can be among the first k and becomes a candidate;
 //   3. candidate i in lane i, in index order: its float64 score, its rank among
-//      the candidates, the weights of the first k.
+//      the candidates, the weights of the first k; four tokens' at a time by one
+//      wavefront of four.
 // Groups are chosen from the keys too, or from float64 scores where two group
 // scores at the border are within the margins.  Where the candidates exceed the
 // 64 lanes (many equal scores) the token takes float64 rounds over all experts.
-// Every way gives the same result.
+// Every way gives the same result.  8192 tokens of 64 experts take 5.6 us, 16384
+// of 256 in 8 groups 18, bound by instruction issue (steps 1 and 2); one token 2.7,
+// a chain of two loads and the float64 step.
 #include <float.h>
 
 #include <utility>
