@@ -265,8 +265,8 @@ __global__ __launch_bounds__(256, 3) void mx_small_kernel(MxK p) {
 // 2.5 PF (the clock under this load bounds it: registers alone reach 3.5); e2m1
 // rows 151 us, 3.65 PF (the loads' way through the caches; 158 us with stages of
 // 128 inputs, as their loads are under way only half as long).  512 tokens x 2 of 8
-// experts, 4096 x 14336, e2m1 rows: 73 us, of which 53 us are the weights' bytes
-// (79 us with stages of 128).
+// experts, 4096 x 14336, e2m1 rows: 74 us, of which 53 us are the weights' bytes
+// (79 us with stages of 128; 65 us with K split, below).
 //
 // Each XCD (workgroups are dealt to the 8 of them in turn) takes a contiguous
 // range of tiles, so that the weights and rows its CUs share stay in its L2.
@@ -616,31 +616,31 @@ __device__ __forceinline__ void mx_tile_body(const MxK& p, int n_nb, u32x4* x0, 
     // rounded up to even); then the groups exchange sums, each keeps half the rows.
     auto barriers = [](int chunks) { return AF == kE4M3 ? 2 * chunks : (chunks + 1) / 2 * 2; };
     for (int i = barriers(n); i < barriers(per_group); ++i) __builtin_amdgcn_s_barrier();
-    constexpr int Q = RT / 2 * 2 * 4;  // 16-byte quarters of the sums that a lane gives away
+    constexpr int Q = RT / 2 * 4;  // 16-byte quarters of the sums that a lane gives away at a time
     f32x4* const out = red + (size_t)all * Q * 64 + lane;
     const f32x4* const in = red + (size_t)(all ^ 4) * Q * 64 + lane;
 #pragma unroll
-    for (int t = 0; t < RT / 2; ++t)
+    for (int u = 0; u < 2; ++u) {
 #pragma unroll
-      for (int u = 0; u < 2; ++u)
+      for (int t = 0; t < RT / 2; ++t)
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
           f32x4 v;
 #pragma unroll
           for (int i = 0; i < 4; ++i) v[i] = grp ? acc[t][u][4 * g + i] : acc[RT / 2 + t][u][4 * g + i];
-          out[((t * 2 + u) * 4 + g) * 64] = v;
+          out[(t * 4 + g) * 64] = v;
         }
-    __syncthreads();
+      __syncthreads();
 #pragma unroll
-    for (int t = 0; t < RT / 2; ++t)
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
+      for (int t = 0; t < RT / 2; ++t)
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
-          const f32x4 v = in[((t * 2 + u) * 4 + g) * 64];
+          const f32x4 v = in[(t * 4 + g) * 64];
 #pragma unroll
           for (int i = 0; i < 4; ++i) acc[t][u][4 * g + i] = (grp ? acc[RT / 2 + t][u][4 * g + i] : acc[t][u][4 * g + i]) + v[i];
         }
+      if (u == 0) __syncthreads();
+    }
     first = grp * (RT / 2);
   }
 #pragma unroll
@@ -724,12 +724,13 @@ __global__ __launch_bounds__(256, TM == 128 ? 2 : 3) void mx_tile_kernel(MxK p, 
 }
 // Two groups of four wavefronts, each with stages of its own, take half of K each
 // (K > 256): alone on its CU, a workgroup waits for loads most of the time.
-template <int AF, int EPI>
+template <int AF, int EPI, int TM>
 __global__ __launch_bounds__(512, 2) void mx_tile_split_kernel(MxK p, int n_nb) {
-  __shared__ u32x4 x0[2 * 64 * 8], x1[2 * 64 * 8];
+  constexpr int X = 2 * TM * 8, R = TM / 64 * 8 * 4 * 64;
+  __shared__ u32x4 x0[X], x1[X];
   __shared__ uint32_t s0[512], s1[512];
-  __shared__ f32x4 red[8 * 8 * 64];
-  mx_tile_body<AF, EPI, 64, 2>(p, n_nb, x0, x1, s0, s1, red);
+  __shared__ f32x4 red[R];
+  mx_tile_body<AF, EPI, TM, 2>(p, n_nb, x0, x1, s0, s1, red);
 }
 
 template <int AF, int EPI>
@@ -750,9 +751,9 @@ int launch_tile(const MxK& k, bool split, hipStream_t s) {
   const int64_t tiles = (int64_t)k.M_total / TM + (k.E < k.M_total ? k.E : k.M_total);
   const int64_t wgs = (tiles * n_nb + 7) / 8 * 8;
   if (wgs >= ((int64_t)1 << 24)) return (int)hipErrorInvalidConfiguration;
-  if constexpr (TM == 64) {
+  if constexpr (TM == 64 || AF == kE2M1) {
     if (split) {
-      hipLaunchKernelGGL((mx_tile_split_kernel<AF, EPI>), dim3((unsigned)wgs), dim3(512), 0, s, k, n_nb);
+      hipLaunchKernelGGL((mx_tile_split_kernel<AF, EPI, TM>), dim3((unsigned)wgs), dim3(512), 0, s, k, n_nb);
       return (int)hipGetLastError();
     }
   }
@@ -762,7 +763,7 @@ int launch_tile(const MxK& k, bool split, hipStream_t s) {
 template <int AF, int EPI>
 int launch_path(const MxK& k, int path, hipStream_t s) {
   if (path == 64 || path == kMxSplit) return launch_tile<AF, EPI, 64>(k, path == kMxSplit, s);
-  if (path == 128) return launch_tile<AF, EPI, 128>(k, false, s);
+  if (path == 128 || path == kMxSplit128) return launch_tile<AF, EPI, 128>(k, path == kMxSplit128, s);
   return launch_small<AF, EPI>(k, s);
 }
 template <int AF>
@@ -787,7 +788,7 @@ int launch_mxgemm(const MxGemmArgs& a, void* stream) {
   const MxK k{a.wcodes, a.wscales, a.N, a.K, a.a, a.as, (uint32_t)(a.A_rows * row_codes),
               (uint32_t)((size_t)a.A_rows * (a.K / 32)), a.A_rows, a.gather, (uint32_t)((((uint64_t)1 << (31 + sh)) + div - 1) / div), sh, a.seg, a.E, a.M_total,
               a.out, a.out_scales};
-  const int path = mxgemm_path(a.M_total, a.E, a.N, a.K, a.kernel);
+  const int path = mxgemm_path(a.M_total, a.E, a.N, a.K, a.a_fmt == kE2M1, a.kernel);
   return a.a_fmt == kE4M3 ? launch_fmt<kE4M3>(k, a.epilogue, path, s) : launch_fmt<kE2M1>(k, a.epilogue, path, s);
 }
 

@@ -435,29 +435,32 @@ def test_product_sizes(kernel, act, E, N, K, counts):
     check_product(p, q.MOE_EPI_NONE, kernel, f"{act} {N}x{K} {counts}")
 
 
-@pytest.mark.parametrize("act", ["e4m3", "e2m1"])
+SPLIT = [("e4m3", q.MOE_KERNEL_TILE64_SPLIT_K), ("e2m1", q.MOE_KERNEL_TILE64_SPLIT_K), ("e2m1", q.MOE_KERNEL_TILE128_SPLIT_K)]
+
+
+@pytest.mark.parametrize("act,kernel", SPLIT)
 @pytest.mark.parametrize("epi", [q.MOE_EPI_NONE, q.MOE_EPI_SWIGLU, q.MOE_EPI_NONE_F32, q.MOE_EPI_NONE_F16,
                                  q.MOE_EPI_SWIGLU_E4M3, q.MOE_EPI_SWIGLU_E2M1])
 @pytest.mark.parametrize("K", [384, 512, 640, 2176, 2304, 2560, 4224])
-def test_product_long_k(act, epi, K):
-    """64-row tiles whose K is split over two groups of wavefronts: even, odd and half chunks of 256."""
+def test_product_long_k(act, kernel, epi, K):
+    """Tiles whose K is split over two groups of wavefronts: even, odd and half chunks of 256."""
     p = Product(K, 3, 320, K, act, [1, 0, 133], k=3)
-    check_product(p, epi, q.MOE_KERNEL_TILE64_SPLIT_K, f"{act} 320x{K}")
+    check_product(p, epi, kernel, f"{act} 320x{K}")
 
 
-@pytest.mark.parametrize("act", ["e4m3", "e2m1"])
-def test_product_long_k_other_rows_and_not_a_number(act):
+@pytest.mark.parametrize("act,kernel", SPLIT)
+def test_product_long_k_other_rows_and_not_a_number(act, kernel):
     p = Product(21, 2, 64, 2304, act, [70, 30], gather=False, lead=5)
     for row, block in ((8, 3), (70, 71)):
         p.A.scales[row, block] = 255
     out = torch.full((p.lead + p.M + 4, 64), 7.0, device=DEV)
     p.A = q.MxRows(torch.cat([p.A.codes] * 2), torch.cat([p.A.scales] * 2), p.A.fmt)
-    q.moe_grouped_mxgemm(p.tiled, p.A, dev(p.seg), out.shape[0], q.MOE_EPI_NONE_F32, out=out, kernel=q.MOE_KERNEL_TILE64_SPLIT_K)
+    q.moe_grouped_mxgemm(p.tiled, p.A, dev(p.seg), out.shape[0], q.MOE_EPI_NONE_F32, out=out, kernel=kernel)
     assert (out[:5] == 7).all() and (out[-4:] == 7).all()
     nan = torch.isnan(out).all(-1)
     assert nan[8] and nan[70] and int(nan.sum()) == 2 and int(torch.isnan(out).any(-1).sum()) == 2
     again = q.moe_grouped_mxgemm(p.tiled, p.A, dev(p.seg), out.shape[0], q.MOE_EPI_NONE_F32, out=torch.full_like(out, 7.0),
-                                 kernel=q.MOE_KERNEL_TILE64_SPLIT_K)
+                                 kernel=kernel)
     assert torch.equal(out.view(torch.int32), again.view(torch.int32))
 
 

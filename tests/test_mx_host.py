@@ -145,9 +145,10 @@ def test_grouped_mxgemm_validation(lib):
         d = d or mxdesc()
         return lib.moe_grouped_mxgemm(ctypes.byref(d), a, s, fmt, rows, gather, k, seg, M, epi, kernel, out, osc, None)
     assert gemm(mxdesc(q.MOE_LAYOUT_CANONICAL)) == gemm(mxdesc(version=2)) == gemm(fmt=0) == gemm(epi=6) == BAD_FORMAT
-    assert gemm(epi=-1) == gemm(kernel=9) == gemm(kernel=-1) == BAD_FORMAT
+    assert gemm(epi=-1) == gemm(kernel=10) == gemm(kernel=-1) == BAD_FORMAT
     assert gemm(kernel=q.MOE_KERNEL_LDS_DMA) == gemm(kernel=q.MOE_KERNEL_SMALL_PER_WIDTH) == UNSUPPORTED
     assert gemm(kernel=q.MOE_KERNEL_TILE64_SPLIT_K) == UNSUPPORTED              # K = 256
+    assert gemm(mxdesc(K=512), kernel=q.MOE_KERNEL_TILE128_SPLIT_K) == UNSUPPORTED  # e4m3 rows
     assert gemm(mxdesc(N=96), epi=q.MOE_EPI_SWIGLU) == gemm(mxdesc(N=48)) == gemm(mxdesc(K=160)) == UNSUPPORTED
     assert gemm(M=-1) == gemm(rows=-1) == gemm(k=0) == gemm(rows=63) == gemm(gather=None, rows=127) == BAD_SHAPE
     assert gemm(out=A) == BAD_SHAPE                                             # in place
@@ -176,7 +177,7 @@ def test_mx_layer_validation(lib):
         return lib.moe_mx_layer(ctypes.byref(layer), None)
     assert lib.moe_mx_layer(None, None) == NULL_ARG
     assert call(abi_version=2) == call(x_dtype=5) == call(x_fmt=0) == call(h_fmt=3) == call(y_dtype=3) == BAD_FORMAT
-    assert call(score=2) == call(kernel=9) == BAD_FORMAT
+    assert call(score=2) == call(kernel=10) == BAD_FORMAT
     assert call(kernel=6) == call(kernel=q.MOE_KERNEL_TILE64_SPLIT_K) == UNSUPPORTED  # I = 256
     assert call(I=320) == call(E_down=5) == call(N_down=256) == BAD_SHAPE            # the two products do not fit
     assert call(T=-1) == call(k=5) == call(n_group=3) == call(scale=float("nan")) == BAD_SHAPE
