@@ -153,12 +153,13 @@ size_t mx_layer_workspace_bytes(int T, int k, int E) {
 // LDS-staged tiles of that many rows.  AUTO takes the least of three estimates
 //     a + K * max(b, c * (workgroups / 256 + d))      (microseconds)
 // a: launch and set-up, b: one workgroup alone on its CU, c: a CU's throughput,
-// d: its last workgroups running alone.  Fitted to 98 measured problems (E 8 to
-// 64, 4 to 512 rows per expert, N 448 to 4096, K 512 to 8192, 8- and 4-bit
+// d: its last workgroups running alone.  Fitted to 346 measured problems (E 8 to
+// 64, 1 to 1024 rows per expert, N 448 to 28672, K 512 to 14336, 8- and 4-bit
 // rows); the estimates are within about 20 % of the times, and where two paths
-// are that close either is taken.  E.g. 8 experts of 2048 x 2048, us for
-// 32-row / 64-row / 128-row tiles: 6.5 / 9.8 / 14.1 at 16 rows per expert,
-// 17.9 / 11.2 / 14.6 at 128; 64 experts at 512 rows: 450 / 148 / 131.
+// are that close either is taken: on average 1.3 % above the better.  E.g. 8
+// experts of 2048 x 2048, us for 32-row / 64-row / 128-row tiles: 6.5 / 9.8 / 10.0 at
+// 16 rows per expert, 17.9 / 11.2 / 14.6 at 128; 64 experts at 512 rows: 450 / 148 /
+// 131.
 // 64-row tiles split K over two groups of wavefronts where K is long and every
 // workgroup has a CU of its own: 8 experts of 4096 x 14336, 32 rows each 52 -> 43
 // us, 16 of 448 x 4096, 256 rows 19.7 -> 17.3, 8 of 2048 x 2048, 192 rows 11.5 ->
@@ -180,11 +181,13 @@ int mxgemm_path(int M_total, int E, int N, int K, bool e2m1, int kernel) {
   int best = 0;
   double least = 0.0;
   const int rows[3] = {32, 64, 128}, path[3] = {0, path64, path128};
-  const double a[3] = {2.6, 2.7, 3.8}, b[3] = {1.2e-3, 3.0e-3, 4.8e-3}, c[3] = {1.71e-3, 4.0e-3, 6.9e-3},
-               d[3] = {0.5, 0.5, 0.25};
+  const double a[3] = {2.6, 2.7, 3.8}, b[3] = {1.2e-3, 3.0e-3, 3.0e-3}, c[3] = {1.71e-3, 4.0e-3, 6.9e-3},
+               d[3] = {0.5, 0.5, 0.4};
+  // the partial tile per expert, and its least work: fewer rows take a smaller body
+  const double partial[3] = {0.5, 0.4, 0.125}, fewest[3] = {1.0, 1.0, 0.5};
   for (int i = 0; i < 3; ++i) {
-    double tiles = (double)M_total / rows[i] + 0.5 * active;  // a partial tile per expert
-    if (tiles < active) tiles = active;
+    double tiles = (double)M_total / rows[i] + partial[i] * active;
+    if (tiles < fewest[i] * active) tiles = fewest[i] * active;
     const double wide = i == 0 ? 2.0 : 8.0;  // channel tiles of a workgroup
     const double blocks = (nt + wide - 1.0) / wide;
     // 32-row tiles read only the rows there are

@@ -435,6 +435,16 @@ def test_product_sizes(kernel, act, E, N, K, counts):
     check_product(p, q.MOE_EPI_NONE, kernel, f"{act} {N}x{K} {counts}")
 
 
+@pytest.mark.parametrize("kernel", KERNELS)
+@pytest.mark.parametrize("act", ["e4m3", "e2m1"])
+@pytest.mark.parametrize("epi", [q.MOE_EPI_NONE_F32, q.MOE_EPI_SWIGLU_E4M3])
+@pytest.mark.parametrize("K", [128, 640])
+def test_product_last_rows(kernel, act, epi, K):
+    """Segments whose last tile holds up to a quarter, a half, three quarters and all of its rows."""
+    p = Product(K + 7, 10, 64, K, act, [32, 33, 64, 65, 96, 97, 160, 161, 224, 225], k=2)
+    check_product(p, epi, kernel, f"{act} 64x{K}")
+
+
 SPLIT = [("e4m3", q.MOE_KERNEL_TILE64_SPLIT_K), ("e2m1", q.MOE_KERNEL_TILE64_SPLIT_K), ("e2m1", q.MOE_KERNEL_TILE128_SPLIT_K)]
 
 
