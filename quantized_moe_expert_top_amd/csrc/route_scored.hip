@@ -211,6 +211,7 @@ constexpr int kSpare = 6;  // candidates beyond k that cost less than another st
 // SOFT_ALL: the softmax denominator is needed (a bias, weights that are not
 // renormalised, sums of two scores per group): float64 exponentials of all
 // experts give it and the keys.
+//
 // The first two steps for token t by this wavefront: the number of candidates,
 // listed at the start of buf (64 * NS doubles of LDS of the wavefront's own); or
 // -1 where they exceed the lanes and the token was settled over all experts.
@@ -442,10 +443,15 @@ __device__ __forceinline__ double row_value(double v) {  // of lane J of the row
   const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(u >> 32), 0x150 + J, 0xF, 0xF, true);
   return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
 }
+template <int J>
+__device__ __forceinline__ int row_before(double c, int i) {  // whether lane J's candidate precedes this one
+  const double v = row_value<J>(c);  // by all lanes, outside any condition
+  return (int)(v > c) | ((int)(v == c) & (int)(J < i));
+}
 template <int... J>
 __device__ __forceinline__ int row_rank(std::integer_sequence<int, J...>, double c, int i) {
   int rank = 0;
-  ((rank += (row_value<J>(c) > c || (row_value<J>(c) == c && J < i)) ? 1 : 0), ...);
+  ((rank += row_before<J>(c, i)), ...);
   return rank;
 }
 template <int... J>
