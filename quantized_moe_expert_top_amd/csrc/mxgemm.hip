@@ -263,10 +263,9 @@ __global__ __launch_bounds__(256, 3) void mx_small_kernel(MxK p) {
 //
 // Measured, 65536 rows over 64 experts of 2048 x 2048, SwiGLU: e4m3 rows 217 us,
 // 2.5 PF (the clock under this load bounds it: registers alone reach 3.5); e2m1
-// rows 151 us, 3.65 PF (the loads' way through the caches; 158 us with stages of
+// rows 147 us, 3.7 PF (the loads' way through the caches; 158 us with stages of
 // 128 inputs, as their loads are under way only half as long).  512 tokens x 2 of 8
-// experts, 4096 x 14336, e2m1 rows: 74 us, of which 53 us are the weights' bytes
-// (79 us with stages of 128; 65 us with K split, below).
+// experts, 4096 x 14336, e2m1 rows: 66 us, of which 53 us are the weights' bytes.
 //
 // Each XCD (workgroups are dealt to the 8 of them in turn) takes a contiguous
 // range of tiles, so that the weights and rows its CUs share stay in its L2.
@@ -477,9 +476,13 @@ __device__ __forceinline__ void mx_tile_body(const MxK& p, const Tile& c, u32x4*
   f32x16 acc[RT][2];
   Frag f[RT];
   // Step j of a chunk: multiplies f and replaces it, row tile by row tile, with
-  // the next step's fragments (of stage xs; not after the last).
+  // the next step's fragments (of stage xs; not after the last).  128-row tiles at
+  // raised priority, which also keeps the compiler from moving loads into it: 512
+  // tokens x 2 of 8 experts, 4096 x 14336, e2m1 rows 74 -> 66 us, 65536 rows 152 ->
+  // 147, e4m3 rows 1 % less; 64-row tiles take 5 % longer with it.
   auto step = [&](auto j_tag, const Scales& sc, const RowScales& xsc, auto first_tag, const u32x4* xs, auto next_tag) {
     constexpr int J = decltype(j_tag)::value, S = J % SS;
+    if constexpr (TM == 128) __builtin_amdgcn_s_setprio(1);
 #pragma unroll
     for (int t = 0; t < RT; ++t) {
       i32x8 xf;
@@ -492,6 +495,7 @@ __device__ __forceinline__ void mx_tile_body(const MxK& p, const Tile& c, u32x4*
       }
       if constexpr (decltype(next_tag)::value) f[t] = read(xs, (S + 1) % SS, t);
     }
+    if constexpr (TM == 128) __builtin_amdgcn_s_setprio(0);
   };
   const std::integral_constant<int, 0> zero{};
   const std::integral_constant<int, 1> one{};
@@ -747,16 +751,15 @@ __global__ __launch_bounds__(256, TM == 128 ? 2 : 3) void mx_tile_kernel(MxK p, 
 }
 // Two groups of four wavefronts, each with stages of its own, take half of K each
 // (K > 256): alone on its CU, a workgroup waits for loads most of the time.
-template <int AF, int EPI, int TM>
+template <int AF, int EPI>
 __global__ __launch_bounds__(512, 2) void mx_tile_split_kernel(MxK p, int n_nb) {
 #ifdef __HIP_DEVICE_COMPILE__
-  constexpr int X = 2 * TM * 8, X0 = X > 8 * kEpiChunks ? X : 8 * kEpiChunks, R = TM / 64 * 8 * 4 * 64;
-  __shared__ u32x4 x0[X0], x1[X];
+  __shared__ u32x4 x0[8 * kEpiChunks], x1[2 * 64 * 8];
   __shared__ uint32_t s0[512], s1[512];
-  __shared__ f32x4 red[R];
+  __shared__ f32x4 red[8 * 4 * 64];
   Tile c;
-  if (!own_tile<TM>(p, n_nb, c)) return;
-  mx_tile_body<AF, EPI, TM, 2>(p, c, x0, x1, s0, s1, red);
+  if (!own_tile<64>(p, n_nb, c)) return;
+  mx_tile_body<AF, EPI, 64, 2>(p, c, x0, x1, s0, s1, red);
 #endif
 }
 
@@ -778,9 +781,9 @@ int launch_tile(const MxK& k, bool split, hipStream_t s) {
   const int64_t tiles = (int64_t)k.M_total / TM + (k.E < k.M_total ? k.E : k.M_total);
   const int64_t wgs = (tiles * n_nb + 7) / 8 * 8;
   if (wgs >= ((int64_t)1 << 24)) return (int)hipErrorInvalidConfiguration;
-  if constexpr (TM == 64 || AF == kE2M1) {
+  if constexpr (TM == 64) {
     if (split) {
-      hipLaunchKernelGGL((mx_tile_split_kernel<AF, EPI, TM>), dim3((unsigned)wgs), dim3(512), 0, s, k, n_nb);
+      hipLaunchKernelGGL((mx_tile_split_kernel<AF, EPI>), dim3((unsigned)wgs), dim3(512), 0, s, k, n_nb);
       return (int)hipGetLastError();
     }
   }
@@ -790,7 +793,7 @@ int launch_tile(const MxK& k, bool split, hipStream_t s) {
 template <int AF, int EPI>
 int launch_path(const MxK& k, int path, hipStream_t s) {
   if (path == 64 || path == kMxSplit) return launch_tile<AF, EPI, 64>(k, path == kMxSplit, s);
-  if (path == 128 || path == kMxSplit128) return launch_tile<AF, EPI, 128>(k, path == kMxSplit128, s);
+  if (path == 128) return launch_tile<AF, EPI, 128>(k, false, s);
   return launch_small<AF, EPI>(k, s);
 }
 template <int AF>
@@ -815,7 +818,7 @@ int launch_mxgemm(const MxGemmArgs& a, void* stream) {
   const MxK k{a.wcodes, a.wscales, a.N, a.K, a.a, a.as, (uint32_t)(a.A_rows * row_codes),
               (uint32_t)((size_t)a.A_rows * (a.K / 32)), a.A_rows, a.gather, (uint32_t)((((uint64_t)1 << (31 + sh)) + div - 1) / div), sh, a.seg, a.E, a.M_total,
               a.out, a.out_scales};
-  const int path = mxgemm_path(a.M_total, a.E, a.N, a.K, a.a_fmt == kE2M1, a.kernel);
+  const int path = mxgemm_path(a.M_total, a.E, a.N, a.K, a.kernel);
   return a.a_fmt == kE4M3 ? launch_fmt<kE4M3>(k, a.epilogue, path, s) : launch_fmt<kE2M1>(k, a.epilogue, path, s);
 }
 

@@ -163,24 +163,19 @@ size_t mx_layer_workspace_bytes(int T, int k, int E) {
 // 64-row tiles split K over two groups of wavefronts where K is long and every
 // workgroup has a CU of its own: 8 experts of 4096 x 14336, 32 rows each 52 -> 43
 // us, 16 of 448 x 4096, 256 rows 19.7 -> 17.3, 8 of 2048 x 2048, 192 rows 11.5 ->
-// 11.0; with 288 workgroups 15.9 -> 20.2, with K = 1024 6.8 -> 7.5.  128-row tiles
-// do so with e2m1 rows, which multiply in half the time, so that waiting is more of it:
-// 8 of 4096 x 14336, 128 rows each 74 -> 65 us, 192 rows 77 -> 66; 8 of 2048 x 2048,
-// 256 rows 13.0 -> 13.0; e4m3 rows 0.97 to 1.1 of the time without.
-int mxgemm_path(int M_total, int E, int N, int K, bool e2m1, int kernel) {
+// 11.0; with 288 workgroups 15.9 -> 20.2, with K = 1024 6.8 -> 7.5.
+int mxgemm_path(int M_total, int E, int N, int K, int kernel) {
   if (kernel == 1) return 0;
   const double active = M_total < E ? M_total : E;  // experts that can have rows
   const double nt = N / 32.0;
   const double wide_blocks = (double)(int64_t)((nt + 7.0) / 8.0);
   const int path64 = K >= 2048 && wide_blocks * (M_total / 64.0 + 0.5 * active) <= 256.0 ? kMxSplit : 64;
-  const int path128 = e2m1 && K >= 4096 && wide_blocks * (M_total / 128.0 + 0.5 * active) <= 256.0 ? kMxSplit128 : 128;
   if (kernel == 4) return 64;
   if (kernel == 8) return kMxSplit;
   if (kernel == 5) return 128;
-  if (kernel == 9) return kMxSplit128;
   int best = 0;
   double least = 0.0;
-  const int rows[3] = {32, 64, 128}, path[3] = {0, path64, path128};
+  const int rows[3] = {32, 64, 128}, path[3] = {0, path64, 128};
   const double a[3] = {2.6, 2.7, 3.8}, b[3] = {1.2e-3, 3.0e-3, 3.0e-3}, c[3] = {1.71e-3, 4.0e-3, 6.9e-3},
                d[3] = {0.5, 0.5, 0.4};
   // the partial tile per expert, and its least work: fewer rows take a smaller body

@@ -173,13 +173,11 @@ int main() {
     for (int E : {1, 8, 1024})
       for (int N : {32, 512, 1 << 20})
         for (int K : {128, 256, 512, 4096, 1 << 20})
-          for (int kernel : {0, 1, 4, 5, 8, 9})
-            for (bool e2m1 : {false, true}) {
-              const int path = moe::mxgemm_path(M, E, N, K, e2m1, kernel);
-              CHECK(path == 0 || path == 64 || path == 128 || path == moe::kMxSplit || path == moe::kMxSplit128);
-              CHECK(kernel != 0 || (path != moe::kMxSplit && path != moe::kMxSplit128) || K > 256);
-              CHECK(kernel != 0 || path != moe::kMxSplit128 || e2m1);
-            }
+          for (int kernel : {0, 1, 4, 5, 8}) {
+            const int path = moe::mxgemm_path(M, E, N, K, kernel);
+            CHECK(path == 0 || path == 64 || path == 128 || path == moe::kMxSplit);
+            CHECK(kernel != 0 || path != moe::kMxSplit || K > 256);
+          }
   const moe_mxdesc wide = desc(MOE_LAYOUT_CANONICAL, 1024, 32, 384, 0x30000);
   CHECK(moe_mx_field_bytes(&wide, MOE_FIELD_CODES) == (size_t)1024 * 32 * 192);
   const moe_mxdesc tiled = desc(MOE_LAYOUT_TILED, 1024, 32, 384, 0x40000);

@@ -445,7 +445,7 @@ def test_product_last_rows(kernel, act, epi, K):
     check_product(p, epi, kernel, f"{act} 64x{K}")
 
 
-SPLIT = [("e4m3", q.MOE_KERNEL_TILE64_SPLIT_K), ("e2m1", q.MOE_KERNEL_TILE64_SPLIT_K), ("e2m1", q.MOE_KERNEL_TILE128_SPLIT_K)]
+SPLIT = [("e4m3", q.MOE_KERNEL_TILE64_SPLIT_K), ("e2m1", q.MOE_KERNEL_TILE64_SPLIT_K)]
 
 
 @pytest.mark.parametrize("act,kernel", SPLIT)
