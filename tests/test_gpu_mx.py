@@ -633,10 +633,67 @@ def test_layer_call_equals_its_parts(T, E, k, given, dt):
             assert torch.equal(buf.x.codes, rows.codes) and torch.equal(buf.x.scales, rows.scales)
 
 
-def test_layer_captured_and_on_other_streams():
+@pytest.mark.parametrize("y_dtype,epi", [(torch.float32, q.MOE_EPI_NONE_F32), (torch.bfloat16, q.MOE_EPI_NONE),
+                                         (torch.float16, q.MOE_EPI_NONE_F16)])
+@pytest.mark.parametrize("kernel", KERNELS + [q.MOE_KERNEL_TILE64_SPLIT_K])
+@pytest.mark.parametrize("h_fmt", [q.MOE_MX_E4M3, q.MOE_MX_E2M1])
+def test_layer_choices(y_dtype, epi, kernel, h_fmt):
+    """Expert outputs of every type, hidden rows of either format, every kernel: the parts' bits."""
+    E, H, I, k, T = 6, 384, 512, 3, 70
+    g = torch.Generator(device=DEV).manual_seed(3)
+    r = lambda *s: torch.randn(*s, device=DEV, generator=g)  # noqa: E731
+    gu = q.moe_mx_repack(q.mx_experts(q.moe_quantize_mx(r(E, 2 * I, H), q.MOE_MX_E2M1)))
+    dn = q.moe_mx_repack(q.mx_experts(q.moe_quantize_mx(r(E, H, I) / 20, q.MOE_MX_E2M1)))
+    x, logits = r(T, H).half(), r(T, E)
+    show("layer choices", y_dtype, kernel, h_fmt)
+    buf = q.alloc_mx_layer(T, E, k, H, I, DEV, h_fmt=h_fmt, y_dtype=y_dtype)
+    q.moe_mx_layer_forward(x, logits, k, gu, dn, buf=buf, kernel=kernel)
+    ids, w = q.moe_route_scored(logits, k)
+    p = q.moe_permute(ids, E)
+    h = q.moe_grouped_mxgemm(gu, q.moe_quantize_mx(x), p.seg_offsets, T * k,
+                             q.MOE_EPI_SWIGLU_E4M3 if h_fmt == q.MOE_MX_E4M3 else q.MOE_EPI_SWIGLU_E2M1,
+                             gather_pair=p.sorted_pair, k=k, kernel=kernel)
+    y = q.moe_grouped_mxgemm(dn, h, p.seg_offsets, T * k, epi, kernel=kernel)
+    assert y.dtype == y_dtype and torch.equal(buf.y_perm, y) and torch.equal(buf.h.codes, h.codes)
+    assert torch.equal(buf.out, q.moe_unpermute_combine(y, p.pair_pos, w, T, k, n_valid=p.seg_offsets[-1:]))
+
+
+def test_layers_at_once():
+    """Two layers on two streams, and the same layer from two threads with buffers of their own: the bits of calls
+    one after another."""
+    import threading
+    E, H, I, k, T = 8, 256, 384, 2, 300
+    g = torch.Generator(device=DEV).manual_seed(8)
+    r = lambda *s: torch.randn(*s, device=DEV, generator=g)  # noqa: E731
+    gu = q.moe_mx_repack(q.mx_experts(q.moe_quantize_mx(r(E, 2 * I, H), q.MOE_MX_E2M1)))
+    dn = q.moe_mx_repack(q.mx_experts(q.moe_quantize_mx(r(E, H, I), q.MOE_MX_E2M1)))
+    x, logits = [r(T, H).bfloat16() for _ in range(2)], [r(T, E) for _ in range(2)]
+    want = [q.moe_mx_layer_forward(x[i], logits[i], k, gu, dn).out for i in range(2)]
+    bufs = [q.alloc_mx_layer(T, E, k, H, I, DEV) for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+
+    def work(i):
+        for _ in range(20):
+            q.moe_mx_layer_forward(x[i], logits[i], k, gu, dn, buf=bufs[i], stream=streams[i])
+    for how in ("streams", "threads"):
+        for b in bufs:
+            b.out.zero_()
+        torch.cuda.synchronize()
+        if how == "streams":
+            work(0), work(1)
+        else:
+            ts = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+            [t.start() for t in ts], [t.join() for t in ts]
+        torch.cuda.synchronize()
+        assert torch.equal(bufs[0].out, want[0]) and torch.equal(bufs[1].out, want[1]), how
+
+
+@pytest.mark.parametrize("T", [8, 24, 3000])
+def test_layer_captured_and_on_other_streams(T):
     """The run of operators captured into a graph, replayed on new inputs with eager work between the replays, and
     issued on a side stream: the eager bits each time."""
-    E, H, I, k, T = 8, 256, 256, 2, 24
+    E, H, I, k = 8, 256, 256, 2
     gu = q.moe_mx_repack(q.mx_experts(q.moe_quantize_mx(torch.randn(E, 2 * I, H, device=DEV), q.MOE_MX_E2M1)))
     dn = q.moe_mx_repack(q.mx_experts(q.moe_quantize_mx(torch.randn(E, H, I, device=DEV), q.MOE_MX_E2M1)))
     wn = torch.ones(H, device=DEV).bfloat16()
