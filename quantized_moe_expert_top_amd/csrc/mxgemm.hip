@@ -83,11 +83,12 @@ __device__ __forceinline__ int source_row(const MxK& p, int row) {
 // -------------------------------------------------------- few rows per expert
 // A workgroup takes 64 output channels of one expert (SwiGLU: 32 gate and the
 // matching 32 up channels) and 32 of the expert's rows (every gridDim.z-th
-// group of 32); its NW wavefronts split K and add their sums through LDS.  Weights and activations
-// go from memory straight to the operand registers: each weight byte is read
-// once per 32 rows.  Bound by the weights' bytes (141 MB of 64 experts of 2048 x
-// 2048 touched by 256 pairs: 22 us from memory) and, with few workgroups, by the
-// latency of a wavefront's K / 4 range: 6.5 us for 8 experts of 2048 x 2048.
+// group of 32); its NW wavefronts split K and add their sums through LDS.  Weights
+// and activations go from memory straight to the operand registers: each weight
+// byte is read once per 32 rows.  Bound by the weights' bytes (8 experts of 4096 x
+// 14336, 32 rows in all: 249 MB in 45 us, 5.5 TB/s with what the 256 MB cache still
+// holds) and, with few workgroups, by the latency of a wavefront's K / 4 range:
+// 6.5 us for 8 experts of 2048 x 2048.
 template <int AF>
 struct SmallBlock {  // operands of one K block of 128
   u32x4 w[2][2];     // [channel tile][step]
@@ -768,7 +769,7 @@ int launch_small(const MxK& k, hipStream_t s) {
   const int NT = k.N / 32;
   // one workgroup per 32 rows up to twice the mean rows of an expert; fuller
   // experts' workgroups go round
-  const int gz = (2 * (k.M_total / k.E) + 31) / 32;
+  const int gz = (k.M_total / k.E - 1) / 16 + 1;
   const dim3 grid(is_swiglu(EPI) ? NT / 2 : (NT + 1) / 2, k.E, gz < 1 ? 1 : gz > 64 ? 64 : gz);
   hipLaunchKernelGGL((mx_small_kernel<AF, EPI>), grid, dim3(256), 0, s, k);
   return (int)hipGetLastError();
@@ -780,7 +781,7 @@ int launch_tile(const MxK& k, bool split, hipStream_t s) {
   // upper bound of the row tiles: one partial tile per segment that has rows
   const int64_t tiles = (int64_t)k.M_total / TM + (k.E < k.M_total ? k.E : k.M_total);
   const int64_t wgs = (tiles * n_nb + 7) / 8 * 8;
-  if (wgs >= ((int64_t)1 << 24)) return (int)hipErrorInvalidConfiguration;
+  if (wgs >= ((int64_t)1 << 23)) return (int)hipErrorInvalidConfiguration;  // 2^32 threads in 512s
   if constexpr (TM == 64) {
     if (split) {
       hipLaunchKernelGGL((mx_tile_split_kernel<AF, EPI>), dim3((unsigned)wgs), dim3(512), 0, s, k, n_nb);
