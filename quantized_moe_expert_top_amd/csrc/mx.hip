@@ -115,10 +115,10 @@ __device__ __forceinline__ float round_to(float f) {
 }
 
 template <int DT, int FMT, int TPR, int NV>
-__global__ __launch_bounds__(kThreads) void rmsnorm_mx_kernel(NormArgs a) {
+__global__ __launch_bounds__(TPR > kThreads ? TPR : kThreads) void rmsnorm_mx_kernel(NormArgs a) {
 #pragma clang fp contract(off)  // hi + lo below must not become m * fhi + lo
-  constexpr int kRows = kThreads / TPR, kWaves = TPR / 64;
-  __shared__ double part[kThreads / 64];
+  constexpr int kRows = TPR > kThreads ? 1 : kThreads / TPR, kWaves = TPR / 64;
+  __shared__ double part[kRows * kWaves];
   const int sub = threadIdx.x / TPR, t = threadIdx.x % TPR;
   const size_t row = (size_t)blockIdx.x * kRows + sub;
   const bool live = row < (size_t)a.rows;
@@ -219,15 +219,23 @@ inline unsigned blocks_for(size_t n, size_t per) { return (unsigned)((n + per - 
 template <int DT, int FMT>
 void norm_rows(const NormArgs& a, hipStream_t s) {
   // Threads per row: the whole workgroup for a wide row (8 values per thread
-  // and step), one wavefront for narrow ones.
-#define MOE_NORM(TPR, NV)                                                                                    \
-  hipLaunchKernelGGL((rmsnorm_mx_kernel<DT, FMT, TPR, NV>), dim3(blocks_for(a.rows, kThreads / TPR)),        \
-                     dim3(kThreads), 0, s, a)
+  // and step), one wavefront for narrow ones.  Few rows leave the chip empty and
+  // wait for one row's chain of additions: 8 values per thread.  Rows of 4096 /
+  // 8192 bf16 in us, with more threads / fewer: 3.4 / 4.0 and 4.5 / 5.9 (64 rows),
+  // 5.1 / 5.2 and 8.3 / 8.3 (512), 13.9 / 13.1 and 24.1 / 20.6 (2048); rows of
+  // 16384 6.3 / 9.8 (64), 39.0 / 37.9 (2048), 161 / 182 (8192).
+  const bool few = a.rows <= 512;
+#define MOE_NORM(TPR, NV)                                                                                  \
+  hipLaunchKernelGGL((rmsnorm_mx_kernel<DT, FMT, TPR, NV>),                                                \
+                     dim3(blocks_for(a.rows, TPR > kThreads ? 1 : kThreads / TPR)),                        \
+                     dim3(TPR > kThreads ? TPR : kThreads), 0, s, a)
   if (a.H <= 512) MOE_NORM(64, 1);
   else if (a.H <= 2048) MOE_NORM(256, 1);
+  else if (a.H <= 4096 && few) MOE_NORM(512, 1);
   else if (a.H <= 4096) MOE_NORM(256, 2);
+  else if (a.H <= 8192 && few) MOE_NORM(1024, 1);
   else if (a.H <= 8192) MOE_NORM(256, 4);
-  else MOE_NORM(256, 8);
+  else MOE_NORM(1024, 2);
 #undef MOE_NORM
 }
 template <int DT>

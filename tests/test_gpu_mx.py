@@ -210,7 +210,8 @@ def check_mx_near(got, ref, tol, F, what):
     close(got, ref, np.maximum(rel * np.abs(ref), least * np.exp2(p + 1.0)) + 1.5 * tol, what)
 
 
-@pytest.mark.parametrize("rows,H", [(1, 32), (7, 96), (5, 512), (3, 544), (33, 2048), (2, 4096), (3, 8160), (2, 16384)])
+@pytest.mark.parametrize("rows,H", [(1, 32), (7, 96), (5, 512), (3, 544), (33, 2048), (2, 4096), (3, 8160), (2, 16384),
+                                    (513, 2080), (520, 4096), (515, 5120), (514, 8192)])
 @pytest.mark.parametrize("dt", ["bf16", "fp16", "fp32"])
 @pytest.mark.parametrize("fmt", ["e4m3", "e2m1"])
 def test_rmsnorm(rows, H, dt, fmt):
