@@ -257,9 +257,9 @@ __global__ __launch_bounds__(256, 3) void mx_small_kernel(MxK p) {
 // A workgroup of 4 wavefronts takes TM rows of one expert and 8 channel tiles
 // (256 channels; SwiGLU: 128 gate and the matching 128 up channels), a
 // wavefront all TM rows and 2 of the tiles (a gate and its up tile).  Rows and
-// their scales go through two LDS stages of 128 bytes a row (128 inputs of e4m3,
-// 256 of e2m1) filled by LDS-DMA and shared by the wavefronts; weights, which only
-// one wavefront uses, straight into its registers.  Workgroups share a CU (2 of
+// their scales go through two LDS stages of 256 inputs (128 of e4m3 rows in
+// 128-row tiles) filled by LDS-DMA and shared by the wavefronts; weights, which
+// only one wavefront uses, straight into its registers.  Workgroups share a CU (2 of
 // 128 rows, 3 of 64), so one multiplies while another waits at its barrier.
 //
 // Measured, 65536 rows over 64 experts of 2048 x 2048, SwiGLU: e4m3 rows 217 us,
@@ -267,6 +267,9 @@ __global__ __launch_bounds__(256, 3) void mx_small_kernel(MxK p) {
 // rows 147 us, 3.7 PF (the loads' way through the caches; 158 us with stages of
 // 128 inputs, as their loads are under way only half as long).  512 tokens x 2 of 8
 // experts, 4096 x 14336, e2m1 rows: 66 us, of which 53 us are the weights' bytes.
+// Stages of 256 e4m3 inputs for 128: 64-row tiles 914 -> 853 us (8192 rows over 8
+// experts of 28672 x 4096), with K split 65 -> 60 (512 rows, 4096 x 14336); 128-row
+// tiles, short of registers with them, 218 -> 223 and 46 -> 50 (above, 1280 x 8).
 //
 // Each XCD (workgroups are dealt to the 8 of them in turn) takes a contiguous
 // range of tiles, so that the weights and rows its CUs share stay in its L2.
@@ -275,7 +278,12 @@ __global__ __launch_bounds__(256, 3) void mx_small_kernel(MxK p) {
 // the lanes of a fragment read (32 rows, one chunk) fall on different banks,
 // whether 8 or 16 of them are served at once.  A DMA writes 64 chunks in a row,
 // so the lanes fetch them in swizzled order.
-__device__ __forceinline__ int swizzle(int row) { return (row & 7) ^ ((row >> 3) & 1); }
+template <int XC>
+__device__ __forceinline__ int swizzle(int row) {
+  return XC == 16 ? ((row >> 1) & 7) | ((row & 1) << 3) : (row & 7) ^ ((row >> 3) & 1);
+}
+// 16-byte chunks of a row in a stage of the TM-row kernel.
+constexpr int stage_chunks(int af, int tm) { return af == kE4M3 && tm == 64 ? 16 : 8; }
 
 // Tiles (row tile, channel block) are numbered expert by expert, within an
 // expert in groups of 8 row tiles by channel block.
@@ -355,11 +363,11 @@ __device__ __forceinline__ void store_tile16(const uint32_t lohi[8], uint16_t* a
 }
 
 constexpr int kEpiChunks = 256;  // 16-byte chunks of LDS per wavefront in the epilogue
-template <int AF, int EPI, int TM, int KS>
+// XC: 16-byte chunks of a row in a stage.
+template <int AF, int EPI, int TM, int KS, int XC>
 __device__ __forceinline__ void mx_tile_body(const MxK& p, const Tile& c, u32x4* x0, u32x4* x1, uint32_t* s0, uint32_t* s1,
                                              f32x4* red) {
-  constexpr int XC = 8;                      // 16-byte chunks of a row in a stage
-  constexpr int SS = AF == kE4M3 ? 2 : 4;    // steps of 64 inputs in a stage
+  constexpr int SS = XC / (AF == kE4M3 ? 4 : 2);  // steps of 64 inputs in a stage
   constexpr int RT = TM / 32;                // row tiles
   constexpr int XI = TM * XC / 256;          // row DMAs per wavefront and stage
   constexpr int RW = TM == 64 ? 16 : 32;     // rows whose scales a wavefront fetches
@@ -428,20 +436,20 @@ __device__ __forceinline__ void mx_tile_body(const MxK& p, const Tile& c, u32x4*
 #pragma unroll
   for (int i = 0; i < XI; ++i) {
     const int at = (wv * XI + i) * 64 + lane;
-    xo[i] = (uint32_t)src[i] * (uint32_t)(KB * (AF == kE4M3 ? 128 : 64)) + 16 * ((at % XC) ^ swizzle(at / XC));
+    xo[i] = (uint32_t)src[i] * (uint32_t)(KB * (AF == kE4M3 ? 128 : 64)) + 16 * ((at % XC) ^ swizzle<XC>(at / XC));
   }
   uint32_t xso = (uint32_t)src[XI] * (uint32_t)(KB * 4);
-  // 4-bit rows: a stage is two blocks of 128; the lanes of the second fetch the
-  // first again where K ends between the two (the weights there are zeros)
-  const bool high = ((lane % XC) ^ swizzle(lane / XC)) >= 4, high_s = (lane / RW) & 1;
-  if (AF == kE2M1 && high_s) xso += 4;
+  // A stage of 256 inputs is two blocks: the lanes of the second fetch the first
+  // again where K ends between the two (the weights there are zeros)
+  const bool high = ((lane % XC) ^ swizzle<XC>(lane / XC)) >= XC / 2, high_s = (lane / RW) & 1;
+  if (SS == 4 && high_s) xso += 4;
 
   // XI + 1 loads of the group's stage st, rows and scales
-  const int st0 = AF == kE4M3 ? 2 * c0 : c0, last = (AF == kE4M3 ? KB : KC) - 1;
+  const int st0 = SS == 2 ? 2 * c0 : c0, last = (SS == 2 ? KB : KC) - 1;
   auto issue = [&](u32x4* xs, uint32_t* ss, int rel) {
     const int st = min(st0 + rel, last);
-    const bool half_stage = AF == kE2M1 && 2 * st + 1 == KB;
-    const uint32_t back = half_stage && high ? 64 : 0, back_s = half_stage && high_s ? 4 : 0;
+    const bool half_stage = SS == 4 && 2 * st + 1 == KB;
+    const uint32_t back = half_stage && high ? XC * 8 : 0, back_s = half_stage && high_s ? 4 : 0;
 #pragma unroll
     for (int i = 0; i < XI; ++i)
       __builtin_amdgcn_raw_ptr_buffer_load_lds(ar, xs + (wv * XI + i) * 64, 16, xo[i] - back, st * (XC * 16), 0, 0);
@@ -452,7 +460,7 @@ __device__ __forceinline__ void mx_tile_body(const MxK& p, const Tile& c, u32x4*
   };
   auto read = [&](const u32x4* xs, int S, int t) {
     Frag f;
-    const int row = 32 * t + col, z = swizzle(row);
+    const int row = 32 * t + col, z = swizzle<XC>(row);
     if constexpr (AF == kE4M3) {
       f.x[0] = xs[row * XC + ((4 * S + half) ^ z)];
       f.x[1] = xs[row * XC + ((4 * S + 2 + half) ^ z)];
@@ -522,7 +530,7 @@ __device__ __forceinline__ void mx_tile_body(const MxK& p, const Tile& c, u32x4*
   // whole chunk, whose missing half multiplies them with the other half's rows.
   issue(x0, s0, 0);
   ready(zero);
-  if constexpr (AF == kE4M3) {  // two stages in a chunk
+  if constexpr (SS == 2) {  // two stages in a chunk
     issue(x1, s1, 1);
     __builtin_amdgcn_sched_barrier(0);
     load_weights(0, 2);
@@ -617,9 +625,9 @@ __device__ __forceinline__ void mx_tile_body(const MxK& p, const Tile& c, u32x4*
 
   int first = 0;  // the row tile of acc[0]
   if constexpr (KS == 2) {
-    // A group with a chunk less waits at as many barriers (A8: 2 a chunk; A4: one,
-    // rounded up to even); then the groups exchange sums, each keeps half the rows.
-    auto barriers = [](int chunks) { return AF == kE4M3 ? 2 * chunks : (chunks + 1) / 2 * 2; };
+    // A group with a chunk less waits at as many barriers (one a stage; stages of a
+    // chunk are taken in twos); then the groups exchange sums, each keeps half the rows.
+    auto barriers = [](int chunks) { return SS == 2 ? 2 * chunks : (chunks + 1) / 2 * 2; };
     for (int i = barriers(n); i < barriers(per_group); ++i) __builtin_amdgcn_s_barrier();
     constexpr int Q = RT / 2 * 4;  // 16-byte quarters of the sums that a lane gives away at a time
     f32x4* const out = red + (size_t)all * Q * 64 + lane;
@@ -737,17 +745,17 @@ __device__ __forceinline__ void mx_tile_body(const MxK& p, const Tile& c, u32x4*
 template <int AF, int EPI, int TM>
 __global__ __launch_bounds__(256, TM == 128 ? 2 : 3) void mx_tile_kernel(MxK p, int n_nb) {
 #ifdef __HIP_DEVICE_COMPILE__
-  constexpr int X = TM * 8, X0 = X > 4 * kEpiChunks ? X : 4 * kEpiChunks;
+  constexpr int XC = stage_chunks(AF, TM), X = TM * XC, X0 = X > 4 * kEpiChunks ? X : 4 * kEpiChunks;
   __shared__ u32x4 x0[X0], x1[X];
   __shared__ uint32_t s0[256], s1[256];
   Tile c;
   if (!own_tile<TM>(p, n_nb, c)) return;
   // a segment's last rows: as few row tiles as hold them
   const int left = c.s1 - c.r0;
-  if (left <= 32) mx_tile_body<AF, EPI, 32, 1>(p, c, x0, x1, s0, s1, nullptr);
-  else if (TM == 64 || left <= 64) mx_tile_body<AF, EPI, 64, 1>(p, c, x0, x1, s0, s1, nullptr);
-  else if (left <= 96) mx_tile_body<AF, EPI, 96, 1>(p, c, x0, x1, s0, s1, nullptr);
-  else mx_tile_body<AF, EPI, TM, 1>(p, c, x0, x1, s0, s1, nullptr);
+  if (left <= 32) mx_tile_body<AF, EPI, 32, 1, XC>(p, c, x0, x1, s0, s1, nullptr);
+  else if (TM == 64 || left <= 64) mx_tile_body<AF, EPI, 64, 1, XC>(p, c, x0, x1, s0, s1, nullptr);
+  else if (left <= 96) mx_tile_body<AF, EPI, 96, 1, XC>(p, c, x0, x1, s0, s1, nullptr);
+  else mx_tile_body<AF, EPI, TM, 1, XC>(p, c, x0, x1, s0, s1, nullptr);
 #endif
 }
 // Two groups of four wavefronts, each with stages of its own, take half of K each
@@ -755,12 +763,13 @@ __global__ __launch_bounds__(256, TM == 128 ? 2 : 3) void mx_tile_kernel(MxK p, 
 template <int AF, int EPI>
 __global__ __launch_bounds__(512, 2) void mx_tile_split_kernel(MxK p, int n_nb) {
 #ifdef __HIP_DEVICE_COMPILE__
-  __shared__ u32x4 x0[8 * kEpiChunks], x1[2 * 64 * 8];
+  constexpr int XC = stage_chunks(AF, 64);
+  __shared__ u32x4 x0[8 * kEpiChunks], x1[2 * 64 * XC];
   __shared__ uint32_t s0[512], s1[512];
   __shared__ f32x4 red[8 * 4 * 64];
   Tile c;
   if (!own_tile<64>(p, n_nb, c)) return;
-  mx_tile_body<AF, EPI, 64, 2>(p, c, x0, x1, s0, s1, red);
+  mx_tile_body<AF, EPI, 64, 2, XC>(p, c, x0, x1, s0, s1, red);
 #endif
 }
 
