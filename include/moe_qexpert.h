@@ -208,7 +208,8 @@ moe_status moe_route_permute(const float* logits, int32_t T, int32_t E, int32_t 
                                         workspace); nested MWQ: 16-row chunks of all widths */
 #define MOE_KERNEL_LDS_DMA_PER_WIDTH 7 /* nested MWQ only: the LDS-DMA kernel on row tiles of one
                                           width each, loading only that width's planes */
-#define MOE_KERNEL_TILE64_SPLIT_K 8  /* MX only: 64-row tiles, K split over two groups of wavefronts */
+#define MOE_KERNEL_TILE64_SPLIT_K 8  /* MX with e2m1 rows only: 64-row tiles, K split over two groups of
+                                        wavefronts */
 
 #define MOE_EPI_NONE 0      /* out bf16 [M_total][N] */
 #define MOE_EPI_SWIGLU 1    /* N = 2*I; rows [0,I) gate, [I,2I) up; out = bf16(silu(gate) * up), width I */
@@ -485,8 +486,8 @@ moe_status moe_mx_repack(const moe_mxdesc* src, const moe_mxdesc* dst, void* str
  * clamped to 0 .. M_total and gathered rows to A_rows - 1.
  * kernel: MOE_KERNEL_AUTO, MOE_KERNEL_SMALL (32-row tiles straight from memory:
  * decode batches), MOE_KERNEL_TILE64 / _TILE128 (LDS-staged tiles of that many
- * rows) or MOE_KERNEL_TILE64_SPLIT_K (64 rows, K > 256 split over two groups of
- * wavefronts: few tiles and long K).  Sums over K are added in the kernel's order,
+ * rows) or MOE_KERNEL_TILE64_SPLIT_K (64 e2m1 rows, K > 256 split over two groups
+ * of wavefronts: few tiles and long K).  Sums over K are added in the kernel's order,
  * so bits can differ between them, and with AUTO between batch sizes.  No workspace; out overlaps no input.  a_codes and w: 16-byte aligned, a_scales: 4-byte, out:
  * 16-byte.  a_codes below 4 GiB.
  */

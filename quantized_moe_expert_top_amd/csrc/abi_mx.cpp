@@ -64,7 +64,7 @@ moe_status check_route(const float* logits, const float* bias, int32_t T, int32_
   return MOE_OK;
 }
 
-moe_status check_kernel(int32_t kernel, int32_t K) {
+moe_status check_kernel(int32_t kernel, int32_t K, bool e2m1) {
   if (kernel < MOE_KERNEL_AUTO || kernel > MOE_KERNEL_TILE64_SPLIT_K)
     return fail(MOE_ERR_BAD_FORMAT, "unknown kernel choice %d", kernel);
   if (kernel != MOE_KERNEL_AUTO && kernel != MOE_KERNEL_SMALL && kernel != MOE_KERNEL_TILE64 &&
@@ -72,6 +72,7 @@ moe_status check_kernel(int32_t kernel, int32_t K) {
     return fail(MOE_ERR_UNSUPPORTED, "kernel choice %d does not run MX weights", kernel);
   if (kernel == MOE_KERNEL_TILE64_SPLIT_K && K <= 256)
     return fail(MOE_ERR_UNSUPPORTED, "K=%d is not split (more than 256)", K);
+  if (kernel == MOE_KERNEL_TILE64_SPLIT_K && !e2m1) return fail(MOE_ERR_UNSUPPORTED, "K is split for e2m1 rows only");
   return MOE_OK;
 }
 
@@ -196,7 +197,7 @@ moe_status moe_grouped_mxgemm(const moe_mxdesc* w, const uint8_t* a_codes, const
   const bool mx_out = epilogue == MOE_EPI_SWIGLU_E4M3 || epilogue == MOE_EPI_SWIGLU_E2M1;
   if ((epilogue == MOE_EPI_SWIGLU || mx_out) && w->N % 64 != 0)
     return fail(MOE_ERR_UNSUPPORTED, "N=%d must be a multiple of 64 with a SwiGLU epilogue", w->N);
-  st = check_kernel(kernel, w->K);
+  st = check_kernel(kernel, w->K, a_fmt == MOE_MX_E2M1);
   if (st != MOE_OK) return st;
   if (gather_pair) {
     if (k < 1) return fail(MOE_ERR_BAD_SHAPE, "k=%d with gather_pair", k);
@@ -245,7 +246,7 @@ moe_status moe_mx_layer(const moe_mxlayer* l, void* stream) {
   if (!known_fmt(l->x_fmt) || !known_fmt(l->h_fmt))
     return fail(MOE_ERR_BAD_FORMAT, "unknown MX format (x %d, h %d)", l->x_fmt, l->h_fmt);
   if (!known_dtype(l->y_dtype)) return fail(MOE_ERR_BAD_FORMAT, "y_dtype %d", l->y_dtype);
-  st = check_kernel(l->kernel, H < I ? H : I);
+  st = check_kernel(l->kernel, H < I ? H : I, l->x_fmt == MOE_MX_E2M1 && l->h_fmt == MOE_MX_E2M1);
   if (st != MOE_OK) return st;
   st = check_code_bytes(T, H, l->x_fmt);
   if (st != MOE_OK) return st;

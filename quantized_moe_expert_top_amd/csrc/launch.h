@@ -189,8 +189,8 @@ struct MxGemmArgs {
 int launch_mx_repack(const uint8_t* codes, const uint8_t* scales, int E, int N, int K, uint8_t* tcodes,
                      uint8_t* tscales, void* stream);
 // Planning (plan.cpp): 0, 64 or 128.
-constexpr int kMxSplit = 65;  // 64-row tiles with K split over two groups of wavefronts
-int mxgemm_path(int M_total, int E, int N, int K, int kernel);
+constexpr int kMxSplit = 65;  // 64-row tiles (e2m1 rows) with K split over two groups of wavefronts
+int mxgemm_path(int M_total, int E, int N, int K, bool e2m1, int kernel);
 int launch_mxgemm(const MxGemmArgs& a, void* stream);
 
 }  // namespace moe

@@ -268,7 +268,7 @@ __global__ __launch_bounds__(256, 3) void mx_small_kernel(MxK p) {
 // 128 inputs, as their loads are under way only half as long).  512 tokens x 2 of 8
 // experts, 4096 x 14336, e2m1 rows: 66 us, of which 53 us are the weights' bytes.
 // Stages of 256 e4m3 inputs for 128: 64-row tiles 914 -> 853 us (8192 rows over 8
-// experts of 28672 x 4096), with K split 65 -> 60 (512 rows, 4096 x 14336); 128-row
+// experts of 28672 x 4096), 19.4 -> 15.4 (192 rows each, 16 of 448 x 4096); 128-row
 // tiles, short of registers with them, 218 -> 223 and 46 -> 50 (above, 1280 x 8).
 //
 // Each XCD (workgroups are dealt to the 8 of them in turn) takes a contiguous
@@ -759,7 +759,8 @@ __global__ __launch_bounds__(256, TM == 128 ? 2 : 3) void mx_tile_kernel(MxK p, 
 #endif
 }
 // Two groups of four wavefronts, each with stages of its own, take half of K each
-// (K > 256): alone on its CU, a workgroup waits for loads most of the time.
+// (K > 256): alone on its CU, a workgroup of e2m1 rows waits for loads most of the
+// time.
 template <int AF, int EPI>
 __global__ __launch_bounds__(512, 2) void mx_tile_split_kernel(MxK p, int n_nb) {
 #ifdef __HIP_DEVICE_COMPILE__
@@ -791,7 +792,7 @@ int launch_tile(const MxK& k, bool split, hipStream_t s) {
   const int64_t tiles = (int64_t)k.M_total / TM + (k.E < k.M_total ? k.E : k.M_total);
   const int64_t wgs = (tiles * n_nb + 7) / 8 * 8;
   if (wgs >= ((int64_t)1 << 23)) return (int)hipErrorInvalidConfiguration;  // 2^32 threads in 512s
-  if constexpr (TM == 64) {
+  if constexpr (TM == 64 && AF == kE2M1) {
     if (split) {
       hipLaunchKernelGGL((mx_tile_split_kernel<AF, EPI>), dim3((unsigned)wgs), dim3(512), 0, s, k, n_nb);
       return (int)hipGetLastError();
@@ -828,7 +829,7 @@ int launch_mxgemm(const MxGemmArgs& a, void* stream) {
   const MxK k{a.wcodes, a.wscales, a.N, a.K, a.a, a.as, (uint32_t)(a.A_rows * row_codes),
               (uint32_t)((size_t)a.A_rows * (a.K / 32)), a.A_rows, a.gather, (uint32_t)((((uint64_t)1 << (31 + sh)) + div - 1) / div), sh, a.seg, a.E, a.M_total,
               a.out, a.out_scales};
-  const int path = mxgemm_path(a.M_total, a.E, a.N, a.K, a.kernel);
+  const int path = mxgemm_path(a.M_total, a.E, a.N, a.K, a.a_fmt == kE2M1, a.kernel);
   return a.a_fmt == kE4M3 ? launch_fmt<kE4M3>(k, a.epilogue, path, s) : launch_fmt<kE2M1>(k, a.epilogue, path, s);
 }
 

@@ -156,20 +156,21 @@ size_t mx_layer_workspace_bytes(int T, int k, int E) {
 // d: its last workgroups running alone.  Fitted to 346 measured problems (E 8 to
 // 64, 1 to 1024 rows per expert, N 448 to 28672, K 512 to 14336, 8- and 4-bit
 // rows); the estimates are within about 20 % of the times, and where two paths
-// are that close either is taken: on average 1.3 % above the better.  E.g. 8
+// are that close either is taken: on average 1 % above the better.  E.g. 8
 // experts of 2048 x 2048, us for 32-row / 64-row / 128-row tiles: 6.5 / 9.8 / 10.0 at
 // 16 rows per expert, 17.9 / 11.2 / 14.6 at 128; 64 experts at 512 rows: 450 / 148 /
 // 131.
-// 64-row tiles split K over two groups of wavefronts where K is long and every
-// workgroup has a CU of its own: 8 experts of 4096 x 14336, 32 rows each 52 -> 43
-// us, 16 of 448 x 4096, 256 rows 19.7 -> 17.3, 8 of 2048 x 2048, 192 rows 11.5 ->
-// 11.0; with 288 workgroups 15.9 -> 20.2, with K = 1024 6.8 -> 7.5.
-int mxgemm_path(int M_total, int E, int N, int K, int kernel) {
+// 64-row tiles of e2m1 rows split K over two groups of wavefronts where K is long
+// and every workgroup has a CU of its own: 8 experts of 4096 x 14336, 32 rows each
+// 45 -> 40 us, 16 of 448 x 4096, 192 rows 14.9 -> 13.8; with K = 2048 9.6 -> 9.8, with
+// 320 workgroups 56 -> 59.  With e4m3 rows, whose stages hold twice the bytes, the
+// split loses (15.4 -> 16.2).
+int mxgemm_path(int M_total, int E, int N, int K, bool e2m1, int kernel) {
   if (kernel == 1) return 0;
   const double active = M_total < E ? M_total : E;  // experts that can have rows
   const double nt = N / 32.0;
   const double wide_blocks = (double)(int64_t)((nt + 7.0) / 8.0);
-  const int path64 = K >= 2048 && wide_blocks * (M_total / 64.0 + 0.5 * active) <= 256.0 ? kMxSplit : 64;
+  const int path64 = e2m1 && K >= 4096 && wide_blocks * (M_total / 64.0 + 0.5 * active) <= 256.0 ? kMxSplit : 64;
   if (kernel == 4) return 64;
   if (kernel == 8) return kMxSplit;
   if (kernel == 5) return 128;

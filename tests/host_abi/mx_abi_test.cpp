@@ -174,9 +174,10 @@ int main() {
       for (int N : {32, 512, 1 << 20})
         for (int K : {128, 256, 512, 4096, 1 << 20})
           for (int kernel : {0, 1, 4, 5, 8}) {
-            const int path = moe::mxgemm_path(M, E, N, K, kernel);
+            const bool e2m1 = kernel == 8 || (M & 1);
+            const int path = moe::mxgemm_path(M, E, N, K, e2m1, kernel);
             CHECK(path == 0 || path == 64 || path == 128 || path == moe::kMxSplit);
-            CHECK(kernel != 0 || path != moe::kMxSplit || K > 256);
+            CHECK(path != moe::kMxSplit || (e2m1 && (K > 256 || kernel == 8)));
           }
   const moe_mxdesc wide = desc(MOE_LAYOUT_CANONICAL, 1024, 32, 384, 0x30000);
   CHECK(moe_mx_field_bytes(&wide, MOE_FIELD_CODES) == (size_t)1024 * 32 * 192);

@@ -446,7 +446,7 @@ def test_product_last_rows(kernel, act, epi, K):
     check_product(p, epi, kernel, f"{act} 64x{K}")
 
 
-SPLIT = [("e4m3", q.MOE_KERNEL_TILE64_SPLIT_K), ("e2m1", q.MOE_KERNEL_TILE64_SPLIT_K)]
+SPLIT = [("e4m3", q.MOE_KERNEL_TILE64), ("e2m1", q.MOE_KERNEL_TILE64_SPLIT_K)]
 
 
 @pytest.mark.parametrize("act,kernel", SPLIT)
@@ -454,7 +454,7 @@ SPLIT = [("e4m3", q.MOE_KERNEL_TILE64_SPLIT_K), ("e2m1", q.MOE_KERNEL_TILE64_SPL
                                  q.MOE_EPI_SWIGLU_E4M3, q.MOE_EPI_SWIGLU_E2M1])
 @pytest.mark.parametrize("K", [384, 512, 640, 2176, 2304, 2560, 4224])
 def test_product_long_k(act, kernel, epi, K):
-    """Tiles whose K is split over two groups of wavefronts: even, odd and half chunks of 256."""
+    """64-row tiles (of e2m1 rows with K split over two groups of wavefronts): even, odd and half chunks of 256."""
     p = Product(K, 3, 320, K, act, [1, 0, 133], k=3)
     check_product(p, epi, kernel, f"{act} 320x{K}")
 
@@ -647,11 +647,16 @@ def test_layer_choices(y_dtype, epi, kernel, h_fmt):
     dn = q.moe_mx_repack(q.mx_experts(q.moe_quantize_mx(r(E, H, I) / 20, q.MOE_MX_E2M1)))
     x, logits = r(T, H).half(), r(T, E)
     show("layer choices", y_dtype, kernel, h_fmt)
-    buf = q.alloc_mx_layer(T, E, k, H, I, DEV, h_fmt=h_fmt, y_dtype=y_dtype)
+    act = q.MOE_MX_E2M1 if kernel == q.MOE_KERNEL_TILE64_SPLIT_K else q.MOE_MX_E4M3
+    buf = q.alloc_mx_layer(T, E, k, H, I, DEV, act=act, h_fmt=h_fmt, y_dtype=y_dtype)
+    if kernel == q.MOE_KERNEL_TILE64_SPLIT_K and h_fmt == q.MOE_MX_E4M3:
+        with pytest.raises(RuntimeError, match="e2m1"):
+            q.moe_mx_layer_forward(x, logits, k, gu, dn, buf=buf, kernel=kernel)
+        return
     q.moe_mx_layer_forward(x, logits, k, gu, dn, buf=buf, kernel=kernel)
     ids, w = q.moe_route_scored(logits, k)
     p = q.moe_permute(ids, E)
-    h = q.moe_grouped_mxgemm(gu, q.moe_quantize_mx(x), p.seg_offsets, T * k,
+    h = q.moe_grouped_mxgemm(gu, q.moe_quantize_mx(x, act), p.seg_offsets, T * k,
                              q.MOE_EPI_SWIGLU_E4M3 if h_fmt == q.MOE_MX_E4M3 else q.MOE_EPI_SWIGLU_E2M1,
                              gather_pair=p.sorted_pair, k=k, kernel=kernel)
     y = q.moe_grouped_mxgemm(dn, h, p.seg_offsets, T * k, epi, kernel=kernel)

@@ -147,7 +147,8 @@ def test_grouped_mxgemm_validation(lib):
     assert gemm(mxdesc(q.MOE_LAYOUT_CANONICAL)) == gemm(mxdesc(version=2)) == gemm(fmt=0) == gemm(epi=6) == BAD_FORMAT
     assert gemm(epi=-1) == gemm(kernel=10) == gemm(kernel=-1) == BAD_FORMAT
     assert gemm(kernel=q.MOE_KERNEL_LDS_DMA) == gemm(kernel=q.MOE_KERNEL_SMALL_PER_WIDTH) == UNSUPPORTED
-    assert gemm(kernel=q.MOE_KERNEL_TILE64_SPLIT_K) == UNSUPPORTED              # K = 256
+    assert gemm(fmt=2, kernel=q.MOE_KERNEL_TILE64_SPLIT_K) == UNSUPPORTED       # K = 256
+    assert gemm(mxdesc(K=512), kernel=q.MOE_KERNEL_TILE64_SPLIT_K) == UNSUPPORTED  # e4m3 rows
     assert gemm(mxdesc(N=96), epi=q.MOE_EPI_SWIGLU) == gemm(mxdesc(N=48)) == gemm(mxdesc(K=160)) == UNSUPPORTED
     assert gemm(M=-1) == gemm(rows=-1) == gemm(k=0) == gemm(rows=63) == gemm(gather=None, rows=127) == BAD_SHAPE
     assert gemm(out=A) == BAD_SHAPE                                             # in place
