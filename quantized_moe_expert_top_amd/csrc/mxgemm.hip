@@ -511,9 +511,12 @@ __device__ __forceinline__ void mx_tile_body(const MxK& p, const Tile& c, u32x4*
   const std::integral_constant<int, 2> two{};
   const std::integral_constant<int, 3> three{};
   // Everyone's fragments of the current block have arrived, and the next block's
-  // rows.  Loads complete in order: `left` newer ones, the weights loaded since
-  // those rows were issued (at least that many; the scheduling barriers keep them
-  // between the two), may be on their way.  Waiting for them too cost 3 to 30 %.
+  // rows.  Loads complete in order: `left` newer ones, weights and their scales
+  // loaded since those rows were issued, may be on their way.  At least that many
+  // are (in the one-stage loop 6 of weights and 2 of scales before its first wait,
+  // 10 before the others; 6 or more of weights in the two-stage loop); the
+  // scheduling barriers keep them between the two.  Waiting for them too cost 3 to
+  // 30 %.
   auto ready = [&](auto left_tag) {
     __builtin_amdgcn_sched_barrier(0);
     __builtin_amdgcn_s_waitcnt(0x0070 | decltype(left_tag)::value);  // vmcnt `left`, lgkmcnt 0
@@ -568,6 +571,7 @@ __device__ __forceinline__ void mx_tile_body(const MxK& p, const Tile& c, u32x4*
   } else {  // one
     const int k1 = min(1, n - 1);
     issue(x1, s1, k1);
+    __builtin_amdgcn_sched_barrier(0);  // the loop's first wait counts the scales' loads too
     Scales next = load_scales(k1);
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
