@@ -381,8 +381,8 @@ moe_status moe_unpermute_combine(const void* y_perm, int32_t y_dtype, const int3
  *     w   = s of the chosen experts (without the bias), divided by their sum if
  *           renormalize != 0, times scale, rounded once to float32
  * A logit of -inf or NaN, or a bias of -inf or NaN, bars its expert: its score
- * is 0 and it is never chosen (+inf counts as FLT_MAX; a group without
- * eligible experts ranks last).  Slots left over when fewer than k experts are
+ * is 0 and it is never chosen (a logit of +inf counts as FLT_MAX; a bias of +inf
+ * puts its expert first; a group without eligible experts ranks last).  Slots left over when fewer than k experts are
  * eligible hold id -1 and weight 0; moe_permute places such pairs after every
  * valid segment, and the combine adds nothing for them.  A sum of chosen
  * scores that is 0 gives weights 0.

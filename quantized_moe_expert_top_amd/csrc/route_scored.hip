@@ -308,7 +308,8 @@ __device__ __forceinline__ int route_candidates(const ScoredArgs& a, int t, doub
     const bool mine = g < a.n_group;
     // bit g: group g is open
     uint64_t open = 0;
-    if (__ballot(mine && sure < a.topk_group && maybe >= a.topk_group)) {
+    // (an infinite bound, from biases of +inf or sums past FLT_MAX, orders nothing)
+    if (!(err < __builtin_inff()) || __ballot(mine && sure < a.topk_group && maybe >= a.topk_group)) {
       double score[NS], c[NS];
       wave_fence();
       exact_scores<NS>(a, t, top, score, c);
