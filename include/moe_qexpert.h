@@ -432,8 +432,8 @@ moe_status moe_dequantize_mx(const uint8_t* codes, const uint8_t* scales, int64_
  * and weight [H] of `dtype` (MOE_DTYPE_*).  sum (needs residual), y and the MX
  * output (fmt 0: codes and scales NULL) are each optional; at least one output
  * is needed.  sum and y may each be x's or residual's own buffer, not the same
- * one; no other buffers may overlap.  The sum of squares
- * and the norm's factor are float64.
+ * one; no other buffers may overlap.  The sum of squares, the
+ * norm's factor and n are float64; n past the largest float32 counts as infinite.
  * 0 <= rows < 2^24, H % 32 == 0, 32 <= H <= 16384, rows * H < 2^34, eps >= 0 and
  * finite; 16-byte aligned buffers, except scales.
  */

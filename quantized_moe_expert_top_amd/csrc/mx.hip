@@ -99,14 +99,16 @@ __global__ __launch_bounds__(kThreads) void dequantize_mx_kernel(const uint8_t* 
 // ------------------------------------------------------------------- RMS norm
 // TPR threads hold one row in registers (NV groups of 8 values each), so x and
 // residual are read once: v = x + residual rounded to the row's type, the sum
-// of squares in float64 (hidden behind the loads; it cannot overflow either),
-// then n = (v * weight) * factor.  v * weight of 16-bit values is exact in fp32
-// (8 + 8 or 11 + 11 significant bits) and the factor is a float64 split into two
-// floats.  n is rounded to nearest for an fp32 y; what is rounded again, to 16
-// bits or to an MX element, is rounded to odd first (an inexact n gets an odd
-// last bit), so that the second rounding is that of the exact value and not of
-// an fp32 number on the border.  8192 rows of
-// 4096 bf16 with residual, sum, y and 8-bit blocks: 61 us, 5.0 TB/s.
+// of squares in float64 (squares and their sum neither overflow nor lose small
+// rows there), then n = v * weight * factor in float64 too: the product of two
+// floats is exact in it, while in fp32 it can leave the range on either side
+// although n does not, and the factor alone can.  n is rounded to nearest for an
+// fp32 y; what is rounded again, to 16 bits or to an MX element, is rounded to odd
+// first (an inexact n gets an odd last bit), so that the second rounding is that of
+// the exact value and not of an fp32 number on the border.  Past the largest float
+// n is infinite.  HBM bounds it: 8192 rows of 4096 with residual, sum, y and 8-bit
+// blocks 54 us in bf16, 109 in fp32 (n in fp32 pairs, which is wrong at the ends of
+// the range: 52.5 and 110; 16384 rows of 512 16.4 and 14.7, 64 rows of 4096 3.8 both).
 template <int DT>
 __device__ __forceinline__ float round_to(float f) {
   if constexpr (DT == 0) return bf16_to_f32(f32_to_bf16(f));
@@ -116,7 +118,7 @@ __device__ __forceinline__ float round_to(float f) {
 
 template <int DT, int FMT, int TPR, int NV>
 __global__ __launch_bounds__(TPR > kThreads ? TPR : kThreads) void rmsnorm_mx_kernel(NormArgs a) {
-#pragma clang fp contract(off)  // hi + lo below must not become m * fhi + lo
+#pragma clang fp contract(off)  // sums are rounded before they are rounded to 16 bits; rest is that of the rounded d
   constexpr int kRows = TPR > kThreads ? 1 : kThreads / TPR, kWaves = TPR / 64;
   __shared__ double part[kRows * kWaves];
   const int sub = threadIdx.x / TPR, t = threadIdx.x % TPR;
@@ -154,7 +156,6 @@ __global__ __launch_bounds__(TPR > kThreads ? TPR : kThreads) void rmsnorm_mx_ke
     for (int w = 0; w < kWaves; ++w) sum += part[sub * kWaves + w];
   }
   const double f = 1.0 / sqrt(sum / a.H + (double)a.eps);
-  const float fhi = (float)f, flo = (float)(f - (double)fhi);
 #pragma unroll
   for (int j = 0; j < NV; ++j) {
     const int c = t + j * TPR;
@@ -164,17 +165,13 @@ __global__ __launch_bounds__(TPR > kThreads ? TPR : kThreads) void rmsnorm_mx_ke
     unpack8<DT>(load8<DT>(a.weight, c), w);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-      const float m = v[j][i] * w[i];
-      const float hi = m * fhi;
-      float lo = __builtin_fmaf(m, flo, __builtin_fmaf(m, fhi, -hi));
-      if constexpr (DT == 1) lo = __builtin_fmaf(__builtin_fmaf(v[j][i], w[i], -m), fhi, lo);
-      const float n = hi + lo;
-      const float rest = lo - (n - hi);
+      const double d = (double)v[j][i] * (double)w[i] * f + 0.0;  // (a zero is +0)
+      const float n = (float)d;
+      const double rest = __builtin_fabs(d) - __builtin_fabs((double)n);
       nearest[i] = n;
-      const int b = __builtin_bit_cast(int, n);
-      // the neighbour on the side of the rest (NaN: not greater, stays)
-      const int odd = b + ((rest > 0.0f) == (b > 0) ? 1 : -1);
-      v[j][i] = (__builtin_fabsf(rest) > 0.0f && !(b & 1)) ? __builtin_bit_cast(float, odd) : n;
+      // the neighbour on the side of the rest (infinities and NaN stay)
+      const int b = __builtin_bit_cast(int, n), odd = b + (rest > 0.0 ? 1 : -1);
+      v[j][i] = (__builtin_isfinite(rest) && rest != 0.0 && !(b & 1)) ? __builtin_bit_cast(float, odd) : n;
     }
     if (a.y) store8<DT>(a.y, r8 + c, DT == 1 ? nearest : v[j]);
     if constexpr (FMT != 0) store_mx8<FMT>(v[j], quad_umax(absmax_bits(v[j])), r8 + c, a.codes, a.scales);

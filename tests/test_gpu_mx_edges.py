@@ -1,12 +1,17 @@
 """GPU checks of the MX operators at the ends of their ranges, against the
 float64 references (oracle/mx_oracle.py).
 
-Tolerances are those of test_gpu_mx.py.
+Tolerances are those of test_gpu_mx.py; a rounding to a 16-bit type is off by
+half a step, relative to the value or, below the type's smallest normal number,
+of its subnormal step.
 """
 import numpy as np
 import pytest
+import torch
 
-from tests.test_gpu_mx import check_route
+import quantized_moe_expert_top_amd as q
+from oracle import mx_oracle as mx
+from tests.test_gpu_mx import DEV, DT, FMT, NORM, check_route, close, decoded, dev, f64, show
 
 pytestmark = pytest.mark.gpu
 
@@ -43,3 +48,59 @@ def test_route_groups_of_huge_biases(sigmoid, gt, low, high, E, G, tg, k):
     check_route(logits, k, sigmoid=sigmoid, bias=bias, n_group=G, topk_group=tg, group_top=gt)
     bias[: E // G] = 0.25  # one ordinary group
     check_route(logits, k, sigmoid=sigmoid, bias=bias, n_group=G, topk_group=tg, group_top=gt)
+
+
+# -------------------------------------------------------------------- the norm
+def norm_rows(rng, kind, rows, H):
+    """Rows and weights whose products, or whose norm's factor, leave float32's normal range, with finite norms."""
+    x, w = rng.standard_normal((rows, H)), 1 + 0.2 * rng.standard_normal(H)
+    if kind == "products past the largest":   # v * w up to 2^129, norms near 2
+        return np.clip(x, -3, 3) * 2.0 ** 125, w * 2
+    if kind == "products below the smallest":
+        return x * 1e-20, w * 1e-19
+    if kind == "subnormal rows":
+        return x * 2.0 ** -130, w
+    if kind == "subnormal rows, large weights":
+        return x * 2.0 ** -130, w * 2.0 ** 100
+    if kind == "largest rows":                # a factor below the smallest normal number
+        return np.where(rng.random((rows, H)) < 0.5, 1.0, -1.0) * rng.uniform(0.6, 1.0, (rows, H)) * 3.3e38, w
+    if kind == "far apart in a row":          # large weights bring small values back
+        e = rng.integers(-90, 91, (rows, H))
+        e[:, 0] = 90
+        return x * np.exp2(e.astype(float)), np.where(rng.random(H) < 0.5, w, w * 2.0 ** 120)
+    if kind == "norms below the smallest":
+        return x, w * np.exp2(-rng.integers(120, 150, H).astype(float))
+    raise KeyError(kind)
+
+
+@pytest.mark.parametrize("kind", ["products past the largest", "products below the smallest", "subnormal rows",
+                                  "subnormal rows, large weights", "largest rows", "far apart in a row",
+                                  "norms below the smallest"])
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+@pytest.mark.parametrize("rows,H", [(3, 96), (5, 2048), (600, 4096), (2, 16384)])
+def test_rmsnorm_ends_of_the_range(kind, dt, rows, H):
+    rng = np.random.default_rng(H + rows)
+    x, w = (dev(a.astype(np.float32), DT[dt]) for a in norm_rows(rng, kind, rows, H))
+    show("norm", kind, dt, rows, H)
+    n = mx.rmsnorm(f64(x), f64(w), 0.0)
+    assert np.isfinite(n).all() and np.abs(n).max() < 2.0 ** 127.9
+    info = torch.finfo(DT[dt])
+    for fmt in ("e4m3", "e2m1"):
+        o = q.moe_rmsnorm_mx(x, w, 0.0, fmt=FMT[fmt], want_y=True)
+        step = info.tiny * info.eps  # of subnormal numbers
+        close(f64(o.y), n, (info.eps / 2 + NORM) * np.abs(n) + step / 2 * (1 + NORM), "y")
+        assert np.array_equal(decoded(o.rows), mx.values(*mx.quantize(n, FMT[fmt]), FMT[fmt]))
+
+
+@pytest.mark.parametrize("dt", ["bf16", "fp32"])
+def test_rmsnorm_past_the_largest(dt):
+    """Norms past the largest float32 are infinite: y has that infinity, the block is not a number; others stay."""
+    x = torch.ones(2, 128, device=DEV, dtype=DT[dt])
+    x[1, 5] = -1
+    w = torch.ones(128, device=DEV, dtype=DT[dt])
+    w[5] = 3.3e38
+    x[:, 5] *= 4  # mean square 1.12: the norm there 4 / 1.06 * 3.3e38
+    o = q.moe_rmsnorm_mx(x, w, 0.0, want_y=True)
+    y = f64(o.y)
+    assert y[0, 5] == np.inf and y[1, 5] == -np.inf and np.isfinite(np.delete(y, 5, 1)).all()
+    assert (o.rows.scales[:, 0] == 255).all() and (o.rows.scales[:, 1:] != 255).all()
