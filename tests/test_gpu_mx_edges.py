@@ -104,3 +104,24 @@ def test_rmsnorm_past_the_largest(dt):
     y = f64(o.y)
     assert y[0, 5] == np.inf and y[1, 5] == -np.inf and np.isfinite(np.delete(y, 5, 1)).all()
     assert (o.rows.scales[:, 0] == 255).all() and (o.rows.scales[:, 1:] != 255).all()
+
+
+# ------------------------------------------------------- the calls of README.md
+README_CALLS = """\
+w13 = q.moe_mx_repack(q.mx_experts(q.moe_quantize_mx(gate_up, q.MOE_MX_E2M1)))   # [E][2I][H]: gate rows, then up rows
+w2 = q.moe_mx_repack(q.mx_experts(q.moe_quantize_mx(down, q.MOE_MX_E2M1)))       # [E][H][I]
+n = q.moe_rmsnorm_mx(x, norm_weight, 1e-5, residual=residual, fmt=q.MOE_MX_E4M3) # n.rows feeds the experts
+routing = q.ScoredRouting(score=q.MOE_SCORE_SIGMOID, bias=bias)
+out = q.moe_mx_layer_forward(n.rows, logits, k, w13, w2, routing).out            # bf16 [T][H]
+"""
+
+
+def test_calls_that_the_readme_shows():
+    T, E, H, I, k = 12, 4, 256, 128, 2
+    r = lambda *s: torch.randn(*s, device=DEV)  # noqa: E731
+    names = dict(q=q, x=r(T, H).bfloat16(), residual=r(T, H).bfloat16(), norm_weight=r(H).bfloat16(), logits=r(T, E),
+                 bias=r(E), k=k, gate_up=r(E, 2 * I, H).bfloat16(), down=r(E, H, I).bfloat16())
+    exec(README_CALLS, names)  # noqa: S102
+    out = names["out"]
+    assert isinstance(out, torch.Tensor) and out.shape == (T, H) and out.dtype == torch.bfloat16
+    assert torch.isfinite(out).all() and out.abs().sum() > 0
