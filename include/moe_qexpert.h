@@ -508,7 +508,8 @@ moe_status moe_grouped_mxgemm(const moe_mxdesc* w, const uint8_t* a_codes, const
  *   routing as for moe_route_scored; grouping buffers as for moe_permute (S = 1),
  *           workspace at least moe_mx_layer_workspace_size(T, k, E) bytes; its
  *           contents need not start at zero; calls that share one must be ordered
- *   h       MX rows [T*k][I] in h_fmt; y [T*k][H] of y_dtype (MOE_DTYPE_*)
+ *   h       MX rows [T*k][I] in h_fmt; y [T*k][H] of y_dtype (MOE_DTYPE_*; F16 holds
+ *           magnitudes up to 65504, larger expert outputs become infinite there)
  *   out     bf16 [T][H]
  * Alignment as for those calls.  Every argument is checked before anything is
  * launched; T == 0 writes nothing.  T * k < 2^31, k <= E.

@@ -361,7 +361,8 @@ class MxLayerBuffers:
 def alloc_mx_layer(T: int, E: int, k: int, H: int, I: int, device, act: int = MOE_MX_E4M3, h_fmt: int = MOE_MX_E4M3,
                    y_dtype: torch.dtype = torch.float16) -> MxLayerBuffers:
     """act: MX format of the layer's input rows; h_fmt: of the SwiGLU activations; y_dtype: the experts' outputs
-    before the combine."""
+    before the combine: float16 (default, as in alloc_layer: half the bytes of float32, 11 significant bits, and
+    infinities past 65504), float32 (as the product sums them) or bfloat16 (8 bits, float32's range)."""
     if y_dtype not in _DTYPE_EPI:
         raise ValueError(f"expert outputs in {y_dtype}: float16, float32 or bfloat16")
     i32 = dict(dtype=torch.int32, device=device)
@@ -380,7 +381,8 @@ def moe_mx_layer_forward(x: Union[torch.Tensor, MxRows], logits: torch.Tensor, k
                          down: MxExperts, routing: ScoredRouting = None, buf: MxLayerBuffers = None, stream=None,
                          kernel: int = MOE_KERNEL_AUTO) -> MxLayerBuffers:
     """Scored routing -> grouping -> gate_up with SwiGLU, its activations quantised to MX rows -> down -> combine,
-    one stream.  x: bf16, fp16 or fp32 [T][H], quantised to buf.x's format, or MX rows (moe_rmsnorm_mx)."""
+    one stream.  x: bf16, fp16 or fp32 [T][H], quantised to buf.x's format, or MX rows (moe_rmsnorm_mx).  Buffers made
+    here (buf None) have alloc_mx_layer's defaults: expert outputs past 65504 need buffers with another y_dtype."""
     T, H = x.shape
     E = logits.shape[1]
     I = gate_up.N // 2

@@ -11,7 +11,7 @@ import torch
 
 import quantized_moe_expert_top_amd as q
 from oracle import mx_oracle as mx
-from tests.test_gpu_mx import DEV, DT, FMT, NORM, check_route, close, decoded, dev, f64, show
+from tests.test_gpu_mx import DEV, DT, FMT, NORM, check_route, close, decoded, dev, f64, layer_reference, show
 
 pytestmark = pytest.mark.gpu
 
@@ -104,6 +104,30 @@ def test_rmsnorm_past_the_largest(dt):
     y = f64(o.y)
     assert y[0, 5] == np.inf and y[1, 5] == -np.inf and np.isfinite(np.delete(y, 5, 1)).all()
     assert (o.rows.scales[:, 0] == 255).all() and (o.rows.scales[:, 1:] != 255).all()
+
+
+# ------------------------------------------------------------------- the layer
+def test_layer_outputs_past_float16():
+    """Expert outputs past 65504: finite where they travel to the combine as float32 or bfloat16, infinite as float16
+    (the default), as the documentation says."""
+    T, E, H, I, k = 20, 4, 128, 256, 2
+    rng = np.random.default_rng(2)
+    g = lambda *s: rng.standard_normal(s).astype(np.float32)  # noqa: E731
+    gu = q.moe_quantize_mx(dev(2 * g(E, 2 * I, H)), q.MOE_MX_E2M1)
+    dn = q.moe_quantize_mx(dev(64 * g(E, H, I)), q.MOE_MX_E2M1)
+    x, logits = q.moe_quantize_mx(dev(g(T, H))), g(T, E)
+    _, _, ref, _ = layer_reference(decoded(x), logits, k, decoded(gu), decoded(dn), mx.E4M3, {})
+    assert np.abs(ref).max() > 2 * 65504
+    t13, t2 = (q.moe_mx_repack(q.mx_experts(v)) for v in (gu, dn))
+    for y_dtype in (torch.float32, torch.bfloat16, torch.float16):
+        show("past float16", y_dtype)
+        buf = q.alloc_mx_layer(T, E, k, H, I, DEV, y_dtype=y_dtype)
+        out = f64(q.moe_mx_layer_forward(x, dev(logits), k, t13, t2, buf=buf).out)
+        if y_dtype == torch.float16:
+            assert np.isinf(f64(buf.y_perm)).any()
+        else:
+            assert np.isfinite(out).all()
+            assert np.linalg.norm(out - ref) <= 5e-3 * np.linalg.norm(ref)
 
 
 # ------------------------------------------------------- the calls of README.md
