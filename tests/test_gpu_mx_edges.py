@@ -11,7 +11,8 @@ import torch
 
 import quantized_moe_expert_top_amd as q
 from oracle import mx_oracle as mx
-from tests.test_gpu_mx import DEV, DT, FMT, NORM, check_route, close, decoded, dev, f64, layer_reference, show
+from tests.test_gpu_mx import (DEV, DT, FMT, NORM, Product, check_product, check_route, close, decoded, dev, f64,
+                               layer_reference, show)
 
 pytestmark = pytest.mark.gpu
 
@@ -104,6 +105,53 @@ def test_rmsnorm_past_the_largest(dt):
     y = f64(o.y)
     assert y[0, 5] == np.inf and y[1, 5] == -np.inf and np.isfinite(np.delete(y, 5, 1)).all()
     assert (o.rows.scales[:, 0] == 255).all() and (o.rows.scales[:, 1:] != 255).all()
+
+
+# ----------------------------------------------------------------- the product
+def sparse_counts(E, rng):
+    """Rows of E experts: mostly none, one or several row tiles next to the multiples of 64 and at the ends."""
+    c = np.zeros(E, int)
+    for e in (0, 3, 62, 63, 64, 65, 126, 127, 128, 129, 191, 192, 511, 640, 959, 960, E - 2, E - 1):
+        if 0 <= e < E:
+            c[e] = rng.choice([0, 1, 31, 64, 65, 129, 200])
+    c[min(E - 1, 64)] = 130
+    return [int(v) for v in c]
+
+
+MANY = [("e4m3", q.MOE_KERNEL_SMALL), ("e4m3", q.MOE_KERNEL_TILE64), ("e4m3", q.MOE_KERNEL_TILE128),
+        ("e2m1", q.MOE_KERNEL_TILE64), ("e2m1", q.MOE_KERNEL_TILE128), ("e2m1", q.MOE_KERNEL_TILE64_SPLIT_K)]
+
+
+@pytest.mark.parametrize("act,kernel", MANY)
+@pytest.mark.parametrize("E,N,K", [(64, 320, 384), (65, 320, 384), (128, 64, 384), (130, 320, 512), (1000, 64, 384),
+                                   (1024, 64, 384)])
+def test_product_many_experts(act, kernel, E, N, K):
+    """Tiles found over several groups of 64 segments, against float64."""
+    p = Product(E + N, E, N, K, act, sparse_counts(E, np.random.default_rng(E)), k=2)
+    check_product(p, q.MOE_EPI_NONE_F32, kernel, f"{act} {E} experts {N}x{K}")
+    check_product(p, q.MOE_EPI_SWIGLU_E4M3, kernel, f"{act} {E} experts {N}x{K}")
+
+
+@pytest.mark.parametrize("act,kernel", MANY)
+def test_product_of_blocks_that_are_not_numbers(act, kernel):
+    """Blocks as the quantisation leaves them for an infinity or NaN (scale byte 255, codes 0), in rows and in weights:
+    the whole row, the expert's channel."""
+    E, N, K = 2, 64, 512
+    g = torch.Generator(device=DEV).manual_seed(4)
+    wv, xv = torch.randn(E, N, K, device=DEV, generator=g), torch.randn(150, K, device=DEV, generator=g)
+    wv[1, 33, 200], xv[7, 450], xv[100, 3] = float("inf"), float("nan"), float("-inf")
+    w = q.moe_mx_repack(q.mx_experts(q.moe_quantize_mx(wv, q.MOE_MX_E2M1)))
+    a = q.moe_quantize_mx(xv, FMT[act])
+    show("not numbers", act, kernel)
+    y = q.moe_grouped_mxgemm(w, a, dev(np.array([0, 90, 150], np.int32)), 150, q.MOE_EPI_NONE_F32, kernel=kernel)
+    want = torch.zeros(150, N, dtype=torch.bool, device=DEV)
+    want[7], want[100] = True, True
+    want[90:, 33] = True
+    assert torch.equal(torch.isnan(y), want)
+    h = q.moe_grouped_mxgemm(w, a, dev(np.array([0, 90, 150], np.int32)), 150, q.MOE_EPI_SWIGLU_E4M3, kernel=kernel)
+    bad = torch.zeros(150, 1, dtype=torch.bool, device=DEV)
+    bad[7], bad[100], bad[90:] = True, True, True
+    assert torch.equal(h.scales == 255, bad)
 
 
 # ------------------------------------------------------------------- the layer
