@@ -512,7 +512,7 @@ moe_status moe_grouped_mxgemm(const moe_mxdesc* w, const uint8_t* a_codes, const
  *           magnitudes up to 65504, larger expert outputs become infinite there)
  *   out     bf16 [T][H]
  * Alignment as for those calls.  Every argument is checked before anything is
- * launched; T == 0 writes nothing.  T * k < 2^31, k <= E.
+ * launched; T == 0 writes nothing.  T < 2^24, T * k < 2^31, k <= E.
  */
 typedef struct moe_mxlayer {
   int32_t abi_version; /* MOE_ABI_VERSION */

@@ -242,6 +242,8 @@ moe_status moe_mx_layer(const moe_mxlayer* l, void* stream) {
   st = check_route(l->logits, l->bias, T, E, k, l->score, l->n_group, l->topk_group, l->group_top, l->scale,
                    l->topk_ids, l->topk_w);
   if (st != MOE_OK) return st;
+  // (the combine's launch, 256 threads a token, has fewer than 2^32 threads)
+  if (T >= 1 << 24) return fail(MOE_ERR_BAD_SHAPE, "T=%d (fewer than 2^24)", T);
   if (l->x && !known_dtype(l->x_dtype)) return fail(MOE_ERR_BAD_FORMAT, "x_dtype %d", l->x_dtype);
   if (!known_fmt(l->x_fmt) || !known_fmt(l->h_fmt))
     return fail(MOE_ERR_BAD_FORMAT, "unknown MX format (x %d, h %d)", l->x_fmt, l->h_fmt);
