@@ -541,6 +541,7 @@ typedef struct moe_mxlayer {
   void* y;
   uint16_t* out;
 } moe_mxlayer;
+/* 0 for arguments that no layer takes. */
 size_t moe_mx_layer_workspace_size(int32_t T, int32_t k, int32_t E);
 moe_status moe_mx_layer(const moe_mxlayer* layer, void* stream);
 

@@ -2,6 +2,7 @@
 // and the MX grouped product: host-side validation, then one stream-ordered
 // launch.  Plain C++, the manner of abi.cpp.
 #include <math.h>
+#include <stdint.h>
 
 #include "moe_qexpert.h"
 #include "abi_util.h"
@@ -223,7 +224,8 @@ moe_status moe_grouped_mxgemm(const moe_mxdesc* w, const uint8_t* a_codes, const
 }
 
 size_t moe_mx_layer_workspace_size(int32_t T, int32_t k, int32_t E) {
-  if (T < 0 || k < 1 || E < 1 || E > 1024 || T >= 1 << 25 || (int64_t)T * k >= ((int64_t)1 << 31)) return 0;
+  // (pairs are rounded up to whole chunks in 32 bits)
+  if (T < 0 || k < 1 || E < 1 || E > 1024 || T >= 1 << 25 || (int64_t)T * k > INT32_MAX - moe::kPermuteChunk) return 0;
   return moe::mx_layer_workspace_bytes(T, k, E);
 }
 

@@ -41,3 +41,13 @@ def test_layer_refuses_more_tokens_than_its_combine_takes(lib):
         assert layer_call(lib, T, y_dtype=9) == BAD_SHAPE
         assert b"2^24" in lib.moe_last_error_detail()
     assert layer_call(lib, (1 << 24) - 1, y_dtype=9) == BAD_FORMAT
+
+
+def test_layer_workspace_next_to_the_largest_pair_count(lib):
+    """No size comes from a pair count that overflows when it is rounded up to whole chunks."""
+    size = lib.moe_mx_layer_workspace_size
+    for T, k in ((2099201, 1023), (33038209, 65), (8259545, 260)):
+        assert 2 ** 31 - 2048 < T * k < 2 ** 31 and size(T, k, 1024) == 0
+    nb = -(-2097000 * 1023 // 2048)  # chunks of pairs, a flag and 1025 counters each
+    up = lambda v: -(-v // 256) * 256  # noqa: E731
+    assert size(2097000, 1023, 1024) == 256 + up(4 * nb) + up(4 * 1025 * nb)
