@@ -56,13 +56,20 @@ __device__ __forceinline__ i32x8 operand(u32x4 lo, u32x4 hi) {
   const i32x4 a = __builtin_bit_cast(i32x4, lo), b = __builtin_bit_cast(i32x4, hi);
   return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
 }
-// STEP (0, 1): weight scale in byte WB of ws, activation scale in byte 2 * STEP
-// of as (shifted by the lane's half beforehand).
+// Weight scale in byte WB of ws, activation scale in byte AB of as (shifted by the
+// lane's half beforehand).
 template <int AF, int WB, int AB>
 __device__ __forceinline__ f32x16 mx_mfma(i32x8 w, i32x8 x, f32x16 c, uint32_t ws, uint32_t as) {
   return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(w, x, c, 4, AF == kE4M3 ? 0 : 4, WB, (int)ws, AB, (int)as);
 }
 
+// Fast exponential and reciprocal, as in the library's other SwiGLU epilogues.  The
+// exponential's argument is off by 1.5 |g| 2^-24 (log2 e and the product rounded),
+// it, the sum, the reciprocal and the products by 7 * 2^-24 together, relative: below
+// 2^-21 for g >= 0, where the sum damps the first term, (1.5 |g| + 7) 2^-24 for g < 0
+// (2^-19 at -16); below -88 the exponential is infinite and the result 0, as in
+// float32 arithmetic.  What follows rounds to bf16 (2^-9) or an MX element (2^-4 or
+// more).
 __device__ __forceinline__ float silu_mul(float g, float u) {
   return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)) * u;
 }
@@ -629,9 +636,10 @@ __device__ __forceinline__ void mx_tile_body(const MxK& p, const Tile& c, u32x4*
 
   int first = 0;  // the row tile of acc[0]
   if constexpr (KS == 2) {
-    // A group with a chunk less waits at as many barriers (one a stage; stages of a
-    // chunk are taken in twos); then the groups exchange sums, each keeps half the rows.
-    auto barriers = [](int chunks) { return SS == 2 ? 2 * chunks : (chunks + 1) / 2 * 2; };
+    // A group with a chunk less waits at as many barriers (the loop takes chunks in
+    // twos); then the groups exchange sums, each keeps half the rows.
+    static_assert(SS == 4, "barriers counts the one-stage loop's");
+    auto barriers = [](int chunks) { return (chunks + 1) / 2 * 2; };
     for (int i = barriers(n); i < barriers(per_group); ++i) __builtin_amdgcn_s_barrier();
     constexpr int Q = RT / 2 * 4;  // 16-byte quarters of the sums that a lane gives away at a time
     f32x4* const out = red + (size_t)all * Q * 64 + lane;
