@@ -93,9 +93,8 @@ __device__ __forceinline__ int source_row(const MxK& p, int row) {
 // group of 32); its NW wavefronts split K and add their sums through LDS.  Weights
 // and activations go from memory straight to the operand registers: each weight
 // byte is read once per 32 rows.  Bound by the weights' bytes (8 experts of 4096 x
-// 14336, 32 rows in all: 249 MB in 45 us, 5.5 TB/s with what the 256 MB cache still
-// holds) and, with few workgroups, by the latency of a wavefront's K / 4 range:
-// 6.5 us for 8 experts of 2048 x 2048.
+// 14336, 32 rows in all: 249 MB in 47 us, 5.3 TB/s) and, with few workgroups, by the
+// latency of a wavefront's K / 4 range: 8.1 us for 8 experts of 2048 x 2048.
 template <int AF>
 struct SmallBlock {  // operands of one K block of 128
   u32x4 w[2][2];     // [channel tile][step]
@@ -269,14 +268,18 @@ __global__ __launch_bounds__(256, 3) void mx_small_kernel(MxK p) {
 // only one wavefront uses, straight into its registers.  Workgroups share a CU (2 of
 // 128 rows, 3 of 64), so one multiplies while another waits at its barrier.
 //
-// Measured, 65536 rows over 64 experts of 2048 x 2048, SwiGLU: e4m3 rows 217 us,
-// 2.5 PF (the clock under this load bounds it: registers alone reach 3.5); e2m1
-// rows 147 us, 3.7 PF (the loads' way through the caches; 158 us with stages of
-// 128 inputs, as their loads are under way only half as long).  512 tokens x 2 of 8
-// experts, 4096 x 14336, e2m1 rows: 66 us, of which 53 us are the weights' bytes.
-// Stages of 256 e4m3 inputs for 128: 64-row tiles 914 -> 853 us (8192 rows over 8
-// experts of 28672 x 4096), 19.4 -> 15.4 (192 rows each, 16 of 448 x 4096); 128-row
-// tiles, short of registers with them, 218 -> 223 and 46 -> 50 (above, 1280 x 8).
+// Measured with weights from memory (sets of 1 GB and more in turn), 65536 rows over
+// 64 experts of 2048 x 2048, SwiGLU to MX rows: e4m3 rows 227 us, 2.4 PF (the clock
+// under this load bounds it: registers alone reach 3.5); e2m1 rows 164 us, 3.4 PF
+// (the loads' way through the caches).  512 tokens x 2 of 8 experts, 4096 x 14336,
+// e2m1 rows: 74 to 78 us, of which 53 are the weights' bytes.
+// Variants below were compared with the same weights call after call, which stay in
+// the 256 MB cache where they fit, and are faster by that.
+// Stages of 256 e2m1 inputs for 128: 158 -> 147 us (above; loads are under way twice
+// as long).  Of 256 e4m3 inputs: 64-row tiles 914 -> 853 us (8192 rows over 8 experts
+// of 28672 x 4096), 19.4 -> 15.4 (192 rows each, 16 of 448 x 4096; one register of
+// the SwiGLU and fp32 kernels is spilled over the loop); 128-row tiles, short of
+// registers with them, 218 -> 223 and 46 -> 50 (above, 1280 x 8).
 //
 // Each XCD (workgroups are dealt to the 8 of them in turn) takes a contiguous
 // range of tiles, so that the weights and rows its CUs share stay in its L2.
@@ -493,9 +496,10 @@ __device__ __forceinline__ void mx_tile_body(const MxK& p, const Tile& c, u32x4*
   Frag f[RT];
   // Step j of a chunk: multiplies f and replaces it, row tile by row tile, with
   // the next step's fragments (of stage xs; not after the last).  128-row tiles at
-  // raised priority, which also keeps the compiler from moving loads into it: 512
-  // tokens x 2 of 8 experts, 4096 x 14336, e2m1 rows 74 -> 66 us, 65536 rows 152 ->
-  // 147, e4m3 rows 1 % less; 64-row tiles take 5 % longer with it.
+  // raised priority, which also keeps the compiler from moving loads into it (with
+  // weights from memory: 512 tokens x 2 of 8 experts, 4096 x 14336, e2m1 rows 86 -> 78
+  // us, 65536 rows 170 -> 164, e4m3 rows the same); 64-row tiles take 5 % longer with
+  // it.
   auto step = [&](auto j_tag, const Scales& sc, const RowScales& xsc, auto first_tag, const u32x4* xs, auto next_tag) {
     constexpr int J = decltype(j_tag)::value, S = J % SS;
     if constexpr (TM == 128) __builtin_amdgcn_s_setprio(1);

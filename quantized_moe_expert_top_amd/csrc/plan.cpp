@@ -155,16 +155,19 @@ size_t mx_layer_workspace_bytes(int T, int k, int E) {
 // a: launch and set-up, b: one workgroup alone on its CU, c: a CU's throughput,
 // d: its last workgroups running alone.  Fitted to 346 measured problems (E 8 to
 // 64, 1 to 1024 rows per expert, N 448 to 28672, K 512 to 14336, 8- and 4-bit
-// rows); the estimates are within about 20 % of the times, and where two paths
-// are that close either is taken: on average 1 % above the better.  E.g. 8
-// experts of 2048 x 2048, us for 32-row / 64-row / 128-row tiles: 6.5 / 9.8 / 10.0 at
-// 16 rows per expert, 17.9 / 11.2 / 14.6 at 128; 64 experts at 512 rows: 450 / 148 /
-// 131.
+// rows alike) with weights that stay in the cache where they fit, and before the
+// kernels' last changes.  They rank the paths rather than tell the time: over 260
+// problems with weights from memory four in five times are 0.72 to 1.45 of the
+// estimate (all 0.59 to 1.94), the path taken 1.3 % above the best of all on average,
+// over 10 % in 10 of them, 33 % at most (8 experts of 2048 x 2048, 32 e2m1 rows each:
+// 12.0 for 9.0 us).  E.g. 8 experts of 2048 x 2048, e4m3 rows, us for 32-row / 64-row /
+// 128-row tiles: 8.4 / 11.2 / 11.0 at 16 rows per expert, 18.8 / 12.2 / 17.5 at 128; 64
+// experts at 512 rows: 453 / 134 / 126.
 // 64-row tiles of e2m1 rows split K over two groups of wavefronts where K is long
 // and every workgroup has a CU of its own: 8 experts of 4096 x 14336, 32 rows each
-// 45 -> 40 us, 16 of 448 x 4096, 192 rows 14.9 -> 13.8; with K = 2048 9.6 -> 9.8, with
-// 320 workgroups 56 -> 59.  With e4m3 rows, whose stages hold twice the bytes, the
-// split loses (15.4 -> 16.2).
+// 72 -> 65 us, 16 of 448 x 4096, 192 rows 18.6 -> 17.4; with K = 2048 11.9 both, with
+// 768 workgroups 48 -> 58.  With e4m3 rows, whose stages hold twice the bytes, the
+// split lost (15.4 -> 16.2).
 int mxgemm_path(int M_total, int E, int N, int K, bool e2m1, int kernel) {
   if (kernel == 1) return 0;
   const double active = M_total < E ? M_total : E;  // experts that can have rows
