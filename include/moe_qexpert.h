@@ -369,7 +369,8 @@ moe_status moe_unpermute_combine(const void* y_perm, int32_t y_dtype, const int3
 /* ---------------------------------------------------------- scored routing
  * Top-k expert choice from scores of all experts, with an optional choice bias
  * and expert groups (moe_route_topk is the expert gate on bare logits).
- * All scores, sums and comparisons are float64; per token:
+ * All scores, sums and comparisons are float64 (scores apart by no more than that
+ * type's rounding may come in either order); per token:
  *     s_e = softmax over the E logits (MOE_SCORE_SOFTMAX) or
  *           1 / (1 + exp(-logit_e))   (MOE_SCORE_SIGMOID)
  *     c_e = s_e + bias[e]             (choice score; bias NULL: c_e = s_e)
