@@ -210,6 +210,7 @@ moe_status moe_route_permute(const float* logits, int32_t T, int32_t E, int32_t 
                                           width each, loading only that width's planes */
 #define MOE_KERNEL_TILE64_SPLIT_K 8  /* MX with e2m1 rows only: 64-row tiles, K split over two groups of
                                         wavefronts */
+#define MOE_KERNEL_TILE256 9         /* 16-bit weights only: 256 x 256 output tiles */
 
 #define MOE_EPI_NONE 0      /* out bf16 [M_total][N] */
 #define MOE_EPI_SWIGLU 1    /* N = 2*I; rows [0,I) gate, [I,2I) up; out = bf16(silu(gate) * up), width I */
@@ -365,6 +366,107 @@ moe_status moe_grouped_qgemm_noalloc(const moe_wdesc* w, const uint16_t* A, int3
 moe_status moe_unpermute_combine(const void* y_perm, int32_t y_dtype, const int32_t* pair_pos,
                                  const int32_t* n_valid, const float* topk_w, int32_t T, int32_t k, int32_t H,
                                  uint16_t* out, void* stream);
+
+/* ------------------------------------------------------- experts in 16 bits
+ * Experts whose weights stay in bf16 or fp16: the grouped product, its two
+ * gradients and the combine's, so that a layer can run, and learn, in the form
+ * its compressed weights are made from (ME-Switch page: a shared base and
+ * fine-tuned experts; D2MoE page, pipeline equation: 16-bit GEMMs).
+ *
+ * For every segment e = 0..E-1 of seg_offsets and every row i in
+ * [seg_offsets[e], seg_offsets[e+1]), with W_e = w[e] ([N][K], row-major) and
+ * a_i = A[gather_pair[i] / k] (gather_pair != NULL, A_rows rows) or A[i]:
+ *
+ *   moe_grouped_gemm               y_i = W_e a_i                 (N values)
+ *     MOE_EPI_NONE, _NONE_F16, _NONE_F32   out[i] = y_i as bf16, fp16 or fp32
+ *     MOE_EPI_SWIGLU                       out[i] = silu(y_i[:I]) * y_i[I:] in `dtype`, I = N/2;
+ *                                          pre[i] = y_i in `dtype` too, unless pre is NULL
+ *   moe_grouped_gemm_grad_rows     d_i = W_e^T dy_i              (K values)
+ *     MOE_EPI_NONE, _NONE_F16, _NONE_F32   out[i] = d_i as bf16, fp16 or fp32
+ *     MOE_EPI_SWIGLU_GRAD                  d_i is the gradient by h = silu(g) * u, with g = pre[i][:K]
+ *                                          and u = pre[i][K:] (2K values of `dtype`):
+ *                                          out[i] = [ d_i u s (1 + g (1 - s)), d_i g s ], s = 1/(1 + e^-g),
+ *                                          2K values of `dtype`
+ *   moe_grouped_gemm_grad_weights  dW_e = sum over the segment's rows i of dy_i a_i^T
+ *     MOE_EPI_NONE, _NONE_F16, _NONE_F32   out[e] = dW_e ([N][K]) as bf16, fp16 or fp32; zeros for an
+ *                                          expert without rows
+ *
+ * Products are accumulated in fp32; every output is rounded once.  The order of
+ * the sums depends on the sizes and the kernel choice alone: a call's results are
+ * bitwise repeatable.  Infinities and NaN spread as in the sums above (rows of
+ * other segments never enter, and columns past N or K never do).
+ *
+ *   dtype       MOE_DTYPE_BF16 or MOE_DTYPE_F16: type of w, A, dy and pre
+ *   w           [E][N][K]; 1 <= E <= 1024; N and K multiples of 8 (SwiGLU: N of 16)
+ *   seg_offsets i32 [E + 1] from moe_permute (device), or a slice of a longer
+ *               ascending table; rows outside [seg_offsets[0], seg_offsets[E]) are
+ *               not written (nor read, in the gradients)
+ *   M_total     host upper bound of the rows; out, dy and pre have M_total rows
+ *               (without gather_pair A has at least as many)
+ *   kernel      MOE_KERNEL_AUTO, or MOE_KERNEL_SMALL, _TILE128 or _TILE256
+ *   workspace   grad_weights: moe_grouped_gemm_grad_weights_workspace_size(...) bytes of
+ *               device memory (fp32 partial sums where a few experts' rows are split
+ *               over workgroups; 0, NULL allowed, for most sizes); nothing in it
+ *               needs to start at zero; calls that share one must be ordered on a stream
+ * One expert's weights take less than 4 GiB, as does A where it is gathered
+ * (MOE_ERR_UNSUPPORTED).  16-byte aligned buffers (offsets and pairs 4); no output
+ * may overlap an input.
+ */
+#define MOE_EPI_SWIGLU_GRAD 6
+moe_status moe_grouped_gemm(const void* w, int32_t dtype, int32_t E, int32_t N, int32_t K, const void* A, int32_t A_rows,
+                            const int32_t* gather_pair, int32_t k, const int32_t* seg_offsets, int32_t M_total,
+                            int32_t epilogue, int32_t kernel, void* pre, void* out, void* stream);
+moe_status moe_grouped_gemm_grad_rows(const void* w, int32_t dtype, int32_t E, int32_t N, int32_t K, const void* dy,
+                                      const int32_t* seg_offsets, int32_t M_total, int32_t epilogue, int32_t kernel,
+                                      const void* pre, void* out, void* stream);
+size_t moe_grouped_gemm_grad_weights_workspace_size(int32_t E, int32_t N, int32_t K, int32_t M_total, int32_t kernel);
+moe_status moe_grouped_gemm_grad_weights(const void* dy, const void* A, int32_t dtype, int32_t E, int32_t N, int32_t K,
+                                         int32_t A_rows, const int32_t* gather_pair, int32_t k,
+                                         const int32_t* seg_offsets, int32_t M_total, int32_t epilogue, int32_t kernel,
+                                         void* out, void* workspace, size_t workspace_bytes, void* stream);
+
+/* The gradient of moe_unpermute_combine, out[t] = sum_j w[t][j] * y_perm[pos(t, j)],
+ * and of the gates before it (moe_route_topk: softmax over the selected logits):
+ *     dy[pos(t, j)]         = w[t][j] * dout[t]       (of dy_dtype)
+ *     dw[t][j]              = sum_h dout[t][h] * y_perm[pos(t, j)][h]
+ *     dlogits[t][ids[t][j]] = w[t][j] * (dw[t][j] - sum_i w[t][i] * dw[t][i]), 0 elsewhere
+ * A pair whose pair_pos is at or past *n_valid has dw 0, no row of dy (left as it
+ * is) and no logit.  Sums in fp32, in an order that the sizes alone decide.
+ *   dout bf16 [T][H]; y_perm [T*k][H] of y_dtype (MOE_DTYPE_*); topk_w f32 [T][k]
+ *   (NULL: weight 1, and no dlogits); ids i32 [T][k] in [0, E) (others add nothing) and dlogits
+ *   f32 [T][E], both or neither NULL; dy [T*k][H] of dy_dtype (MOE_DTYPE_BF16 or
+ *   MOE_DTYPE_F16), dw f32 [T][k]
+ * H % 8 == 0, 1 <= k <= 1024, 1 <= E <= 1024, T < 2^24, T*k < 2^31; dout, y_perm and dy 16-byte
+ * aligned; no output may overlap an input.
+ */
+moe_status moe_unpermute_combine_grad(const uint16_t* dout, const void* y_perm, int32_t y_dtype, const int32_t* pair_pos,
+                                      const int32_t* n_valid, const float* topk_w, const int32_t* ids, int32_t T,
+                                      int32_t k, int32_t H, int32_t E, int32_t dy_dtype, void* dy, float* dw,
+                                      float* dlogits, void* stream);
+
+/* ------------------------------------------------------- low-rank adapters
+ * Many requests' adapters added to the output of a projection that they share
+ * (the other way, beside DELTA2, to serve many fine-tuned models over one base):
+ *     out[t] = y[t] + scale[a] * B_a (A_a x[t])     token t of adapter a
+ *     out[t] = y[t]                                 token without an adapter
+ * Tokens are grouped by adapter with moe_permute (k = 1, E = n, topk_ids = the
+ * tokens' adapters; an id outside [0, n), e.g. -1, means none), once for all the
+ * projections that a batch goes through.
+ *   y, out      [T][N] of y_dtype (MOE_DTYPE_*); out may be y itself
+ *   x           [T][K] of dtype (MOE_DTYPE_BF16 or MOE_DTYPE_F16), A [n][r][K] and
+ *               B [n][N][r] too
+ *   scale       f32 [n], or NULL for 1
+ *   seg_offsets i32 [n + 1], rows i32 [T]: moe_permute's seg_offsets and sorted_pair
+ * Both products are accumulated in fp32; scale * (A_a x) enters the second one as a
+ * sum of two 16-bit numbers (16 significant bits in bf16, 22 in fp16), and out is
+ * rounded once.  In fp16, scale * (A_a x) past 65504 is infinite.
+ * 1 <= n <= 1024, T < 2^24, r a multiple of 8 up to 128 (pad others with zeros), K and N
+ * multiples of 8; x, A and B less than 4 GiB each; 16-byte aligned buffers (scale, offsets
+ * and rows 4); no other buffers may overlap.
+ */
+moe_status moe_adapter_add(const void* y, int32_t y_dtype, const void* x, const void* A, const void* B, int32_t dtype,
+                           const float* scale, int32_t n, int32_t r, int32_t K, int32_t N, const int32_t* seg_offsets,
+                           const int32_t* rows, int32_t T, void* out, void* stream);
 
 /* ---------------------------------------------------------- scored routing
  * Top-k expert choice from scores of all experts, with an optional choice bias

@@ -21,6 +21,7 @@ MOE_W_INT4_GROUP, MOE_W_MWQ_2_3_4, MOE_W_DELTA2_SALIENT, MOE_W_INT_PER_EXPERT = 
 MOE_LAYOUT_CANONICAL, MOE_LAYOUT_TILED = 0, 1
 MOE_EPI_NONE, MOE_EPI_SWIGLU, MOE_EPI_NONE_F32, MOE_EPI_NONE_F16 = 0, 1, 2, 3
 MOE_EPI_SWIGLU_E4M3, MOE_EPI_SWIGLU_E2M1 = 4, 5  # grouped MX product only
+MOE_EPI_SWIGLU_GRAD = 6  # gradient by the rows of a 16-bit product only
 MOE_DTYPE_BF16, MOE_DTYPE_F32, MOE_DTYPE_F16 = 0, 1, 2
 MOE_MX_E4M3, MOE_MX_E2M1 = 1, 2
 MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
@@ -28,7 +29,8 @@ MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
 _EPI_DTYPE = {MOE_EPI_NONE_F32: torch.float32, MOE_EPI_NONE_F16: torch.float16}
 _DTYPE_EPI = {torch.float32: MOE_EPI_NONE_F32, torch.float16: MOE_EPI_NONE_F16, torch.bfloat16: MOE_EPI_NONE}
 (MOE_KERNEL_AUTO, MOE_KERNEL_SMALL, MOE_KERNEL_SMALL_PER_WIDTH, MOE_KERNEL_TILE64_WIDE, MOE_KERNEL_TILE64,
- MOE_KERNEL_TILE128, MOE_KERNEL_LDS_DMA, MOE_KERNEL_LDS_DMA_PER_WIDTH, MOE_KERNEL_TILE64_SPLIT_K) = range(9)
+ MOE_KERNEL_TILE128, MOE_KERNEL_LDS_DMA, MOE_KERNEL_LDS_DMA_PER_WIDTH, MOE_KERNEL_TILE64_SPLIT_K,
+ MOE_KERNEL_TILE256) = range(10)
 (MOE_FIELD_CODES, MOE_FIELD_PLANE3, MOE_FIELD_PLANE4, MOE_FIELD_SCALES,
  MOE_FIELD_SALIENT_IDX, MOE_FIELD_SALIENT_VAL, MOE_FIELD_BASE) = range(7)
 
@@ -39,6 +41,8 @@ EXPORTED = [
     "moe_grouped_qgemm_noalloc", "moe_grouped_qgemm_noalloc_scratch_bytes", "moe_copy_rows_async",
     "moe_route_scored", "moe_quantize_mx", "moe_dequantize_mx", "moe_rmsnorm_mx", "moe_mx_field_bytes",
     "moe_mx_repack", "moe_grouped_mxgemm", "moe_mx_layer", "moe_mx_layer_workspace_size",
+    "moe_grouped_gemm", "moe_grouped_gemm_grad_rows", "moe_grouped_gemm_grad_weights",
+    "moe_grouped_gemm_grad_weights_workspace_size", "moe_unpermute_combine_grad", "moe_adapter_add",
 ]
 
 
@@ -110,6 +114,13 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "moe_grouped_mxgemm": (i32, [mxd, vp, vp, i32, i32, vp, i32, vp, i32, i32, i32, vp, vp, vp]),
         "moe_mx_layer_workspace_size": (sz, [i32, i32, i32]),
         "moe_mx_layer": (i32, [ctypes.POINTER(MxLayer), vp]),
+        "moe_grouped_gemm": (i32, [vp, i32, i32, i32, i32, vp, i32, vp, i32, vp, i32, i32, i32, vp, vp, vp]),
+        "moe_grouped_gemm_grad_rows": (i32, [vp, i32, i32, i32, i32, vp, vp, i32, i32, i32, vp, vp, vp]),
+        "moe_grouped_gemm_grad_weights_workspace_size": (sz, [i32, i32, i32, i32, i32]),
+        "moe_grouped_gemm_grad_weights": (i32, [vp, vp, i32, i32, i32, i32, i32, vp, i32, vp, i32, i32, i32, vp, vp, sz,
+                                                vp]),
+        "moe_unpermute_combine_grad": (i32, [vp, vp, i32, vp, vp, vp, vp, i32, i32, i32, i32, i32, vp, vp, vp, vp]),
+        "moe_adapter_add": (i32, [vp, i32, vp, vp, vp, i32, vp, i32, i32, i32, i32, vp, vp, i32, vp, vp]),
     }
     for name, (res, args) in sig.items():
         f = getattr(lib, name)
@@ -465,3 +476,7 @@ from .mx import (  # noqa: E402  (the MX path builds on the names above)
     MxExperts, MxLayerBuffers, MxRows, NormOutput, ScoredRouting, alloc_mx_layer, alloc_mx_rows, moe_dequantize_mx,
     moe_grouped_mxgemm, moe_mx_field_bytes, moe_mx_layer_forward, moe_mx_repack, moe_quantize_mx, moe_rmsnorm_mx,
     moe_route_scored, mx_experts)
+from .dense import (  # noqa: E402
+    CombineGrad, ExpertLayerBuffers, ExpertLayerGrads, alloc_expert_layer, moe_adapter_add, moe_expert_layer_backward,
+    moe_expert_layer_forward, moe_grouped_gemm, moe_grouped_gemm_grad_rows, moe_grouped_gemm_grad_weights,
+    moe_grouped_gemm_grad_weights_workspace_size, moe_unpermute_combine_grad)

@@ -14,8 +14,8 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libmoe_qexpert.so")
 PROBE_LIB = os.path.join(HERE, "libmoe_probe.so")  # measurement-only ceiling probes (bench.py)
 SOURCES = ["route.hip", "permute.hip", "qgemm.hip", "combine.hip", "repack.hip", "runtime.hip",
-           "route_scored.hip", "mx.hip", "mxgemm.hip"]
-HOST_SOURCES = ["abi.cpp", "abi_mx.cpp", "plan.cpp"]  # validation and launch planning: plain C++, no HIP headers
+           "route_scored.hip", "mx.hip", "mxgemm.hip", "gemm16.hip", "combine_grad.hip", "adapter.hip"]
+HOST_SOURCES = ["abi.cpp", "abi_mx.cpp", "abi_dense.cpp", "plan.cpp"]  # validation and launch planning: plain C++, no HIP headers
 
 HIPCC = os.environ.get("HIPCC", shutil.which("hipcc") or "/opt/rocm/bin/hipcc")
 CXX = os.environ.get("CXX", shutil.which("g++") or "g++")

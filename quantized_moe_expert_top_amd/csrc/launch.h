@@ -193,4 +193,63 @@ constexpr int kMxSplit = 65;  // 64-row tiles (e2m1 rows) with K split over two 
 int mxgemm_path(int M_total, int E, int N, int K, bool e2m1, int kernel);
 int launch_mxgemm(const MxGemmArgs& a, void* stream);
 
+// ------------------------------------------------------- experts in 16 bits
+// Rows by expert segment, [seg[e], seg[e + 1]), clamped to M_total.
+struct Gemm16Args {
+  const void* w;   // [E][N][K] (not in the weights' gradient)
+  const void* a;   // [A_rows][K], gathered or grouped (forward, weights' gradient)
+  const void* dy;  // [M_total][N] (gradients)
+  int dtype;       // MOE_DTYPE_BF16 or MOE_DTYPE_F16
+  int E, N, K;
+  int A_rows;
+  const int32_t* gather;
+  int k;
+  const int32_t* seg;
+  int M_total;
+  int epilogue;  // MOE_EPI_*
+  int kernel;    // MOE_KERNEL_*
+  const void* pre_in;
+  void* pre_out;
+  void* out;
+  void* ws;
+};
+int launch_gemm16(const Gemm16Args& a, void* stream);
+int launch_gemm16_grad_rows(const Gemm16Args& a, void* stream);
+size_t gemm16_grad_weights_workspace_bytes(int E, int N, int K, int M_total, int kernel);
+int launch_gemm16_grad_weights(const Gemm16Args& a, void* stream);
+
+struct CombineGradArgs {
+  const uint16_t* dout;
+  const void* y;
+  int y_dtype;  // MOE_DTYPE_*
+  const int32_t* pos;
+  const int32_t* n_valid;  // or nullptr
+  const float* w;          // or nullptr
+  const int32_t* ids;      // or nullptr
+  int T, k, H, E;
+  int dy_dtype;  // MOE_DTYPE_BF16 or MOE_DTYPE_F16
+  void* dy;
+  float* dw;
+  float* dlogits;  // or nullptr
+};
+int launch_combine_grad(const CombineGradArgs& a, void* stream);
+
+// ------------------------------------------------------- low-rank adapters
+struct AdapterArgs {
+  const void* y;
+  int y_dtype;  // MOE_DTYPE_*
+  const void* x;
+  const void* A;
+  const void* B;
+  int dtype;           // MOE_DTYPE_BF16 or MOE_DTYPE_F16
+  const float* scale;  // or nullptr
+  int n, r, K, N;
+  const int32_t* seg;
+  const int32_t* rows;
+  int T;
+  void* out;
+};
+constexpr int kAdapterMaxRank = 128;
+int launch_adapter_add(const AdapterArgs& a, void* stream);
+
 }  // namespace moe
