@@ -222,6 +222,8 @@ __device__ __forceinline__ void tile_body(const GemmK& p, const Tile& c, int epi
   // DMAs of step st into a stage; past the sum's end zeros.
   auto issue = [&](char* stage, int st) {
     const int left = red - 64 * st;  // k of this step and later ones
+    // (as a scalar: the compiler clamps on the vector side, and would loop over the lanes for the descriptor)
+    const uint32_t rows = (uint32_t)__builtin_amdgcn_readfirstlane(max(min(left, 64), 0));
     const uint32_t adv = (uint32_t)min(st, n - 1) * 128u;
     if constexpr (PT) {
       if constexpr (GATHER) {
@@ -240,7 +242,7 @@ __device__ __forceinline__ void tile_body(const GemmK& p, const Tile& c, int epi
           __builtin_amdgcn_raw_ptr_buffer_load_lds(pr, (__attribute__((address_space(3))) void*)(stage + (4 * wv + i) * 1024), 16, off[i], 0, 0, 0);
       } else {
         const uint32_t row = 2u * (uint32_t)na;  // bytes
-        const rsrc_t pr = make_rsrc(pbase + (size_t)(64 * st) * na, (uint32_t)max(min(left, 64), 0) * row);
+        const rsrc_t pr = make_rsrc(pbase + (size_t)(64 * st) * na, rows * row);
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           __builtin_amdgcn_raw_ptr_buffer_load_lds(pr, (__attribute__((address_space(3))) void*)(stage + (4 * wv + i) * 1024), 16, po[i], 0, 0, 0);
@@ -253,7 +255,7 @@ __device__ __forceinline__ void tile_body(const GemmK& p, const Tile& c, int epi
                                                  pk[i & 1] < left ? po[i] : kOut, adv, 0, 0);
     }
     if constexpr (QT) {
-      const rsrc_t qr = make_rsrc(qbase + (size_t)(64 * st) * p.N, (uint32_t)max(min(left, 64), 0) * (2u * (uint32_t)p.N));
+      const rsrc_t qr = make_rsrc(qbase + (size_t)(64 * st) * p.N, rows * (2u * (uint32_t)p.N));
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         __builtin_amdgcn_raw_ptr_buffer_load_lds(qr, (__attribute__((address_space(3))) void*)(stage + 32768 + (4 * wv + i) * 1024), 16, qo[i], 0, 0, 0);
@@ -273,8 +275,8 @@ __device__ __forceinline__ void tile_body(const GemmK& p, const Tile& c, int epi
   auto read_direct = [&](const char* at, int row, int s) {
     return *reinterpret_cast<const u32x4*>(at + row * 128 + (((2 * s + half) ^ swz(row)) << 4));
   };
-  auto read_trans = [&](const char* at, int x0, int s) {  // 32 columns from x0
-    const int j = (lane >> 2) & 3, u = (x0 >> 4) + ((lane >> 4) & 1);
+  auto read_trans = [&](const char* at, int x0, int s) {  // 16 columns from x0, 16 from x0 + 64
+    const int j = (lane >> 2) & 3, u = (x0 >> 4) + 4 * ((lane >> 4) & 1);
     const char* from = at + (16 * s + 8 * half + j) * 512 + ((u ^ j) << 5) + ((lane & 3) << 3);
     const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(from));
     const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(from + 2048));
@@ -285,18 +287,20 @@ __device__ __forceinline__ void tile_body(const GemmK& p, const Tile& c, int epi
     Frags f;
 #pragma unroll
     for (int t = 0; t < 2; ++t)
-      f.p[t] = PT ? read_trans(stage, 64 * wa + 32 * t, s) : read_direct(stage, 64 * wa + 32 * t + col, s);
+      f.p[t] = PT ? read_trans(stage, 128 * (wa >> 1) + 32 * (wa & 1) + 16 * t, s) : read_direct(stage, 64 * wa + 32 * t + col, s);
 #pragma unroll
     for (int j = 0; j < NB; ++j)
-      f.q[j] = QT ? read_trans(stage + 32768, 64 * j + 32 * wb, s) : read_direct(stage + 32768, 64 * j + 32 * wb + col, s);
+      f.q[j] = QT ? read_trans(stage + 32768, 128 * (j >> 1) + 32 * (j & 1) + 16 * wb, s) : read_direct(stage + 32768, 64 * j + 32 * wb + col, s);
     return f;
   };
   f32x16 acc[2][NB] = {};
   auto mul = [&](const Frags& f) {
+    __builtin_amdgcn_s_setprio(1);
 #pragma unroll
     for (int t = 0; t < 2; ++t)
 #pragma unroll
       for (int j = 0; j < NB; ++j) acc[t][j] = mfma32t<F16>(f.p[t], f.q[j], acc[t][j]);
+    __builtin_amdgcn_s_setprio(0);
   };
   // Every wavefront's reads of a stage are done and the other stage's DMAs landed.
   auto ready = [&] {
@@ -339,7 +343,11 @@ __device__ __forceinline__ void tile_body(const GemmK& p, const Tile& c, int epi
   // neighbouring lanes store 128 bytes and more in a row.  Lane (half, col) holds
   // b = col and of tile t a = 32t + 8g + 4*half + 0..3 in registers 4g ...
   char* const eb = sA + wv * 8192;
-  const int a0 = GLU && MODE == kForward ? 128 * c.ab + 32 * wa : 256 * c.ab + 64 * wa;
+  const int a0 = GLU && MODE == kForward ? 128 * c.ab + 32 * wa : PT ? 256 * c.ab + 128 * (wa >> 1) + 32 * (wa & 1) : 256 * c.ab + 64 * wa;
+  // channel of place x of the wavefront's 64
+  auto a_of = [&](int x) { return a0 + (PT ? (x & 31) + 64 * (x >> 5) : x); };
+  // the places of 8 channels (fp32: 4) of tile t, register group g
+  auto chunk16 = [&](int t, int g) { return PT ? 4 * (g >> 1) + 2 * t + (g & 1) : 4 * t + g; };
   auto put16 = [&](int ck, float v0, float v1, float v2, float v3, bool f16) {  // 8 chunks a row
     const u32x2 d = f16 ? u32x2{pack16x2<true>(v0, v1), pack16x2<true>(v2, v3)} : u32x2{pack_bf16x2(v0, v1), pack_bf16x2(v2, v3)};
     *reinterpret_cast<u32x2*>(eb + col * 128 + ((ck ^ (col & 7)) << 4) + 8 * half) = d;
@@ -347,7 +355,8 @@ __device__ __forceinline__ void tile_body(const GemmK& p, const Tile& c, int epi
   auto get16 = [&](int r, int ck) { return *reinterpret_cast<const u32x4*>(eb + r * 128 + ((ck ^ (r & 7)) << 4)); };
 #pragma unroll
   for (int j = 0; j < NB; ++j) {
-    const int b = c.b0 + 64 * j + 32 * wb;  // + row within the 32
+    const int b = c.b0 + (QT ? 128 * (j >> 1) + 32 * (j & 1) + 16 * wb : 64 * j + 32 * wb);  // of the 32's first row
+    auto b_of = [&](int r) { return b + (QT ? (r & 15) + 64 * (r >> 4) : r); };
     const int bend = MODE == kWeights ? p.N : c.s1;
     const size_t out0 = MODE == kWeights ? (size_t)c.e * p.N : 0;
     if constexpr (GLU && MODE == kForward) {
@@ -361,8 +370,8 @@ __device__ __forceinline__ void tile_body(const GemmK& p, const Tile& c, int epi
         for (int i = 0; i < 4; ++i) {
           const int r = 8 * i + (lane >> 3), ck = lane & 7, ch = a0 + 8 * (ck & 3);
           const u32x4 v = get16(r, ck);
-          if (b + r < bend && ch < I)
-            *reinterpret_cast<u32x4*>(p.pre_out + (size_t)(b + r) * p.N + (ck >> 2 ? I : 0) + ch) = v;
+          if (b_of(r) < bend && ch < I)
+            *reinterpret_cast<u32x4*>(p.pre_out + (size_t)b_of(r) * p.N + (ck >> 2 ? I : 0) + ch) = v;
         }
       }
 #pragma unroll
@@ -379,25 +388,25 @@ __device__ __forceinline__ void tile_body(const GemmK& p, const Tile& c, int epi
       for (int i = 0; i < 2; ++i) {
         const int r = 16 * i + (lane >> 2), ck = lane & 3;
         const u32x4 v = get16(r, ck);
-        if (b + r < bend && a0 + 8 * ck < I)
-          *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(p.out) + (size_t)(b + r) * I + a0 + 8 * ck) = v;
+        if (b_of(r) < bend && a0 + 8 * ck < I)
+          *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(p.out) + (size_t)b_of(r) * I + a0 + 8 * ck) = v;
       }
     } else if (GLU || epi == kEpiF32) {
 #pragma unroll
       for (int t = 0; t < 2; ++t)
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
-          const int ck = 8 * t + 2 * g + half;  // 16 chunks a row
+          const int ck = 2 * chunk16(t, g) + half;  // 16 chunks a row
           *reinterpret_cast<f32x4*>(eb + col * 256 + ((ck ^ (col & 15)) << 4)) =
               f32x4{acc[t][j][4 * g], acc[t][j][4 * g + 1], acc[t][j][4 * g + 2], acc[t][j][4 * g + 3]};
         }
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const int r = 4 * i + (lane >> 4), ck = lane & 15, ch = a0 + 4 * ck;
+        const int r = 4 * i + (lane >> 4), ck = lane & 15, ch = a_of(4 * ck);
         const f32x4 v = *reinterpret_cast<const f32x4*>(eb + r * 256 + ((ck ^ (r & 15)) << 4));
-        if (b + r >= bend || ch >= na) continue;
+        if (b_of(r) >= bend || ch >= na) continue;
         if constexpr (GLU) {
-          const size_t at = (size_t)(b + r) * 2 * p.K + ch;
+          const size_t at = (size_t)b_of(r) * 2 * p.K + ch;
           const u32x2 gv = *reinterpret_cast<const u32x2*>(p.pre_in + at), uv = *reinterpret_cast<const u32x2*>(p.pre_in + at + p.K);
           float dg[4], du[4];
 #pragma unroll
@@ -413,7 +422,7 @@ __device__ __forceinline__ void tile_body(const GemmK& p, const Tile& c, int epi
           *reinterpret_cast<u32x2*>(o) = u32x2{pack16x2<F16>(dg[0], dg[1]), pack16x2<F16>(dg[2], dg[3])};
           *reinterpret_cast<u32x2*>(o + p.K) = u32x2{pack16x2<F16>(du[0], du[1]), pack16x2<F16>(du[2], du[3])};
         } else {
-          *reinterpret_cast<f32x4*>(static_cast<float*>(p.out) + (out0 + b + r) * na + ch) = v;
+          *reinterpret_cast<f32x4*>(static_cast<float*>(p.out) + (out0 + b_of(r)) * na + ch) = v;
         }
       }
     } else {
@@ -421,13 +430,13 @@ __device__ __forceinline__ void tile_body(const GemmK& p, const Tile& c, int epi
       for (int t = 0; t < 2; ++t)
 #pragma unroll
         for (int g = 0; g < 4; ++g)
-          put16(4 * t + g, acc[t][j][4 * g], acc[t][j][4 * g + 1], acc[t][j][4 * g + 2], acc[t][j][4 * g + 3], epi == kEpiF16);
+          put16(chunk16(t, g), acc[t][j][4 * g], acc[t][j][4 * g + 1], acc[t][j][4 * g + 2], acc[t][j][4 * g + 3], epi == kEpiF16);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const int r = 8 * i + (lane >> 3), ck = lane & 7, ch = a0 + 8 * ck;
+        const int r = 8 * i + (lane >> 3), ck = lane & 7, ch = a_of(8 * ck);
         const u32x4 v = get16(r, ck);
-        if (b + r < bend && ch < na)
-          *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(p.out) + (out0 + b + r) * na + ch) = v;
+        if (b_of(r) < bend && ch < na)
+          *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(p.out) + (out0 + b_of(r)) * na + ch) = v;
       }
     }
   }
