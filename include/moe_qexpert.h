@@ -397,7 +397,7 @@ moe_status moe_unpermute_combine(const void* y_perm, int32_t y_dtype, const int3
  * other segments never enter, and columns past N or K never do).
  *
  *   dtype       MOE_DTYPE_BF16 or MOE_DTYPE_F16: type of w, A, dy and pre
- *   w           [E][N][K]; 1 <= E <= 1024; N and K multiples of 8 (SwiGLU: N of 16)
+ *   w           [E][N][K]; 1 <= E <= 1024; N and K multiples of 8 (SwiGLU: N of 16) up to 2^20
  *   seg_offsets i32 [E + 1] from moe_permute (device), or a slice of a longer
  *               ascending table; rows outside [seg_offsets[0], seg_offsets[E]) are
  *               not written (nor read, in the gradients)

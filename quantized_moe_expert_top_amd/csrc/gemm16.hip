@@ -1,6 +1,8 @@
 // Grouped product of rows with the experts' 16-bit weights, and its gradients by
 // the rows and by the weights, on v_mfma_f32_32x32x16 (bf16 or fp16 operands,
 // fp32 sums).
+#include <type_traits>
+
 #include "segments.h"
 
 namespace moe {
@@ -130,8 +132,10 @@ __global__ __launch_bounds__(256) void gemm16_kernel(GemmK p, int epi, int n_ab)
 // k lie next to each other in memory ("direct") is kept [256][64], one whose a or
 // b do [64][256], read back transposed (ds_read_b64_tr_b16).
 typedef short s16x4 __attribute__((ext_vector_type(4)));
-constexpr int kStage = 65536;   // bytes: P, then Q
-constexpr uint32_t kOut = ~0u;  // a buffer offset past any buffer: reads zero
+constexpr int kCUs = 256;
+constexpr int kStage = 32768;            // bytes of one operand's
+constexpr uint32_t kOut = ~0u;          // a buffer offset past any buffer: reads zero
+constexpr uint32_t kDrop = 0x80000000u;  // past any output tile, also with a row added: not stored
 
 // [256][64] of 16 bits in 16-byte chunks, 8 a row: chunk c of row r at place c ^ swz(r).
 __device__ __forceinline__ int swz(int row) { return (row & 7) ^ ((row >> 3) & 1); }
@@ -140,138 +144,193 @@ struct Tile {
   int e, ab, b0, s0, s1;  // expert, a block, first b; the segment's rows (weights: the sum's)
 };
 
-template <bool F16, int MODE, bool GATHER, bool GLU, int NB>
-__device__ __forceinline__ void tile_body(const GemmK& p, const Tile& c, int epi, char* sA, char* sB) {
+// Tiles in an order that neighbours share operands in an XCD's L2: within a
+// segment in groups of 8 row tiles by a block.
+__device__ __forceinline__ void grouped_order(int idx, int tiles, int n_ab, int& tile, int& ab) {
+  const int g = idx / (8 * n_ab), gm = min(8, tiles - 8 * g), in = idx - g * 8 * n_ab;
+  ab = in / gm;
+  tile = 8 * g + in % gm;
+}
+
+// A workgroup of 8 wavefronts, alone on its CU, takes tile after tile; a wavefront 64
+// a and up to 128 b of each.  The last two steps of a tile issue the first two of the
+// next one, so that only the first tile waits for its loads, and a tile's stores go
+// out under the next one's products.
+template <bool F16, int MODE, bool GATHER, bool GLU>
+__device__ __forceinline__ void tile_loop(const GemmK& p, int epi, int n_ab, int n_bb, char* pA, char* pB, char* qA, char* qB, char* sE) {
   constexpr bool PT = MODE != kForward, QT = MODE == kWeights;  // transposed operands
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int wa = wv & 3, wb = wv >> 2, half = lane >> 5, col = lane & 31;
   const int I = p.N / 2;
-  const int red = MODE == kForward ? p.K : MODE == kRows ? p.N : c.s1 - c.s0;
   const int na = MODE == kForward ? p.N : p.K;  // a's extent (and a transposed P's row length)
 
-  // This lane's part of the wavefront's DMAs: 4 of P, NB of Q (4 transposed).
-  constexpr int QD = QT ? 4 : NB;
-  uint32_t po[4], qo[QD];
-  int pk[2], qk[2];  // direct operands: first k of the lane's chunk, DMAs of even and odd number
-  const uint16_t* pbase;  // of step 0
-  const uint16_t* qbase;
-  uint32_t pbytes = 0, qbytes = 0;
-  int src[4];
-  auto pair_row = [&](int i, int step) {  // gathered P: grouped row of DMA i's lane
-    return min(c.s0 + 64 * step + 2 * (4 * wv + i) + (lane >> 5), c.s1 - 1);
-  };
-  if constexpr (PT) {
-    const int k2 = lane >> 5, s16 = lane & 31;  // row of the DMA's two, 16-byte place in it
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int k = 2 * (4 * wv + i) + k2;
-      const int ch = 256 * c.ab + 8 * ((((s16 >> 1) ^ (k & 3)) << 1) + (s16 & 1));
-      po[i] = ch < na ? (GATHER ? (uint32_t)ch : (uint32_t)k * (uint32_t)na + ch) * 2 : kOut;
-    }
-    pbase = MODE == kRows ? p.w + (size_t)c.e * p.N * p.K : GATHER ? p.a : p.a + (size_t)c.s0 * p.K;
-    if constexpr (GATHER) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) src[i] = red > 0 ? p.gather[pair_row(i, 0)] : 0;
-      pbytes = (uint32_t)((size_t)p.A_rows * p.K * 2);
-    }
+  // Which tiles: workgroups are dealt to the 8 XCDs in turn, each XCD takes a
+  // contiguous range.  The first 64 segments stay in registers, one per lane.
+  int seg_n = 0, seg_end = 0, seg0 = 0, seg1 = 0, total;
+  if constexpr (MODE == kWeights) {
+    total = p.E * n_ab * n_bb;
   } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int idx = 4 * wv + i, r = 8 * idx + (lane >> 3), ck = (lane & 7) ^ swz(r);
-      if (i < 2) pk[i] = 8 * ck;
-      int ch, end = p.N;
-      if constexpr (GLU) {
-        // rows 64w .. 64w + 31 are gate channels of wavefront column w, 64w + 32 .. 64w + 63 their up channels
-        const int x = 128 * c.ab + 32 * (r >> 6) + (r & 31);
-        ch = r & 32 ? I + x : x;
-        end = r & 32 ? p.N : I;
+    seg_n = segment_tiles<256>(p.seg, p.E, p.M_total, lane, seg0, seg1);
+    seg_end = lane_scan(seg_n);
+    total = (p.E <= 64 ? __builtin_amdgcn_readlane(seg_end, 63) : count_tiles<256>(p.seg, p.E, p.M_total)) * n_ab;
+  }
+  const int per = (total + 7) >> 3, xcd = (int)blockIdx.x & 7;
+  int idx = xcd * per + ((int)blockIdx.x >> 3);
+  const int idx_end = min(total, (xcd + 1) * per), idx_step = (int)gridDim.x >> 3;
+  if (idx >= idx_end) return;
+  auto locate = [&](int at) {
+    Tile c;
+    int tile;
+    if constexpr (MODE == kWeights) {
+      c.e = at / (n_ab * n_bb);
+      grouped_order(at - c.e * (n_ab * n_bb), n_bb, n_ab, tile, c.ab);
+      c.b0 = 256 * tile;
+      c.s0 = c.s1 = 0;
+      if (p.M_total > 0) segment_rows(p.seg, c.e, p.M_total, c.s0, c.s1);
+    } else {
+      RowTile t;
+      if (p.E <= 64) {
+        t.e = __builtin_ctzll(__ballot(at < seg_end * n_ab));
+        t.tiles = __builtin_amdgcn_readlane(seg_n, t.e);
+        t.r0 = __builtin_amdgcn_readlane(seg0, t.e);
+        t.s1 = __builtin_amdgcn_readlane(seg1, t.e);
+        at -= (__builtin_amdgcn_readlane(seg_end, t.e) - t.tiles) * n_ab;
       } else {
-        ch = 256 * c.ab + r;
+        find_tile<256>(p.seg, p.E, p.M_total, n_ab, at, t);
       }
-      po[i] = ch < end ? ((uint32_t)ch * (uint32_t)p.K + 8 * ck) * 2 : kOut;
+      grouped_order(at, t.tiles, n_ab, tile, c.ab);
+      c.e = t.e;
+      c.b0 = t.r0 + 256 * tile;
+      c.s0 = t.r0;
+      c.s1 = t.s1;
     }
-    pbase = p.w + (size_t)c.e * p.N * p.K;
-    pbytes = (uint32_t)((size_t)p.N * p.K * 2);
-  }
-  if constexpr (QT) {
-    const int k2 = lane >> 5, s16 = lane & 31;
+    return c;
+  };
+
+  // The DMAs of a tile: a wavefront fetches 4 KB of P and 4 of Q a step, 1 KB each;
+  // DMAs i and i + 2 differ by a fixed number of bytes (not where rows are gathered).
+  // Rows past an operand's end lie past the descriptor's bytes and read zero.
+  constexpr int QO = GATHER && MODE == kForward ? 4 : 2;
+  uint32_t po[2], qo[QO];                 // byte offsets of this lane's 16 bytes, or kOut
+  int pk = 0, qk = 0;                     // direct operands: first k of the lane's chunk in even DMAs (odd: ^ 8)
+  const uint16_t *pbase = p.w, *qbase = p.w;
+  uint32_t pbytes = 0, qbytes = 0;
+  int red = 0, ls0 = 0, ls1 = 0;
+  int src[4];                             // gathered rows' pairs: forward b rows, weights the next step's k
+  // A copy of the lane's number that the compiler knows nothing about: what a tile
+  // needs once is computed there, and not kept in registers over the products.
+  auto lane_here = [&] {
+    int l = lane;
+    asm volatile("" : "+v"(l));
+    return l;
+  };
+  const int dr = 8 * wv + (lane >> 5);   // transposed: k of DMA i is dr + 2i
+  auto pairs = [&](const Tile& c, int step, int (&to)[4]) {
+    if constexpr (GATHER) {
+      const int br = 32 * wv + (lane_here() >> 3);  // direct: row of DMA i is br + 8i
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int k = 2 * (4 * wv + i) + k2;
-      const int ch = c.b0 + 8 * ((((s16 >> 1) ^ (k & 3)) << 1) + (s16 & 1));
-      qo[i] = ch < p.N ? ((uint32_t)k * (uint32_t)p.N + ch) * 2 : kOut;
+      for (int i = 0; i < 4; ++i)
+        to[i] = p.gather[max(min(MODE == kForward ? c.b0 + br + 8 * i : c.s0 + 64 * step + dr + 2 * i, c.s1 - 1), 0)];
     }
-    qbase = p.dy + (size_t)c.s0 * p.N;
-  } else {
-    const int ld = MODE == kForward ? p.K : p.N;
-    const bool gather = MODE == kForward && p.gather;
+  };
+  auto token = [&](int pair) { return (uint32_t)min(max(p.div(pair), 0), p.A_rows - 1); };
+  auto trans_ch = [&](int lane, int k) {  // first of the 8 columns that this lane fetches of row k
+    const int s16 = lane & 31;
+    return 8 * ((((s16 >> 1) ^ (k & 3)) << 1) + (s16 & 1));
+  };
+  auto setup = [&](const Tile& c, bool on, const int (&rows)[4]) {
+    const int lane = lane_here(), dr = 8 * wv + (lane >> 5), br = 32 * wv + (lane >> 3), ck = (lane & 7) ^ swz(br);
+    red = !on ? 0 : MODE == kForward ? p.K : MODE == kRows ? p.N : c.s1 - c.s0;
+    ls0 = c.s0;
+    ls1 = c.s1;
+    if constexpr (PT) {
 #pragma unroll
-    for (int i = 0; i < NB; ++i) {
-      const int idx = NB * wv + i, r = 8 * idx + (lane >> 3), ck = (lane & 7) ^ swz(r);
-      if (i < 2) qk[i] = 8 * ck;
-      const int row = c.b0 + r;
-      uint32_t from = r;
-      if (gather) from = source_row(p, min(row, c.s1 - 1));
-      qo[i] = row < c.s1 ? (from * (uint32_t)ld + 8 * ck) * 2 : kOut;
+      for (int i = 0; i < 2; ++i) {
+        const int k = dr + 2 * i, ch = 256 * c.ab + trans_ch(lane, k);
+        po[i] = ch < na ? (GATHER ? (uint32_t)ch : (uint32_t)k * (uint32_t)na + ch) * 2 : kOut;
+      }
+      pbase = MODE == kRows ? p.w + (size_t)c.e * p.N * p.K : GATHER ? p.a : p.a + (size_t)c.s0 * p.K;
+      if constexpr (GATHER) {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) src[i] = rows[i];
+        pbytes = (uint32_t)((size_t)p.A_rows * p.K * 2);
+      }
+    } else {
+      // SwiGLU: rows 64w .. 64w + 31 are gate channels of wavefront column w, 64w + 32 .. 64w + 63
+      // their up channels (past the last gate channel: up ones, never stored)
+      pk = qk = 8 * ck;
+      const int ch = GLU ? 128 * c.ab + 32 * (wv >> 1) + (lane >> 3) + (wv & 1 ? I : 0) : 256 * c.ab + br;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) po[i] = ((uint32_t)(ch + 8 * i) * (uint32_t)p.K + 8 * (ck ^ i)) * 2;
+      pbase = p.w + (size_t)c.e * p.N * p.K;
+      pbytes = (uint32_t)((size_t)p.N * p.K * 2);
     }
-    qbase = MODE == kForward ? (gather ? p.a : p.a + (size_t)c.b0 * ld) : p.dy + (size_t)c.b0 * ld;
-    qbytes = gather ? (uint32_t)((size_t)p.A_rows * ld * 2) : (uint32_t)((size_t)min(c.s1 - c.b0, 256) * ld * 2);
-  }
-  const int n = (red + 63) >> 6;
+    if constexpr (QT) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        const int k = dr + 2 * i, ch = c.b0 + trans_ch(lane, k);
+        qo[i] = ch < p.N ? ((uint32_t)k * (uint32_t)p.N + ch) * 2 : kOut;
+      }
+      qbase = p.dy + (size_t)c.s0 * p.N;
+    } else {
+      const int ld = MODE == kForward ? p.K : p.N;
+      qk = 8 * ck;
+#pragma unroll
+      for (int i = 0; i < QO; ++i) {
+        const int r = br + 8 * i;
+        const uint32_t from = GATHER ? token(rows[i]) : r;
+        qo[i] = (from * (uint32_t)ld + 8 * (ck ^ (i & 1))) * 2;
+        if (GATHER && c.b0 + r >= c.s1) qo[i] = kOut;
+      }
+      qbase = MODE == kForward ? (GATHER ? p.a : p.a + (size_t)c.b0 * ld) : p.dy + (size_t)c.b0 * ld;
+      qbytes = GATHER ? (uint32_t)((size_t)p.A_rows * ld * 2) : (uint32_t)((size_t)min(c.s1 - c.b0, 256) * ld * 2);
+    }
+  };
 
   // DMAs of step st into a stage; past the sum's end zeros.
-  auto issue = [&](char* stage, int st) {
+  auto dma = [&](rsrc_t r, char* to, uint32_t off, uint32_t adv) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (__attribute__((address_space(3))) void*)to, 16, off, adv, 0, 0);
+  };
+  auto issue = [&](char* ps, char* qs, int st) {
     const int left = red - 64 * st;  // k of this step and later ones
     // (as a scalar: the compiler clamps on the vector side, and would loop over the lanes for the descriptor)
     const uint32_t rows = (uint32_t)__builtin_amdgcn_readfirstlane(max(min(left, 64), 0));
-    const uint32_t adv = (uint32_t)min(st, n - 1) * 128u;
-    if constexpr (PT) {
-      if constexpr (GATHER) {
-        const rsrc_t pr = make_rsrc(pbase, pbytes);
-        uint32_t off[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int row = min(max(p.div(src[i]), 0), p.A_rows - 1);
-          const int k = 2 * (4 * wv + i) + (lane >> 5);
-          off[i] = k < left && po[i] != kOut ? (uint32_t)row * (uint32_t)(2 * p.K) + po[i] : kOut;
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) src[i] = p.gather[pair_row(i, st + 1)];
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          __builtin_amdgcn_raw_ptr_buffer_load_lds(pr, (__attribute__((address_space(3))) void*)(stage + (4 * wv + i) * 1024), 16, off[i], 0, 0, 0);
-      } else {
-        const uint32_t row = 2u * (uint32_t)na;  // bytes
-        const rsrc_t pr = make_rsrc(pbase + (size_t)(64 * st) * na, rows * row);
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          __builtin_amdgcn_raw_ptr_buffer_load_lds(pr, (__attribute__((address_space(3))) void*)(stage + (4 * wv + i) * 1024), 16, po[i], 0, 0, 0);
-      }
-    } else {
+    const uint32_t adv = left > 0 ? (uint32_t)st * 128u : 0u;
+    char* const pd = ps + wv * 4096;
+    char* const qd = qs + wv * 4096;
+    if constexpr (PT && GATHER) {
       const rsrc_t pr = make_rsrc(pbase, pbytes);
+      uint32_t off[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(pr, (__attribute__((address_space(3))) void*)(stage + (4 * wv + i) * 1024), 16,
-                                                 pk[i & 1] < left ? po[i] : kOut, adv, 0, 0);
+        off[i] = dr + 2 * i < left && po[i & 1] != kOut ? token(src[i]) * (uint32_t)(2 * p.K) + po[i & 1] : kOut;
+      pairs(Tile{0, 0, 0, ls0, ls1}, st + 1, src);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) dma(pr, pd + 1024 * i, off[i], 0);
+    } else if constexpr (PT) {
+      const rsrc_t pr = make_rsrc(pbase + (size_t)(64 * st) * na, rows * (2u * (uint32_t)na));
+#pragma unroll
+      for (int i = 0; i < 4; ++i) dma(pr, pd + 1024 * i, po[i & 1], i < 2 ? 0u : 8u * (uint32_t)na);
+    } else {
+      const rsrc_t pr = make_rsrc(pbase, pbytes);
+      const uint32_t even = pk < left ? po[0] : kOut, odd = (pk ^ 8) < left ? po[1] : kOut;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) dma(pr, pd + 1024 * i, i & 1 ? odd : even, i < 2 ? adv : adv + 32u * (uint32_t)p.K);
     }
     if constexpr (QT) {
       const rsrc_t qr = make_rsrc(qbase + (size_t)(64 * st) * p.N, rows * (2u * (uint32_t)p.N));
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(qr, (__attribute__((address_space(3))) void*)(stage + 32768 + (4 * wv + i) * 1024), 16, qo[i], 0, 0, 0);
+      for (int i = 0; i < 4; ++i) dma(qr, qd + 1024 * i, qo[i & 1], i < 2 ? 0u : 8u * (uint32_t)p.N);
     } else {
       const rsrc_t qr = make_rsrc(qbase, qbytes);
+      const int ld = MODE == kForward ? p.K : p.N;
 #pragma unroll
-      for (int i = 0; i < NB; ++i)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(qr, (__attribute__((address_space(3))) void*)(stage + 32768 + (NB * wv + i) * 1024), 16,
-                                                 qk[i & 1] < left ? qo[i] : kOut, adv, 0, 0);
+      for (int i = 0; i < 4; ++i)
+        dma(qr, qd + 1024 * i, (i & 1 ? qk ^ 8 : qk) < left ? qo[QO == 4 ? i : i & 1] : kOut,
+            QO == 4 || i < 2 ? adv : adv + 32u * (uint32_t)ld);
     }
   };
 
-  // Fragments of 16 k: 2 of P (32 a each), NB of Q.
-  struct Frags {
-    u32x4 p[2], q[NB];
-  };
   auto read_direct = [&](const char* at, int row, int s) {
     return *reinterpret_cast<const u32x4*>(at + row * 128 + (((2 * s + half) ^ swz(row)) << 4));
   };
@@ -283,25 +342,6 @@ __device__ __forceinline__ void tile_body(const GemmK& p, const Tile& c, int epi
     const u32x2 l = __builtin_bit_cast(u32x2, lo), h = __builtin_bit_cast(u32x2, hi);
     return u32x4{l[0], l[1], h[0], h[1]};
   };
-  auto read = [&](const char* stage, int s) {
-    Frags f;
-#pragma unroll
-    for (int t = 0; t < 2; ++t)
-      f.p[t] = PT ? read_trans(stage, 128 * (wa >> 1) + 32 * (wa & 1) + 16 * t, s) : read_direct(stage, 64 * wa + 32 * t + col, s);
-#pragma unroll
-    for (int j = 0; j < NB; ++j)
-      f.q[j] = QT ? read_trans(stage + 32768, 128 * (j >> 1) + 32 * (j & 1) + 16 * wb, s) : read_direct(stage + 32768, 64 * j + 32 * wb + col, s);
-    return f;
-  };
-  f32x16 acc[2][NB] = {};
-  auto mul = [&](const Frags& f) {
-    __builtin_amdgcn_s_setprio(1);
-#pragma unroll
-    for (int t = 0; t < 2; ++t)
-#pragma unroll
-      for (int j = 0; j < NB; ++j) acc[t][j] = mfma32t<F16>(f.p[t], f.q[j], acc[t][j]);
-    __builtin_amdgcn_s_setprio(0);
-  };
   // Every wavefront's reads of a stage are done and the other stage's DMAs landed.
   auto ready = [&] {
     __builtin_amdgcn_sched_barrier(0);
@@ -309,182 +349,245 @@ __device__ __forceinline__ void tile_body(const GemmK& p, const Tile& c, int epi
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
   };
-  if (n > 0) {
-    issue(sA, 0);
-    ready();
-    issue(sB, 1);
-    Frags f = read(sA, 0), g;
+
+  Tile cur = locate(idx), nxt;
+  bool more;
+  // One tile with b in NB x 64.
+  auto body = [&](auto nb_tag) {
+    constexpr int NB = decltype(nb_tag)::value;
+    struct Frags {  // of 16 k: 2 of P (32 a each), NB of Q
+      u32x4 p[2], q[NB];
+    };
+    auto read = [&](const char* ps, const char* qs, int s) {
+      Frags f;
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+        f.p[t] = PT ? read_trans(ps, 128 * (wa >> 1) + 32 * (wa & 1) + 16 * t, s) : read_direct(ps, 64 * wa + 32 * t + col, s);
+#pragma unroll
+      for (int j = 0; j < NB; ++j)
+        f.q[j] = QT ? read_trans(qs, 128 * (j >> 1) + 32 * (j & 1) + 16 * wb, s)
+                    : read_direct(qs, 64 * j + 32 * wb + col, s);
+      return f;
+    };
+    f32x16 acc[2][NB] = {};
+    auto mul = [&](const Frags& f) {
+      __builtin_amdgcn_s_setprio(1);
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int j = 0; j < NB; ++j) acc[t][j] = mfma32t<F16>(f.p[t], f.q[j], acc[t][j]);
+      __builtin_amdgcn_s_setprio(0);
+    };
+    int next_src[4];
+    pairs(nxt, 0, next_src);
+    // an even number of steps, 2 at least: past the sum's end they multiply zeros
+    const int n = max((red + 127) >> 7 << 1, 2);
+    Frags f = read(pA, qA, 0), g;
     for (int st = 0; st < n; st += 2) {
-      g = read(sA, 1);
+      g = read(pA, qA, 1);
       mul(f);
-      f = read(sA, 2);
+      f = read(pA, qA, 2);
       mul(g);
-      g = read(sA, 3);
+      g = read(pA, qA, 3);
       mul(f);
       ready();
-      issue(sA, st + 2);
-      f = read(sB, 0);
+      const bool last = st + 2 >= n;
+      if (last) setup(nxt, more, next_src);
+      issue(pA, qA, last ? 0 : st + 2);
+      f = read(pB, qB, 0);
       mul(g);
-      g = read(sB, 1);
+      g = read(pB, qB, 1);
       mul(f);
-      f = read(sB, 2);
+      f = read(pB, qB, 2);
       mul(g);
-      g = read(sB, 3);
+      g = read(pB, qB, 3);
       mul(f);
       ready();
-      issue(sB, st + 3);
-      f = read(sA, 0);
+      issue(pB, qB, last ? 1 : st + 3);
+      f = read(pA, qA, 0);
       mul(g);
     }
-    ready();
-  }
 
-  // Epilogue: a wavefront's 32 b x 64 a at a time through 8 KB of LDS, so that
-  // neighbouring lanes store 128 bytes and more in a row.  Lane (half, col) holds
-  // b = col and of tile t a = 32t + 8g + 4*half + 0..3 in registers 4g ...
-  char* const eb = sA + wv * 8192;
-  const int a0 = GLU && MODE == kForward ? 128 * c.ab + 32 * wa : PT ? 256 * c.ab + 128 * (wa >> 1) + 32 * (wa & 1) : 256 * c.ab + 64 * wa;
-  // channel of place x of the wavefront's 64
-  auto a_of = [&](int x) { return a0 + (PT ? (x & 31) + 64 * (x >> 5) : x); };
-  // the places of 8 channels (fp32: 4) of tile t, register group g
-  auto chunk16 = [&](int t, int g) { return PT ? 4 * (g >> 1) + 2 * t + (g & 1) : 4 * t + g; };
-  auto put16 = [&](int ck, float v0, float v1, float v2, float v3, bool f16) {  // 8 chunks a row
-    const u32x2 d = f16 ? u32x2{pack16x2<true>(v0, v1), pack16x2<true>(v2, v3)} : u32x2{pack_bf16x2(v0, v1), pack_bf16x2(v2, v3)};
-    *reinterpret_cast<u32x2*>(eb + col * 128 + ((ck ^ (col & 7)) << 4) + 8 * half) = d;
-  };
-  auto get16 = [&](int r, int ck) { return *reinterpret_cast<const u32x4*>(eb + r * 128 + ((ck ^ (r & 7)) << 4)); };
-#pragma unroll
-  for (int j = 0; j < NB; ++j) {
-    const int b = c.b0 + (QT ? 128 * (j >> 1) + 32 * (j & 1) + 16 * wb : 64 * j + 32 * wb);  // of the 32's first row
-    auto b_of = [&](int r) { return b + (QT ? (r & 15) + 64 * (r >> 4) : r); };
-    const int bend = MODE == kWeights ? p.N : c.s1;
-    const size_t out0 = MODE == kWeights ? (size_t)c.e * p.N : 0;
+    // Epilogue: a wavefront's 32 b x 64 a (fp32: 32) at a time through 4 KB of LDS, so
+    // that neighbouring lanes store 64 bytes and more in a row.  Lane (half, col) holds
+    // b number col and of tile t a numbers 8g + 4*half + 0..3 in registers 4g ..; number i is
+    // a = a0 + 32t + i, of a transposed operand a0 + 16t + i % 16 + 64 * (i / 16) (b alike).
+    // Rows past the end lie past the descriptor's bytes, channels get kDrop: every
+    // lane stores, and the stores are counted.
+    char* const eb = sE + wv * 4096;
+    const int lane = lane_here(), half = lane >> 5, col = lane & 31;
+    const int a0 = GLU && MODE == kForward ? 128 * cur.ab + 32 * wa
+                   : PT ? 256 * cur.ab + 128 * (wa >> 1) + 32 * (wa & 1) : 256 * cur.ab + 64 * wa;
+    const int rows = min((MODE == kWeights ? p.N : cur.s1) - cur.b0, 256);
+    const size_t row0 = (MODE == kWeights ? (size_t)cur.e * p.N : 0) + cur.b0;
+    auto chunk = [&](int r, int ck) { return eb + r * 128 + ((ck ^ (r & 7)) << 4); };  // 8 chunks of 16 bytes a row
+    auto put16 = [&](int ck, const f32x16& v, int g, bool f16) {
+      *reinterpret_cast<u32x2*>(chunk(col, ck) + 8 * half) =
+          f16 ? u32x2{pack16x2<true>(v[4 * g], v[4 * g + 1]), pack16x2<true>(v[4 * g + 2], v[4 * g + 3])}
+              : u32x2{pack_bf16x2(v[4 * g], v[4 * g + 1]), pack_bf16x2(v[4 * g + 2], v[4 * g + 3])};
+    };
+    auto get = [&](int r, int ck) { return *reinterpret_cast<const u32x4*>(chunk(r, ck)); };
+    auto get32 = [&](int r, int ck) { return *reinterpret_cast<const f32x4*>(chunk(r, ck)); };
+    // b of the j-th 32's row x (a multiple of 8), from cur.b0
+    auto row_of = [&](int j, int x) {
+      return QT ? 128 * (j >> 1) + 32 * (j & 1) + 16 * wb + (x & 15) + 64 * (x >> 4) : 64 * j + 32 * wb + x;
+    };
+    auto store = [&](rsrc_t r, u32x4 v, uint32_t off, int row, uint32_t ld) {
+      typedef unsigned int b128 __attribute__((ext_vector_type(4)));
+      // The row's offset is added here: with a scalar register as the instruction's
+      // offset the compiler sees no hazard in overwriting the data in the next
+      // instruction, but gfx950 then stores some of the new values.
+      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(b128, v), r, off + (uint32_t)row * ld, 0, 0);
+    };
     if constexpr (GLU && MODE == kForward) {
-      if (p.pre_out) {
+      const uint32_t ldo = 2u * (uint32_t)I, ldp = 2u * (uint32_t)p.N;
+      const rsrc_t ro = make_rsrc(static_cast<uint16_t*>(p.out) + row0 * I, (uint32_t)rows * ldo);
+      const int ch = a0 + 8 * (lane & 3);
+      const uint32_t oo = ch < I ? (uint32_t)(lane >> 2) * ldo + 2 * ch : kDrop;
+      const uint32_t op = ch < I ? (uint32_t)(lane >> 3) * ldp + 2 * (ch + (lane & 4 ? I : 0)) : kDrop;
+#pragma unroll
+      for (int j = 0; j < NB; ++j) {
+        if (p.pre_out) {
+          const rsrc_t rp = make_rsrc(p.pre_out + row0 * p.N, (uint32_t)rows * ldp);
+#pragma unroll
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int g = 0; g < 4; ++g) put16(4 * t + g, acc[t][j], g, F16);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) store(rp, get(8 * i + (lane >> 3), lane & 7), op, row_of(j, 8 * i), ldp);
+        }
+        f32x16 h;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) h[i] = acc[0][j][i] * __builtin_amdgcn_rcpf(1.0f + __expf(-acc[0][j][i])) * acc[1][j][i];
+#pragma unroll
+        for (int g = 0; g < 4; ++g) put16(g, h, g, F16);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) store(ro, get(16 * i + (lane >> 2), lane & 3), oo, row_of(j, 16 * i), ldo);
+      }
+    } else if constexpr (GLU) {
+      const uint32_t ld = 4u * (uint32_t)p.K;
+      const rsrc_t ro = make_rsrc(static_cast<uint16_t*>(p.out) + row0 * 2 * p.K, (uint32_t)rows * ld);
+      const rsrc_t rp = make_rsrc(p.pre_in + row0 * 2 * p.K, (uint32_t)rows * ld);
+      const int x = 8 * (lane & 3);
+      // 8 channels of 16 rows a load: gate and up, for both tiles and row halves of one j
+      struct Pre {
+        u32x4 g[2][2], u[2][2];
+      };
+      uint32_t off[2];
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const int ch = a0 + 16 * t + (x & 15) + 64 * (x >> 4);
+        off[t] = ch < p.K ? (uint32_t)(lane >> 2) * ld + 2 * ch : kDrop;
+      }
+      auto fetch = [&](int j) {
+        Pre v;
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
-          for (int g = 0; g < 4; ++g)
-            put16(4 * t + g, acc[t][j][4 * g], acc[t][j][4 * g + 1], acc[t][j][4 * g + 2], acc[t][j][4 * g + 3], F16);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int r = 8 * i + (lane >> 3), ck = lane & 7, ch = a0 + 8 * (ck & 3);
-          const u32x4 v = get16(r, ck);
-          if (b_of(r) < bend && ch < I)
-            *reinterpret_cast<u32x4*>(p.pre_out + (size_t)b_of(r) * p.N + (ck >> 2 ? I : 0) + ch) = v;
-        }
-      }
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        float h[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const float x = acc[0][j][4 * g + i];
-          h[i] = x * __builtin_amdgcn_rcpf(1.0f + __expf(-x)) * acc[1][j][4 * g + i];
-        }
-        put16(g, h[0], h[1], h[2], h[3], F16);
-      }
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        const int r = 16 * i + (lane >> 2), ck = lane & 3;
-        const u32x4 v = get16(r, ck);
-        if (b_of(r) < bend && a0 + 8 * ck < I)
-          *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(p.out) + (size_t)b_of(r) * I + a0 + 8 * ck) = v;
-      }
-    } else if (GLU || epi == kEpiF32) {
-#pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const int ck = 2 * chunk16(t, g) + half;  // 16 chunks a row
-          *reinterpret_cast<f32x4*>(eb + col * 256 + ((ck ^ (col & 15)) << 4)) =
-              f32x4{acc[t][j][4 * g], acc[t][j][4 * g + 1], acc[t][j][4 * g + 2], acc[t][j][4 * g + 3]};
-        }
-#pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const int r = 4 * i + (lane >> 4), ck = lane & 15, ch = a_of(4 * ck);
-        const f32x4 v = *reinterpret_cast<const f32x4*>(eb + r * 256 + ((ck ^ (r & 15)) << 4));
-        if (b_of(r) >= bend || ch >= na) continue;
-        if constexpr (GLU) {
-          const size_t at = (size_t)b_of(r) * 2 * p.K + ch;
-          const u32x2 gv = *reinterpret_cast<const u32x2*>(p.pre_in + at), uv = *reinterpret_cast<const u32x2*>(p.pre_in + at + p.K);
-          float dg[4], du[4];
-#pragma unroll
-          for (int q = 0; q < 4; ++q) {
-            const uint32_t gw = gv[q >> 1], uw = uv[q >> 1];
-            const float g = widen16<F16>((uint16_t)(q & 1 ? gw >> 16 : gw & 0xFFFFu));
-            const float u = widen16<F16>((uint16_t)(q & 1 ? uw >> 16 : uw & 0xFFFFu));
-            const float s = __builtin_amdgcn_rcpf(1.0f + __expf(-g));
-            dg[q] = v[q] * u * s * (1.0f + g * (1.0f - s));
-            du[q] = v[q] * g * s;
+          for (int i = 0; i < 2; ++i) {
+            v.g[t][i] = buf_x4(rp, off[t], (uint32_t)row_of(j, 16 * i) * ld);
+            v.u[t][i] = buf_x4(rp, off[t] + ld / 2, (uint32_t)row_of(j, 16 * i) * ld);
           }
-          uint16_t* const o = static_cast<uint16_t*>(p.out) + at;
-          *reinterpret_cast<u32x2*>(o) = u32x2{pack16x2<F16>(dg[0], dg[1]), pack16x2<F16>(dg[2], dg[3])};
-          *reinterpret_cast<u32x2*>(o + p.K) = u32x2{pack16x2<F16>(du[0], du[1]), pack16x2<F16>(du[2], du[3])};
-        } else {
-          *reinterpret_cast<f32x4*>(static_cast<float*>(p.out) + (out0 + b_of(r)) * na + ch) = v;
+        return v;
+      };
+      Pre pre = fetch(0), ahead;
+#pragma unroll
+      for (int j = 0; j < NB; ++j) {
+        if (j + 1 < NB) ahead = fetch(j + 1);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+#pragma unroll
+          for (int g = 0; g < 4; ++g)
+            *reinterpret_cast<f32x4*>(chunk(col, 2 * g + half)) =
+                f32x4{acc[t][j][4 * g], acc[t][j][4 * g + 1], acc[t][j][4 * g + 2], acc[t][j][4 * g + 3]};
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            const int r = 16 * i + (lane >> 2);
+            u32x4 dg, du;
+#pragma unroll
+            for (int q = 0; q < 2; ++q) {
+              const f32x4 d = get32(r, 2 * (lane & 3) + q);
+#pragma unroll
+              for (int w = 0; w < 2; ++w) {
+                const uint32_t gw = pre.g[t][i][2 * q + w], uw = pre.u[t][i][2 * q + w];
+                float og[2], ou[2];
+#pragma unroll
+                for (int z = 0; z < 2; ++z) {
+                  const float g = widen16<F16>((uint16_t)(z ? gw >> 16 : gw & 0xFFFFu));
+                  const float u = widen16<F16>((uint16_t)(z ? uw >> 16 : uw & 0xFFFFu));
+                  const float s = __builtin_amdgcn_rcpf(1.0f + __expf(-g));
+                  og[z] = d[2 * w + z] * u * s * (1.0f + g * (1.0f - s));
+                  ou[z] = d[2 * w + z] * g * s;
+                }
+                dg[2 * q + w] = pack16x2<F16>(og[0], og[1]);
+                du[2 * q + w] = pack16x2<F16>(ou[0], ou[1]);
+              }
+            }
+            store(ro, dg, off[t], row_of(j, 16 * i), ld);
+            store(ro, du, off[t] + ld / 2, row_of(j, 16 * i), ld);
+          }
+        }
+        pre = ahead;
+      }
+    } else if (epi == kEpiF32) {
+      const uint32_t ld = 4u * (uint32_t)na;
+      const rsrc_t ro = make_rsrc(static_cast<float*>(p.out) + row0 * na, (uint32_t)rows * ld);
+      const int x = 4 * (lane & 7);
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        const int ch = a0 + (PT ? 16 * t + (x & 15) + 64 * (x >> 4) : 32 * t + x);
+        const uint32_t off = ch < na ? (uint32_t)(lane >> 3) * ld + 4 * ch : kDrop;
+#pragma unroll
+        for (int j = 0; j < NB; ++j) {
+#pragma unroll
+          for (int g = 0; g < 4; ++g)
+            *reinterpret_cast<f32x4*>(chunk(col, 2 * g + half)) =
+                f32x4{acc[t][j][4 * g], acc[t][j][4 * g + 1], acc[t][j][4 * g + 2], acc[t][j][4 * g + 3]};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) store(ro, get(8 * i + (lane >> 3), lane & 7), off, row_of(j, 8 * i), ld);
         }
       }
     } else {
+      const uint32_t ld = 2u * (uint32_t)na;
+      const rsrc_t ro = make_rsrc(static_cast<uint16_t*>(p.out) + row0 * na, (uint32_t)rows * ld);
+      const int x = 8 * (lane & 7), ch = a0 + (PT ? (x & 31) + 64 * (x >> 5) : x);
+      const uint32_t off = ch < na ? (uint32_t)(lane >> 3) * ld + 2 * ch : kDrop;
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
+      for (int j = 0; j < NB; ++j) {
 #pragma unroll
-        for (int g = 0; g < 4; ++g)
-          put16(chunk16(t, g), acc[t][j][4 * g], acc[t][j][4 * g + 1], acc[t][j][4 * g + 2], acc[t][j][4 * g + 3], epi == kEpiF16);
+        for (int t = 0; t < 2; ++t)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = 8 * i + (lane >> 3), ck = lane & 7, ch = a_of(8 * ck);
-        const u32x4 v = get16(r, ck);
-        if (b_of(r) < bend && ch < na)
-          *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(p.out) + (out0 + b_of(r)) * na + ch) = v;
+          for (int g = 0; g < 4; ++g) put16(PT ? 4 * (g >> 1) + 2 * t + (g & 1) : 4 * t + g, acc[t][j], g, epi == kEpiF16);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) store(ro, get(8 * i + (lane >> 3), lane & 7), off, row_of(j, 8 * i), ld);
       }
     }
-  }
-}
+  };
 
-// Tiles in an order that neighbours share operands in an XCD's L2: workgroups are
-// dealt to the 8 XCDs in turn, each takes a contiguous range; within a segment in
-// groups of 8 row tiles by a block.
-__device__ __forceinline__ bool xcd_index(int wgs, int& idx) {
-  const int per = (wgs + 7) >> 3;
-  idx = ((int)blockIdx.x & 7) * per + ((int)blockIdx.x >> 3);
-  return ((int)blockIdx.x >> 3) < per && idx < wgs;
-}
-__device__ __forceinline__ void grouped_order(int idx, int tiles, int n_ab, int& tile, int& ab) {
-  const int g = idx / (8 * n_ab), gm = min(8, tiles - 8 * g), in = idx - g * 8 * n_ab;
-  ab = in / gm;
-  tile = 8 * g + in % gm;
+  pairs(cur, 0, src);
+  setup(cur, true, src);
+  issue(pA, qA, 0);
+  issue(pB, qB, 1);
+  ready();
+  while (true) {
+    idx += idx_step;
+    more = idx < idx_end;
+    nxt = more ? locate(idx) : cur;
+    const int left = MODE == kWeights ? 256 : cur.s1 - cur.b0;
+    if (left <= 64) body(std::integral_constant<int, 1>{});
+    else if (left <= 128) body(std::integral_constant<int, 2>{});
+    else if (left <= 192) body(std::integral_constant<int, 3>{});
+    else body(std::integral_constant<int, 4>{});
+    if (!more) break;
+    cur = nxt;
+  }
 }
 
 template <bool F16, int MODE, bool GATHER, bool GLU>
 __global__ __launch_bounds__(512, 2) void tile256_kernel(GemmK p, int epi, int n_ab, int n_bb) {
 #ifdef __HIP_DEVICE_COMPILE__
-  __shared__ __attribute__((aligned(1024))) char sA[kStage], sB[kStage];
-  Tile c;
-  int idx, tile;
-  if constexpr (MODE == kWeights) {
-    if (!xcd_index(p.E * n_ab * n_bb, idx)) return;
-    c.e = idx / (n_ab * n_bb);
-    grouped_order(idx % (n_ab * n_bb), n_bb, n_ab, tile, c.ab);
-    c.b0 = 256 * tile;
-    c.s0 = c.s1 = 0;
-    if (p.M_total > 0) segment_rows(p.seg, c.e, p.M_total, c.s0, c.s1);
-    tile_body<F16, MODE, GATHER, GLU, 4>(p, c, epi, sA, sB);
-  } else {
-    if (!xcd_index(count_tiles<256>(p.seg, p.E, p.M_total) * n_ab, idx)) return;
-    RowTile t;
-    if (!find_tile<256>(p.seg, p.E, p.M_total, n_ab, idx, t)) return;
-    grouped_order(idx, t.tiles, n_ab, tile, c.ab);
-    c.e = t.e;
-    c.b0 = t.r0 + 256 * tile;
-    c.s0 = t.r0;
-    c.s1 = t.s1;
-    const int left = c.s1 - c.b0;
-    if (left <= 64) tile_body<F16, MODE, GATHER, GLU, 1>(p, c, epi, sA, sB);
-    else if (left <= 128) tile_body<F16, MODE, GATHER, GLU, 2>(p, c, epi, sA, sB);
-    else if (left <= 192) tile_body<F16, MODE, GATHER, GLU, 3>(p, c, epi, sA, sB);
-    else tile_body<F16, MODE, GATHER, GLU, 4>(p, c, epi, sA, sB);
-  }
+  __shared__ __attribute__((aligned(1024))) char pA[kStage], pB[kStage], qA[kStage], qB[kStage], sE[8 * 4096];
+  tile_loop<F16, MODE, GATHER, GLU>(p, epi, n_ab, n_bb, pA, pB, qA, qB, sE);
 #endif
 }
 
@@ -508,8 +611,9 @@ int launch_rowwise(const Gemm16Args& a, int n_ab, hipStream_t s) {
 template <bool F16, int MODE, bool GATHER, bool GLU>
 int launch256(const Gemm16Args& a, hipStream_t s) {
   const int na = MODE == kForward ? (GLU ? a.N : a.N) : a.K, n_ab = (na + 255) / 256, n_bb = (a.N + 255) / 256;
-  const int64_t wgs = ((MODE == kWeights ? (int64_t)a.E * n_bb : row_tiles(a.M_total, a.E, 256)) * n_ab + 7) / 8 * 8;
-  if (wgs >= ((int64_t)1 << 22)) return (int)hipErrorInvalidConfiguration;
+  const int64_t tiles = (MODE == kWeights ? (int64_t)a.E * n_bb : row_tiles(a.M_total, a.E, 256)) * n_ab;
+  if (tiles >= ((int64_t)1 << 30)) return (int)hipErrorInvalidConfiguration;
+  const int64_t wgs = tiles < kCUs ? (tiles + 7) / 8 * 8 : kCUs;
   hipLaunchKernelGGL((tile256_kernel<F16, MODE, GATHER, GLU>), dim3((unsigned)wgs), dim3(512), 0, s, kernel_args(a), a.epilogue, n_ab, n_bb);
   return (int)hipGetLastError();
 }
@@ -520,8 +624,10 @@ int launch256t(const Gemm16Args& a, void* s) {
 }  // namespace
 
 int launch_gemm16(const Gemm16Args& a, void* stream) {
-  if (a.kernel == 9 || a.kernel == 0)
+  if (a.kernel == 9 || a.kernel == 0) {
+    if (a.gather) return a.epilogue == kEpiSwiglu ? launch256t<kForward, true, true>(a, stream) : launch256t<kForward, true, false>(a, stream);
     return a.epilogue == kEpiSwiglu ? launch256t<kForward, false, true>(a, stream) : launch256t<kForward, false, false>(a, stream);
+  }
   const int n_ab = a.epilogue == kEpiSwiglu ? (a.N / 2 + 31) / 32 : (a.N + 63) / 64;
   return launch_rowwise<kForward>(a, n_ab, static_cast<hipStream_t>(stream));
 }
@@ -533,7 +639,7 @@ int launch_gemm16_grad_rows(const Gemm16Args& a, void* stream) {
 size_t gemm16_grad_weights_workspace_bytes(int E, int N, int K, int M_total, int kernel) { return 0; }
 int launch_gemm16_grad_weights(const Gemm16Args& a, void* stream) {
   if (a.kernel == 9 || a.kernel == 0)
-    return a.gather ? launch256t<kWeights, true, false>(a, stream) : launch256t<kWeights, false, false>(a, stream);
+    return a.gather && a.M_total > 0 ? launch256t<kWeights, true, false>(a, stream) : launch256t<kWeights, false, false>(a, stream);
   const hipStream_t s = static_cast<hipStream_t>(stream);
   const dim3 grid((a.K + 63) / 64, (a.N + 63) / 64, a.E);
   if (grid.y > 65535) return (int)hipErrorInvalidConfiguration;
