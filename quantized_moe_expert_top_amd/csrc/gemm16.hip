@@ -2,6 +2,7 @@
 // the rows and by the weights, on v_mfma_f32_32x32x16 (bf16 or fp16 operands,
 // fp32 sums).
 #include <type_traits>
+#include <utility>
 
 #include "segments.h"
 
@@ -140,6 +141,10 @@ constexpr uint32_t kDrop = 0x80000000u;  // past any output tile, also with a ro
 // [256][64] of 16 bits in 16-byte chunks, 8 a row: chunk c of row r at place c ^ swz(r).
 __device__ __forceinline__ int swz(int row) { return (row & 7) ^ ((row >> 3) & 1); }
 
+// [64][256] of 16 bits in 32-byte units, 16 a row: unit u of row k at place u ^ tswz(k): the
+// four rows of a transposing read's 16 lanes and the eight of 32 lanes fall on different banks.
+__device__ __forceinline__ int tswz(int k) { return (k & 3) | ((k >> 1) & 4); }
+
 struct Tile {
   int e, ab, b0, s0, s1;  // expert, a block, first b; the segment's rows (weights: the sum's)
 };
@@ -160,7 +165,7 @@ template <bool F16, int MODE, bool GATHER, bool GLU>
 __device__ __forceinline__ void tile_loop(const GemmK& p, int epi, int n_ab, int n_bb, char* pA, char* pB, char* qA, char* qB, char* sE) {
   constexpr bool PT = MODE != kForward, QT = MODE == kWeights;  // transposed operands
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  const int wa = wv & 3, wb = wv >> 2, half = lane >> 5, col = lane & 31;
+  const int wa = wv & 3, wb = wv >> 2, col = lane & 15, quad = lane >> 4;
   const int I = p.N / 2;
   const int na = MODE == kForward ? p.N : p.K;  // a's extent (and a transposed P's row length)
 
@@ -236,7 +241,7 @@ __device__ __forceinline__ void tile_loop(const GemmK& p, int epi, int n_ab, int
   auto token = [&](int pair) { return (uint32_t)min(max(p.div(pair), 0), p.A_rows - 1); };
   auto trans_ch = [&](int lane, int k) {  // first of the 8 columns that this lane fetches of row k
     const int s16 = lane & 31;
-    return 8 * ((((s16 >> 1) ^ (k & 3)) << 1) + (s16 & 1));
+    return 8 * ((((s16 >> 1) ^ tswz(k)) << 1) + (s16 & 1));
   };
   auto setup = [&](const Tile& c, bool on, const int (&rows)[4]) {
     const int lane = lane_here(), dr = 8 * wv + (lane >> 5), br = 32 * wv + (lane >> 3), ck = (lane & 7) ^ swz(br);
@@ -331,16 +336,23 @@ __device__ __forceinline__ void tile_loop(const GemmK& p, int epi, int n_ab, int
     }
   };
 
-  auto read_direct = [&](const char* at, int row, int s) {
-    return *reinterpret_cast<const u32x4*>(at + row * 128 + (((2 * s + half) ^ swz(row)) << 4));
+  // Fragments of 16 rows (of a or b) x 32 k (half s of a stage), for 16 x 16 x 32.
+  auto read_direct = [&](const char* at, int row0, int s) {
+    return *reinterpret_cast<const u32x4*>(at + (row0 + col) * 128 + (((4 * s + quad) ^ swz(col)) << 4));
   };
-  auto read_trans = [&](const char* at, int x0, int s) {  // 16 columns from x0, 16 from x0 + 64
-    const int j = (lane >> 2) & 3, u = (x0 >> 4) + 4 * ((lane >> 4) & 1);
-    const char* from = at + (16 * s + 8 * half + j) * 512 + ((u ^ j) << 5) + ((lane & 3) << 3);
+  auto read_trans = [&](const char* at, int x0, int s) {
+    const int j = (lane >> 2) & 3, k = 32 * s + 8 * quad + j;
+    const char* from = at + k * 512 + (((x0 >> 4) ^ tswz(k)) << 5) + ((lane & 3) << 3);
     const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(from));
     const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(from + 2048));
     const u32x2 l = __builtin_bit_cast(u32x2, lo), h = __builtin_bit_cast(u32x2, hi);
     return u32x4{l[0], l[1], h[0], h[1]};
+  };
+  auto read_p = [&](const char* ps, int t, int s) { return PT ? read_trans(ps, 64 * wa + 16 * t, s) : read_direct(ps, 64 * wa + 16 * t, s); };
+  // the wavefront's b: 32 rows of every 64
+  auto read_q = [&](const char* qs, int j, int s) {
+    const int x = 64 * (j >> 1) + 32 * wb + 16 * (j & 1);
+    return QT ? read_trans(qs, x, s) : read_direct(qs, x, s);
   };
   // Every wavefront's reads of a stage are done and the other stage's DMAs landed.
   auto ready = [&] {
@@ -355,83 +367,80 @@ __device__ __forceinline__ void tile_loop(const GemmK& p, int epi, int n_ab, int
   // One tile with b in NB x 64.
   auto body = [&](auto nb_tag) {
     constexpr int NB = decltype(nb_tag)::value;
-    struct Frags {  // of 16 k: 2 of P (32 a each), NB of Q
-      u32x4 p[2], q[NB];
-    };
-    auto read = [&](const char* ps, const char* qs, int s) {
-      Frags f;
+    constexpr int J = 2 * NB;            // b tiles of 16
+    constexpr int D = J < 4 ? J : 4;     // Q fragments read ahead
+    f32x4 acc[4][J] = {};
+    u32x4 pf[2][4], qf[D];
+    // One stage: 2 J slots of 4 products (one Q fragment with 4 of P), each followed by
+    // the reads for later ones.  All of the stage's reads are done D slots before its
+    // end: there the wavefronts meet, the stage is filled again, and the last slots'
+    // products cover the first reads of the other stage.
+    auto stage = [&](const char* ps, const char* qs, const char* pn, const char* qn, auto meet) {
+      auto slot = [&](auto x_tag) {
+        constexpr int X = decltype(x_tag)::value, S = X / J, JJ = X % J, Y = X + D;
+        if constexpr (X == 2 * J - D) meet();
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
-        f.p[t] = PT ? read_trans(ps, 128 * (wa >> 1) + 32 * (wa & 1) + 16 * t, s) : read_direct(ps, 64 * wa + 32 * t + col, s);
+        for (int t = 0; t < 4; ++t) acc[t][JJ] = mfma16t<F16>(pf[S][t], qf[X % D], acc[t][JJ]);
+        qf[X % D] = Y < 2 * J ? read_q(qs, Y % J, Y / J) : read_q(qn, Y % J, 0);
+        if constexpr (X < D) {  // the second half's P
 #pragma unroll
-      for (int j = 0; j < NB; ++j)
-        f.q[j] = QT ? read_trans(qs, 128 * (j >> 1) + 32 * (j & 1) + 16 * wb, s)
-                    : read_direct(qs, 64 * j + 32 * wb + col, s);
-      return f;
-    };
-    f32x16 acc[2][NB] = {};
-    auto mul = [&](const Frags& f) {
-      __builtin_amdgcn_s_setprio(1);
+          for (int t = X * 4 / D; t < (X + 1) * 4 / D; ++t) pf[1][t] = read_p(ps, t, 1);
+        }
+        if constexpr (X >= 2 * J - D && X < 2 * J - D + 2) {  // the other stage's
 #pragma unroll
-      for (int t = 0; t < 2; ++t)
-#pragma unroll
-        for (int j = 0; j < NB; ++j) acc[t][j] = mfma32t<F16>(f.p[t], f.q[j], acc[t][j]);
-      __builtin_amdgcn_s_setprio(0);
+          for (int t = 2 * (X - 2 * J + D); t < 2 * (X - 2 * J + D) + 2; ++t) pf[0][t] = read_p(pn, t, 0);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      };
+      [&]<int... X>(std::integer_sequence<int, X...>) { (slot(std::integral_constant<int, X>{}), ...); }(std::make_integer_sequence<int, 2 * J>{});
     };
     int next_src[4];
     pairs(nxt, 0, next_src);
     // an even number of steps, 2 at least: past the sum's end they multiply zeros
     const int n = max((red + 127) >> 7 << 1, 2);
-    Frags f = read(pA, qA, 0), g;
-    for (int st = 0; st < n; st += 2) {
-      g = read(pA, qA, 1);
-      mul(f);
-      f = read(pA, qA, 2);
-      mul(g);
-      g = read(pA, qA, 3);
-      mul(f);
-      ready();
-      const bool last = st + 2 >= n;
-      if (last) setup(nxt, more, next_src);
-      issue(pA, qA, last ? 0 : st + 2);
-      f = read(pB, qB, 0);
-      mul(g);
-      g = read(pB, qB, 1);
-      mul(f);
-      f = read(pB, qB, 2);
-      mul(g);
-      g = read(pB, qB, 3);
-      mul(f);
-      ready();
-      issue(pB, qB, last ? 1 : st + 3);
-      f = read(pA, qA, 0);
-      mul(g);
+#pragma unroll
+    for (int t = 0; t < 4; ++t) pf[0][t] = read_p(pA, t, 0);
+#pragma unroll
+    for (int x = 0; x < D; ++x) qf[x] = read_q(qA, x, 0);
+    for (int st = 2; st < n; st += 2) {
+      stage(pA, qA, pB, qB, [&] {
+        ready();
+        issue(pA, qA, st);
+      });
+      stage(pB, qB, pA, qA, [&] {
+        ready();
+        issue(pB, qB, st + 1);
+      });
     }
+    stage(pA, qA, pB, qB, [&] {
+      ready();
+      setup(nxt, more, next_src);
+      issue(pA, qA, 0);
+    });
+    stage(pB, qB, pA, qA, [&] {
+      ready();
+      issue(pB, qB, 1);
+    });
 
     // Epilogue: a wavefront's 32 b x 64 a (fp32: 32) at a time through 4 KB of LDS, so
-    // that neighbouring lanes store 64 bytes and more in a row.  Lane (half, col) holds
-    // b number col and of tile t a numbers 8g + 4*half + 0..3 in registers 4g ..; number i is
-    // a = a0 + 32t + i, of a transposed operand a0 + 16t + i % 16 + 64 * (i / 16) (b alike).
+    // that neighbouring lanes store 64 bytes and more in a row.  Of tile (t, x)
+    // lane (quad, col) holds a = a0 + 16t + 4*quad + 0..3 and b = 16x + col.
     // Rows past the end lie past the descriptor's bytes, channels get kDrop: every
     // lane stores, and the stores are counted.
     char* const eb = sE + wv * 4096;
-    const int lane = lane_here(), half = lane >> 5, col = lane & 31;
-    const int a0 = GLU && MODE == kForward ? 128 * cur.ab + 32 * wa
-                   : PT ? 256 * cur.ab + 128 * (wa >> 1) + 32 * (wa & 1) : 256 * cur.ab + 64 * wa;
+    const int lane = lane_here(), quad = lane >> 4, col = lane & 15;
+    const int a0 = GLU && MODE == kForward ? 128 * cur.ab + 32 * wa : 256 * cur.ab + 64 * wa;
     const int rows = min((MODE == kWeights ? p.N : cur.s1) - cur.b0, 256);
     const size_t row0 = (MODE == kWeights ? (size_t)cur.e * p.N : 0) + cur.b0;
-    auto chunk = [&](int r, int ck) { return eb + r * 128 + ((ck ^ (r & 7)) << 4); };  // 8 chunks of 16 bytes a row
-    auto put16 = [&](int ck, const f32x16& v, int g, bool f16) {
-      *reinterpret_cast<u32x2*>(chunk(col, ck) + 8 * half) =
-          f16 ? u32x2{pack16x2<true>(v[4 * g], v[4 * g + 1]), pack16x2<true>(v[4 * g + 2], v[4 * g + 3])}
-              : u32x2{pack_bf16x2(v[4 * g], v[4 * g + 1]), pack_bf16x2(v[4 * g + 2], v[4 * g + 3])};
+    auto chunk = [&](int r, int ck) { return eb + r * 128 + ((ck ^ swz(r)) << 4); };  // 8 chunks of 16 bytes a row
+    auto put16 = [&](int t, int x, const f32x4& v, bool f16) {
+      *reinterpret_cast<u32x2*>(chunk(16 * x + col, 2 * t + (quad >> 1)) + 8 * (quad & 1)) =
+          f16 ? u32x2{pack16x2<true>(v[0], v[1]), pack16x2<true>(v[2], v[3])} : u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
     };
+    auto put32 = [&](int t, int x, const f32x4& v) { *reinterpret_cast<f32x4*>(chunk(16 * x + col, 4 * t + quad)) = v; };
     auto get = [&](int r, int ck) { return *reinterpret_cast<const u32x4*>(chunk(r, ck)); };
     auto get32 = [&](int r, int ck) { return *reinterpret_cast<const f32x4*>(chunk(r, ck)); };
-    // b of the j-th 32's row x (a multiple of 8), from cur.b0
-    auto row_of = [&](int j, int x) {
-      return QT ? 128 * (j >> 1) + 32 * (j & 1) + 16 * wb + (x & 15) + 64 * (x >> 4) : 64 * j + 32 * wb + x;
-    };
+    auto row_of = [&](int j, int x) { return 64 * j + 32 * wb + x; };  // of the j-th 32's row x, from cur.b0
     auto store = [&](rsrc_t r, u32x4 v, uint32_t off, int row, uint32_t ld) {
       typedef unsigned int b128 __attribute__((ext_vector_type(4)));
       // The row's offset is added here: with a scalar register as the instruction's
@@ -450,17 +459,22 @@ __device__ __forceinline__ void tile_loop(const GemmK& p, int epi, int n_ab, int
         if (p.pre_out) {
           const rsrc_t rp = make_rsrc(p.pre_out + row0 * p.N, (uint32_t)rows * ldp);
 #pragma unroll
-          for (int t = 0; t < 2; ++t)
+          for (int t = 0; t < 4; ++t)
 #pragma unroll
-            for (int g = 0; g < 4; ++g) put16(4 * t + g, acc[t][j], g, F16);
+            for (int x = 0; x < 2; ++x) put16(t, x, acc[t][2 * j + x], F16);
 #pragma unroll
           for (int i = 0; i < 4; ++i) store(rp, get(8 * i + (lane >> 3), lane & 7), op, row_of(j, 8 * i), ldp);
         }
-        f32x16 h;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) h[i] = acc[0][j][i] * __builtin_amdgcn_rcpf(1.0f + __expf(-acc[0][j][i])) * acc[1][j][i];
+        for (int t = 0; t < 2; ++t)
 #pragma unroll
-        for (int g = 0; g < 4; ++g) put16(g, h, g, F16);
+          for (int x = 0; x < 2; ++x) {
+            const f32x4 &g = acc[t][2 * j + x], &u = acc[t + 2][2 * j + x];
+            f32x4 h;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) h[i] = g[i] * __builtin_amdgcn_rcpf(1.0f + __expf(-g[i])) * u[i];
+            put16(t, x, h, F16);
+          }
 #pragma unroll
         for (int i = 0; i < 2; ++i) store(ro, get(16 * i + (lane >> 2), lane & 3), oo, row_of(j, 16 * i), ldo);
       }
@@ -476,7 +490,7 @@ __device__ __forceinline__ void tile_loop(const GemmK& p, int epi, int n_ab, int
       uint32_t off[2];
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
-        const int ch = a0 + 16 * t + (x & 15) + 64 * (x >> 4);
+        const int ch = a0 + 32 * t + x;
         off[t] = ch < p.K ? (uint32_t)(lane >> 2) * ld + 2 * ch : kDrop;
       }
       auto fetch = [&](int j) {
@@ -497,9 +511,7 @@ __device__ __forceinline__ void tile_loop(const GemmK& p, int epi, int n_ab, int
 #pragma unroll
         for (int t = 0; t < 2; ++t) {
 #pragma unroll
-          for (int g = 0; g < 4; ++g)
-            *reinterpret_cast<f32x4*>(chunk(col, 2 * g + half)) =
-                f32x4{acc[t][j][4 * g], acc[t][j][4 * g + 1], acc[t][j][4 * g + 2], acc[t][j][4 * g + 3]};
+          for (int h = 0; h < 4; ++h) put32(h >> 1, h & 1, acc[2 * t + (h >> 1)][2 * j + (h & 1)]);
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
             const int r = 16 * i + (lane >> 2);
@@ -535,14 +547,12 @@ __device__ __forceinline__ void tile_loop(const GemmK& p, int epi, int n_ab, int
       const int x = 4 * (lane & 7);
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
-        const int ch = a0 + (PT ? 16 * t + (x & 15) + 64 * (x >> 4) : 32 * t + x);
+        const int ch = a0 + 32 * t + x;
         const uint32_t off = ch < na ? (uint32_t)(lane >> 3) * ld + 4 * ch : kDrop;
 #pragma unroll
         for (int j = 0; j < NB; ++j) {
 #pragma unroll
-          for (int g = 0; g < 4; ++g)
-            *reinterpret_cast<f32x4*>(chunk(col, 2 * g + half)) =
-                f32x4{acc[t][j][4 * g], acc[t][j][4 * g + 1], acc[t][j][4 * g + 2], acc[t][j][4 * g + 3]};
+          for (int h = 0; h < 4; ++h) put32(h >> 1, h & 1, acc[2 * t + (h >> 1)][2 * j + (h & 1)]);
 #pragma unroll
           for (int i = 0; i < 4; ++i) store(ro, get(8 * i + (lane >> 3), lane & 7), off, row_of(j, 8 * i), ld);
         }
@@ -550,14 +560,14 @@ __device__ __forceinline__ void tile_loop(const GemmK& p, int epi, int n_ab, int
     } else {
       const uint32_t ld = 2u * (uint32_t)na;
       const rsrc_t ro = make_rsrc(static_cast<uint16_t*>(p.out) + row0 * na, (uint32_t)rows * ld);
-      const int x = 8 * (lane & 7), ch = a0 + (PT ? (x & 31) + 64 * (x >> 5) : x);
+      const int x = 8 * (lane & 7), ch = a0 + x;
       const uint32_t off = ch < na ? (uint32_t)(lane >> 3) * ld + 2 * ch : kDrop;
 #pragma unroll
       for (int j = 0; j < NB; ++j) {
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
+        for (int t = 0; t < 4; ++t)
 #pragma unroll
-          for (int g = 0; g < 4; ++g) put16(PT ? 4 * (g >> 1) + 2 * t + (g & 1) : 4 * t + g, acc[t][j], g, epi == kEpiF16);
+          for (int x = 0; x < 2; ++x) put16(t, x, acc[t][2 * j + x], epi == kEpiF16);
 #pragma unroll
         for (int i = 0; i < 4; ++i) store(ro, get(8 * i + (lane >> 3), lane & 7), off, row_of(j, 8 * i), ld);
       }
