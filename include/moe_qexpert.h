@@ -408,8 +408,8 @@ moe_status moe_unpermute_combine(const void* y_perm, int32_t y_dtype, const int3
  *               device memory (fp32 partial sums where a few experts' rows are split
  *               over workgroups; 0, NULL allowed, for most sizes); nothing in it
  *               needs to start at zero; calls that share one must be ordered on a stream
- * One expert's weights take less than 4 GiB, as does A where it is gathered
- * (MOE_ERR_UNSUPPORTED).  16-byte aligned buffers (offsets and pairs 4); no output
+ * One expert's weights take less than 4 GiB, A where it is gathered less than
+ * 4 GiB - 4 MiB (MOE_ERR_UNSUPPORTED).  16-byte aligned buffers (offsets and pairs 4); no output
  * may overlap an input.
  */
 #define MOE_EPI_SWIGLU_GRAD 6

@@ -44,8 +44,8 @@ moe_status check_rows(int32_t K, int32_t A_rows, const int32_t* gather_pair, int
   if (gather_pair) {
     if (k < 1) return fail(MOE_ERR_BAD_SHAPE, "k=%d with gather_pair", k);
     if ((int64_t)A_rows * k < M_total) return fail(MOE_ERR_BAD_SHAPE, "A_rows*k < M_total");
-    if ((int64_t)A_rows * K * 2 >= kMaxBytes)
-      return fail(MOE_ERR_UNSUPPORTED, "gathered rows of %lld bytes (4 GiB or more)", (long long)A_rows * K * 2);
+    if ((int64_t)A_rows * K * 2 >= moe::kGatherBytes)
+      return fail(MOE_ERR_UNSUPPORTED, "gathered rows of %lld bytes (fewer than 4 GiB - 4 MiB)", (long long)A_rows * K * 2);
   } else if (A_rows < M_total) {
     return fail(MOE_ERR_BAD_SHAPE, "A_rows=%d < M_total=%d", A_rows, M_total);
   }

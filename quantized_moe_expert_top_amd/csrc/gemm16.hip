@@ -136,6 +136,7 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 constexpr int kCUs = 256;
 constexpr int kStage = 32768;            // bytes of one operand's
 constexpr uint32_t kOut = ~0u;          // a buffer offset past any buffer: reads zero
+constexpr uint32_t kLastGather = kGatherBytes;  // the same for a gathered row, also with a column added
 constexpr uint32_t kDrop = 0x80000000u;  // past any output tile, also with a row added: not stored
 
 // [256][64] of 16 bits in 16-byte chunks, 8 a row: chunk c of row r at place c ^ swz(r).
@@ -221,7 +222,7 @@ __device__ __forceinline__ void tile_loop(const GemmK& p, int epi, int n_ab, int
   const uint16_t *pbase = p.w, *qbase = p.w;
   uint32_t pbytes = 0, qbytes = 0;
   int red = 0, ls0 = 0, ls1 = 0;
-  int src[4];                             // gathered rows' pairs: forward b rows, weights the next step's k
+  int src = 0;                            // weights: the pair of the next step's row 8 wv + lane % 8
   // A copy of the lane's number that the compiler knows nothing about: what a tile
   // needs once is computed there, and not kept in registers over the products.
   auto lane_here = [&] {
@@ -230,20 +231,19 @@ __device__ __forceinline__ void tile_loop(const GemmK& p, int epi, int n_ab, int
     return l;
   };
   const int dr = 8 * wv + (lane >> 5);   // transposed: k of DMA i is dr + 2i
-  auto pairs = [&](const Tile& c, int step, int (&to)[4]) {
-    if constexpr (GATHER) {
-      const int br = 32 * wv + (lane_here() >> 3);  // direct: row of DMA i is br + 8i
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        to[i] = p.gather[max(min(MODE == kForward ? c.b0 + br + 8 * i : c.s0 + 64 * step + dr + 2 * i, c.s1 - 1), 0)];
-    }
+  // The pair of one of the wavefront's gathered rows: of forward's 32 b row lane % 32, of
+  // weights' 8 k of a step row lane % 8.
+  auto pair_of = [&](const Tile& c, int step) {
+    if constexpr (!GATHER) return 0;
+    const int l = lane_here();
+    return p.gather[max(min(MODE == kForward ? c.b0 + 32 * wv + (l & 31) : c.s0 + 64 * step + 8 * wv + (l & 7), c.s1 - 1), 0)];
   };
   auto token = [&](int pair) { return (uint32_t)min(max(p.div(pair), 0), p.A_rows - 1); };
   auto trans_ch = [&](int lane, int k) {  // first of the 8 columns that this lane fetches of row k
     const int s16 = lane & 31;
     return 8 * ((((s16 >> 1) ^ tswz(k)) << 1) + (s16 & 1));
   };
-  auto setup = [&](const Tile& c, bool on, const int (&rows)[4]) {
+  auto setup = [&](const Tile& c, bool on, int pair) {
     const int lane = lane_here(), dr = 8 * wv + (lane >> 5), br = 32 * wv + (lane >> 3), ck = (lane & 7) ^ swz(br);
     red = !on ? 0 : MODE == kForward ? p.K : MODE == kRows ? p.N : c.s1 - c.s0;
     ls0 = c.s0;
@@ -256,8 +256,7 @@ __device__ __forceinline__ void tile_loop(const GemmK& p, int epi, int n_ab, int
       }
       pbase = MODE == kRows ? p.w + (size_t)c.e * p.N * p.K : GATHER ? p.a : p.a + (size_t)c.s0 * p.K;
       if constexpr (GATHER) {
-#pragma unroll
-        for (int i = 0; i < 4; ++i) src[i] = rows[i];
+        src = pair;
         pbytes = (uint32_t)((size_t)p.A_rows * p.K * 2);
       }
     } else {
@@ -283,7 +282,7 @@ __device__ __forceinline__ void tile_loop(const GemmK& p, int epi, int n_ab, int
 #pragma unroll
       for (int i = 0; i < QO; ++i) {
         const int r = br + 8 * i;
-        const uint32_t from = GATHER ? token(rows[i]) : r;
+        const uint32_t from = GATHER ? (uint32_t)__shfl((int)token(pair), 8 * i + (lane >> 3), 64) : r;
         qo[i] = (from * (uint32_t)ld + 8 * (ck ^ (i & 1))) * 2;
         if (GATHER && c.b0 + r >= c.s1) qo[i] = kOut;
       }
@@ -298,36 +297,39 @@ __device__ __forceinline__ void tile_loop(const GemmK& p, int epi, int n_ab, int
   };
   auto issue = [&](char* ps, char* qs, int st) {
     const int left = red - 64 * st;  // k of this step and later ones
-    // (as a scalar: the compiler clamps on the vector side, and would loop over the lanes for the descriptor)
-    const uint32_t rows = (uint32_t)__builtin_amdgcn_readfirstlane(max(min(left, 64), 0));
+    const uint32_t rows = (uint32_t)max(min(left, 64), 0);
     const uint32_t adv = left > 0 ? (uint32_t)st * 128u : 0u;
     char* const pd = ps + wv * 4096;
     char* const qd = qs + wv * 4096;
     if constexpr (PT && GATHER) {
-      const rsrc_t pr = make_rsrc(pbase, pbytes);
-      uint32_t off[4];
+      const rsrc_t pr = scalar_rsrc(pbase, pbytes);
+      // row 8 wv + lane % 8's offset, past the segment one that no column brings back (kLastGather)
+      const int l = lane_here();
+      uint32_t from = token(src) * (uint32_t)(2 * p.K);
+      asm volatile("" : "+v"(from));  // (a select, not a branch around the loads)
+      if (8 * wv + (l & 7) >= left) from = kLastGather;
+      src = pair_of(Tile{0, 0, 0, ls0, ls1}, st + 1);
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        off[i] = dr + 2 * i < left && po[i & 1] != kOut ? token(src[i]) * (uint32_t)(2 * p.K) + po[i & 1] : kOut;
-      pairs(Tile{0, 0, 0, ls0, ls1}, st + 1, src);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) dma(pr, pd + 1024 * i, off[i], 0);
+      for (int i = 0; i < 4; ++i) {
+        const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)from, 2 * i), hi = (uint32_t)__builtin_amdgcn_readlane((int)from, 2 * i + 1);
+        dma(pr, pd + 1024 * i, po[i & 1] == kOut ? kOut : (l & 32 ? hi : lo) + po[i & 1], 0);
+      }
     } else if constexpr (PT) {
-      const rsrc_t pr = make_rsrc(pbase + (size_t)(64 * st) * na, rows * (2u * (uint32_t)na));
+      const rsrc_t pr = scalar_rsrc(pbase + (size_t)(64 * st) * na, rows * (2u * (uint32_t)na));
 #pragma unroll
       for (int i = 0; i < 4; ++i) dma(pr, pd + 1024 * i, po[i & 1], i < 2 ? 0u : 8u * (uint32_t)na);
     } else {
-      const rsrc_t pr = make_rsrc(pbase, pbytes);
+      const rsrc_t pr = scalar_rsrc(pbase, pbytes);
       const uint32_t even = pk < left ? po[0] : kOut, odd = (pk ^ 8) < left ? po[1] : kOut;
 #pragma unroll
       for (int i = 0; i < 4; ++i) dma(pr, pd + 1024 * i, i & 1 ? odd : even, i < 2 ? adv : adv + 32u * (uint32_t)p.K);
     }
     if constexpr (QT) {
-      const rsrc_t qr = make_rsrc(qbase + (size_t)(64 * st) * p.N, rows * (2u * (uint32_t)p.N));
+      const rsrc_t qr = scalar_rsrc(qbase + (size_t)(64 * st) * p.N, rows * (2u * (uint32_t)p.N));
 #pragma unroll
       for (int i = 0; i < 4; ++i) dma(qr, qd + 1024 * i, qo[i & 1], i < 2 ? 0u : 8u * (uint32_t)p.N);
     } else {
-      const rsrc_t qr = make_rsrc(qbase, qbytes);
+      const rsrc_t qr = scalar_rsrc(qbase, qbytes);
       const int ld = MODE == kForward ? p.K : p.N;
 #pragma unroll
       for (int i = 0; i < 4; ++i)
@@ -336,23 +338,30 @@ __device__ __forceinline__ void tile_loop(const GemmK& p, int epi, int n_ab, int
     }
   };
 
-  // Fragments of 16 rows (of a or b) x 32 k (half s of a stage), for 16 x 16 x 32.
-  auto read_direct = [&](const char* at, int row0, int s) {
-    return *reinterpret_cast<const u32x4*>(at + (row0 + col) * 128 + (((4 * s + quad) ^ swz(col)) << 4));
+  // Fragments of 16 rows (of a or b) x 32 k (half s of a stage), for 16 x 16 x 32:
+  // lane (quad, col) holds row col, k = 8 quad .. 8 quad + 7.  The lane's place of the
+  // first fragment; others differ in bits that no other term has (x, s) or by constants.
+  const int dk = 8 * quad + ((lane >> 2) & 3);  // transposed: the lane reads 8 bytes of row dk (and dk + 4)
+  uint32_t pat = PT ? dk * 512 + (((4 * wa) ^ tswz(dk)) << 5) + ((lane & 3) << 3) : wa * 8192 + col * 128 + ((quad ^ swz(col)) << 4);
+  uint32_t qat = QT ? dk * 512 + (((2 * wb) ^ tswz(dk)) << 5) + ((lane & 3) << 3) : wb * 4096 + col * 128 + ((quad ^ swz(col)) << 4);
+  auto read_at = [&](const char* stage, uint32_t at, auto trans_tag) {
+    if constexpr (decltype(trans_tag)::value) {
+      const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(stage + at));
+      const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(stage + at + 2048));
+      const u32x2 l = __builtin_bit_cast(u32x2, lo), h = __builtin_bit_cast(u32x2, hi);
+      return u32x4{l[0], l[1], h[0], h[1]};
+    } else {
+      return *reinterpret_cast<const u32x4*>(stage + at);
+    }
   };
-  auto read_trans = [&](const char* at, int x0, int s) {
-    const int j = (lane >> 2) & 3, k = 32 * s + 8 * quad + j;
-    const char* from = at + k * 512 + (((x0 >> 4) ^ tswz(k)) << 5) + ((lane & 3) << 3);
-    const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(from));
-    const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(from + 2048));
-    const u32x2 l = __builtin_bit_cast(u32x2, lo), h = __builtin_bit_cast(u32x2, hi);
-    return u32x4{l[0], l[1], h[0], h[1]};
+  auto read_p = [&](const char* ps, uint32_t at, int t, int s) {  // a = 64 wa + 16 t + col
+    return PT ? read_at(ps + 16384 * s, at ^ (t << 5), std::integral_constant<bool, PT>{})
+              : read_at(ps + 2048 * t, at ^ (s << 6), std::integral_constant<bool, PT>{});
   };
-  auto read_p = [&](const char* ps, int t, int s) { return PT ? read_trans(ps, 64 * wa + 16 * t, s) : read_direct(ps, 64 * wa + 16 * t, s); };
-  // the wavefront's b: 32 rows of every 64
-  auto read_q = [&](const char* qs, int j, int s) {
-    const int x = 64 * (j >> 1) + 32 * wb + 16 * (j & 1);
-    return QT ? read_trans(qs, x, s) : read_direct(qs, x, s);
+  // the wavefront's b: 32 rows of every 64, b = 64 (j / 2) + 32 wb + 16 (j % 2) + col
+  auto read_q = [&](const char* qs, uint32_t at, int j, int s) {
+    return QT ? read_at(qs + 16384 * s + 256 * (j >> 2), at ^ ((4 * ((j >> 1) & 1) + (j & 1)) << 5), std::integral_constant<bool, QT>{})
+              : read_at(qs + 8192 * (j >> 1) + 2048 * (j & 1), at ^ (s << 6), std::integral_constant<bool, QT>{});
   };
   // Every wavefront's reads of a stage are done and the other stage's DMAs landed.
   auto ready = [&] {
@@ -376,32 +385,33 @@ __device__ __forceinline__ void tile_loop(const GemmK& p, int epi, int n_ab, int
     // end: there the wavefronts meet, the stage is filled again, and the last slots'
     // products cover the first reads of the other stage.
     auto stage = [&](const char* ps, const char* qs, const char* pn, const char* qn, auto meet) {
+      // (opaque: the places of the other fragments are worked out here, not kept in registers)
+      asm volatile("" : "+v"(pat), "+v"(qat));
       auto slot = [&](auto x_tag) {
         constexpr int X = decltype(x_tag)::value, S = X / J, JJ = X % J, Y = X + D;
         if constexpr (X == 2 * J - D) meet();
 #pragma unroll
         for (int t = 0; t < 4; ++t) acc[t][JJ] = mfma16t<F16>(pf[S][t], qf[X % D], acc[t][JJ]);
-        qf[X % D] = Y < 2 * J ? read_q(qs, Y % J, Y / J) : read_q(qn, Y % J, 0);
+        qf[X % D] = Y < 2 * J ? read_q(qs, qat, Y % J, Y / J) : read_q(qn, qat, Y % J, 0);
         if constexpr (X < D) {  // the second half's P
 #pragma unroll
-          for (int t = X * 4 / D; t < (X + 1) * 4 / D; ++t) pf[1][t] = read_p(ps, t, 1);
+          for (int t = X * 4 / D; t < (X + 1) * 4 / D; ++t) pf[1][t] = read_p(ps, pat, t, 1);
         }
         if constexpr (X >= 2 * J - D && X < 2 * J - D + 2) {  // the other stage's
 #pragma unroll
-          for (int t = 2 * (X - 2 * J + D); t < 2 * (X - 2 * J + D) + 2; ++t) pf[0][t] = read_p(pn, t, 0);
+          for (int t = 2 * (X - 2 * J + D); t < 2 * (X - 2 * J + D) + 2; ++t) pf[0][t] = read_p(pn, pat, t, 0);
         }
         __builtin_amdgcn_sched_barrier(0);
       };
       [&]<int... X>(std::integer_sequence<int, X...>) { (slot(std::integral_constant<int, X>{}), ...); }(std::make_integer_sequence<int, 2 * J>{});
     };
-    int next_src[4];
-    pairs(nxt, 0, next_src);
+    const int next_pair = pair_of(nxt, 0);
     // an even number of steps, 2 at least: past the sum's end they multiply zeros
     const int n = max((red + 127) >> 7 << 1, 2);
 #pragma unroll
-    for (int t = 0; t < 4; ++t) pf[0][t] = read_p(pA, t, 0);
+    for (int t = 0; t < 4; ++t) pf[0][t] = read_p(pA, pat, t, 0);
 #pragma unroll
-    for (int x = 0; x < D; ++x) qf[x] = read_q(qA, x, 0);
+    for (int x = 0; x < D; ++x) qf[x] = read_q(qA, qat, x, 0);
     for (int st = 2; st < n; st += 2) {
       stage(pA, qA, pB, qB, [&] {
         ready();
@@ -414,7 +424,7 @@ __device__ __forceinline__ void tile_loop(const GemmK& p, int epi, int n_ab, int
     }
     stage(pA, qA, pB, qB, [&] {
       ready();
-      setup(nxt, more, next_src);
+      setup(nxt, more, next_pair);
       issue(pA, qA, 0);
     });
     stage(pB, qB, pA, qA, [&] {
@@ -450,14 +460,14 @@ __device__ __forceinline__ void tile_loop(const GemmK& p, int epi, int n_ab, int
     };
     if constexpr (GLU && MODE == kForward) {
       const uint32_t ldo = 2u * (uint32_t)I, ldp = 2u * (uint32_t)p.N;
-      const rsrc_t ro = make_rsrc(static_cast<uint16_t*>(p.out) + row0 * I, (uint32_t)rows * ldo);
+      const rsrc_t ro = scalar_rsrc(static_cast<uint16_t*>(p.out) + row0 * I, (uint32_t)rows * ldo);
       const int ch = a0 + 8 * (lane & 3);
       const uint32_t oo = ch < I ? (uint32_t)(lane >> 2) * ldo + 2 * ch : kDrop;
       const uint32_t op = ch < I ? (uint32_t)(lane >> 3) * ldp + 2 * (ch + (lane & 4 ? I : 0)) : kDrop;
 #pragma unroll
       for (int j = 0; j < NB; ++j) {
         if (p.pre_out) {
-          const rsrc_t rp = make_rsrc(p.pre_out + row0 * p.N, (uint32_t)rows * ldp);
+          const rsrc_t rp = scalar_rsrc(p.pre_out + row0 * p.N, (uint32_t)rows * ldp);
 #pragma unroll
           for (int t = 0; t < 4; ++t)
 #pragma unroll
@@ -480,8 +490,8 @@ __device__ __forceinline__ void tile_loop(const GemmK& p, int epi, int n_ab, int
       }
     } else if constexpr (GLU) {
       const uint32_t ld = 4u * (uint32_t)p.K;
-      const rsrc_t ro = make_rsrc(static_cast<uint16_t*>(p.out) + row0 * 2 * p.K, (uint32_t)rows * ld);
-      const rsrc_t rp = make_rsrc(p.pre_in + row0 * 2 * p.K, (uint32_t)rows * ld);
+      const rsrc_t ro = scalar_rsrc(static_cast<uint16_t*>(p.out) + row0 * 2 * p.K, (uint32_t)rows * ld);
+      const rsrc_t rp = scalar_rsrc(p.pre_in + row0 * 2 * p.K, (uint32_t)rows * ld);
       const int x = 8 * (lane & 3);
       // 8 channels of 16 rows a load: gate and up, for both tiles and row halves of one j
       struct Pre {
@@ -543,7 +553,7 @@ __device__ __forceinline__ void tile_loop(const GemmK& p, int epi, int n_ab, int
       }
     } else if (epi == kEpiF32) {
       const uint32_t ld = 4u * (uint32_t)na;
-      const rsrc_t ro = make_rsrc(static_cast<float*>(p.out) + row0 * na, (uint32_t)rows * ld);
+      const rsrc_t ro = scalar_rsrc(static_cast<float*>(p.out) + row0 * na, (uint32_t)rows * ld);
       const int x = 4 * (lane & 7);
 #pragma unroll
       for (int t = 0; t < 2; ++t) {
@@ -559,7 +569,7 @@ __device__ __forceinline__ void tile_loop(const GemmK& p, int epi, int n_ab, int
       }
     } else {
       const uint32_t ld = 2u * (uint32_t)na;
-      const rsrc_t ro = make_rsrc(static_cast<uint16_t*>(p.out) + row0 * na, (uint32_t)rows * ld);
+      const rsrc_t ro = scalar_rsrc(static_cast<uint16_t*>(p.out) + row0 * na, (uint32_t)rows * ld);
       const int x = 8 * (lane & 7), ch = a0 + x;
       const uint32_t off = ch < na ? (uint32_t)(lane >> 3) * ld + 2 * ch : kDrop;
 #pragma unroll
@@ -574,8 +584,7 @@ __device__ __forceinline__ void tile_loop(const GemmK& p, int epi, int n_ab, int
     }
   };
 
-  pairs(cur, 0, src);
-  setup(cur, true, src);
+  setup(cur, true, pair_of(cur, 0));
   issue(pA, qA, 0);
   issue(pB, qB, 1);
   ready();

@@ -213,6 +213,8 @@ struct Gemm16Args {
   void* out;
   void* ws;
 };
+// A gathered A has fewer bytes: 4 GiB less a row of the widest (2^20 inputs) on either side.
+constexpr uint32_t kGatherBytes = 0xFFC00000u;
 int launch_gemm16(const Gemm16Args& a, void* stream);
 int launch_gemm16_grad_rows(const Gemm16Args& a, void* stream);
 size_t gemm16_grad_weights_workspace_bytes(int E, int N, int K, int M_total, int kernel);

@@ -39,12 +39,21 @@ __device__ __forceinline__ uint32_t pack16x2(float lo, float hi) {
   else return pack_bf16x2(lo, hi);
 }
 
+// make_rsrc with its parts forced into scalar registers: values that the compiler
+// worked out on the vector side (clamps, what came by shuffles) would make every
+// access through the descriptor a loop over the lanes.
+__device__ __forceinline__ rsrc_t scalar_rsrc(const void* base, uint32_t bytes) {
+  const uint64_t b = reinterpret_cast<uint64_t>(base);
+  const uint32_t lo = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)b), hi = (uint32_t)__builtin_amdgcn_readfirstlane((int)(uint32_t)(b >> 32));
+  return make_rsrc(reinterpret_cast<const void*>((uint64_t)hi << 32 | lo), (uint32_t)__builtin_amdgcn_readfirstlane((int)bytes));
+}
+
 // pair / div = (pair * mul) >> (31 + shift), 0 <= pair < 2^31
 struct PairDiv {
   uint32_t mul;
   int shift;
   __device__ __forceinline__ int operator()(int pair) const {
-    return (int)(((uint64_t)(uint32_t)pair * mul) >> (31 + shift));
+    return (int)(__umulhi(2u * (uint32_t)pair, mul) >> shift);
   }
 };
 inline PairDiv pair_div(int div) {
