@@ -401,7 +401,7 @@ __device__ __forceinline__ void tile_loop(const GemmK& p, int epi, int n_ab, int
 #pragma unroll
           for (int t = 2 * (X - 2 * J + D); t < 2 * (X - 2 * J + D) + 2; ++t) pf[0][t] = read_p(pn, pat, t, 0);
         }
-        __builtin_amdgcn_sched_barrier(0);
+        if constexpr (X & 1) __builtin_amdgcn_sched_barrier(0);
       };
       [&]<int... X>(std::integer_sequence<int, X...>) { (slot(std::integral_constant<int, X>{}), ...); }(std::make_integer_sequence<int, 2 * J>{});
     };
@@ -451,13 +451,18 @@ __device__ __forceinline__ void tile_loop(const GemmK& p, int epi, int n_ab, int
     auto get = [&](int r, int ck) { return *reinterpret_cast<const u32x4*>(chunk(r, ck)); };
     auto get32 = [&](int r, int ck) { return *reinterpret_cast<const f32x4*>(chunk(r, ck)); };
     auto row_of = [&](int j, int x) { return 64 * j + 32 * wb + x; };  // of the j-th 32's row x, from cur.b0
-    auto store = [&](rsrc_t r, u32x4 v, uint32_t off, int row, uint32_t ld) {
+    auto store = [&](rsrc_t r, u32x4 v, uint32_t off, int row, uint32_t ld, auto stream_tag) {
       typedef unsigned int b128 __attribute__((ext_vector_type(4)));
       // The row's offset is added here: with a scalar register as the instruction's
       // offset the compiler sees no hazard in overwriting the data in the next
       // instruction, but gfx950 then stores some of the new values.
-      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(b128, v), r, off + (uint32_t)row * ld, 0, 0);
+      __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(b128, v), r, off + (uint32_t)row * ld, 0, decltype(stream_tag)::value ? 2 : 0);
     };
+    // Whole lines of 128 bytes go past the caches (65536 rows of 2048 channels, us with and without:
+    // 87 / 122 with 256 inputs, 134 / 168 with 512, 265 / 267 with 1024), halves of lines, which
+    // the L2 joins, do not (SwiGLU with what enters it 546 / 529).
+    const std::true_type whole_lines{};
+    const std::false_type half_lines{};
     if constexpr (GLU && MODE == kForward) {
       const uint32_t ldo = 2u * (uint32_t)I, ldp = 2u * (uint32_t)p.N;
       const rsrc_t ro = scalar_rsrc(static_cast<uint16_t*>(p.out) + row0 * I, (uint32_t)rows * ldo);
@@ -473,7 +478,7 @@ __device__ __forceinline__ void tile_loop(const GemmK& p, int epi, int n_ab, int
 #pragma unroll
             for (int x = 0; x < 2; ++x) put16(t, x, acc[t][2 * j + x], F16);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) store(rp, get(8 * i + (lane >> 3), lane & 7), op, row_of(j, 8 * i), ldp);
+          for (int i = 0; i < 4; ++i) store(rp, get(8 * i + (lane >> 3), lane & 7), op, row_of(j, 8 * i), ldp, half_lines);
         }
 #pragma unroll
         for (int t = 0; t < 2; ++t)
@@ -486,7 +491,7 @@ __device__ __forceinline__ void tile_loop(const GemmK& p, int epi, int n_ab, int
             put16(t, x, h, F16);
           }
 #pragma unroll
-        for (int i = 0; i < 2; ++i) store(ro, get(16 * i + (lane >> 2), lane & 3), oo, row_of(j, 16 * i), ldo);
+        for (int i = 0; i < 2; ++i) store(ro, get(16 * i + (lane >> 2), lane & 3), oo, row_of(j, 16 * i), ldo, half_lines);
       }
     } else if constexpr (GLU) {
       const uint32_t ld = 4u * (uint32_t)p.K;
@@ -545,8 +550,8 @@ __device__ __forceinline__ void tile_loop(const GemmK& p, int epi, int n_ab, int
                 du[2 * q + w] = pack16x2<F16>(ou[0], ou[1]);
               }
             }
-            store(ro, dg, off[t], row_of(j, 16 * i), ld);
-            store(ro, du, off[t] + ld / 2, row_of(j, 16 * i), ld);
+            store(ro, dg, off[t], row_of(j, 16 * i), ld, half_lines);
+            store(ro, du, off[t] + ld / 2, row_of(j, 16 * i), ld, half_lines);
           }
         }
         pre = ahead;
@@ -564,7 +569,7 @@ __device__ __forceinline__ void tile_loop(const GemmK& p, int epi, int n_ab, int
 #pragma unroll
           for (int h = 0; h < 4; ++h) put32(h >> 1, h & 1, acc[2 * t + (h >> 1)][2 * j + (h & 1)]);
 #pragma unroll
-          for (int i = 0; i < 4; ++i) store(ro, get(8 * i + (lane >> 3), lane & 7), off, row_of(j, 8 * i), ld);
+          for (int i = 0; i < 4; ++i) store(ro, get(8 * i + (lane >> 3), lane & 7), off, row_of(j, 8 * i), ld, whole_lines);
         }
       }
     } else {
@@ -579,7 +584,7 @@ __device__ __forceinline__ void tile_loop(const GemmK& p, int epi, int n_ab, int
 #pragma unroll
           for (int x = 0; x < 2; ++x) put16(t, x, acc[t][2 * j + x], epi == kEpiF16);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) store(ro, get(8 * i + (lane >> 3), lane & 7), off, row_of(j, 8 * i), ld);
+        for (int i = 0; i < 4; ++i) store(ro, get(8 * i + (lane >> 3), lane & 7), off, row_of(j, 8 * i), ld, whole_lines);
       }
     }
   };
