@@ -134,7 +134,6 @@ __global__ __launch_bounds__(256) void gemm16_kernel(GemmK p, int epi, int n_ab)
 // b do [64][256], read back transposed (ds_read_b64_tr_b16).
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 constexpr int kCUs = 256;
-constexpr int kStage = 32768;            // bytes of one operand's
 constexpr uint32_t kOut = ~0u;          // a buffer offset past any buffer: reads zero
 constexpr uint32_t kLastGather = kGatherBytes;  // the same for a gathered row, also with a column added
 constexpr uint32_t kDrop = 0x80000000u;  // past any output tile, also with a row added: not stored
@@ -162,11 +161,12 @@ __device__ __forceinline__ void grouped_order(int idx, int tiles, int n_ab, int&
 // a and up to 128 b of each.  The last two steps of a tile issue the first two of the
 // next one, so that only the first tile waits for its loads, and a tile's stores go
 // out under the next one's products.
-template <bool F16, int MODE, bool GATHER, bool GLU>
+template <int T, bool F16, int MODE, bool GATHER, bool GLU>
 __device__ __forceinline__ void tile_loop(const GemmK& p, int epi, int n_ab, int n_bb, char* pA, char* pB, char* qA, char* qB, char* sE) {
   constexpr bool PT = MODE != kForward, QT = MODE == kWeights;  // transposed operands
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  const int wa = wv & 3, wb = wv >> 2, col = lane & 15, quad = lane >> 4;
+  constexpr int WA = T / 64;  // wavefronts along a; two along b
+  const int wa = wv & (WA - 1), wb = wv / WA, col = lane & 15, quad = lane >> 4;
   const int I = p.N / 2;
   const int na = MODE == kForward ? p.N : p.K;  // a's extent (and a transposed P's row length)
 
@@ -176,9 +176,9 @@ __device__ __forceinline__ void tile_loop(const GemmK& p, int epi, int n_ab, int
   if constexpr (MODE == kWeights) {
     total = p.E * n_ab * n_bb;
   } else {
-    seg_n = segment_tiles<256>(p.seg, p.E, p.M_total, lane, seg0, seg1);
+    seg_n = segment_tiles<T>(p.seg, p.E, p.M_total, lane, seg0, seg1);
     seg_end = lane_scan(seg_n);
-    total = (p.E <= 64 ? __builtin_amdgcn_readlane(seg_end, 63) : count_tiles<256>(p.seg, p.E, p.M_total)) * n_ab;
+    total = (p.E <= 64 ? __builtin_amdgcn_readlane(seg_end, 63) : count_tiles<T>(p.seg, p.E, p.M_total)) * n_ab;
   }
   const int per = (total + 7) >> 3, xcd = (int)blockIdx.x & 7;
   int idx = xcd * per + ((int)blockIdx.x >> 3);
@@ -190,7 +190,7 @@ __device__ __forceinline__ void tile_loop(const GemmK& p, int epi, int n_ab, int
     if constexpr (MODE == kWeights) {
       c.e = at / (n_ab * n_bb);
       grouped_order(at - c.e * (n_ab * n_bb), n_bb, n_ab, tile, c.ab);
-      c.b0 = 256 * tile;
+      c.b0 = T * tile;
       c.s0 = c.s1 = 0;
       if (p.M_total > 0) segment_rows(p.seg, c.e, p.M_total, c.s0, c.s1);
     } else {
@@ -202,11 +202,11 @@ __device__ __forceinline__ void tile_loop(const GemmK& p, int epi, int n_ab, int
         t.s1 = __builtin_amdgcn_readlane(seg1, t.e);
         at -= (__builtin_amdgcn_readlane(seg_end, t.e) - t.tiles) * n_ab;
       } else {
-        find_tile<256>(p.seg, p.E, p.M_total, n_ab, at, t);
+        find_tile<T>(p.seg, p.E, p.M_total, n_ab, at, t);
       }
       grouped_order(at, t.tiles, n_ab, tile, c.ab);
       c.e = t.e;
-      c.b0 = t.r0 + 256 * tile;
+      c.b0 = t.r0 + T * tile;
       c.s0 = t.r0;
       c.s1 = t.s1;
     }
@@ -230,28 +230,33 @@ __device__ __forceinline__ void tile_loop(const GemmK& p, int epi, int n_ab, int
     asm volatile("" : "+v"(l));
     return l;
   };
-  const int dr = 8 * wv + (lane >> 5);   // transposed: k of DMA i is dr + 2i
+  // Transposed operands: a row of a stage is T columns, a DMA RK rows; DMA i fetches k
+  // = dr + RK i.  Two DMAs whose rows are 4 apart have the same places (tswz).
+  constexpr int RK = 512 / T, LR = T / 8;  // (lanes of a row)
+  const int dr = 4 * RK * wv + lane / LR;
+  constexpr auto twin = [](int i) { return T == 256 ? i & 1 : i >> 1; };    // which of the two kinds
+  constexpr auto second = [](int i) { return T == 256 ? i >> 1 : i & 1; };  // whether the later one
   // The pair of one of the wavefront's gathered rows: of forward's 32 b row lane % 32, of
-  // weights' 8 k of a step row lane % 8.
+  // weights' 4 RK k of a step row lane % (4 RK).
   auto pair_of = [&](const Tile& c, int step) {
     if constexpr (!GATHER) return 0;
     const int l = lane_here();
-    return p.gather[max(min(MODE == kForward ? c.b0 + 32 * wv + (l & 31) : c.s0 + 64 * step + 8 * wv + (l & 7), c.s1 - 1), 0)];
+    return p.gather[max(min(MODE == kForward ? c.b0 + 32 * wv + (l & 31) : c.s0 + 64 * step + 4 * RK * wv + (l & (4 * RK - 1)), c.s1 - 1), 0)];
   };
   auto token = [&](int pair) { return (uint32_t)min(max(p.div(pair), 0), p.A_rows - 1); };
   auto trans_ch = [&](int lane, int k) {  // first of the 8 columns that this lane fetches of row k
-    const int s16 = lane & 31;
+    const int s16 = lane & (LR - 1);
     return 8 * ((((s16 >> 1) ^ tswz(k)) << 1) + (s16 & 1));
   };
   auto setup = [&](const Tile& c, bool on, int pair) {
-    const int lane = lane_here(), dr = 8 * wv + (lane >> 5), br = 32 * wv + (lane >> 3), ck = (lane & 7) ^ swz(br);
+    const int lane = lane_here(), dr = 4 * RK * wv + lane / LR, br = 32 * wv + (lane >> 3), ck = (lane & 7) ^ swz(br);
     red = !on ? 0 : MODE == kForward ? p.K : MODE == kRows ? p.N : c.s1 - c.s0;
     ls0 = c.s0;
     ls1 = c.s1;
     if constexpr (PT) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int k = dr + 2 * i, ch = 256 * c.ab + trans_ch(lane, k);
+        const int k = dr + (T == 256 ? 2 : 8) * i, ch = T * c.ab + trans_ch(lane, k);
         po[i] = ch < na ? (GATHER ? (uint32_t)ch : (uint32_t)k * (uint32_t)na + ch) * 2 : kOut;
       }
       pbase = MODE == kRows ? p.w + (size_t)c.e * p.N * p.K : GATHER ? p.a : p.a + (size_t)c.s0 * p.K;
@@ -263,7 +268,7 @@ __device__ __forceinline__ void tile_loop(const GemmK& p, int epi, int n_ab, int
       // SwiGLU: rows 64w .. 64w + 31 are gate channels of wavefront column w, 64w + 32 .. 64w + 63
       // their up channels (past the last gate channel: up ones, never stored)
       pk = qk = 8 * ck;
-      const int ch = GLU ? 128 * c.ab + 32 * (wv >> 1) + (lane >> 3) + (wv & 1 ? I : 0) : 256 * c.ab + br;
+      const int ch = GLU ? T / 2 * c.ab + 32 * (wv >> 1) + (lane >> 3) + (wv & 1 ? I : 0) : T * c.ab + br;
 #pragma unroll
       for (int i = 0; i < 2; ++i) po[i] = ((uint32_t)(ch + 8 * i) * (uint32_t)p.K + 8 * (ck ^ i)) * 2;
       pbase = p.w + (size_t)c.e * p.N * p.K;
@@ -272,7 +277,7 @@ __device__ __forceinline__ void tile_loop(const GemmK& p, int epi, int n_ab, int
     if constexpr (QT) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        const int k = dr + 2 * i, ch = c.b0 + trans_ch(lane, k);
+        const int k = dr + (T == 256 ? 2 : 8) * i, ch = c.b0 + trans_ch(lane, k);
         qo[i] = ch < p.N ? ((uint32_t)k * (uint32_t)p.N + ch) * 2 : kOut;
       }
       qbase = p.dy + (size_t)c.s0 * p.N;
@@ -287,7 +292,7 @@ __device__ __forceinline__ void tile_loop(const GemmK& p, int epi, int n_ab, int
         if (GATHER && c.b0 + r >= c.s1) qo[i] = kOut;
       }
       qbase = MODE == kForward ? (GATHER ? p.a : p.a + (size_t)c.b0 * ld) : p.dy + (size_t)c.b0 * ld;
-      qbytes = GATHER ? (uint32_t)((size_t)p.A_rows * ld * 2) : (uint32_t)((size_t)min(c.s1 - c.b0, 256) * ld * 2);
+      qbytes = GATHER ? (uint32_t)((size_t)p.A_rows * ld * 2) : (uint32_t)((size_t)min(c.s1 - c.b0, T) * ld * 2);
     }
   };
 
@@ -303,21 +308,27 @@ __device__ __forceinline__ void tile_loop(const GemmK& p, int epi, int n_ab, int
     char* const qd = qs + wv * 4096;
     if constexpr (PT && GATHER) {
       const rsrc_t pr = scalar_rsrc(pbase, pbytes);
-      // row 8 wv + lane % 8's offset, past the segment one that no column brings back (kLastGather)
+      // row 4 RK wv + lane % (4 RK)'s offset, past the segment one that no column brings back (kLastGather)
       const int l = lane_here();
       uint32_t from = token(src) * (uint32_t)(2 * p.K);
       asm volatile("" : "+v"(from));  // (a select, not a branch around the loads)
-      if (8 * wv + (l & 7) >= left) from = kLastGather;
+      if (4 * RK * wv + (l & (4 * RK - 1)) >= left) from = kLastGather;
       src = pair_of(Tile{0, 0, 0, ls0, ls1}, st + 1);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)from, 2 * i), hi = (uint32_t)__builtin_amdgcn_readlane((int)from, 2 * i + 1);
-        dma(pr, pd + 1024 * i, po[i & 1] == kOut ? kOut : (l & 32 ? hi : lo) + po[i & 1], 0);
+        uint32_t at;
+        if constexpr (T == 256) {
+          const uint32_t lo = (uint32_t)__builtin_amdgcn_readlane((int)from, 2 * i), hi = (uint32_t)__builtin_amdgcn_readlane((int)from, 2 * i + 1);
+          at = l & 32 ? hi : lo;
+        } else {
+          at = (uint32_t)__shfl((int)from, 4 * i + (l >> 4), 64);
+        }
+        dma(pr, pd + 1024 * i, po[twin(i)] == kOut ? kOut : at + po[twin(i)], 0);
       }
     } else if constexpr (PT) {
       const rsrc_t pr = scalar_rsrc(pbase + (size_t)(64 * st) * na, rows * (2u * (uint32_t)na));
 #pragma unroll
-      for (int i = 0; i < 4; ++i) dma(pr, pd + 1024 * i, po[i & 1], i < 2 ? 0u : 8u * (uint32_t)na);
+      for (int i = 0; i < 4; ++i) dma(pr, pd + 1024 * i, po[twin(i)], second(i) ? 8u * (uint32_t)na : 0u);
     } else {
       const rsrc_t pr = scalar_rsrc(pbase, pbytes);
       const uint32_t even = pk < left ? po[0] : kOut, odd = (pk ^ 8) < left ? po[1] : kOut;
@@ -327,7 +338,7 @@ __device__ __forceinline__ void tile_loop(const GemmK& p, int epi, int n_ab, int
     if constexpr (QT) {
       const rsrc_t qr = scalar_rsrc(qbase + (size_t)(64 * st) * p.N, rows * (2u * (uint32_t)p.N));
 #pragma unroll
-      for (int i = 0; i < 4; ++i) dma(qr, qd + 1024 * i, qo[i & 1], i < 2 ? 0u : 8u * (uint32_t)p.N);
+      for (int i = 0; i < 4; ++i) dma(qr, qd + 1024 * i, qo[twin(i)], second(i) ? 8u * (uint32_t)p.N : 0u);
     } else {
       const rsrc_t qr = scalar_rsrc(qbase, qbytes);
       const int ld = MODE == kForward ? p.K : p.N;
@@ -342,12 +353,13 @@ __device__ __forceinline__ void tile_loop(const GemmK& p, int epi, int n_ab, int
   // lane (quad, col) holds row col, k = 8 quad .. 8 quad + 7.  The lane's place of the
   // first fragment; others differ in bits that no other term has (x, s) or by constants.
   const int dk = 8 * quad + ((lane >> 2) & 3);  // transposed: the lane reads 8 bytes of row dk (and dk + 4)
-  uint32_t pat = PT ? dk * 512 + (((4 * wa) ^ tswz(dk)) << 5) + ((lane & 3) << 3) : wa * 8192 + col * 128 + ((quad ^ swz(col)) << 4);
-  uint32_t qat = QT ? dk * 512 + (((2 * wb) ^ tswz(dk)) << 5) + ((lane & 3) << 3) : wb * 4096 + col * 128 + ((quad ^ swz(col)) << 4);
+  constexpr int RB = 2 * T;  // bytes of a transposed row
+  uint32_t pat = PT ? dk * RB + (((4 * wa) ^ tswz(dk)) << 5) + ((lane & 3) << 3) : wa * 8192 + col * 128 + ((quad ^ swz(col)) << 4);
+  uint32_t qat = QT ? dk * RB + (((2 * wb) ^ tswz(dk)) << 5) + ((lane & 3) << 3) : wb * 4096 + col * 128 + ((quad ^ swz(col)) << 4);
   auto read_at = [&](const char* stage, uint32_t at, auto trans_tag) {
     if constexpr (decltype(trans_tag)::value) {
       const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(stage + at));
-      const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(stage + at + 2048));
+      const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(stage + at + 4 * RB));
       const u32x2 l = __builtin_bit_cast(u32x2, lo), h = __builtin_bit_cast(u32x2, hi);
       return u32x4{l[0], l[1], h[0], h[1]};
     } else {
@@ -355,12 +367,12 @@ __device__ __forceinline__ void tile_loop(const GemmK& p, int epi, int n_ab, int
     }
   };
   auto read_p = [&](const char* ps, uint32_t at, int t, int s) {  // a = 64 wa + 16 t + col
-    return PT ? read_at(ps + 16384 * s, at ^ (t << 5), std::integral_constant<bool, PT>{})
+    return PT ? read_at(ps + 32 * RB * s, at ^ (t << 5), std::integral_constant<bool, PT>{})
               : read_at(ps + 2048 * t, at ^ (s << 6), std::integral_constant<bool, PT>{});
   };
   // the wavefront's b: 32 rows of every 64, b = 64 (j / 2) + 32 wb + 16 (j % 2) + col
   auto read_q = [&](const char* qs, uint32_t at, int j, int s) {
-    return QT ? read_at(qs + 16384 * s + 256 * (j >> 2), at ^ ((4 * ((j >> 1) & 1) + (j & 1)) << 5), std::integral_constant<bool, QT>{})
+    return QT ? read_at(qs + 32 * RB * s + 256 * (j >> 2), at ^ ((4 * ((j >> 1) & 1) + (j & 1)) << 5), std::integral_constant<bool, QT>{})
               : read_at(qs + 8192 * (j >> 1) + 2048 * (j & 1), at ^ (s << 6), std::integral_constant<bool, QT>{});
   };
   // Every wavefront's reads of a stage are done and the other stage's DMAs landed.
@@ -439,8 +451,8 @@ __device__ __forceinline__ void tile_loop(const GemmK& p, int epi, int n_ab, int
     // lane stores, and the stores are counted.
     char* const eb = sE + wv * 4096;
     const int lane = lane_here(), quad = lane >> 4, col = lane & 15;
-    const int a0 = GLU && MODE == kForward ? 128 * cur.ab + 32 * wa : 256 * cur.ab + 64 * wa;
-    const int rows = min((MODE == kWeights ? p.N : cur.s1) - cur.b0, 256);
+    const int a0 = GLU && MODE == kForward ? T / 2 * cur.ab + 32 * wa : T * cur.ab + 64 * wa;
+    const int rows = min((MODE == kWeights ? p.N : cur.s1) - cur.b0, T);
     const size_t row0 = (MODE == kWeights ? (size_t)cur.e * p.N : 0) + cur.b0;
     auto chunk = [&](int r, int ck) { return eb + r * 128 + ((ck ^ swz(r)) << 4); };  // 8 chunks of 16 bytes a row
     auto put16 = [&](int t, int x, const f32x4& v, bool f16) {
@@ -597,21 +609,26 @@ __device__ __forceinline__ void tile_loop(const GemmK& p, int epi, int n_ab, int
     idx += idx_step;
     more = idx < idx_end;
     nxt = more ? locate(idx) : cur;
-    const int left = MODE == kWeights ? 256 : cur.s1 - cur.b0;
-    if (left <= 64) body(std::integral_constant<int, 1>{});
-    else if (left <= 128) body(std::integral_constant<int, 2>{});
-    else if (left <= 192) body(std::integral_constant<int, 3>{});
-    else body(std::integral_constant<int, 4>{});
+    const int left = MODE == kWeights ? T : cur.s1 - cur.b0;
+    if constexpr (T == 256) {
+      if (left <= 64) body(std::integral_constant<int, 1>{});
+      else if (left <= 128) body(std::integral_constant<int, 2>{});
+      else if (left <= 192) body(std::integral_constant<int, 3>{});
+      else body(std::integral_constant<int, 4>{});
+    } else {
+      if (left <= 64) body(std::integral_constant<int, 1>{});
+      else body(std::integral_constant<int, 2>{});
+    }
     if (!more) break;
     cur = nxt;
   }
 }
 
-template <bool F16, int MODE, bool GATHER, bool GLU>
-__global__ __launch_bounds__(512, 2) void tile256_kernel(GemmK p, int epi, int n_ab, int n_bb) {
+template <int T, bool F16, int MODE, bool GATHER, bool GLU>
+__global__ __launch_bounds__(2 * T, 2) void tile_kernel(GemmK p, int epi, int n_ab, int n_bb) {
 #ifdef __HIP_DEVICE_COMPILE__
-  __shared__ __attribute__((aligned(1024))) char pA[kStage], pB[kStage], qA[kStage], qB[kStage], sE[8 * 4096];
-  tile_loop<F16, MODE, GATHER, GLU>(p, epi, n_ab, n_bb, pA, pB, qA, qB, sE);
+  __shared__ __attribute__((aligned(1024))) char pA[128 * T], pB[128 * T], qA[128 * T], qB[128 * T], sE[T / 32 * 4096];
+  tile_loop<T, F16, MODE, GATHER, GLU>(p, epi, n_ab, n_bb, pA, pB, qA, qB, sE);
 #endif
 }
 
@@ -632,38 +649,48 @@ int launch_rowwise(const Gemm16Args& a, int n_ab, hipStream_t s) {
   return (int)hipGetLastError();
 }
 
-template <bool F16, int MODE, bool GATHER, bool GLU>
-int launch256(const Gemm16Args& a, hipStream_t s) {
-  const int na = MODE == kForward ? (GLU ? a.N : a.N) : a.K, n_ab = (na + 255) / 256, n_bb = (a.N + 255) / 256;
-  const int64_t tiles = (MODE == kWeights ? (int64_t)a.E * n_bb : row_tiles(a.M_total, a.E, 256)) * n_ab;
+template <int T, bool F16, int MODE, bool GATHER, bool GLU>
+int launch_tile(const Gemm16Args& a, hipStream_t s) {
+  const int na = MODE == kForward ? a.N : a.K, n_ab = (na + T - 1) / T, n_bb = (a.N + T - 1) / T;
+  const int64_t tiles = (MODE == kWeights ? (int64_t)a.E * n_bb : row_tiles(a.M_total, a.E, T)) * n_ab;
   if (tiles >= ((int64_t)1 << 30)) return (int)hipErrorInvalidConfiguration;
-  const int64_t wgs = tiles < kCUs ? (tiles + 7) / 8 * 8 : kCUs;
-  hipLaunchKernelGGL((tile256_kernel<F16, MODE, GATHER, GLU>), dim3((unsigned)wgs), dim3(512), 0, s, kernel_args(a), a.epilogue, n_ab, n_bb);
+  const int64_t most = T == 256 ? kCUs : 2 * kCUs;  // workgroups that fit the chip at once
+  const int64_t wgs = tiles < most ? (tiles + 7) / 8 * 8 : most;
+  hipLaunchKernelGGL((tile_kernel<T, F16, MODE, GATHER, GLU>), dim3((unsigned)wgs), dim3(2 * T), 0, s, kernel_args(a), a.epilogue, n_ab, n_bb);
   return (int)hipGetLastError();
 }
+template <int T, int MODE, bool GATHER, bool GLU>
+int launch_typed(const Gemm16Args& a, hipStream_t s) {
+  return a.dtype == 2 ? launch_tile<T, true, MODE, GATHER, GLU>(a, s) : launch_tile<T, false, MODE, GATHER, GLU>(a, s);
+}
 template <int MODE, bool GATHER, bool GLU>
-int launch256t(const Gemm16Args& a, void* s) {
-  return a.dtype == 2 ? launch256<true, MODE, GATHER, GLU>(a, static_cast<hipStream_t>(s)) : launch256<false, MODE, GATHER, GLU>(a, static_cast<hipStream_t>(s));
+int launch_sized(const Gemm16Args& a, int t, void* s) {
+  return t == 256 ? launch_typed<256, MODE, GATHER, GLU>(a, static_cast<hipStream_t>(s)) : launch_typed<128, MODE, GATHER, GLU>(a, static_cast<hipStream_t>(s));
 }
 }  // namespace
 
 int launch_gemm16(const Gemm16Args& a, void* stream) {
-  if (a.kernel == 9 || a.kernel == 0) {
-    if (a.gather) return a.epilogue == kEpiSwiglu ? launch256t<kForward, true, true>(a, stream) : launch256t<kForward, true, false>(a, stream);
-    return a.epilogue == kEpiSwiglu ? launch256t<kForward, false, true>(a, stream) : launch256t<kForward, false, false>(a, stream);
+  if (a.kernel == 9 || a.kernel == 0 || a.kernel == 5) {
+    const int t = a.kernel == 5 ? 128 : 256;
+    if (a.gather) return a.epilogue == kEpiSwiglu ? launch_sized<kForward, true, true>(a, t, stream) : launch_sized<kForward, true, false>(a, t, stream);
+    return a.epilogue == kEpiSwiglu ? launch_sized<kForward, false, true>(a, t, stream) : launch_sized<kForward, false, false>(a, t, stream);
   }
   const int n_ab = a.epilogue == kEpiSwiglu ? (a.N / 2 + 31) / 32 : (a.N + 63) / 64;
   return launch_rowwise<kForward>(a, n_ab, static_cast<hipStream_t>(stream));
 }
 int launch_gemm16_grad_rows(const Gemm16Args& a, void* stream) {
-  if (a.kernel == 9 || a.kernel == 0)
-    return a.epilogue == kEpiSwigluGrad ? launch256t<kRows, false, true>(a, stream) : launch256t<kRows, false, false>(a, stream);
+  if (a.kernel == 9 || a.kernel == 0 || a.kernel == 5) {
+    const int t = a.kernel == 5 ? 128 : 256;
+    return a.epilogue == kEpiSwigluGrad ? launch_sized<kRows, false, true>(a, t, stream) : launch_sized<kRows, false, false>(a, t, stream);
+  }
   return launch_rowwise<kRows>(a, (a.K + 63) / 64, static_cast<hipStream_t>(stream));
 }
 size_t gemm16_grad_weights_workspace_bytes(int E, int N, int K, int M_total, int kernel) { return 0; }
 int launch_gemm16_grad_weights(const Gemm16Args& a, void* stream) {
-  if (a.kernel == 9 || a.kernel == 0)
-    return a.gather && a.M_total > 0 ? launch256t<kWeights, true, false>(a, stream) : launch256t<kWeights, false, false>(a, stream);
+  if (a.kernel == 9 || a.kernel == 0 || a.kernel == 5) {
+    const int t = a.kernel == 5 ? 128 : 256;
+    return a.gather && a.M_total > 0 ? launch_sized<kWeights, true, false>(a, t, stream) : launch_sized<kWeights, false, false>(a, t, stream);
+  }
   const hipStream_t s = static_cast<hipStream_t>(stream);
   const dim3 grid((a.K + 63) / 64, (a.N + 63) / 64, a.E);
   if (grid.y > 65535) return (int)hipErrorInvalidConfiguration;
