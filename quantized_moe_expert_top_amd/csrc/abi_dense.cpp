@@ -19,16 +19,16 @@ bool dtype16(int d) { return d == MOE_DTYPE_BF16 || d == MOE_DTYPE_F16; }
 bool known_dtype(int d) { return dtype16(d) || d == MOE_DTYPE_F32; }
 bool plain(int epi) { return epi == MOE_EPI_NONE || epi == MOE_EPI_NONE_F16 || epi == MOE_EPI_NONE_F32; }
 
-moe_status check_kernel(int32_t kernel) {
+moe_status check_kernel(int32_t kernel, bool small) {
   if (kernel < MOE_KERNEL_AUTO || kernel > MOE_KERNEL_TILE256)
     return fail(MOE_ERR_BAD_FORMAT, "unknown kernel choice %d", kernel);
-  if (kernel != MOE_KERNEL_AUTO && kernel != MOE_KERNEL_SMALL && kernel != MOE_KERNEL_TILE128 &&
+  if (kernel != MOE_KERNEL_AUTO && !(small && kernel == MOE_KERNEL_SMALL) && kernel != MOE_KERNEL_TILE128 &&
       kernel != MOE_KERNEL_TILE256)
-    return fail(MOE_ERR_UNSUPPORTED, "kernel choice %d does not run 16-bit weights", kernel);
+    return fail(MOE_ERR_UNSUPPORTED, "kernel choice %d does not run this product of 16-bit weights", kernel);
   return MOE_OK;
 }
 
-moe_status check_sizes(int32_t dtype, int32_t E, int32_t N, int32_t K, int32_t M_total, int32_t kernel) {
+moe_status check_sizes(int32_t dtype, int32_t E, int32_t N, int32_t K, int32_t M_total, int32_t kernel, bool small) {
   if (!dtype16(dtype)) return fail(MOE_ERR_BAD_FORMAT, "dtype %d (bf16 or fp16)", dtype);
   if (E < 1 || E > 1024 || N < 1 || K < 1) return fail(MOE_ERR_BAD_SHAPE, "E=%d N=%d K=%d out of range", E, N, K);
   if (N % 8 != 0 || K % 8 != 0) return fail(MOE_ERR_UNSUPPORTED, "N=%d and K=%d must be multiples of 8", N, K);
@@ -36,7 +36,7 @@ moe_status check_sizes(int32_t dtype, int32_t E, int32_t N, int32_t K, int32_t M
   if (M_total < 0) return fail(MOE_ERR_BAD_SHAPE, "M_total=%d < 0", M_total);
   if ((int64_t)N * K * 2 >= kMaxBytes)
     return fail(MOE_ERR_UNSUPPORTED, "an expert's weights of %lld bytes (4 GiB or more)", (long long)N * K * 2);
-  return check_kernel(kernel);
+  return check_kernel(kernel, small);
 }
 
 moe_status check_rows(int32_t K, int32_t A_rows, const int32_t* gather_pair, int32_t k, int32_t M_total) {
@@ -58,7 +58,7 @@ extern "C" {
 moe_status moe_grouped_gemm(const void* w, int32_t dtype, int32_t E, int32_t N, int32_t K, const void* A, int32_t A_rows,
                             const int32_t* gather_pair, int32_t k, const int32_t* seg_offsets, int32_t M_total,
                             int32_t epilogue, int32_t kernel, void* pre, void* out, void* stream) {
-  moe_status st = check_sizes(dtype, E, N, K, M_total, kernel);
+  moe_status st = check_sizes(dtype, E, N, K, M_total, kernel, true);
   if (st != MOE_OK) return st;
   if (!plain(epilogue) && epilogue != MOE_EPI_SWIGLU)
     return fail(MOE_ERR_BAD_FORMAT, "epilogue %d of a 16-bit product", epilogue);
@@ -85,7 +85,7 @@ moe_status moe_grouped_gemm(const void* w, int32_t dtype, int32_t E, int32_t N, 
 moe_status moe_grouped_gemm_grad_rows(const void* w, int32_t dtype, int32_t E, int32_t N, int32_t K, const void* dy,
                                       const int32_t* seg_offsets, int32_t M_total, int32_t epilogue, int32_t kernel,
                                       const void* pre, void* out, void* stream) {
-  moe_status st = check_sizes(dtype, E, N, K, M_total, kernel);
+  moe_status st = check_sizes(dtype, E, N, K, M_total, kernel, true);
   if (st != MOE_OK) return st;
   if (!plain(epilogue) && epilogue != MOE_EPI_SWIGLU_GRAD)
     return fail(MOE_ERR_BAD_FORMAT, "epilogue %d of a gradient by the rows", epilogue);
@@ -105,7 +105,7 @@ moe_status moe_grouped_gemm_grad_rows(const void* w, int32_t dtype, int32_t E, i
 }
 
 size_t moe_grouped_gemm_grad_weights_workspace_size(int32_t E, int32_t N, int32_t K, int32_t M_total, int32_t kernel) {
-  if (check_sizes(MOE_DTYPE_BF16, E, N, K, M_total, kernel) != MOE_OK) return 0;
+  if (check_sizes(MOE_DTYPE_BF16, E, N, K, M_total, kernel, false) != MOE_OK) return 0;
   ok();
   return moe::gemm16_grad_weights_workspace_bytes(E, N, K, M_total, kernel);
 }
@@ -114,7 +114,7 @@ moe_status moe_grouped_gemm_grad_weights(const void* dy, const void* A, int32_t 
                                          int32_t A_rows, const int32_t* gather_pair, int32_t k,
                                          const int32_t* seg_offsets, int32_t M_total, int32_t epilogue, int32_t kernel,
                                          void* out, void* workspace, size_t workspace_bytes, void* stream) {
-  moe_status st = check_sizes(dtype, E, N, K, M_total, kernel);
+  moe_status st = check_sizes(dtype, E, N, K, M_total, kernel, false);
   if (st != MOE_OK) return st;
   if (!plain(epilogue)) return fail(MOE_ERR_BAD_FORMAT, "epilogue %d of a gradient by the weights", epilogue);
   st = check_rows(K, A_rows, gather_pair, k, M_total);

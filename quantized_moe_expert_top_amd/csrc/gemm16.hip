@@ -23,105 +23,8 @@ struct GemmK {  // kernel arguments
   const uint16_t* pre_in;
   uint16_t* pre_out;
   void* out;
+  int splits;  // weights: parts of a segment's rows, each with fp32 sums of its own (out: [splits][E][N][K])
 };
-
-__device__ __forceinline__ int source_row(const GemmK& p, int row) {
-  const int r = p.gather ? p.div(p.gather[row]) : row;
-  return min(max(r, 0), p.A_rows - 1);
-}
-__device__ __forceinline__ void store_one(void* out, size_t at, int epi, float v) {
-  if (epi == kEpiF32) static_cast<float*>(out)[at] = v;
-  else static_cast<uint16_t*>(out)[at] = epi == kEpiF16 ? f32_to_f16(v) : f32_to_bf16(v);
-}
-
-// 64 x 64 tiles, operands element by element through LDS.
-template <bool F16, int MODE>
-__global__ __launch_bounds__(256) void gemm16_kernel(GemmK p, int epi, int n_ab) {
-  __shared__ __attribute__((aligned(16))) uint16_t P[64][40], Q[64][40];
-  __shared__ float C[64][65];
-  const int lane = threadIdx.x & 63, wv = threadIdx.x >> 6, wa = wv & 1, wb = wv >> 1;
-  const bool sw = epi == kEpiSwiglu;
-  int e, ab, b0, s0 = 0, s1 = 0, red;
-  if constexpr (MODE == kWeights) {
-    e = blockIdx.z;
-    ab = blockIdx.x;
-    b0 = blockIdx.y * 64;
-    if (p.M_total > 0) segment_rows(p.seg, e, p.M_total, s0, s1);
-    red = s1 - s0;
-  } else {
-    int idx = blockIdx.x;
-    RowTile t;
-    if (!find_tile<64>(p.seg, p.E, p.M_total, n_ab, idx, t)) return;
-    e = t.e;
-    ab = idx % n_ab;
-    b0 = t.r0 + idx / n_ab * 64;
-    s1 = t.s1;
-    red = MODE == kForward ? p.K : p.N;
-  }
-  const int I = p.N / 2;
-  const uint16_t* const w = MODE == kWeights ? nullptr : p.w + (size_t)e * p.N * p.K;
-  f32x16 acc = {};
-  for (int k0 = 0; k0 < red; k0 += 32) {
-    for (int i = threadIdx.x; i < 64 * 32; i += 256) {
-      uint16_t pv = 0, qv = 0;
-      const int r = i >> 5, kk = k0 + (i & 31);
-      if constexpr (MODE == kForward) {
-        const int ch = sw ? (r < 32 ? 32 * ab + r : 32 * ab + r - 32) : 64 * ab + r;
-        if (kk < red && ch < (sw ? I : p.N)) pv = w[(size_t)(sw && r >= 32 ? I + ch : ch) * p.K + kk];
-        if (kk < red && b0 + r < s1) qv = p.a[(size_t)source_row(p, b0 + r) * p.K + kk];
-      } else if constexpr (MODE == kRows) {
-        if (kk < red && 64 * ab + r < p.K) pv = w[(size_t)kk * p.K + 64 * ab + r];
-        if (kk < red && b0 + r < s1) qv = p.dy[(size_t)(b0 + r) * p.N + kk];
-      } else if (kk < red) {
-        if (64 * ab + r < p.K) pv = p.a[(size_t)source_row(p, s0 + kk) * p.K + 64 * ab + r];
-        if (b0 + r < p.N) qv = p.dy[(size_t)(s0 + kk) * p.N + b0 + r];
-      }
-      P[r][i & 31] = pv;
-      Q[r][i & 31] = qv;
-    }
-    __syncthreads();
-#pragma unroll
-    for (int s = 0; s < 2; ++s) {
-      const int c = 16 * s + 8 * (lane >> 5);
-      acc = mfma32t<F16>(*reinterpret_cast<const u32x4*>(&P[32 * wa + (lane & 31)][c]),
-                         *reinterpret_cast<const u32x4*>(&Q[32 * wb + (lane & 31)][c]), acc);
-    }
-    __syncthreads();
-  }
-#pragma unroll
-  for (int r = 0; r < 16; ++r) C[32 * wb + (lane & 31)][32 * wa + acc_row(r, lane)] = acc[r];
-  __syncthreads();
-  for (int i = threadIdx.x; i < 64 * 64; i += 256) {
-    const int b = b0 + (i >> 6), a = i & 63;
-    const float v = C[i >> 6][a];
-    if constexpr (MODE == kForward) {
-      if (b >= s1) continue;
-      if (sw) {
-        const int ch = 32 * ab + (a & 31);
-        if (ch >= I) continue;
-        if (p.pre_out) p.pre_out[(size_t)b * p.N + (a < 32 ? ch : I + ch)] = round16<F16>(v);
-        if (a < 32)
-          static_cast<uint16_t*>(p.out)[(size_t)b * I + ch] = round16<F16>(v / (1.0f + __expf(-v)) * C[i >> 6][32 + a]);
-      } else if (64 * ab + a < p.N) {
-        store_one(p.out, (size_t)b * p.N + 64 * ab + a, epi, v);
-      }
-    } else if constexpr (MODE == kRows) {
-      const int ch = 64 * ab + a;
-      if (b >= s1 || ch >= p.K) continue;
-      if (epi == kEpiSwigluGrad) {
-        const size_t at = (size_t)b * 2 * p.K + ch;
-        const float g = widen16<F16>(p.pre_in[at]), u = widen16<F16>(p.pre_in[at + p.K]);
-        const float s = 1.0f / (1.0f + __expf(-g));
-        static_cast<uint16_t*>(p.out)[at] = round16<F16>(v * u * s * (1.0f + g * (1.0f - s)));
-        static_cast<uint16_t*>(p.out)[at + p.K] = round16<F16>(v * g * s);
-      } else {
-        store_one(p.out, (size_t)b * p.K + ch, epi, v);
-      }
-    } else if (b < p.N && 64 * ab + a < p.K) {
-      store_one(p.out, ((size_t)e * p.N + b) * p.K + 64 * ab + a, epi, v);
-    }
-  }
-}
 
 // ------------------------------------------------------------ tiles of 256 x 256
 // out[b][a] = sum_k P[a][k] Q[b][k]: a runs along the output's rows (contiguous),
@@ -145,8 +48,26 @@ __device__ __forceinline__ int swz(int row) { return (row & 7) ^ ((row >> 3) & 1
 // four rows of a transposing read's 16 lanes and the eight of 32 lanes fall on different banks.
 __device__ __forceinline__ int tswz(int k) { return (k & 3) | ((k >> 1) & 4); }
 
+// The same for [32][64] of 16 bits, four units a row.
+__device__ __forceinline__ int tswz4(int k) { return ((k >> 1) & 1) | ((k >> 2) & 2); }
+
+// Fast exponential and reciprocal, as in the library's other SwiGLU epilogues (2^-19
+// relative down to gates of -16, 0 below -88).
+__device__ __forceinline__ float silu(float g) { return g * __builtin_amdgcn_rcpf(1.0f + __expf(-g)); }
+// Gradient of silu(g) * u from d, by g and u (16-bit numbers).
+template <bool F16>
+__device__ __forceinline__ float2 swiglu_grad(float d, uint16_t g16, uint16_t u16) {
+  const float g = widen16<F16>(g16), u = widen16<F16>(u16), s = __builtin_amdgcn_rcpf(1.0f + __expf(-g));
+  return {d * u * s * (1.0f + g * (1.0f - s)), d * g * s};
+}
+template <typename F, int... X>
+__device__ __forceinline__ void for_each(F&& f, std::integer_sequence<int, X...>) {
+  (f(std::integral_constant<int, X>{}), ...);
+}
+
 struct Tile {
   int e, ab, b0, s0, s1;  // expert, a block, first b; the segment's rows (weights: the sum's)
+  int part;               // weights: which of the splits
 };
 
 // Tiles in an order that neighbours share operands in an XCD's L2: within a
@@ -174,7 +95,7 @@ __device__ __forceinline__ void tile_loop(const GemmK& p, int epi, int n_ab, int
   // contiguous range.  The first 64 segments stay in registers, one per lane.
   int seg_n = 0, seg_end = 0, seg0 = 0, seg1 = 0, total;
   if constexpr (MODE == kWeights) {
-    total = p.E * n_ab * n_bb;
+    total = p.E * p.splits * n_ab * n_bb;
   } else {
     seg_n = segment_tiles<T>(p.seg, p.E, p.M_total, lane, seg0, seg1);
     seg_end = lane_scan(seg_n);
@@ -188,11 +109,19 @@ __device__ __forceinline__ void tile_loop(const GemmK& p, int epi, int n_ab, int
     Tile c;
     int tile;
     if constexpr (MODE == kWeights) {
-      c.e = at / (n_ab * n_bb);
-      grouped_order(at - c.e * (n_ab * n_bb), n_bb, n_ab, tile, c.ab);
+      const int ep = at / (n_ab * n_bb);
+      grouped_order(at - ep * (n_ab * n_bb), n_bb, n_ab, tile, c.ab);
+      c.e = ep / p.splits;
+      c.part = ep - c.e * p.splits;
       c.b0 = T * tile;
       c.s0 = c.s1 = 0;
       if (p.M_total > 0) segment_rows(p.seg, c.e, p.M_total, c.s0, c.s1);
+      if (p.splits > 1) {  // whole steps of 64 rows
+        const int64_t steps = (c.s1 - c.s0 + 63) >> 6;
+        const int from = (int)(steps * c.part / p.splits) * 64, to = (int)(steps * (c.part + 1) / p.splits) * 64;
+        c.s1 = min(c.s1, c.s0 + to);
+        c.s0 = min(c.s1, c.s0 + from);
+      }
     } else {
       RowTile t;
       if (p.E <= 64) {
@@ -313,7 +242,7 @@ __device__ __forceinline__ void tile_loop(const GemmK& p, int epi, int n_ab, int
       uint32_t from = token(src) * (uint32_t)(2 * p.K);
       asm volatile("" : "+v"(from));  // (a select, not a branch around the loads)
       if (4 * RK * wv + (l & (4 * RK - 1)) >= left) from = kLastGather;
-      src = pair_of(Tile{0, 0, 0, ls0, ls1}, st + 1);
+      src = pair_of(Tile{0, 0, 0, ls0, ls1, 0}, st + 1);
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         uint32_t at;
@@ -415,7 +344,7 @@ __device__ __forceinline__ void tile_loop(const GemmK& p, int epi, int n_ab, int
         }
         if constexpr (X & 1) __builtin_amdgcn_sched_barrier(0);
       };
-      [&]<int... X>(std::integer_sequence<int, X...>) { (slot(std::integral_constant<int, X>{}), ...); }(std::make_integer_sequence<int, 2 * J>{});
+      for_each(slot, std::make_integer_sequence<int, 2 * J>{});
     };
     const int next_pair = pair_of(nxt, 0);
     // an even number of steps, 2 at least: past the sum's end they multiply zeros
@@ -453,7 +382,7 @@ __device__ __forceinline__ void tile_loop(const GemmK& p, int epi, int n_ab, int
     const int lane = lane_here(), quad = lane >> 4, col = lane & 15;
     const int a0 = GLU && MODE == kForward ? T / 2 * cur.ab + 32 * wa : T * cur.ab + 64 * wa;
     const int rows = min((MODE == kWeights ? p.N : cur.s1) - cur.b0, T);
-    const size_t row0 = (MODE == kWeights ? (size_t)cur.e * p.N : 0) + cur.b0;
+    const size_t row0 = (MODE == kWeights ? ((size_t)cur.part * p.E + cur.e) * p.N : 0) + cur.b0;
     auto chunk = [&](int r, int ck) { return eb + r * 128 + ((ck ^ swz(r)) << 4); };  // 8 chunks of 16 bytes a row
     auto put16 = [&](int t, int x, const f32x4& v, bool f16) {
       *reinterpret_cast<u32x2*>(chunk(16 * x + col, 2 * t + (quad >> 1)) + 8 * (quad & 1)) =
@@ -499,7 +428,7 @@ __device__ __forceinline__ void tile_loop(const GemmK& p, int epi, int n_ab, int
             const f32x4 &g = acc[t][2 * j + x], &u = acc[t + 2][2 * j + x];
             f32x4 h;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) h[i] = g[i] * __builtin_amdgcn_rcpf(1.0f + __expf(-g[i])) * u[i];
+            for (int i = 0; i < 4; ++i) h[i] = silu(g[i]) * u[i];
             put16(t, x, h, F16);
           }
 #pragma unroll
@@ -552,11 +481,9 @@ __device__ __forceinline__ void tile_loop(const GemmK& p, int epi, int n_ab, int
                 float og[2], ou[2];
 #pragma unroll
                 for (int z = 0; z < 2; ++z) {
-                  const float g = widen16<F16>((uint16_t)(z ? gw >> 16 : gw & 0xFFFFu));
-                  const float u = widen16<F16>((uint16_t)(z ? uw >> 16 : uw & 0xFFFFu));
-                  const float s = __builtin_amdgcn_rcpf(1.0f + __expf(-g));
-                  og[z] = d[2 * w + z] * u * s * (1.0f + g * (1.0f - s));
-                  ou[z] = d[2 * w + z] * g * s;
+                  const float2 o = swiglu_grad<F16>(d[2 * w + z], (uint16_t)(z ? gw >> 16 : gw & 0xFFFFu), (uint16_t)(z ? uw >> 16 : uw & 0xFFFFu));
+                  og[z] = o.x;
+                  ou[z] = o.y;
                 }
                 dg[2 * q + w] = pack16x2<F16>(og[0], og[1]);
                 du[2 * q + w] = pack16x2<F16>(ou[0], ou[1]);
@@ -632,71 +559,271 @@ __global__ __launch_bounds__(2 * T, 2) void tile_kernel(GemmK p, int epi, int n_
 #endif
 }
 
+// -------------------------------------------------------- few rows per expert
+// A workgroup takes up to 32 rows of one expert and 32 channels (SwiGLU: 16 gate and
+// their 16 up channels; gradient by the rows: 64 inputs).  Its four wavefronts take
+// every fourth step of the sum and add their sums through LDS; each keeps four
+// stages of weights of its own (4 KB: 32 channels x 64 inputs, or 32 channels x 64
+// inputs transposed), filled by LDS-DMA three steps ahead, and the rows' part in
+// registers: no barrier before the end.
+template <bool F16, int MODE, bool GATHER, bool GLU>
+__device__ __forceinline__ void small_body(const GemmK& p, int epi, int n_cb, char* r0, char* r1, char* r2, char* r3) {
+  constexpr int AT = MODE == kForward ? 2 : 4;       // a tiles of 16
+  constexpr int ST = MODE == kForward ? 64 : 32;     // k of a step
+  constexpr int SUB = ST / 32, NS = 4, OPS = 4 + 2 * SUB;
+  const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+  const int col = lane & 15, quad = lane >> 4, I = p.N / 2;
+  int idx = blockIdx.x;
+  RowTile t;
+  if (!find_tile<32>(p.seg, p.E, p.M_total, n_cb, idx, t)) return;
+  const int cb = idx % n_cb, b0 = t.r0 + idx / n_cb * 32, s1 = t.s1;
+  const int red = MODE == kForward ? p.K : p.N, na = MODE == kForward ? p.N : p.K;
+  const uint16_t* const w = p.w + (size_t)t.e * p.N * p.K;
+
+  // this lane's part of a step's four DMAs, and its rows
+  uint32_t po[4];
+  int ck[2] = {0, 0};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = 8 * i + (lane >> 3);
+    if constexpr (MODE == kForward) {
+      const int c = (lane & 7) ^ swz(r);
+      if (i < 2) ck[i] = 8 * c;
+      const int ch = GLU ? (i < 2 ? 16 * cb + r : I + 16 * cb + r - 16) : 32 * cb + r;
+      po[i] = ((uint32_t)ch * (uint32_t)p.K + 8 * c) * 2;  // past the last channel: past the weights
+    } else {
+      const int ch = 64 * cb + 8 * (((((lane >> 1) & 3) ^ tswz4(r)) << 1) + (lane & 1));
+      po[i] = ch < p.K ? ((uint32_t)r * (uint32_t)p.K + ch) * 2 : kOut;
+    }
+  }
+  uint32_t qo[2];
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    const int r = 16 * x + col;
+    uint32_t from = r;
+    if constexpr (GATHER) from = (uint32_t)min(max(p.div(p.gather[min(b0 + r, s1 - 1)]), 0), p.A_rows - 1);
+    qo[x] = b0 + r < s1 ? (from * (uint32_t)red + 8 * quad) * 2 : kOut;
+  }
+  const uint16_t* const rows = MODE == kForward ? p.a : p.dy;
+  const rsrc_t qr = scalar_rsrc(GATHER ? rows : rows + (size_t)b0 * red,
+                                GATHER ? (uint32_t)((size_t)p.A_rows * red * 2) : (uint32_t)((size_t)min(s1 - b0, 32) * red * 2));
+  char* const ring[NS] = {r0 + wv * 4096, r1 + wv * 4096, r2 + wv * 4096, r3 + wv * 4096};
+  u32x4 q[NS][2][SUB];
+  auto load = [&](auto slot_tag, int step) {
+    constexpr int S = decltype(slot_tag)::value;
+    const int k0 = ST * (4 * step + wv), left = red - k0;
+    const uint32_t adv = left > 0 ? 2u * (uint32_t)k0 : 0u;
+    if constexpr (MODE == kForward) {
+      const rsrc_t pr = scalar_rsrc(w, (uint32_t)((size_t)p.N * p.K * 2));
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(pr, (__attribute__((address_space(3))) void*)(ring[S] + 1024 * i), 16,
+                                                 ck[i & 1] < left ? po[i] : kOut, adv, 0, 0);
+    } else {
+      const rsrc_t pr = scalar_rsrc(w + (size_t)(left > 0 ? k0 : 0) * p.K, (uint32_t)max(min(left, 32), 0) * (2u * (uint32_t)p.K));
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(pr, (__attribute__((address_space(3))) void*)(ring[S] + 1024 * i), 16, po[i], 0, 0, 0);
+    }
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+#pragma unroll
+      for (int u = 0; u < SUB; ++u) q[S][x][u] = buf_x4(qr, 32 * u + 8 * quad < left ? qo[x] + 64 * u : kOut, adv);
+  };
+  f32x4 acc[AT][2] = {};
+  auto multiply = [&](auto slot_tag) {
+    constexpr int S = decltype(slot_tag)::value;
+#pragma unroll
+    for (int u = 0; u < SUB; ++u) {
+      u32x4 a[AT];
+#pragma unroll
+      for (int i = 0; i < AT; ++i) {
+        if constexpr (MODE == kForward) {
+          a[i] = *reinterpret_cast<const u32x4*>(ring[S] + (16 * i + col) * 128 + (((4 * u + quad) ^ swz(col)) << 4));
+        } else {
+          const int k = 8 * quad + ((lane >> 2) & 3);
+          const char* at = ring[S] + k * 128 + ((i ^ tswz4(k)) << 5) + ((lane & 3) << 3);
+          const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(at));
+          // (rows k + 4 .. k + 7: bit 1 of the place flips with neither)
+          const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) s16x4*)(at + 512));
+          const u32x2 l = __builtin_bit_cast(u32x2, lo), h = __builtin_bit_cast(u32x2, hi);
+          a[i] = u32x4{l[0], l[1], h[0], h[1]};
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < AT; ++i)
+#pragma unroll
+        for (int x = 0; x < 2; ++x) acc[i][x] = mfma16t<F16>(a[i], q[S][x][u], acc[i][x]);
+    }
+  };
+  // Steps of a wavefront, a multiple of four: past the sum's end zeros.
+  const int n = ((red + 4 * ST - 1) / (4 * ST) + NS - 1) / NS * NS;
+  load(std::integral_constant<int, 0>{}, 0);
+  load(std::integral_constant<int, 1>{}, 1);
+  load(std::integral_constant<int, 2>{}, 2);
+  auto turn = [&](auto slot_tag, int step) {
+    constexpr int S = decltype(slot_tag)::value;
+    __builtin_amdgcn_sched_barrier(0);
+    load(std::integral_constant<int, (S + 3) % NS>{}, step + 3);
+    __builtin_amdgcn_sched_barrier(0);
+    // three newer steps may be on their way (vmcnt, whose upper two bits lie apart)
+    __builtin_amdgcn_s_waitcnt(0x0F70 | (3 * OPS & 15) | (3 * OPS >> 4) << 14);
+    __builtin_amdgcn_sched_barrier(0);
+    multiply(slot_tag);
+  };
+  for (int step = 0; step < n; step += NS) {
+    turn(std::integral_constant<int, 0>{}, step);
+    turn(std::integral_constant<int, 1>{}, step + 1);
+    turn(std::integral_constant<int, 2>{}, step + 2);
+    turn(std::integral_constant<int, 3>{}, step + 3);
+  }
+  __builtin_amdgcn_sched_barrier(0);
+  __builtin_amdgcn_s_waitcnt(0x0070);  // the last loads too: the stages hold the sums next
+  // a tile's sums of wavefront w at 4 KB of stage i / 2
+  auto sums = [&](int i, int x, int w) { return reinterpret_cast<f32x4*>((i < 2 ? r0 : r1) + w * 4096) + (2 * (i & 1) + x) * 64; };
+#pragma unroll
+  for (int i = 0; i < AT; ++i)
+#pragma unroll
+    for (int x = 0; x < 2; ++x) sums(i, x, wv)[lane] = acc[i][x];
+  __syncthreads();
+  auto total = [&](int i, int x, int l) {
+    f32x4 v = sums(i, x, 0)[l];
+#pragma unroll
+    for (int w = 1; w < 4; ++w) v += sums(i, x, w)[l];
+    return v;
+  };
+  auto narrow = [&](const f32x4& v, bool f16) {
+    return f16 ? u32x2{pack16x2<true>(v[0], v[1]), pack16x2<true>(v[2], v[3])} : u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+  };
+  // Four channels of a row per thread, neighbouring threads the row's next ones.
+  constexpr int TILES = GLU && MODE == kForward ? 1 : AT;
+  for (int o = threadIdx.x; o < TILES * 128; o += 256) {
+    const int i = o / 4 % TILES, r = o / (4 * TILES), qd = o & 3;
+    const int row = b0 + r, x = r >> 4, l = 16 * qd + (r & 15);
+    if (row >= s1) continue;
+    if constexpr (GLU && MODE == kForward) {
+      const int ch = 16 * cb + 4 * qd;
+      if (ch >= I) continue;
+      const f32x4 g = total(0, x, l), u = total(1, x, l);
+      if (p.pre_out) {
+        uint16_t* const pre = p.pre_out + (size_t)row * p.N + ch;
+        *reinterpret_cast<u32x2*>(pre) = narrow(g, F16);
+        *reinterpret_cast<u32x2*>(pre + I) = narrow(u, F16);
+      }
+      f32x4 h;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) h[j] = silu(g[j]) * u[j];
+      *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(p.out) + (size_t)row * I + ch) = narrow(h, F16);
+    } else {
+      const int ch = 16 * AT * cb + 16 * i + 4 * qd;
+      if (ch >= na) continue;
+      const f32x4 v = total(i, x, l);
+      if constexpr (GLU) {
+        const size_t at = (size_t)row * 2 * p.K + ch;
+        const u32x2 gv = *reinterpret_cast<const u32x2*>(p.pre_in + at), uv = *reinterpret_cast<const u32x2*>(p.pre_in + at + p.K);
+        f32x4 dg, du;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t gw = gv[j >> 1], uw = uv[j >> 1];
+          const float2 d = swiglu_grad<F16>(v[j], (uint16_t)(j & 1 ? gw >> 16 : gw & 0xFFFFu), (uint16_t)(j & 1 ? uw >> 16 : uw & 0xFFFFu));
+          dg[j] = d.x;
+          du[j] = d.y;
+        }
+        uint16_t* const d = static_cast<uint16_t*>(p.out) + at;
+        *reinterpret_cast<u32x2*>(d) = narrow(dg, F16);
+        *reinterpret_cast<u32x2*>(d + p.K) = narrow(du, F16);
+      } else if (epi == kEpiF32) {
+        *reinterpret_cast<f32x4*>(static_cast<float*>(p.out) + (size_t)row * na + ch) = v;
+      } else {
+        *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(p.out) + (size_t)row * na + ch) = narrow(v, epi == kEpiF16);
+      }
+    }
+  }
+}
+template <bool F16, int MODE, bool GATHER, bool GLU>
+__global__ __launch_bounds__(256, 2) void small_kernel(GemmK p, int epi, int n_cb) {
+#ifdef __HIP_DEVICE_COMPILE__
+  __shared__ __attribute__((aligned(1024))) char r0[16384], r1[16384], r2[16384], r3[16384];
+  small_body<F16, MODE, GATHER, GLU>(p, epi, n_cb, r0, r1, r2, r3);
+#endif
+}
+
+// The weights' gradient from the splits' sums, added in order.
+__global__ __launch_bounds__(256) void splits_kernel(const f32x4* __restrict__ sums, int splits, size_t n4, int epi, void* __restrict__ out) {
+  for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < n4; i += (size_t)gridDim.x * 256) {
+    f32x4 v = sums[i];
+    for (int k = 1; k < splits; ++k) v += sums[i + (size_t)k * n4];
+    if (epi == kEpiF32) static_cast<f32x4*>(out)[i] = v;
+    else
+      static_cast<u32x2*>(out)[i] = epi == kEpiF16 ? u32x2{pack16x2<true>(v[0], v[1]), pack16x2<true>(v[2], v[3])}
+                                                   : u32x2{pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3])};
+  }
+}
+
 GemmK kernel_args(const Gemm16Args& a) {
   return GemmK{static_cast<const uint16_t*>(a.w), static_cast<const uint16_t*>(a.a), static_cast<const uint16_t*>(a.dy),
                a.E, a.N, a.K, a.A_rows, a.M_total, a.gather, pair_div(a.gather ? a.k : 1), a.seg,
-               static_cast<const uint16_t*>(a.pre_in), static_cast<uint16_t*>(a.pre_out), a.out};
+               static_cast<const uint16_t*>(a.pre_in), static_cast<uint16_t*>(a.pre_out), a.out, 1};
 }
 // Upper bound of the tiles of `rows` rows: one partial tile per segment that has rows.
 int64_t row_tiles(int M_total, int E, int rows) { return (int64_t)M_total / rows + (E < M_total ? E : M_total); }
 
-template <int MODE>
-int launch_rowwise(const Gemm16Args& a, int n_ab, hipStream_t s) {
-  const int64_t wgs = row_tiles(a.M_total, a.E, 64) * n_ab;
-  if (wgs >= ((int64_t)1 << 23)) return (int)hipErrorInvalidConfiguration;
-  if (a.dtype == 2) hipLaunchKernelGGL((gemm16_kernel<true, MODE>), dim3((unsigned)wgs), dim3(256), 0, s, kernel_args(a), a.epilogue, n_ab);
-  else hipLaunchKernelGGL((gemm16_kernel<false, MODE>), dim3((unsigned)wgs), dim3(256), 0, s, kernel_args(a), a.epilogue, n_ab);
-  return (int)hipGetLastError();
-}
-
 template <int T, bool F16, int MODE, bool GATHER, bool GLU>
 int launch_tile(const Gemm16Args& a, hipStream_t s) {
   const int na = MODE == kForward ? a.N : a.K, n_ab = (na + T - 1) / T, n_bb = (a.N + T - 1) / T;
-  const int64_t tiles = (MODE == kWeights ? (int64_t)a.E * n_bb : row_tiles(a.M_total, a.E, T)) * n_ab;
+  GemmK k = kernel_args(a);
+  int epi = a.epilogue;
+  if (MODE == kWeights && T == 128) {
+    k.splits = gemm16_splits(a.E, a.N, a.K, a.M_total, a.kernel);
+    if (k.splits > 1) {
+      k.out = a.ws;
+      epi = kEpiF32;
+    }
+  }
+  const int64_t tiles = (MODE == kWeights ? (int64_t)a.E * k.splits * n_bb : row_tiles(a.M_total, a.E, T)) * n_ab;
   if (tiles >= ((int64_t)1 << 30)) return (int)hipErrorInvalidConfiguration;
   const int64_t most = T == 256 ? kCUs : 2 * kCUs;  // workgroups that fit the chip at once
   const int64_t wgs = tiles < most ? (tiles + 7) / 8 * 8 : most;
-  hipLaunchKernelGGL((tile_kernel<T, F16, MODE, GATHER, GLU>), dim3((unsigned)wgs), dim3(2 * T), 0, s, kernel_args(a), a.epilogue, n_ab, n_bb);
+  hipLaunchKernelGGL((tile_kernel<T, F16, MODE, GATHER, GLU>), dim3((unsigned)wgs), dim3(2 * T), 0, s, k, epi, n_ab, n_bb);
+  const int e = (int)hipGetLastError();
+  if (k.splits == 1 || e != 0) return e;
+  const size_t n4 = (size_t)a.E * a.N * a.K / 4, blocks = (n4 + 255) / 256;
+  hipLaunchKernelGGL(splits_kernel, dim3((unsigned)(blocks < 2048 ? blocks : 2048)), dim3(256), 0, s, static_cast<const f32x4*>(a.ws),
+                     k.splits, n4, a.epilogue, a.out);
   return (int)hipGetLastError();
 }
 template <int T, int MODE, bool GATHER, bool GLU>
 int launch_typed(const Gemm16Args& a, hipStream_t s) {
   return a.dtype == 2 ? launch_tile<T, true, MODE, GATHER, GLU>(a, s) : launch_tile<T, false, MODE, GATHER, GLU>(a, s);
 }
+template <bool F16, int MODE, bool GATHER, bool GLU>
+int launch_small(const Gemm16Args& a, hipStream_t s) {
+  const int n_cb = MODE == kRows ? (a.K + 63) / 64 : (a.N + 31) / 32;
+  const int64_t wgs = row_tiles(a.M_total, a.E, 32) * n_cb;
+  if (wgs >= ((int64_t)1 << 24)) return (int)hipErrorInvalidConfiguration;  // 2^32 threads
+  hipLaunchKernelGGL((small_kernel<F16, MODE, GATHER, GLU>), dim3((unsigned)wgs), dim3(256), 0, s, kernel_args(a), a.epilogue, n_cb);
+  return (int)hipGetLastError();
+}
 template <int MODE, bool GATHER, bool GLU>
-int launch_sized(const Gemm16Args& a, int t, void* s) {
-  return t == 256 ? launch_typed<256, MODE, GATHER, GLU>(a, static_cast<hipStream_t>(s)) : launch_typed<128, MODE, GATHER, GLU>(a, static_cast<hipStream_t>(s));
+int launch(const Gemm16Args& a, void* stream) {
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  const int path = gemm16_path(MODE, a.E, a.N, a.K, a.M_total, a.kernel);
+  if (path == 256) return launch_typed<256, MODE, GATHER, GLU>(a, s);
+  if (path == 128) return launch_typed<128, MODE, GATHER, GLU>(a, s);
+  if constexpr (MODE == kWeights) return (int)hipErrorInvalidValue;
+  else return a.dtype == 2 ? launch_small<true, MODE, GATHER, GLU>(a, s) : launch_small<false, MODE, GATHER, GLU>(a, s);
 }
 }  // namespace
 
 int launch_gemm16(const Gemm16Args& a, void* stream) {
-  if (a.kernel == 9 || a.kernel == 0 || a.kernel == 5) {
-    const int t = a.kernel == 5 ? 128 : 256;
-    if (a.gather) return a.epilogue == kEpiSwiglu ? launch_sized<kForward, true, true>(a, t, stream) : launch_sized<kForward, true, false>(a, t, stream);
-    return a.epilogue == kEpiSwiglu ? launch_sized<kForward, false, true>(a, t, stream) : launch_sized<kForward, false, false>(a, t, stream);
-  }
-  const int n_ab = a.epilogue == kEpiSwiglu ? (a.N / 2 + 31) / 32 : (a.N + 63) / 64;
-  return launch_rowwise<kForward>(a, n_ab, static_cast<hipStream_t>(stream));
+  if (a.gather) return a.epilogue == kEpiSwiglu ? launch<kForward, true, true>(a, stream) : launch<kForward, true, false>(a, stream);
+  return a.epilogue == kEpiSwiglu ? launch<kForward, false, true>(a, stream) : launch<kForward, false, false>(a, stream);
 }
 int launch_gemm16_grad_rows(const Gemm16Args& a, void* stream) {
-  if (a.kernel == 9 || a.kernel == 0 || a.kernel == 5) {
-    const int t = a.kernel == 5 ? 128 : 256;
-    return a.epilogue == kEpiSwigluGrad ? launch_sized<kRows, false, true>(a, t, stream) : launch_sized<kRows, false, false>(a, t, stream);
-  }
-  return launch_rowwise<kRows>(a, (a.K + 63) / 64, static_cast<hipStream_t>(stream));
+  return a.epilogue == kEpiSwigluGrad ? launch<kRows, false, true>(a, stream) : launch<kRows, false, false>(a, stream);
 }
-size_t gemm16_grad_weights_workspace_bytes(int E, int N, int K, int M_total, int kernel) { return 0; }
 int launch_gemm16_grad_weights(const Gemm16Args& a, void* stream) {
-  if (a.kernel == 9 || a.kernel == 0 || a.kernel == 5) {
-    const int t = a.kernel == 5 ? 128 : 256;
-    return a.gather && a.M_total > 0 ? launch_sized<kWeights, true, false>(a, t, stream) : launch_sized<kWeights, false, false>(a, t, stream);
-  }
-  const hipStream_t s = static_cast<hipStream_t>(stream);
-  const dim3 grid((a.K + 63) / 64, (a.N + 63) / 64, a.E);
-  if (grid.y > 65535) return (int)hipErrorInvalidConfiguration;
-  if (a.dtype == 2) hipLaunchKernelGGL((gemm16_kernel<true, kWeights>), grid, dim3(256), 0, s, kernel_args(a), a.epilogue, 0);
-  else hipLaunchKernelGGL((gemm16_kernel<false, kWeights>), grid, dim3(256), 0, s, kernel_args(a), a.epilogue, 0);
-  return (int)hipGetLastError();
+  return a.gather && a.M_total > 0 ? launch<kWeights, true, false>(a, stream) : launch<kWeights, false, false>(a, stream);
 }
 
 }  // namespace moe

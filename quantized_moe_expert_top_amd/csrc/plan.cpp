@@ -201,4 +201,46 @@ int mxgemm_path(int M_total, int E, int N, int K, bool e2m1, int kernel) {
   return best;
 }
 
+// 16-bit products: tiles of 128 or 256 by the rounds that their tiles take on the
+// chip (512 or 256 at a time; a round's length fitted to one expert of 4096 x 4096,
+// 4096 rows: 101 us in one round of 256, 116 in two of 128).  Forward, us for 128 / 256:
+// 8 experts of 4096 x 4096, 256 rows each 90 / 111; 64 of 2048 x 2048, 128 rows each
+// 135 / 141, 256 rows 180 / 153, 1024 rows 594 / 471.
+// Few rows per expert: the kernel that splits a sum over wavefronts while tiles of 128
+// leave it workgroups to add.  Us for it / tiles of 128, weights from memory: forward, 8 experts
+// with a row of 2048 x 2048 17 / 22, 64 with 16 rows 111 / 123, 48 rows 181 / 127, 8 of 28672 x 4096
+// with 4 rows 392 / 324; by the rows 13 / 22, 118 / 93, 181 / 98, 349 / 402.
+int gemm16_path(int what, int E, int N, int K, int M_total, int kernel) {
+  if (kernel == 1 && what != 2) return 0;
+  if (kernel == 5) return 128;
+  if (kernel == 9) return 256;
+  const double active = M_total < E ? M_total : E;
+  double rounds[2];
+  for (int i = 0; i < 2; ++i) {
+    const int t = i ? 256 : 128;
+    const double na = ((what == 0 ? N : K) + t - 1) / t;
+    if (i == 0 && what != 2 && M_total <= 32.0 * active && na * active <= (what == 0 ? 1024 : 256)) return 0;
+    // a segment's last tile is partly empty and takes less
+    const double nb = what == 2 ? (double)E * ((N + t - 1) / t) : (double)M_total / t + 0.2 * active;
+    rounds[i] = na * nb / (i ? 256 : 512);
+    if (rounds[i] < 1.0) rounds[i] = 1.0;
+  }
+  return 1.58 * rounds[1] < 0.9 * rounds[0] ? 256 : 128;
+}
+
+// Few weights and many rows: enough parts to fill the chip with tiles of 128, each of 8
+// steps of 64 rows or more.
+int gemm16_splits(int E, int N, int K, int M_total, int kernel) {
+  if (M_total <= 0 || gemm16_path(2, E, N, K, M_total, kernel) != 128) return 1;
+  const int64_t tiles = (int64_t)E * ((N + 127) / 128) * ((K + 127) / 128);
+  int64_t parts = 512 / tiles;
+  const int64_t most = (int64_t)M_total / E / (8 * 64);
+  if (parts > most) parts = most;
+  return parts > 1 ? (int)parts : 1;
+}
+size_t gemm16_grad_weights_workspace_bytes(int E, int N, int K, int M_total, int kernel) {
+  const int parts = gemm16_splits(E, N, K, M_total, kernel);
+  return parts > 1 ? (size_t)parts * E * N * K * 4 : 0;
+}
+
 }  // namespace moe

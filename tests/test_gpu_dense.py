@@ -28,6 +28,7 @@ TINY = {"bf16": 0.0, "fp16": 2.0 ** -25, "fp32": 0.0}
 EPI = {"bf16": q.MOE_EPI_NONE, "fp16": q.MOE_EPI_NONE_F16, "fp32": q.MOE_EPI_NONE_F32}
 KERNELS = {"auto": q.MOE_KERNEL_AUTO, "small": q.MOE_KERNEL_SMALL, "128": q.MOE_KERNEL_TILE128,
            "256": q.MOE_KERNEL_TILE256}
+TILES = {name: kr for name, kr in KERNELS.items() if name != "small"}  # what runs the weights' gradient
 SWIGLU = 2.0 ** -19
 
 
@@ -68,6 +69,11 @@ def swiglu_grad_bound(dh, err, pre, dt):
     g, u = np.split(np.abs(pre), 2, axis=1)
     own = np.concatenate([np.abs(dh) * u * (1 + g), np.abs(dh) * g], axis=1) * 2.0 ** -21
     return HALF[dt] * (np.abs(out) + np.abs(e)) * 1.01 + TINY[dt] + np.abs(e) + own
+
+
+def tile(kr):
+    """The kernel choice of a weights' gradient beside products by `kr`."""
+    return q.MOE_KERNEL_AUTO if kr == q.MOE_KERNEL_SMALL else kr
 
 
 class Batch:
@@ -140,7 +146,7 @@ def test_grad_rows(lib, size, dt, kernel):
           swiglu_grad_bound(ref, (N + 2) * 2.0 ** -23 * mag, f64(pre), dt), "swiglu_grad")
 
 
-@pytest.mark.parametrize("kernel", KERNELS)
+@pytest.mark.parametrize("kernel", TILES)
 @pytest.mark.parametrize("dt", ["bf16", "fp16"])
 @pytest.mark.parametrize("size", range(len(SIZES)))
 def test_grad_weights(lib, size, dt, kernel):
@@ -162,7 +168,7 @@ def test_grad_weights_long_segments(lib, counts, N, K):
         b = Batch(3, counts, N, K, "bf16", k=2 if gather else 1, gather=gather)
         ref, mag = do.grad_weights(f64(b.dy), b.rows, b.offsets)
         n = np.array(counts).reshape(-1, 1, 1)
-        for kernel in KERNELS.values():
+        for kernel in TILES.values():
             ws = torch.full((q.moe_grouped_gemm_grad_weights_workspace_size(b.E, N, K, b.M, kernel),), 255,
                             dtype=torch.uint8, device=DEV)  # NaNs
             got = q.moe_grouped_gemm_grad_weights(b.dy, b.a, b.seg, b.E, b.M, gather_pair=b.pairs, k=b.k, kernel=kernel,
@@ -187,7 +193,7 @@ def test_rows_of_no_segment_are_left(lib, kernel):
         call(out)
         assert (out[dead] == 7).all() and not (out[~dead] == 7).all()
         assert torch.isfinite(out).all()
-    dw = q.moe_grouped_gemm_grad_weights(b.dy, a, b.seg, b.E, b.M, kernel=kr)
+    dw = q.moe_grouped_gemm_grad_weights(b.dy, a, b.seg, b.E, b.M, kernel=tile(kr))
     live = np.where(b.live[:, None], 1, 0)
     ref, mag = do.grad_weights(np.where(live, f64(b.dy), 0), np.where(live, b.rows, 0), b.offsets)
     close(f64(dw), ref, bound(ref, mag, 130, "fp32"))
@@ -214,7 +220,7 @@ def test_not_finite_values_stay_in_their_rows(lib, kernel, bad):
     close(got[ok], da[ok], bound(da, dmag, 80, "bf16")[ok])
     assert not np.isfinite(got[20]).any()
     # its weights' gradient alone is lost; the experts beside it keep theirs
-    got = f64(q.moe_grouped_gemm_grad_weights(dy, b.a, b.seg, b.E, b.M, kernel=kr))
+    got = f64(q.moe_grouped_gemm_grad_weights(dy, b.a, b.seg, b.E, b.M, kernel=tile(kr)))
     ref, wmag = do.grad_weights(f64(b.dy), b.rows, b.offsets)
     for e in (0, 2):
         close(got[e], ref[e], bound(ref, wmag, 70, "fp32")[e])
@@ -250,7 +256,7 @@ def test_results_repeat_bit_for_bit(lib):
     for kr in KERNELS.values():
         calls = (lambda: q.moe_grouped_gemm(b.w, b.a, b.seg, b.M, gather_pair=b.pairs, k=4, kernel=kr),
                  lambda: q.moe_grouped_gemm_grad_rows(b.w, b.dy, b.seg, b.M, kernel=kr),
-                 lambda: q.moe_grouped_gemm_grad_weights(b.dy, b.a, b.seg, b.E, b.M, gather_pair=b.pairs, k=4, kernel=kr))
+                 lambda: q.moe_grouped_gemm_grad_weights(b.dy, b.a, b.seg, b.E, b.M, gather_pair=b.pairs, k=4, kernel=tile(kr)))
         for f in calls:
             first = f()
             for _ in range(4):
@@ -270,7 +276,7 @@ def test_more_experts_than_lanes(lib):
               bound(y, mag, 40, "fp32"))
         close(f64(q.moe_grouped_gemm_grad_rows(b.w, b.dy, b.seg, b.M, q.MOE_EPI_NONE_F32, kernel=kr)), da,
               bound(da, dmag, 48, "fp32"))
-        close(f64(q.moe_grouped_gemm_grad_weights(b.dy, b.a, b.seg, 200, b.M, gather_pair=b.pairs, k=2, kernel=kr)), dw,
+        close(f64(q.moe_grouped_gemm_grad_weights(b.dy, b.a, b.seg, 200, b.M, gather_pair=b.pairs, k=2, kernel=tile(kr))), dw,
               bound(dw, wmag, 300, "fp32"))
 
 
@@ -294,7 +300,7 @@ def test_offsets_past_32_bits(lib, kernel):
     mag = np.abs(f64(out[at])) @ np.abs(f64(w[1]))
     close(f64(da[at]), ref, bound(ref, mag, N, "fp32"))
     out[:-33] = 0
-    dw = q.moe_grouped_gemm_grad_weights(out, a, seg, 2, M, kernel=kr)
+    dw = q.moe_grouped_gemm_grad_weights(out, a, seg, 2, M, kernel=tile(kr))
     ref = f64(out[-33:]).T @ f64(a[-33:])
     mag = np.abs(f64(out[-33:])).T @ np.abs(f64(a[-33:]))
     close(f64(dw[1]), ref, bound(ref, mag, M, "fp32"))
