@@ -15,7 +15,11 @@
 namespace moe {
 
 namespace {
-constexpr int kTM = 32;  // tokens of a workgroup
+constexpr int kWorkgroups = 256;
+// Tiles of 16 tokens of a workgroup.
+constexpr int token_tiles(int nr) { return nr <= 2 ? 1 : 2; }
+// Wavefronts of a workgroup: the sums that they exchange take 2 KB of LDS each and tile of 16 ranks.
+constexpr int waves(int nr) { return nr <= 4 ? 8 : 4; }
 
 struct AdapterK {
   AdapterArgs a;
@@ -24,18 +28,23 @@ struct AdapterK {
 };
 
 template <bool F16, int YT, int NR>  // NR: tiles of 16 of the rank
-__global__ __launch_bounds__(256) void adapter_kernel(AdapterK p) {
-  constexpr int RP = (16 * NR + 31) / 32 * 32;  // the rank, padded to whole steps
+__global__ __launch_bounds__(64 * waves(NR), NR <= 2 ? 4 : 2) void adapter_kernel(AdapterK p) {
+  constexpr int W = waves(NR), RP = (16 * NR + 31) / 32 * 32;  // the rank, padded to whole steps
+  constexpr int NB = token_tiles(NR), kTM = 16 * NB;           // tokens
+  constexpr int U = NR <= 4 ? 2 : 1;                           // steps of the first product loaded at a time
   const AdapterArgs& a = p.a;
-  __shared__ float red[4][NR][2][4][64];
+  // the first product's sums; then a wavefront's 16 x 64 results of the second
+  constexpr int RED = W * NR * NB * 64 > W * 256 ? W * NR * NB * 64 : W * 256;
+  __shared__ f32x4 lds[RED];
+  auto red = [&](int w, int i, int b) { return lds + ((w * NR + i) * NB + b) * 64; };
   __shared__ __attribute__((aligned(16))) uint16_t vh[kTM][RP + 8], vl[kTM][RP + 8];
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  const int col = lane & 15, q = lane >> 4;
+  const int col = lane & 15, quad = lane >> 4;
   int idx = blockIdx.x;
   RowTile t;
   bool none = false;
   if (!find_tile<kTM>(a.seg, a.n, a.T, p.n_nb, idx, t)) {
-    // tokens without an adapter come behind the others: copied, 32 a workgroup
+    // tokens without an adapter come behind the others: copied a tile a workgroup
     const int end = min(max(a.seg[a.n], 0), a.T);
     if (a.out == a.y || idx >= (a.T - end + kTM - 1) / kTM * p.n_nb) return;
     none = true;
@@ -44,132 +53,182 @@ __global__ __launch_bounds__(256) void adapter_kernel(AdapterK p) {
     t.s1 = a.T;
   }
   const int r0 = t.r0 + idx / p.n_nb * kTM, c0 = idx % p.n_nb * p.per_wg, c1 = min(c0 + p.per_wg, p.n_chunk);
-  int tok[2];  // this lane's tokens of the two column tiles; past the end the last again, never stored
+  int tok[NB];  // this lane's tokens in the first product; past the end the last again, never stored
 #pragma unroll
-  for (int b = 0; b < 2; ++b) tok[b] = min(max(a.rows[min(r0 + 16 * b + col, t.s1 - 1)], 0), a.T - 1);
+  for (int b = 0; b < NB; ++b) tok[b] = min(max(a.rows[min(r0 + 16 * b + col, t.s1 - 1)], 0), a.T - 1);
+
+  // Second product, in chunks of 64 channels.  It leaves a lane four channels of a token
+  // and goes through 4 KB of LDS a wavefront and 16 tokens, so that y is read and out
+  // written 128 bytes and more in a row: 16 bytes a lane, LR lanes a row, RI rows at a time.
+  constexpr int V = YT == 1 ? 4 : 8, LR = 64 / V, RI = 64 / LR, IT = kTM / RI;
+  int row_tok[IT];
+#pragma unroll
+  for (int i = 0; i < IT; ++i) row_tok[i] = min(max(a.rows[min(r0 + RI * i + lane / LR, t.s1 - 1)], 0), a.T - 1);
+  const rsrc_t br = scalar_rsrc(static_cast<const uint16_t*>(a.B) + (size_t)t.e * a.N * a.r, (uint32_t)((size_t)a.N * a.r * 2));
+  constexpr int ES = YT == 1 ? 4 : 2;
+  struct Chunk {
+    u32x4 b[RP / 32][4];
+    u32x4 y[IT];
+  };
+  auto fetch = [&](int c) {
+    Chunk k;
+#pragma unroll
+    for (int s = 0; s < RP / 32; ++s)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int at = 32 * s + 8 * quad, ch = 64 * c + 16 * i + col;
+        k.b[s][i] = buf_x4(br, !none && at < a.r && ch < a.N ? ((uint32_t)ch * (uint32_t)a.r + at) * 2 : ~0u, 0);
+      }
+    const int ch = min(64 * c + V * (lane % LR), a.N - V);
+#pragma unroll
+    for (int i = 0; i < IT; ++i)
+      k.y[i] = *reinterpret_cast<const u32x4*>(static_cast<const char*>(a.y) + ((size_t)row_tok[i] * a.N + ch) * ES);
+    return k;
+  };
+  Chunk next;
+  if constexpr (NR <= 4)
+    if (c0 + wv < c1) next = fetch(c0 + wv);  // under way while the first product is worked out
 
   if (!none) {
-    const rsrc_t xr = make_rsrc(a.x, (uint32_t)((size_t)a.T * a.K * 2));
-    const rsrc_t ar = make_rsrc(static_cast<const uint16_t*>(a.A) + (size_t)t.e * a.r * a.K, (uint32_t)((size_t)a.r * a.K * 2));
-    f32x4 acc[NR][2] = {};
-    for (int k0 = 32 * wv; k0 < a.K; k0 += 128) {
-      const uint32_t k = k0 + 8 * q;
+    // First product: wavefront wv takes steps wv, wv + W, ... of 32 inputs.
+    const rsrc_t xr = scalar_rsrc(a.x, (uint32_t)((size_t)a.T * a.K * 2));
+    const rsrc_t ar = scalar_rsrc(static_cast<const uint16_t*>(a.A) + (size_t)t.e * a.r * a.K, (uint32_t)((size_t)a.r * a.K * 2));
+    struct Step {
+      u32x4 x[NB], w[NR];
+    };
+    auto load = [&](int k0) {
+      Step s;
+      const uint32_t k = k0 + 8 * quad;
       const bool in = (int)k < a.K;
-      u32x4 xv[2], av[NR];
 #pragma unroll
-      for (int b = 0; b < 2; ++b) xv[b] = buf_x4(xr, in ? ((uint32_t)tok[b] * a.K + k) * 2 : ~0u, 0);
+      for (int b = 0; b < NB; ++b) s.x[b] = buf_x4(xr, in ? ((uint32_t)tok[b] * (uint32_t)a.K + k) * 2 : ~0u, 0);
 #pragma unroll
-      for (int i = 0; i < NR; ++i) av[i] = buf_x4(ar, in && 16 * i + col < a.r ? ((16 * i + col) * a.K + k) * 2 : ~0u, 0);
+      for (int i = 0; i < NR; ++i) s.w[i] = buf_x4(ar, in && 16 * i + col < a.r ? ((uint32_t)(16 * i + col) * (uint32_t)a.K + k) * 2 : ~0u, 0);
+      return s;
+    };
+    f32x4 acc[NR][NB] = {};
+    Step s[U];
 #pragma unroll
-      for (int i = 0; i < NR; ++i)
+    for (int u = 0; u < U; ++u) s[u] = load(32 * (wv + W * u));
+    for (int k0 = 32 * wv; k0 < a.K; k0 += 32 * W * U) {
 #pragma unroll
-        for (int b = 0; b < 2; ++b) acc[i][b] = mfma16t<F16>(av[i], xv[b], acc[i][b]);
+      for (int u = 0; u < U; ++u) {
+        const Step now = s[u];
+        s[u] = load(k0 + 32 * W * (U + u));  // (past the end: nothing)
+#pragma unroll
+        for (int i = 0; i < NR; ++i)
+#pragma unroll
+          for (int b = 0; b < NB; ++b) acc[i][b] = mfma16t<F16>(now.w[i], now.x[b], acc[i][b]);
+      }
     }
 #pragma unroll
     for (int i = 0; i < NR; ++i)
 #pragma unroll
-      for (int b = 0; b < 2; ++b)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) red[wv][i][b][r][lane] = acc[i][b][r];
+      for (int b = 0; b < NB; ++b) red(wv, i, b)[lane] = acc[i][b];
     __syncthreads();
-    for (int i = threadIdx.x; i < kTM * RP; i += 256) {
-      const int row = i / RP, c = i % RP;
-      float v = 0.0f;
-      if (c < 16 * NR)
+    for (int o = threadIdx.x; o < kTM * (RP / 4); o += 64 * W) {  // four ranks of a token
+      const int row = o % kTM, c = o / kTM;
+      f32x4 v = {};
+      if (c < 4 * NR)
 #pragma unroll
-        for (int w = 0; w < 4; ++w) v += red[w][c >> 4][row >> 4][c & 3][16 * ((c >> 2) & 3) + (row & 15)];
-      const uint16_t hi = round16<F16>(v);
-      vh[row][c] = hi;
-      vl[row][c] = round16<F16>(v - widen16<F16>(hi));
+        for (int w = 0; w < W; ++w) v += red(w, c >> 2, row >> 4)[16 * (c & 3) + (row & 15)];
+      uint16_t hi[4], lo[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        hi[i] = round16<F16>(v[i]);
+        lo[i] = round16<F16>(v[i] - widen16<F16>(hi[i]));
+      }
+      *reinterpret_cast<u32x2*>(&vh[row][4 * c]) = u32x2{hi[0] | (uint32_t)hi[1] << 16, hi[2] | (uint32_t)hi[3] << 16};
+      *reinterpret_cast<u32x2*>(&vl[row][4 * c]) = u32x2{lo[0] | (uint32_t)lo[1] << 16, lo[2] | (uint32_t)lo[3] << 16};
     }
     __syncthreads();
   }
   const float scale = none ? 0.0f : a.scale ? a.scale[t.e] : 1.0f;
-  const rsrc_t br = make_rsrc(static_cast<const uint16_t*>(a.B) + (size_t)t.e * a.N * a.r, (uint32_t)((size_t)a.N * a.r * 2));
-  for (int c = c0 + wv; c < c1; c += 4) {
-    f32x4 d[4][2] = {};
+  for (int c = c0 + wv; c < c1; c += W) {
+    Chunk k;
+    if constexpr (NR <= 4) {
+      k = next;
+      if (c + W < c1) next = fetch(c + W);
+    } else {
+      k = fetch(c);
+    }
+    f32x4 d[4][NB] = {};
     if (!none) {
-      for (int k0 = 0; k0 < a.r; k0 += 32) {
-        const int k = k0 + 8 * q;
-        u32x4 bv[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int ch = 64 * c + 16 * (col >> 2) + 4 * i + (col & 3);
-          bv[i] = buf_x4(br, k < a.r && ch < a.N ? ((uint32_t)ch * a.r + k) * 2 : ~0u, 0);
+      for (int s = 0; s < RP / 32; ++s)
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          const u32x4 h = *reinterpret_cast<const u32x4*>(&vh[16 * b + col][32 * s + 8 * quad]);
+          const u32x4 l = *reinterpret_cast<const u32x4*>(&vl[16 * b + col][32 * s + 8 * quad]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) d[i][b] = mfma16t<F16>(k.b[s][i], h, mfma16t<F16>(k.b[s][i], l, d[i][b]));
         }
-#pragma unroll
-        for (int b = 0; b < 2; ++b) {
-          const u32x4 h = *reinterpret_cast<const u32x4*>(&vh[16 * b + col][k]);
-          const u32x4 l = *reinterpret_cast<const u32x4*>(&vl[16 * b + col][k]);
-#pragma unroll
-          for (int i = 0; i < 4; ++i) d[i][b] = mfma16t<F16>(bv[i], h, mfma16t<F16>(bv[i], l, d[i][b]));
-        }
-      }
     }
 #pragma unroll
-    for (int b = 0; b < 2; ++b) {
-      const int ch = 64 * c + 16 * q;
-      if (r0 + 16 * b + col >= t.s1) continue;
+    for (int b = 0; b < NB; ++b) {
+      // [16 tokens][64 channels] fp32, chunk k of 16 bytes of row r at place k ^ r
+      f32x4* const at = lds + wv * 256;
 #pragma unroll
-      for (int i = 0; i < 4; i += 2) {  // 8 channels at a time
-        if (ch + 4 * i >= a.N) continue;
-        const size_t at = (size_t)tok[b] * a.N + ch + 4 * i;
-        if constexpr (YT == 1) {
-          const f32x4* y = reinterpret_cast<const f32x4*>(static_cast<const float*>(a.y) + at);
-          f32x4* o = reinterpret_cast<f32x4*>(static_cast<float*>(a.out) + at);
+      for (int i = 0; i < 4; ++i) at[col * 16 + ((4 * i + quad) ^ col)] = d[i][b];
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            f32x4 v = y[j];
-            if (!none)
+      for (int i = b * (16 / RI); i < (b + 1) * (16 / RI); ++i) {
+        const int r = RI * i - 16 * b + lane / LR, ch = 64 * c + V * (lane % LR);
+        f32x4 v[V / 4];
 #pragma unroll
-              for (int r = 0; r < 4; ++r) v[r] = __builtin_fmaf(scale, d[i + j][b][r], v[r]);
-            o[j] = v;
-          }
-        } else {
-          u32x4 v = *reinterpret_cast<const u32x4*>(static_cast<const uint16_t*>(a.y) + at);
-          if (!none) {
+        for (int q = 0; q < V / 4; ++q) v[q] = at[r * 16 + ((V / 4 * (lane % LR) + q) ^ r)];
+        u32x4 o = k.y[i];
+        if (!none) {
+          if constexpr (YT == 1) {
+            f32x4 y = __builtin_bit_cast(f32x4, o);
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const uint32_t x = v[j];
+            for (int q = 0; q < 4; ++q) y[q] = __builtin_fmaf(scale, v[0][q], y[q]);
+            o = __builtin_bit_cast(u32x4, y);
+          } else {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const uint32_t x = o[q];
               const float lo = widen16<YT == 2>((uint16_t)(x & 0xFFFFu)), hi = widen16<YT == 2>((uint16_t)(x >> 16));
-              v[j] = pack16x2<YT == 2>(__builtin_fmaf(scale, d[i + j / 2][b][2 * (j & 1)], lo),
-                                       __builtin_fmaf(scale, d[i + j / 2][b][2 * (j & 1) + 1], hi));
+              o[q] = pack16x2<YT == 2>(__builtin_fmaf(scale, v[q >> 1][2 * (q & 1)], lo), __builtin_fmaf(scale, v[q >> 1][2 * (q & 1) + 1], hi));
             }
           }
-          *reinterpret_cast<u32x4*>(static_cast<uint16_t*>(a.out) + at) = v;
         }
+        if (r0 + RI * i + lane / LR < t.s1 && ch < a.N)
+          *reinterpret_cast<u32x4*>(static_cast<char*>(a.out) + ((size_t)row_tok[i] * a.N + ch) * ES) = o;
       }
     }
   }
 }
 
-template <bool F16, int YT>
-int launch_rank(const AdapterK& p, unsigned wgs, hipStream_t s) {
-  if (p.a.r <= 16) hipLaunchKernelGGL((adapter_kernel<F16, YT, 1>), dim3(wgs), dim3(256), 0, s, p);
-  else if (p.a.r <= 32) hipLaunchKernelGGL((adapter_kernel<F16, YT, 2>), dim3(wgs), dim3(256), 0, s, p);
-  else if (p.a.r <= 64) hipLaunchKernelGGL((adapter_kernel<F16, YT, 4>), dim3(wgs), dim3(256), 0, s, p);
-  else hipLaunchKernelGGL((adapter_kernel<F16, YT, 8>), dim3(wgs), dim3(256), 0, s, p);
+template <bool F16, int YT, int NR>
+int launch_kernel(AdapterK p, hipStream_t s) {
+  // One partial tile per adapter that has tokens, and one of the tokens without; the
+  // channels are split over workgroups, each with the first product of its own, until the
+  // chip is full.
+  const int64_t tiles = (int64_t)p.a.T / (16 * token_tiles(NR)) + (p.a.n < p.a.T ? p.a.n : p.a.T) + 1;
+  const int64_t want = (kWorkgroups + tiles - 1) / tiles, most = (p.n_chunk + waves(NR) - 1) / waves(NR);
+  const int n_nb = (int)(want < most ? want : most);
+  p.per_wg = (p.n_chunk + n_nb - 1) / n_nb;
+  p.n_nb = (p.n_chunk + p.per_wg - 1) / p.per_wg;
+  const int64_t wgs = tiles * p.n_nb;
+  if (wgs >= ((int64_t)1 << 22)) return (int)hipErrorInvalidConfiguration;  // 2^31 threads
+  hipLaunchKernelGGL((adapter_kernel<F16, YT, NR>), dim3((unsigned)wgs), dim3(64 * waves(NR)), 0, s, p);
   return (int)hipGetLastError();
 }
+template <bool F16, int YT>
+int launch_rank(const AdapterK& p, hipStream_t s) {
+  return p.a.r <= 16 ? launch_kernel<F16, YT, 1>(p, s) : p.a.r <= 32 ? launch_kernel<F16, YT, 2>(p, s)
+         : p.a.r <= 64 ? launch_kernel<F16, YT, 4>(p, s) : launch_kernel<F16, YT, 8>(p, s);
+}
 template <bool F16>
-int launch_typed(const AdapterK& p, unsigned wgs, hipStream_t s) {
-  return p.a.y_dtype == 1 ? launch_rank<F16, 1>(p, wgs, s) : p.a.y_dtype == 2 ? launch_rank<F16, 2>(p, wgs, s)
-                                                                              : launch_rank<F16, 0>(p, wgs, s);
+int launch_typed(const AdapterK& p, hipStream_t s) {
+  return p.a.y_dtype == 1 ? launch_rank<F16, 1>(p, s) : p.a.y_dtype == 2 ? launch_rank<F16, 2>(p, s) : launch_rank<F16, 0>(p, s);
 }
 }  // namespace
 
 int launch_adapter_add(const AdapterArgs& a, void* stream) {
-  AdapterK p{a, (a.N + 63) / 64, 0, 0};
-  // tiles: one partial per adapter that has tokens, and one of the tokens without
-  const int64_t tiles = (int64_t)a.T / kTM + (a.n < a.T ? a.n : a.T) + 1;
-  const int64_t want = tiles >= 512 ? 1 : (512 + tiles - 1) / tiles;
-  const int n_nb = (int)(want < (p.n_chunk + 3) / 4 ? want : (p.n_chunk + 3) / 4);
-  p.per_wg = (p.n_chunk + n_nb - 1) / n_nb;
-  p.n_nb = (p.n_chunk + p.per_wg - 1) / p.per_wg;
-  const int64_t wgs = tiles * p.n_nb;
-  if (wgs >= ((int64_t)1 << 23)) return (int)hipErrorInvalidConfiguration;
+  const AdapterK p{a, (a.N + 63) / 64, 0, 0};
   const hipStream_t s = static_cast<hipStream_t>(stream);
-  return a.dtype == 2 ? launch_typed<true>(p, (unsigned)wgs, s) : launch_typed<false>(p, (unsigned)wgs, s);
+  return a.dtype == 2 ? launch_typed<true>(p, s) : launch_typed<false>(p, s);
 }
 
 }  // namespace moe
