@@ -32,7 +32,7 @@ struct GemmK {  // kernel arguments
 //   forward  a: channels (SwiGLU: 128 gate and the matching 128 up channels), b: rows, k: inputs
 //   rows     a: inputs, b: rows, k: channels
 //   weights  a: inputs, b: channels, k: the segment's rows
-// P and Q go through two LDS stages of 64 k, filled by LDS-DMA.  An operand whose
+// P and Q go through two (or three) LDS stages of 64 k, filled by LDS-DMA.  An operand whose
 // k lie next to each other in memory ("direct") is kept [256][64], one whose a or
 // b do [64][256], read back transposed (ds_read_b64_tr_b16).
 typedef short s16x4 __attribute__((ext_vector_type(4)));
@@ -82,11 +82,13 @@ __device__ __forceinline__ void grouped_order(int idx, int tiles, int n_ab, int&
 // a and up to 128 b of each.  The last two steps of a tile issue the first two of the
 // next one, so that only the first tile waits for its loads, and a tile's stores go
 // out under the next one's products.
-template <int T, bool F16, int MODE, bool GATHER, bool GLU>
-__device__ __forceinline__ void tile_loop(const GemmK& p, int epi, int n_ab, int n_bb, char* pA, char* pB, char* qA, char* qB, char* sE) {
+template <int T, int TB, int NS, bool F16, int MODE, bool GATHER, bool GLU>
+__device__ __forceinline__ void tile_loop(const GemmK& p, int epi, int n_ab, int n_bb, char* const (&pS)[NS], char* const (&qS)[NS], char* sE) {
   constexpr bool PT = MODE != kForward, QT = MODE == kWeights;  // transposed operands
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
-  constexpr int WA = T / 64;  // wavefronts along a; two along b
+  constexpr int WA = T / 64;      // wavefronts along a; two along b
+  constexpr int QD = 4 * TB / T;  // DMAs of Q a wavefront and step (of P 4)
+  static_assert(!QT || TB == T, "");
   const int wa = wv & (WA - 1), wb = wv / WA, col = lane & 15, quad = lane >> 4;
   const int I = p.N / 2;
   const int na = MODE == kForward ? p.N : p.K;  // a's extent (and a transposed P's row length)
@@ -97,9 +99,9 @@ __device__ __forceinline__ void tile_loop(const GemmK& p, int epi, int n_ab, int
   if constexpr (MODE == kWeights) {
     total = p.E * p.splits * n_ab * n_bb;
   } else {
-    seg_n = segment_tiles<T>(p.seg, p.E, p.M_total, lane, seg0, seg1);
+    seg_n = segment_tiles<TB>(p.seg, p.E, p.M_total, lane, seg0, seg1);
     seg_end = lane_scan(seg_n);
-    total = (p.E <= 64 ? __builtin_amdgcn_readlane(seg_end, 63) : count_tiles<T>(p.seg, p.E, p.M_total)) * n_ab;
+    total = (p.E <= 64 ? __builtin_amdgcn_readlane(seg_end, 63) : count_tiles<TB>(p.seg, p.E, p.M_total)) * n_ab;
   }
   const int per = (total + 7) >> 3, xcd = (int)blockIdx.x & 7;
   int idx = xcd * per + ((int)blockIdx.x >> 3);
@@ -131,21 +133,21 @@ __device__ __forceinline__ void tile_loop(const GemmK& p, int epi, int n_ab, int
         t.s1 = __builtin_amdgcn_readlane(seg1, t.e);
         at -= (__builtin_amdgcn_readlane(seg_end, t.e) - t.tiles) * n_ab;
       } else {
-        find_tile<T>(p.seg, p.E, p.M_total, n_ab, at, t);
+        find_tile<TB>(p.seg, p.E, p.M_total, n_ab, at, t);
       }
       grouped_order(at, t.tiles, n_ab, tile, c.ab);
       c.e = t.e;
-      c.b0 = t.r0 + T * tile;
+      c.b0 = t.r0 + TB * tile;
       c.s0 = t.r0;
       c.s1 = t.s1;
     }
     return c;
   };
 
-  // The DMAs of a tile: a wavefront fetches 4 KB of P and 4 of Q a step, 1 KB each;
+  // The DMAs of a tile: a wavefront fetches 4 KB of P and QD of Q a step, 1 KB each;
   // DMAs i and i + 2 differ by a fixed number of bytes (not where rows are gathered).
   // Rows past an operand's end lie past the descriptor's bytes and read zero.
-  constexpr int QO = GATHER && MODE == kForward ? 4 : 2;
+  constexpr int QO = GATHER && MODE == kForward ? QD : 2;
   uint32_t po[2], qo[QO];                 // byte offsets of this lane's 16 bytes, or kOut
   int pk = 0, qk = 0;                     // direct operands: first k of the lane's chunk in even DMAs (odd: ^ 8)
   const uint16_t *pbase = p.w, *qbase = p.w;
@@ -165,12 +167,12 @@ __device__ __forceinline__ void tile_loop(const GemmK& p, int epi, int n_ab, int
   const int dr = 4 * RK * wv + lane / LR;
   constexpr auto twin = [](int i) { return T == 256 ? i & 1 : i >> 1; };    // which of the two kinds
   constexpr auto second = [](int i) { return T == 256 ? i >> 1 : i & 1; };  // whether the later one
-  // The pair of one of the wavefront's gathered rows: of forward's 32 b row lane % 32, of
+  // The pair of one of the wavefront's gathered rows: of forward's 8 QD b row lane % (8 QD), of
   // weights' 4 RK k of a step row lane % (4 RK).
   auto pair_of = [&](const Tile& c, int step) {
     if constexpr (!GATHER) return 0;
     const int l = lane_here();
-    return p.gather[max(min(MODE == kForward ? c.b0 + 32 * wv + (l & 31) : c.s0 + 64 * step + 4 * RK * wv + (l & (4 * RK - 1)), c.s1 - 1), 0)];
+    return p.gather[max(min(MODE == kForward ? c.b0 + 8 * QD * wv + (l & (8 * QD - 1)) : c.s0 + 64 * step + 4 * RK * wv + (l & (4 * RK - 1)), c.s1 - 1), 0)];
   };
   auto token = [&](int pair) { return (uint32_t)min(max(p.div(pair), 0), p.A_rows - 1); };
   auto trans_ch = [&](int lane, int k) {  // first of the 8 columns that this lane fetches of row k
@@ -178,7 +180,7 @@ __device__ __forceinline__ void tile_loop(const GemmK& p, int epi, int n_ab, int
     return 8 * ((((s16 >> 1) ^ tswz(k)) << 1) + (s16 & 1));
   };
   auto setup = [&](const Tile& c, bool on, int pair) {
-    const int lane = lane_here(), dr = 4 * RK * wv + lane / LR, br = 32 * wv + (lane >> 3), ck = (lane & 7) ^ swz(br);
+    const int lane = lane_here(), dr = 4 * RK * wv + lane / LR, br = 32 * wv + (lane >> 3), bq = 8 * QD * wv + (lane >> 3), ck = (lane & 7) ^ swz(br);
     red = !on ? 0 : MODE == kForward ? p.K : MODE == kRows ? p.N : c.s1 - c.s0;
     ls0 = c.s0;
     ls1 = c.s1;
@@ -215,13 +217,13 @@ __device__ __forceinline__ void tile_loop(const GemmK& p, int epi, int n_ab, int
       qk = 8 * ck;
 #pragma unroll
       for (int i = 0; i < QO; ++i) {
-        const int r = br + 8 * i;
+        const int r = bq + 8 * i;
         const uint32_t from = GATHER ? (uint32_t)__shfl((int)token(pair), 8 * i + (lane >> 3), 64) : r;
         qo[i] = (from * (uint32_t)ld + 8 * (ck ^ (i & 1))) * 2;
         if (GATHER && c.b0 + r >= c.s1) qo[i] = kOut;
       }
       qbase = MODE == kForward ? (GATHER ? p.a : p.a + (size_t)c.b0 * ld) : p.dy + (size_t)c.b0 * ld;
-      qbytes = GATHER ? (uint32_t)((size_t)p.A_rows * ld * 2) : (uint32_t)((size_t)min(c.s1 - c.b0, T) * ld * 2);
+      qbytes = GATHER ? (uint32_t)((size_t)p.A_rows * ld * 2) : (uint32_t)((size_t)min(c.s1 - c.b0, TB) * ld * 2);
     }
   };
 
@@ -234,7 +236,7 @@ __device__ __forceinline__ void tile_loop(const GemmK& p, int epi, int n_ab, int
     const uint32_t rows = (uint32_t)max(min(left, 64), 0);
     const uint32_t adv = left > 0 ? (uint32_t)st * 128u : 0u;
     char* const pd = ps + wv * 4096;
-    char* const qd = qs + wv * 4096;
+    char* const qd = qs + wv * (1024 * QD);
     if constexpr (PT && GATHER) {
       const rsrc_t pr = scalar_rsrc(pbase, pbytes);
       // row 4 RK wv + lane % (4 RK)'s offset, past the segment one that no column brings back (kLastGather)
@@ -272,9 +274,9 @@ __device__ __forceinline__ void tile_loop(const GemmK& p, int epi, int n_ab, int
       const rsrc_t qr = scalar_rsrc(qbase, qbytes);
       const int ld = MODE == kForward ? p.K : p.N;
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
-        dma(qr, qd + 1024 * i, (i & 1 ? qk ^ 8 : qk) < left ? qo[QO == 4 ? i : i & 1] : kOut,
-            QO == 4 || i < 2 ? adv : adv + 32u * (uint32_t)ld);
+      for (int i = 0; i < QD; ++i)
+        dma(qr, qd + 1024 * i, (i & 1 ? qk ^ 8 : qk) < left ? qo[QO == QD ? i : i & 1] : kOut,
+            QO == QD ? adv : adv + (uint32_t)(i >> 1) * 32u * (uint32_t)ld);
     }
   };
 
@@ -304,10 +306,13 @@ __device__ __forceinline__ void tile_loop(const GemmK& p, int epi, int n_ab, int
     return QT ? read_at(qs + 32 * RB * s + 256 * (j >> 2), at ^ ((4 * ((j >> 1) & 1) + (j & 1)) << 5), std::integral_constant<bool, QT>{})
               : read_at(qs + 8192 * (j >> 1) + 2048 * (j & 1), at ^ (s << 6), std::integral_constant<bool, QT>{});
   };
-  // Every wavefront's reads of a stage are done and the other stage's DMAs landed.
+  // Every wavefront's reads of a stage are done and the next stage's DMAs landed; those of
+  // the stages behind it, 4 + QD each, may be on their way (vmcnt, whose upper two bits lie
+  // apart; anything else in flight only makes it wait longer).
   auto ready = [&] {
+    constexpr int fly = (4 + QD) * (NS - 2);
     __builtin_amdgcn_sched_barrier(0);
-    __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt 0, lgkmcnt 0
+    __builtin_amdgcn_s_waitcnt(0x0070 | (fly & 15) | (fly >> 4) << 14);  // lgkmcnt 0
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_sched_barrier(0);
   };
@@ -347,31 +352,29 @@ __device__ __forceinline__ void tile_loop(const GemmK& p, int epi, int n_ab, int
       for_each(slot, std::make_integer_sequence<int, 2 * J>{});
     };
     const int next_pair = pair_of(nxt, 0);
-    // an even number of steps, 2 at least: past the sum's end they multiply zeros
-    const int n = max((red + 127) >> 7 << 1, 2);
+    // a multiple of NS steps: past the sum's end they multiply zeros
+    const int n = max((red + 64 * NS - 1) / (64 * NS) * NS, NS);
 #pragma unroll
-    for (int t = 0; t < 4; ++t) pf[0][t] = read_p(pA, pat, t, 0);
+    for (int t = 0; t < 4; ++t) pf[0][t] = read_p(pS[0], pat, t, 0);
 #pragma unroll
-    for (int x = 0; x < D; ++x) qf[x] = read_q(qA, qat, x, 0);
-    for (int st = 2; st < n; st += 2) {
-      stage(pA, qA, pB, qB, [&] {
-        ready();
-        issue(pA, qA, st);
-      });
-      stage(pB, qB, pA, qA, [&] {
-        ready();
-        issue(pB, qB, st + 1);
-      });
+    for (int x = 0; x < D; ++x) qf[x] = read_q(qS[0], qat, x, 0);
+    for (int st = NS; st < n; st += NS) {
+      for_each([&](auto u_tag) {
+        constexpr int U = decltype(u_tag)::value, V = (U + 1) % NS;
+        stage(pS[U], qS[U], pS[V], qS[V], [&] {
+          ready();
+          issue(pS[U], qS[U], st + U);
+        });
+      }, std::make_integer_sequence<int, NS>{});
     }
-    stage(pA, qA, pB, qB, [&] {
-      ready();
-      setup(nxt, more, next_pair);
-      issue(pA, qA, 0);
-    });
-    stage(pB, qB, pA, qA, [&] {
-      ready();
-      issue(pB, qB, 1);
-    });
+    for_each([&](auto u_tag) {
+      constexpr int U = decltype(u_tag)::value, V = (U + 1) % NS;
+      stage(pS[U], qS[U], pS[V], qS[V], [&] {
+        ready();
+        if constexpr (U == 0) setup(nxt, more, next_pair);
+        issue(pS[U], qS[U], U);
+      });
+    }, std::make_integer_sequence<int, NS>{});
 
     // Epilogue: a wavefront's 32 b x 64 a (fp32: 32) at a time through 4 KB of LDS, so
     // that neighbouring lanes store 64 bytes and more in a row.  Of tile (t, x)
@@ -381,7 +384,7 @@ __device__ __forceinline__ void tile_loop(const GemmK& p, int epi, int n_ab, int
     char* const eb = sE + wv * 4096;
     const int lane = lane_here(), quad = lane >> 4, col = lane & 15;
     const int a0 = GLU && MODE == kForward ? T / 2 * cur.ab + 32 * wa : T * cur.ab + 64 * wa;
-    const int rows = min((MODE == kWeights ? p.N : cur.s1) - cur.b0, T);
+    const int rows = min((MODE == kWeights ? p.N : cur.s1) - cur.b0, TB);
     const size_t row0 = (MODE == kWeights ? ((size_t)cur.part * p.E + cur.e) * p.N : 0) + cur.b0;
     auto chunk = [&](int r, int ck) { return eb + r * 128 + ((ck ^ swz(r)) << 4); };  // 8 chunks of 16 bytes a row
     auto put16 = [&](int t, int x, const f32x4& v, bool f16) {
@@ -529,15 +532,15 @@ __device__ __forceinline__ void tile_loop(const GemmK& p, int epi, int n_ab, int
   };
 
   setup(cur, true, pair_of(cur, 0));
-  issue(pA, qA, 0);
-  issue(pB, qB, 1);
+#pragma unroll
+  for (int u = 0; u < NS; ++u) issue(pS[u], qS[u], u);
   ready();
   while (true) {
     idx += idx_step;
     more = idx < idx_end;
     nxt = more ? locate(idx) : cur;
     const int left = MODE == kWeights ? T : cur.s1 - cur.b0;
-    if constexpr (T == 256) {
+    if constexpr (TB == 256) {
       if (left <= 64) body(std::integral_constant<int, 1>{});
       else if (left <= 128) body(std::integral_constant<int, 2>{});
       else if (left <= 192) body(std::integral_constant<int, 3>{});
@@ -554,8 +557,32 @@ __device__ __forceinline__ void tile_loop(const GemmK& p, int epi, int n_ab, int
 template <int T, bool F16, int MODE, bool GATHER, bool GLU>
 __global__ __launch_bounds__(2 * T, 2) void tile_kernel(GemmK p, int epi, int n_ab, int n_bb) {
 #ifdef __HIP_DEVICE_COMPILE__
-  __shared__ __attribute__((aligned(1024))) char pA[128 * T], pB[128 * T], qA[128 * T], qB[128 * T], sE[T / 32 * 4096];
-  tile_loop<T, F16, MODE, GATHER, GLU>(p, epi, n_ab, n_bb, pA, pB, qA, qB, sE);
+  __shared__ __attribute__((aligned(1024))) char p0[128 * T], p1[128 * T], q0[128 * T], q1[128 * T], sE[T / 32 * 4096];
+  char *const ps[2] = {p0, p1}, *const qs[2] = {q0, q1};
+  tile_loop<T, T, 2, F16, MODE, GATHER, GLU>(p, epi, n_ab, n_bb, ps, qs, sE);
+#endif
+}
+
+// Few tiles: one workgroup a CU, three stages.  Tiles of 128 x 128, or of 128 a x 256 rows
+// where those of 128 rows would take two rounds, those of 256 one, and no segment has
+// more than 192 (a tile's time goes with its rows): 8 experts of 4096 x 14336 with 110 to 150
+// rows each 217 us, with 128-row tiles 312, with two workgroups a CU 287; by the rows of
+// 28672 x 4096, 20 to 430 rows each, 567 with 128-row tiles, with 256-row ones 788.
+template <bool F16, int MODE, bool GATHER, bool GLU>
+__global__ __launch_bounds__(256, 1) void deep_kernel(GemmK p, int epi, int n_ab) {
+#ifdef __HIP_DEVICE_COMPILE__
+  __shared__ __attribute__((aligned(1024))) char p0[16384], p1[16384], p2[16384], q0[32768], q1[32768], q2[32768], sE[16384];
+  char *const ps[3] = {p0, p1, p2}, *const qs[3] = {q0, q1, q2};
+  bool even = true;
+  for (int e0 = 0; e0 < p.E; e0 += 64) {
+    int s0, s1;
+    segment_tiles<128>(p.seg, p.E, p.M_total, e0 + (threadIdx.x & 63), s0, s1);
+    even = even && __ballot(s1 - s0 > 192) == 0;
+  }
+  if (even && count_tiles<128>(p.seg, p.E, p.M_total) * n_ab > kCUs && count_tiles<256>(p.seg, p.E, p.M_total) * n_ab <= kCUs)
+    tile_loop<128, 256, 3, F16, MODE, GATHER, GLU>(p, epi, n_ab, 0, ps, qs, sE);
+  else
+    tile_loop<128, 128, 3, F16, MODE, GATHER, GLU>(p, epi, n_ab, 0, ps, qs, sE);
 #endif
 }
 
@@ -769,7 +796,7 @@ GemmK kernel_args(const Gemm16Args& a) {
 int64_t row_tiles(int M_total, int E, int rows) { return (int64_t)M_total / rows + (E < M_total ? E : M_total); }
 
 template <int T, bool F16, int MODE, bool GATHER, bool GLU>
-int launch_tile(const Gemm16Args& a, hipStream_t s) {
+int launch_tiles(const Gemm16Args& a, hipStream_t s) {
   const int na = MODE == kForward ? a.N : a.K, n_ab = (na + T - 1) / T, n_bb = (a.N + T - 1) / T;
   GemmK k = kernel_args(a);
   int epi = a.epilogue;
@@ -794,7 +821,16 @@ int launch_tile(const Gemm16Args& a, hipStream_t s) {
 }
 template <int T, int MODE, bool GATHER, bool GLU>
 int launch_typed(const Gemm16Args& a, hipStream_t s) {
-  return a.dtype == 2 ? launch_tile<T, true, MODE, GATHER, GLU>(a, s) : launch_tile<T, false, MODE, GATHER, GLU>(a, s);
+  return a.dtype == 2 ? launch_tiles<T, true, MODE, GATHER, GLU>(a, s) : launch_tiles<T, false, MODE, GATHER, GLU>(a, s);
+}
+template <bool F16, int MODE, bool GATHER, bool GLU>
+int launch_deep(const Gemm16Args& a, hipStream_t s) {
+  const int n_ab = ((MODE == kForward ? a.N : a.K) + 127) / 128;
+  const int64_t tiles = row_tiles(a.M_total, a.E, 128) * n_ab;
+  if (tiles >= ((int64_t)1 << 30)) return (int)hipErrorInvalidConfiguration;
+  const int64_t wgs = tiles < kCUs ? (tiles + 7) / 8 * 8 : kCUs;
+  hipLaunchKernelGGL((deep_kernel<F16, MODE, GATHER, GLU>), dim3((unsigned)wgs), dim3(256), 0, s, kernel_args(a), a.epilogue, n_ab);
+  return (int)hipGetLastError();
 }
 template <bool F16, int MODE, bool GATHER, bool GLU>
 int launch_small(const Gemm16Args& a, hipStream_t s) {
@@ -811,6 +847,7 @@ int launch(const Gemm16Args& a, void* stream) {
   if (path == 256) return launch_typed<256, MODE, GATHER, GLU>(a, s);
   if (path == 128) return launch_typed<128, MODE, GATHER, GLU>(a, s);
   if constexpr (MODE == kWeights) return (int)hipErrorInvalidValue;
+  else if (path == kGemm16Deep) return a.dtype == 2 ? launch_deep<true, MODE, GATHER, GLU>(a, s) : launch_deep<false, MODE, GATHER, GLU>(a, s);
   else return a.dtype == 2 ? launch_small<true, MODE, GATHER, GLU>(a, s) : launch_small<false, MODE, GATHER, GLU>(a, s);
 }
 }  // namespace

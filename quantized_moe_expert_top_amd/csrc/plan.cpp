@@ -210,22 +210,25 @@ int mxgemm_path(int M_total, int E, int N, int K, bool e2m1, int kernel) {
 // leave it workgroups to add.  Us for it / tiles of 128, weights from memory: forward, 8 experts
 // with a row of 2048 x 2048 17 / 22, 64 with 16 rows 111 / 123, 48 rows 181 / 127, 8 of 28672 x 4096
 // with 4 rows 392 / 324; by the rows 13 / 22, 118 / 93, 181 / 98, 349 / 402.
+// Tiles of 128 that leave most of the chip's 512 places empty take a CU's LDS for one
+// workgroup, three stages under way and not one: us so / with two workgroups a CU: 8 experts
+// of 4096 x 14336, 128 rows each (256 tiles) 201 / 258, by the rows of 28672 x 4096 334 / 516,
+// one expert of 4096 x 4096, 2048 rows (512 tiles) 67 / 57.
 int gemm16_path(int what, int E, int N, int K, int M_total, int kernel) {
   if (kernel == 1 && what != 2) return 0;
-  if (kernel == 5) return 128;
   if (kernel == 9) return 256;
   const double active = M_total < E ? M_total : E;
   double rounds[2];
   for (int i = 0; i < 2; ++i) {
     const int t = i ? 256 : 128;
     const double na = ((what == 0 ? N : K) + t - 1) / t;
-    if (i == 0 && what != 2 && M_total <= 32.0 * active && na * active <= (what == 0 ? 1024 : 256)) return 0;
+    if (i == 0 && kernel == 0 && what != 2 && M_total <= 32.0 * active && na * active <= (what == 0 ? 1024 : 256)) return 0;
     // a segment's last tile is partly empty and takes less
     const double nb = what == 2 ? (double)E * ((N + t - 1) / t) : (double)M_total / t + 0.2 * active;
     rounds[i] = na * nb / (i ? 256 : 512);
-    if (rounds[i] < 1.0) rounds[i] = 1.0;
   }
-  return 1.58 * rounds[1] < 0.9 * rounds[0] ? 256 : 128;
+  const bool wide = kernel == 0 && 1.58 * (rounds[1] > 1.0 ? rounds[1] : 1.0) < 0.9 * (rounds[0] > 1.0 ? rounds[0] : 1.0);
+  return wide ? 256 : what != 2 && rounds[0] <= 0.65 ? kGemm16Deep : 128;
 }
 
 // Few weights and many rows: enough parts to fill the chip with tiles of 128, each of 8
