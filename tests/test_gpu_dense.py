@@ -638,3 +638,147 @@ def test_adapters_on_another_stream_and_in_a_graph(lib):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, want)
+
+
+# ------------------------------------------------ every path, beyond one tile each
+@pytest.mark.parametrize("kernel", ["auto", "128", "256"])
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+def test_more_tiles_than_workgroups(lib, dt, kernel):
+    """Workgroups go from tile to tile, the next one's loads under way (560 to 1360 tiles of 128): the ends of one
+    tile and the starts of the next, an odd number of steps, segments and channels that end inside tiles."""
+    kr = KERNELS[kernel]
+    counts = [700, 0, 3, 130, 1200]
+    for gather in (False, True):
+        b = Batch(40, counts, 5128, 72, dt, k=2 if gather else 1, gather=gather)
+        y, mag = do.product(f64(b.w), b.rows, b.offsets)
+        args = dict(gather_pair=b.pairs, k=b.k, kernel=kr)
+        close(f64(q.moe_grouped_gemm(b.w, b.a, b.seg, b.M, EPI[dt], **args)), y, bound(y, mag, 72, dt))
+        pre = torch.empty(b.M, 5120, dtype=DT[dt], device=DEV)
+        got = q.moe_grouped_gemm(b.w[:, :5120].contiguous(), b.a, b.seg, b.M, q.MOE_EPI_SWIGLU, pre=pre, **args)
+        yy, mm = y[:, :5120], mag[:, :5120]
+        close(f64(got), do.swiglu(yy), swiglu_bound(yy, mm, 72, dt), f"gather {gather}")
+        close(f64(pre), yy, bound(yy, mm, 72, dt), f"pre gather {gather}")
+        wide = Batch(41, counts, 520, 5128, dt, k=2 if gather else 1, gather=gather)
+        dw, wmag = do.grad_weights(f64(wide.dy), wide.rows, wide.offsets)
+        got = q.moe_grouped_gemm_grad_weights(wide.dy, wide.a, wide.seg, wide.E, wide.M, EPI[dt], gather_pair=wide.pairs,
+                                              k=wide.k, kernel=kr)
+        close(f64(got), dw, bound(dw, wmag, 1200, dt), f"gather {gather}")
+    b = Batch(42, counts, 72, 5128, dt)
+    da, mag = do.grad_rows(f64(b.w), f64(b.dy), b.offsets)
+    close(f64(q.moe_grouped_gemm_grad_rows(b.w, b.dy, b.seg, b.M, q.MOE_EPI_NONE_F32, kernel=kr)), da, bound(da, mag, 72, "fp32"))
+    p = dev(np.random.default_rng(1).standard_normal((b.M, 2 * 5128)), DT[dt])
+    got = q.moe_grouped_gemm_grad_rows(b.w, b.dy, b.seg, b.M, q.MOE_EPI_SWIGLU_GRAD, pre=p, kernel=kr)
+    close(f64(got), do.swiglu_grad(da, f64(p)), swiglu_grad_bound(da, 74 * 2.0 ** -23 * mag, f64(p), dt))
+
+
+@pytest.mark.parametrize("counts", [[130, 150, 140, 129, 192, 137, 160, 131], [130, 150, 140, 129, 193, 137, 160, 131],
+                                    [20, 300, 0, 15, 64, 65, 1, 128]])
+def test_few_tiles(lib, counts):
+    """Three stages: tiles of 128 rows, or of 256 where all segments have up to 192 and one round does."""
+    for gather, K in ((False, 200), (True, 136)):
+        b = Batch(43, counts, 4096, K, "bf16", k=2 if gather else 1, gather=gather)
+        y, mag = do.product(f64(b.w), b.rows, b.offsets)
+        for kr in (q.MOE_KERNEL_AUTO, q.MOE_KERNEL_TILE128):
+            close(f64(q.moe_grouped_gemm(b.w, b.a, b.seg, b.M, gather_pair=b.pairs, k=b.k, kernel=kr)), y, bound(y, mag, K, "bf16"))
+            got = q.moe_grouped_gemm(b.w, b.a, b.seg, b.M, q.MOE_EPI_SWIGLU, gather_pair=b.pairs, k=b.k, kernel=kr)
+            close(f64(got), do.swiglu(y), swiglu_bound(y, mag, K, "bf16"))
+    b = Batch(44, counts, 264, 4096, "fp16")
+    da, mag = do.grad_rows(f64(b.w), f64(b.dy), b.offsets)
+    pre = dev(np.random.default_rng(2).standard_normal((b.M, 2 * 4096)), torch.float16)
+    for kr in (q.MOE_KERNEL_AUTO, q.MOE_KERNEL_TILE128):
+        close(f64(q.moe_grouped_gemm_grad_rows(b.w, b.dy, b.seg, b.M, q.MOE_EPI_NONE_F16, kernel=kr)), da, bound(da, mag, 264, "fp16"))
+        got = q.moe_grouped_gemm_grad_rows(b.w, b.dy, b.seg, b.M, q.MOE_EPI_SWIGLU_GRAD, pre=pre, kernel=kr)
+        close(f64(got), do.swiglu_grad(da, f64(pre)), swiglu_grad_bound(da, 266 * 2.0 ** -23 * mag, f64(pre), "fp16"))
+
+
+def test_offsets_and_pairs_outside_are_clamped(lib):
+    """A table that runs past M_total, pairs past A's rows, an offset table that falls: rows stay inside the buffers."""
+    b = Batch(45, [5, 5], 32, 24, "bf16")
+    y, mag = do.product(f64(b.w), b.rows, b.offsets)
+    for kr in KERNELS.values():
+        far = i32([-7, 5, 1 << 30])
+        close(f64(q.moe_grouped_gemm(b.w, b.a, far, 10, kernel=kr)), y, bound(y, mag, 24, "bf16"))
+        close(f64(q.moe_grouped_gemm_grad_rows(b.w, b.dy, far, 10, q.MOE_EPI_NONE_F32, kernel=kr)),
+              *(lambda r: (r[0], bound(r[0], r[1], 32, "fp32")))(do.grad_rows(f64(b.w), f64(b.dy), b.offsets)))
+        dw, wmag = do.grad_weights(f64(b.dy), b.rows, b.offsets)
+        close(f64(q.moe_grouped_gemm_grad_weights(b.dy, b.a, far, 2, 10, kernel=tile(kr))), dw, bound(dw, wmag, 5, "fp32"))
+        out = torch.full((10, 32), 7.0, dtype=torch.bfloat16, device=DEV)
+        q.moe_grouped_gemm(b.w, b.a, i32([6, 3, 9]), 10, out=out, kernel=kr)  # the first segment is empty
+        assert (out[:3] == 7).all() and (out[9:] == 7).all() and not (out[3:9] == 7).all()
+        pairs = i32([0, 1, 2, 3, 1 << 30, -5, 6, 7, 8, 9])
+        got = f64(q.moe_grouped_gemm(b.w, b.a, b.seg, 10, gather_pair=pairs, kernel=kr))
+        ok = [0, 1, 2, 3, 6, 7, 8, 9]
+        close(got[ok], y[ok], bound(y, mag, 24, "bf16")[ok])
+
+
+def test_the_same_row_many_times(lib):
+    """Pairs of one token in many segments, and twice in one: the forward pass repeats it, the gradient counts it each time."""
+    b = Batch(46, [40, 3, 90], 64, 72, "bf16", k=4, gather=True)
+    pairs = np.concatenate([np.zeros(43, int), np.full(90, 5)])
+    pairs[7] = 9
+    rows = f64(b.a)[pairs // 4]
+    y, mag = do.product(f64(b.w), rows, b.offsets)
+    dw, wmag = do.grad_weights(f64(b.dy), rows, b.offsets)
+    for kr in KERNELS.values():
+        close(f64(q.moe_grouped_gemm(b.w, b.a, b.seg, b.M, gather_pair=i32(pairs), k=4, kernel=kr)), y, bound(y, mag, 72, "bf16"))
+        close(f64(q.moe_grouped_gemm_grad_weights(b.dy, b.a, b.seg, b.E, b.M, gather_pair=i32(pairs), k=4, kernel=tile(kr))), dw,
+              bound(dw, wmag, 90, "fp32"))
+
+
+def test_combine_grad_of_a_repeated_expert(lib):
+    """The same id in two slots of a token: both shares reach its logit."""
+    ids = i32([[2, 2, 0]])
+    p = q.moe_permute(ids, 3)
+    y, dout = dev(np.random.default_rng(3).standard_normal((3, 16)), torch.float32), dev(np.ones((1, 16)), torch.bfloat16)
+    w = dev([[0.5, 0.25, 0.25]], torch.float32)
+    g = q.moe_unpermute_combine_grad(dout, y, p.pair_pos, w, 1, 3, ids=ids, E=3, n_valid=p.seg_offsets[-1:])
+    dw, wn = f64(g.dw)[0], f64(w)[0]
+    dl = wn * (dw - wn @ dw)
+    close(f64(g.dlogits)[0], np.array([dl[2], 0, dl[0] + dl[1]]), 1e-5 * (1 + np.abs(dw).max()))
+
+
+def test_two_graphs_with_one_workspace(lib):
+    """Weights' gradients with split rows, captured twice with one workspace, replayed in turn between eager work."""
+    cases = [Batch(50 + i, [2500, 700], 64, 40, "bf16") for i in range(2)]
+    need = q.moe_grouped_gemm_grad_weights_workspace_size(2, 64, 40, 3200)
+    assert need > 0
+    ws = torch.empty(need, dtype=torch.uint8, device=DEV)
+    want = [q.moe_grouped_gemm_grad_weights(b.dy, b.a, b.seg, 2, b.M) for b in cases]
+    outs, graphs = [], []
+    for b in cases:
+        out = torch.empty(2, 64, 40, device=DEV)
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            q.moe_grouped_gemm_grad_weights(b.dy, b.a, b.seg, 2, b.M, out=out, workspace=ws)
+        outs.append(out)
+        graphs.append(g)
+    for _ in range(3):
+        for out in outs:
+            out.fill_(float("nan"))
+        for g in graphs:
+            g.replay()
+        torch.cuda.synchronize()
+        ws.fill_(255)
+        for out, ref in zip(outs, want):
+            assert torch.equal(out, ref)
+
+
+def test_largest_batch_of_the_small_kernels(lib):
+    """Row sums, lane sums and adapters over more slots and ranks than one pass takes (k = 300, rank 128, 1000 adapters)."""
+    T, k, E, H = 2, 300, 1024, 2056
+    r = np.random.default_rng(4)
+    ids = np.stack([r.permutation(E)[:k] for _ in range(T)])
+    p = q.moe_permute(i32(ids), E)
+    y, dout = dev(r.standard_normal((T * k, H)), torch.float16), dev(r.standard_normal((T, H)), torch.bfloat16)
+    w = torch.softmax(dev(r.standard_normal((T, k)), torch.float32), -1)
+    g = q.moe_unpermute_combine_grad(dout, y, p.pair_pos, w, T, k, ids=i32(ids), E=E, n_valid=p.seg_offsets[-1:])
+    dy, dw, mag, dl = do.combine_grad(f64(dout), f64(y), p.pair_pos.cpu().numpy().reshape(T, k), f64(w), T * k, ids, E)
+    close(f64(g.dy), dy, (2.0 ** -8 + 2.0 ** -23) * np.abs(dy))
+    close(f64(g.dw), dw, (H + 2) * 2.0 ** -23 * mag)
+    e = (H + 2) * 2.0 ** -23 * mag.max()
+    assert np.abs(f64(g.dlogits) - dl).max() <= f64(w).max() * 2 * (e + (k + 4) * 2.0 ** -23 * np.abs(dw).max())
+    ids = r.integers(0, 1000, 300)
+    x, y, A, B, scale, p = adapter_batch(6, ids.tolist(), 1000, 128, 40, 72, "bf16", "bf16")
+    ref, mag = do.adapters(f64(y), f64(x), f64(A), f64(B), ids, f64(scale))
+    got = q.moe_adapter_add(y, x, A, B, p.seg_offsets, p.sorted_pair, scale=scale)
+    close(f64(got), ref, adapter_bound(ref, f64(y), mag, 40, 128, "bf16", "bf16"))
