@@ -31,7 +31,7 @@ template <bool F16, int YT, int NR>  // NR: tiles of 16 of the rank
 __global__ __launch_bounds__(64 * waves(NR), NR <= 2 ? 4 : 2) void adapter_kernel(AdapterK p) {
   constexpr int W = waves(NR), RP = (16 * NR + 31) / 32 * 32;  // the rank, padded to whole steps
   constexpr int NB = token_tiles(NR), kTM = 16 * NB;           // tokens
-  constexpr int U = NR <= 4 ? 2 : 1;                           // steps of the first product loaded at a time
+  constexpr int U = 2;                                         // steps of the first product loaded at a time
   const AdapterArgs& a = p.a;
   // the first product's sums; then a wavefront's 16 x 64 results of the second
   constexpr int RED = W * NR * NB * 64 > W * 256 ? W * NR * NB * 64 : W * 256;
@@ -85,12 +85,14 @@ __global__ __launch_bounds__(64 * waves(NR), NR <= 2 ? 4 : 2) void adapter_kerne
       k.y[i] = *reinterpret_cast<const u32x4*>(static_cast<const char*>(a.y) + ((size_t)row_tok[i] * a.N + ch) * ES);
     return k;
   };
-  Chunk next;
-  if constexpr (NR <= 4)
-    if (c0 + wv < c1) next = fetch(c0 + wv);  // under way while the first product is worked out
+  constexpr int D = NR <= 4 ? 2 : 1;  // chunks under way, while the first product is worked out too
+  Chunk ring[D];
+#pragma unroll
+  for (int u = 0; u < D; ++u) ring[u] = fetch(c0 + wv + W * u);
 
   if (!none) {
-    // First product: wavefront wv takes steps wv, wv + W, ... of 32 inputs.
+    // First product: wavefront wv takes pairs wv, wv + W, ... of steps of 32 inputs, a
+    // line of 128 bytes of every row (single steps: a line fetched by two wavefronts).
     const rsrc_t xr = scalar_rsrc(a.x, (uint32_t)((size_t)a.T * a.K * 2));
     const rsrc_t ar = scalar_rsrc(static_cast<const uint16_t*>(a.A) + (size_t)t.e * a.r * a.K, (uint32_t)((size_t)a.r * a.K * 2));
     struct Step {
@@ -109,16 +111,18 @@ __global__ __launch_bounds__(64 * waves(NR), NR <= 2 ? 4 : 2) void adapter_kerne
     f32x4 acc[NR][NB] = {};
     Step s[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) s[u] = load(32 * (wv + W * u));
-    for (int k0 = 32 * wv; k0 < a.K; k0 += 32 * W * U) {
+    for (int u = 0; u < U; ++u) s[u] = load(64 * (wv + W * (u >> 1)) + 32 * (u & 1));
+    for (int k0 = 64 * wv; k0 < a.K; k0 += 32 * W * U) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
-        const Step now = s[u];
-        s[u] = load(k0 + 32 * W * (U + u));  // (past the end: nothing)
 #pragma unroll
         for (int i = 0; i < NR; ++i)
 #pragma unroll
-          for (int b = 0; b < NB; ++b) acc[i][b] = mfma16t<F16>(now.w[i], now.x[b], acc[i][b]);
+          for (int b = 0; b < NB; ++b) acc[i][b] = mfma16t<F16>(s[u].w[i], s[u].x[b], acc[i][b]);
+        // (a load moved in front of the products gets other registers, and copies that wait for it)
+        __builtin_amdgcn_sched_barrier(0);
+        s[u] = load(k0 + 32 * W * U + 64 * W * (u >> 1) + 32 * (u & 1));  // (past the end: nothing)
+        __builtin_amdgcn_sched_barrier(0);
       }
     }
 #pragma unroll
@@ -144,14 +148,7 @@ __global__ __launch_bounds__(64 * waves(NR), NR <= 2 ? 4 : 2) void adapter_kerne
     __syncthreads();
   }
   const float scale = none ? 0.0f : a.scale ? a.scale[t.e] : 1.0f;
-  for (int c = c0 + wv; c < c1; c += W) {
-    Chunk k;
-    if constexpr (NR <= 4) {
-      k = next;
-      if (c + W < c1) next = fetch(c + W);
-    } else {
-      k = fetch(c);
-    }
+  auto chunk = [&](const Chunk& k, int c) {
     f32x4 d[4][NB] = {};
     if (!none) {
 #pragma unroll
@@ -192,9 +189,18 @@ __global__ __launch_bounds__(64 * waves(NR), NR <= 2 ? 4 : 2) void adapter_kerne
             }
           }
         }
-        if (r0 + RI * i + lane / LR < t.s1 && ch < a.N)
+        if (r0 + RI * i + lane / LR < t.s1 && ch < a.N && c < c1)
           *reinterpret_cast<u32x4*>(static_cast<char*>(a.out) + ((size_t)row_tok[i] * a.N + ch) * ES) = o;
       }
+    }
+  };
+  for (int c = c0 + wv; c < c1; c += W * D) {
+#pragma unroll
+    for (int u = 0; u < D; ++u) {
+      chunk(ring[u], c + W * u);
+      __builtin_amdgcn_sched_barrier(0);
+      ring[u] = fetch(c + W * (D + u));
+      __builtin_amdgcn_sched_barrier(0);
     }
   }
 }
