@@ -133,14 +133,15 @@ __global__ __launch_bounds__(64 * waves(NR), NR <= 2 ? 4 : 2) void adapter_kerne
     for (int o = threadIdx.x; o < kTM * (RP / 4); o += 64 * W) {  // four ranks of a token
       const int row = o % kTM, c = o / kTM;
       f32x4 v = {};
-      if (c < 4 * NR)
+      if (4 * c < a.r)  // (a padding rank: 0, also where x is infinite and 0 * x is not)
 #pragma unroll
         for (int w = 0; w < W; ++w) v += red(w, c >> 2, row >> 4)[16 * (c & 3) + (row & 15)];
       uint16_t hi[4], lo[4];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         hi[i] = round16<F16>(v[i]);
-        lo[i] = round16<F16>(v[i] - widen16<F16>(hi[i]));
+        const float rest = v[i] - widen16<F16>(hi[i]);
+        lo[i] = fabsf(rest) < INFINITY ? round16<F16>(rest) : (uint16_t)0;  // (hi is then infinite or NaN and stays it)
       }
       *reinterpret_cast<u32x2*>(&vh[row][4 * c]) = u32x2{hi[0] | (uint32_t)hi[1] << 16, hi[2] | (uint32_t)hi[3] << 16};
       *reinterpret_cast<u32x2*>(&vl[row][4 * c]) = u32x2{lo[0] | (uint32_t)lo[1] << 16, lo[2] | (uint32_t)lo[3] << 16};

@@ -442,6 +442,20 @@ def test_adapters_keep_to_their_tokens(lib):
     assert torch.isnan(got[5:8]).all() and torch.isnan(got[8, 0]) and torch.equal(got[8, 1:], y[8, 1:])
 
 
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+def test_adapters_past_the_range(lib, dt):
+    """A row or a first product that is infinite stays so (one sign), and no rank beside the given ones makes a NaN of it."""
+    for r in (8, 24):
+        x, A, B = dev(np.ones((2, 16)), DT[dt]), dev(np.ones((1, r, 16)), DT[dt]), dev(np.ones((1, 40, r)), DT[dt])
+        y, p = dev(np.ones((2, 40)), torch.float32), q.moe_permute(i32([[0], [0]]), 1)
+        x[0, 3] = -float("inf")
+        got = q.moe_adapter_add(y, x, A, B, p.seg_offsets, p.sorted_pair)
+        assert (got[0] == -float("inf")).all() and (got[1] == 1 + 16 * r).all()
+        x[0] = 60000.0  # 16 of them: past fp16's range
+        got = q.moe_adapter_add(y, x, A, B, p.seg_offsets, p.sorted_pair)
+        assert (got[0] == (float("inf") if dt == "fp16" else 1 + r * 16 * float(x[0, 0]))).all() and (got[1] == 1 + 16 * r).all()
+
+
 def test_adapters_beside_a_shared_projection(lib):
     """The projection by the library's product (one expert), then the adapters in place."""
     T, K, N, n, r = 45, 256, 320, 4, 16
