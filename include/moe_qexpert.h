@@ -431,7 +431,7 @@ moe_status moe_grouped_gemm_grad_weights(const void* dy, const void* A, int32_t 
  *     dw[t][j]              = sum_h dout[t][h] * y_perm[pos(t, j)][h]
  *     dlogits[t][ids[t][j]] = w[t][j] * (dw[t][j] - sum_i w[t][i] * dw[t][i]), 0 elsewhere
  * A pair whose pair_pos is at or past *n_valid has dw 0, no row of dy (left as it
- * is) and no logit.  Sums in fp32, in an order that the sizes alone decide.
+ * is), no logit and no part in the sum over i, whatever its weight.  Sums in fp32, in an order that the sizes alone decide.
  *   dout bf16 [T][H]; y_perm [T*k][H] of y_dtype (MOE_DTYPE_*); topk_w f32 [T][k]
  *   (NULL: weight 1, and no dlogits); ids i32 [T][k] in [0, E) (others add nothing) and dlogits
  *   f32 [T][E], both or neither NULL; dy [T*k][H] of dy_dtype (MOE_DTYPE_BF16 or

@@ -124,7 +124,8 @@ __global__ __launch_bounds__(kThreads) void combine_grad_kernel(CombineGradArgs 
   }
   if (!a.dlogits) return;
   float dot = 0.0f;
-  for (int j = 0; j < k; ++j) dot = __builtin_fmaf(ws[j], dws[j], dot);
+  for (int j = 0; j < k; ++j)
+    if (at[j] >= 0) dot = __builtin_fmaf(ws[j], dws[j], dot);  // (a weight that no row got may be anything)
   for (int e = threadIdx.x; e < a.E; e += kThreads) {
     float g = 0.0f;
     for (int j = 0; j < k; ++j)

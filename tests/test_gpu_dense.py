@@ -357,6 +357,21 @@ def test_combine_grad(lib, T, k, E, H, y_dt):
     assert torch.equal(one.dy[:nv], dout[torch.div(p.sorted_pair[:nv], k, rounding_mode="floor").long()])
 
 
+def test_combine_grad_of_weights_without_rows(lib):
+    """The weight of a pair without an expert may be anything: it reaches no gradient."""
+    ids = i32([[1, -1, 2], [0, 2, 7]])
+    p = q.moe_permute(ids, 3)
+    r = np.random.default_rng(8)
+    y, dout = dev(r.standard_normal((6, 24)), torch.float32), dev(r.standard_normal((2, 24)), torch.bfloat16)
+    grads = []
+    for v in (0.0, float("nan"), float("inf")):
+        w = dev([[0.5, v, 0.5], [0.25, 0.75, v]], torch.float32)
+        g = q.moe_unpermute_combine_grad(dout, y, p.pair_pos, w, 2, 3, ids=ids, E=3, n_valid=p.seg_offsets[-1:])
+        grads.append((g.dy[:4], g.dw, g.dlogits))
+    for g in grads:
+        assert all(torch.isfinite(t).all() and torch.equal(t, u) for t, u in zip(g, grads[0]))
+
+
 def test_combine_grad_by_differences(lib):
     """The logits' and outputs' gradients against central differences of <dout, combine(softmax gates)> in float64."""
     T, k, E, H = 4, 3, 6, 64
