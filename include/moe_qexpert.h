@@ -401,7 +401,7 @@ moe_status moe_unpermute_combine(const void* y_perm, int32_t y_dtype, const int3
  *   seg_offsets i32 [E + 1] from moe_permute (device), or a slice of a longer
  *               ascending table; rows outside [seg_offsets[0], seg_offsets[E]) are
  *               not written (nor read, in the gradients)
- *   M_total     host upper bound of the rows; out, dy and pre have M_total rows
+ *   M_total     host upper bound of the rows, fewer than 2^30; out, dy and pre have M_total rows
  *               (without gather_pair A has at least as many)
  *   kernel      MOE_KERNEL_AUTO, or MOE_KERNEL_SMALL (not grad_weights), _TILE128 or _TILE256
  *   workspace   grad_weights: moe_grouped_gemm_grad_weights_workspace_size(...) bytes of

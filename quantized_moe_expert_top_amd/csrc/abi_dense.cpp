@@ -34,6 +34,8 @@ moe_status check_sizes(int32_t dtype, int32_t E, int32_t N, int32_t K, int32_t M
   if (N % 8 != 0 || K % 8 != 0) return fail(MOE_ERR_UNSUPPORTED, "N=%d and K=%d must be multiples of 8", N, K);
   if (N > 1 << 20 || K > 1 << 20) return fail(MOE_ERR_UNSUPPORTED, "N=%d or K=%d above 2^20", N, K);
   if (M_total < 0) return fail(MOE_ERR_BAD_SHAPE, "M_total=%d < 0", M_total);
+  // (room for a partial tile's and a last step's rows in 32 bits)
+  if (M_total >= 1 << 30) return fail(MOE_ERR_UNSUPPORTED, "M_total=%d of 2^30 or more", M_total);
   if ((int64_t)N * K * 2 >= kMaxBytes)
     return fail(MOE_ERR_UNSUPPORTED, "an expert's weights of %lld bytes (4 GiB or more)", (long long)N * K * 2);
   return check_kernel(kernel, small);

@@ -86,6 +86,8 @@ int main() {
   CHECK(product(INT_MAX, 64, 64, 8, 8, MOE_EPI_NONE, 0) == MOE_ERR_BAD_SHAPE);
   CHECK(product(4, INT_MAX - 7, INT_MAX - 7, 8, 8, MOE_EPI_NONE, 0) == MOE_ERR_UNSUPPORTED);
   CHECK(product(4, 64, 64, INT_MAX, INT_MAX, MOE_EPI_NONE, 0, as<int32_t>(0x7000)) == MOE_ERR_UNSUPPORTED);
+  CHECK(product(4, 64, 64, INT_MAX, 1 << 30, MOE_EPI_NONE, 0) == MOE_ERR_UNSUPPORTED);
+  CHECK(weights(4, 64, 64, 1 << 30, nullptr, 0) == MOE_ERR_UNSUPPORTED);
   CHECK(adapters(1024, 128, 1 << 30, 1 << 30, (1 << 24) - 1) == MOE_ERR_UNSUPPORTED);
   CHECK(adapters(INT_MAX, 128, 64, 64, 4) == MOE_ERR_BAD_SHAPE);
   CHECK(product(4, 64, 64, 0, 0, MOE_EPI_NONE, 0) == MOE_OK && adapters(4, 16, 64, 64, 0) == MOE_OK);
@@ -93,7 +95,7 @@ int main() {
   CHECK(weights(4, 64, 64, 0, nullptr, 0) == MOE_OK && stub::launches == n + 1 && last.M_total == 0);
 
   // the largest calls, without gather_pair past 4 GiB too
-  CHECK(product(1024, 1 << 20, 2040, INT_MAX, INT_MAX, MOE_EPI_NONE_F32, 0) == MOE_OK);
+  CHECK(product(1024, 1 << 20, 2040, INT_MAX, (1 << 30) - 1, MOE_EPI_NONE_F32, 0) == MOE_OK);
   CHECK(product(1, 1 << 20, 2048, 8, 8, MOE_EPI_NONE_F32, 0) == MOE_ERR_UNSUPPORTED);  // 4 GiB of weights
 
   // plans at the limits

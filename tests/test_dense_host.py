@@ -75,7 +75,8 @@ def test_product_refusals(lib):
                          dict(gather=A, k=0), dict(gather=A, k=1, rows=9), dict(out=A), dict(out=B),
                          dict(epi=1, pre=B), dict(epi=1, pre=D)]),
             (UNSUPPORTED, [dict(N=12), dict(K=20), dict(N=24, epi=1), dict(kernel=3), dict(kernel=8), dict(N=(1 << 20) + 8),
-                           dict(K=(1 << 20) + 8), dict(N=1 << 16, K=1 << 15), dict(gather=A, rows=1 << 25, K=64, k=1)]),
+                           dict(K=(1 << 20) + 8), dict(N=1 << 16, K=1 << 15), dict(gather=A, rows=1 << 25, K=64, k=1),
+                           dict(M=1 << 30, rows=1 << 30)]),
             (NULL_ARG, [dict(w=None), dict(a=None), dict(seg=None), dict(out=None)]),
             (MISALIGNED, [dict(w=ODD), dict(a=ODD), dict(out=ODD), dict(seg=ctypes.c_void_p(0x3002)),
                           dict(gather=ctypes.c_void_p(0x3002), k=1), dict(epi=1, pre=ODD)])):
@@ -93,7 +94,7 @@ def test_grad_rows_refusals(lib):
     for want, cases in (
             (BAD_FORMAT, [dict(dtype=1), dict(epi=1), dict(epi=5), dict(kernel=99)]),
             (BAD_SHAPE, [dict(E=0), dict(M=-1), dict(out=A), dict(out=B), dict(epi=6, pre=D)]),
-            (UNSUPPORTED, [dict(N=12), dict(K=12), dict(kernel=4)]),
+            (UNSUPPORTED, [dict(N=12), dict(K=12), dict(kernel=4), dict(M=1 << 30)]),
             (NULL_ARG, [dict(w=None), dict(dy=None), dict(seg=None), dict(out=None), dict(epi=6), dict(pre=A)]),
             (MISALIGNED, [dict(w=ODD), dict(dy=ODD), dict(out=ODD), dict(epi=6, pre=ODD)])):
         for kw in cases:
