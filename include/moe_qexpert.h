@@ -198,11 +198,12 @@ moe_status moe_route_permute(const float* logits, int32_t T, int32_t E, int32_t 
    row sums in a different order, so their bits may differ from the others'. */
 #define MOE_KERNEL_AUTO 0            /* chosen from the mean rows per segment */
 #define MOE_KERNEL_SMALL 1           /* 16-row tiles (decode batches); nested MWQ: all widths of an
-                                        expert in one tile; DELTA2: 32-row tiles */
+                                        expert in one tile; DELTA2 and 16-bit weights: 32-row tiles */
 #define MOE_KERNEL_SMALL_PER_WIDTH 2 /* nested MWQ only: 16-row tiles of one width each */
 #define MOE_KERNEL_TILE64_WIDE 3     /* INT4, MWQ: 64-row tiles, 128 SwiGLU / 256 plain channels */
 #define MOE_KERNEL_TILE64 4          /* INT4, MWQ: 64-row tiles, 64 SwiGLU / 128 plain channels */
-#define MOE_KERNEL_TILE128 5         /* INT4, MWQ: 128-row tiles fed through registers */
+#define MOE_KERNEL_TILE128 5         /* INT4, MWQ: 128-row tiles fed through registers; 16-bit weights:
+                                        tiles of 128 output columns */
 #define MOE_KERNEL_LDS_DMA 6         /* INT4, MWQ, DELTA2 with a base and a plain epilogue: 64- or
                                         128-row tiles fed by LDS-DMA (activation row sums in the
                                         workspace); nested MWQ: 16-row chunks of all widths */

@@ -5,6 +5,10 @@
 // reads 8 of each expert's output and writes 8 of its gradient (16 bytes each),
 // so every byte moves once.  The row sums are added in fp32 over a thread's
 // values, the wavefront's lanes and the wavefronts, in that order; no atomics.
+// Bytes bound it: 8192 tokens x 8 of 2048, y in fp16, 570 MB in 108 us (5.3 TB/s, a
+// copy's rate).  What brought it there from 177 us: streaming loads and stores (a row
+// moves once), the slots' places read once through LDS and not by every thread, lane
+// sums by exchanged halves.
 #include "segments.h"
 
 namespace moe {

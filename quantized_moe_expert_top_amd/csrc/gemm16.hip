@@ -1,6 +1,13 @@
 // Grouped product of rows with the experts' 16-bit weights, and its gradients by
-// the rows and by the weights, on v_mfma_f32_32x32x16 (bf16 or fp16 operands,
-// fp32 sums).
+// the rows and by the weights, on v_mfma_f32_16x16x32 (bf16 or fp16 operands,
+// fp32 sums): the matrix units run at the power limit, and random operands cost less
+// in this shape than in 32 x 32 x 16 (from registers alone 1978 and 1695 TFLOP/s; the
+// tiles below, 8192^3: 760 and 831 us).
+// Measured (bf16, random operands): 8192^3 759 us (1449 TFLOP/s), by the rows 769, by
+// the weights 767.  64 experts of 2048 x 2048, 65536 rows gathered, SwiGLU and what
+// enters it 534 us (1029); by the weights 535.  The rest goes to stores: all
+// workgroups' tiles end at about the same time and wait for the memory (a quarter of
+// them storing costs nearly nothing), and to segments' partial last tiles.
 #include <type_traits>
 #include <utility>
 
@@ -9,8 +16,8 @@
 namespace moe {
 
 namespace {
-constexpr int kForward = 0, kRows = 1, kWeights = 2;                               // what a kernel computes
-constexpr int kEpiBf16 = 0, kEpiSwiglu = 1, kEpiF32 = 2, kEpiF16 = 3, kEpiSwigluGrad = 6;  // MOE_EPI_*
+constexpr int kForward = 0, kRows = 1, kWeights = 2;                          // what a kernel computes
+constexpr int kEpiSwiglu = 1, kEpiF32 = 2, kEpiF16 = 3, kEpiSwigluGrad = 6;  // MOE_EPI_* (0: bf16)
 
 struct GemmK {  // kernel arguments
   const uint16_t* w;
@@ -26,7 +33,7 @@ struct GemmK {  // kernel arguments
   int splits;  // weights: parts of a segment's rows, each with fp32 sums of its own (out: [splits][E][N][K])
 };
 
-// ------------------------------------------------------------ tiles of 256 x 256
+// ----------------------------------------- tiles of 256 x 256, 128 x 128, 128 x 256
 // out[b][a] = sum_k P[a][k] Q[b][k]: a runs along the output's rows (contiguous),
 // b over them.
 //   forward  a: channels (SwiGLU: 128 gate and the matching 128 up channels), b: rows, k: inputs
@@ -35,6 +42,9 @@ struct GemmK {  // kernel arguments
 // P and Q go through two (or three) LDS stages of 64 k, filled by LDS-DMA.  An operand whose
 // k lie next to each other in memory ("direct") is kept [256][64], one whose a or
 // b do [64][256], read back transposed (ds_read_b64_tr_b16).
+// A wavefront of 256 x 256 reads 12 KB of LDS for 32 products (64 a x 128 b: half of its
+// registers hold sums), of 128 x 128 8 KB for 16; but two workgroups of those a CU cover
+// each other's ends of tiles, and short segments fill them.  The choice: gemm16_path.
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 constexpr int kCUs = 256;
 constexpr uint32_t kOut = ~0u;          // a buffer offset past any buffer: reads zero
@@ -78,9 +88,9 @@ __device__ __forceinline__ void grouped_order(int idx, int tiles, int n_ab, int&
   tile = 8 * g + in % gm;
 }
 
-// A workgroup of 8 wavefronts, alone on its CU, takes tile after tile; a wavefront 64
-// a and up to 128 b of each.  The last two steps of a tile issue the first two of the
-// next one, so that only the first tile waits for its loads, and a tile's stores go
+// A workgroup (256 a: 8 wavefronts, alone on its CU; 128: 4) takes tile after tile, a
+// wavefront 64 a and up to 128 b of each.  The last NS steps of a tile issue the first ones of the
+// next, so that only the first tile waits for its loads, and a tile's stores go
 // out under the next one's products.
 template <int T, int TB, int NS, bool F16, int MODE, bool GATHER, bool GLU>
 __device__ __forceinline__ void tile_loop(const GemmK& p, int epi, int n_ab, int n_bb, char* const (&pS)[NS], char* const (&qS)[NS], char* sE) {
@@ -566,7 +576,7 @@ __global__ __launch_bounds__(2 * T, 2) void tile_kernel(GemmK p, int epi, int n_
 // Few tiles: one workgroup a CU, three stages.  Tiles of 128 x 128, or of 128 a x 256 rows
 // where those of 128 rows would take two rounds, those of 256 one, and no segment has
 // more than 192 (a tile's time goes with its rows): 8 experts of 4096 x 14336 with 110 to 150
-// rows each 217 us, with 128-row tiles 312, with two workgroups a CU 287; by the rows of
+// rows each 217 us, with two workgroups a CU 287 and 128-row tiles; by the rows of
 // 28672 x 4096, 20 to 430 rows each, 567 with 128-row tiles, with 256-row ones 788.
 template <bool F16, int MODE, bool GATHER, bool GLU>
 __global__ __launch_bounds__(256, 1) void deep_kernel(GemmK p, int epi, int n_ab) {
@@ -592,7 +602,9 @@ __global__ __launch_bounds__(256, 1) void deep_kernel(GemmK p, int epi, int n_ab
 // every fourth step of the sum and add their sums through LDS; each keeps four
 // stages of weights of its own (4 KB: 32 channels x 64 inputs, or 32 channels x 64
 // inputs transposed), filled by LDS-DMA three steps ahead, and the rows' part in
-// registers: no barrier before the end.
+// registers: no barrier before the end.  The weights' bytes bound it: one row for each
+// of 8 experts of 2048 x 2048 16 us (4.1 TB/s), by the rows 12.5; 16 rows of one expert of
+// 4096 x 4096 13 us, where tiles of 128 leave most CUs empty (32).
 template <bool F16, int MODE, bool GATHER, bool GLU>
 __device__ __forceinline__ void small_body(const GemmK& p, int epi, int n_cb, char* r0, char* r1, char* r2, char* r3) {
   constexpr int AT = MODE == kForward ? 2 : 4;       // a tiles of 16
@@ -775,7 +787,8 @@ __global__ __launch_bounds__(256, 2) void small_kernel(GemmK p, int epi, int n_c
 #endif
 }
 
-// The weights' gradient from the splits' sums, added in order.
+// The weights' gradient from the splits' sums, added in order: with it 8192 rows of one
+// expert of 64 x 64 take 16 us and not 159, of 2048 x 2048 76 and not 163.
 __global__ __launch_bounds__(256) void splits_kernel(const f32x4* __restrict__ sums, int splits, size_t n4, int epi, void* __restrict__ out) {
   for (size_t i = (size_t)blockIdx.x * 256 + threadIdx.x; i < n4; i += (size_t)gridDim.x * 256) {
     f32x4 v = sums[i];

@@ -216,7 +216,7 @@ struct Gemm16Args {
 // A gathered A has fewer bytes: 4 GiB less a row of the widest (2^20 inputs) on either side.
 constexpr uint32_t kGatherBytes = 0xFFC00000u;
 // Planning (plan.cpp): 0 = few rows, 128 or 256 = tiles of that size, kGemm16Deep = 128 with
-// four stages.  what: 0 forward, 1 rows, 2 weights.
+// three stages.  what: 0 forward, 1 rows, 2 weights.
 constexpr int kGemm16Deep = 129;
 int gemm16_path(int what, int E, int N, int K, int M_total, int kernel);
 // Parts that a weights' gradient splits the rows into (1: none; 128-row tiles only).

@@ -206,14 +206,17 @@ int mxgemm_path(int M_total, int E, int N, int K, bool e2m1, int kernel) {
 // 4096 rows: 101 us in one round of 256, 116 in two of 128).  Forward, us for 128 / 256:
 // 8 experts of 4096 x 4096, 256 rows each 90 / 111; 64 of 2048 x 2048, 128 rows each
 // 135 / 141, 256 rows 180 / 153, 1024 rows 594 / 471.
-// Few rows per expert: the kernel that splits a sum over wavefronts while tiles of 128
-// leave it workgroups to add.  Us for it / tiles of 128, weights from memory: forward, 8 experts
-// with a row of 2048 x 2048 17 / 22, 64 with 16 rows 111 / 123, 48 rows 181 / 127, 8 of 28672 x 4096
-// with 4 rows 392 / 324; by the rows 13 / 22, 118 / 93, 181 / 98, 349 / 402.
-// Tiles of 128 that leave most of the chip's 512 places empty take a CU's LDS for one
-// workgroup, three stages under way and not one: us so / with two workgroups a CU: 8 experts
-// of 4096 x 14336, 128 rows each (256 tiles) 201 / 258, by the rows of 28672 x 4096 334 / 516,
-// one expert of 4096 x 4096, 2048 rows (512 tiles) 67 / 57.
+// Up to 32 rows per expert: the kernel that splits a sum over wavefronts while tiles of 128
+// leave CUs empty.  Us for it / tiles of 128, weights from memory: forward, one expert of
+// 4096 x 4096 with 16 rows (32 tiles) 13 / 32, 16 of 1024 x 2048 (128) 18 / 24, 16 of 2048 x
+// 2048 (256) 31 / 34, 43 of them (688) 76 / 82, 16 of 2048 x 1024 (256) 19 / 17, 8 of 4096 x
+// 4096 (256) 68 / 61, 64 of 2048 x 1024 (1024) 62 / 51; by the rows 16 of 2048 x 1024 (128)
+// 17 / 21, 8 of 4096 x 4096 (256) 55 / 47, 64 of 2048 x 2048 (1024) 109 / 91.
+// Tiles of 128 that leave half of the chip's 512 places empty take a CU's LDS for one
+// workgroup, three stages under way and not two; up to 0.65 of the places where the tiles
+// may be of 256 rows (deep_kernel).  Us so / with two workgroups a CU: 8 experts of 4096 x
+// 4096, 100 rows each 61 / 71, by the rows of 28672 x 4096, 128 rows each 435 / 586, forward
+// 4096 x 14336 221 / 312; but one expert of 4096 x 4096, 1200 rows (320 tiles) 68 / 49.
 int gemm16_path(int what, int E, int N, int K, int M_total, int kernel) {
   if (kernel == 1 && what != 2) return 0;
   if (kernel == 9) return 256;
@@ -222,13 +225,13 @@ int gemm16_path(int what, int E, int N, int K, int M_total, int kernel) {
   for (int i = 0; i < 2; ++i) {
     const int t = i ? 256 : 128;
     const double na = ((what == 0 ? N : K) + t - 1) / t;
-    if (i == 0 && kernel == 0 && what != 2 && M_total <= 32.0 * active && na * active <= (what == 0 ? 1024 : 256)) return 0;
+    if (i == 0 && kernel == 0 && what != 2 && M_total <= 32.0 * active && na * active < 256) return 0;
     // a segment's last tile is partly empty and takes less
     const double nb = what == 2 ? (double)E * ((N + t - 1) / t) : (double)M_total / t + 0.2 * active;
     rounds[i] = na * nb / (i ? 256 : 512);
   }
   const bool wide = kernel == 0 && 1.58 * (rounds[1] > 1.0 ? rounds[1] : 1.0) < 0.9 * (rounds[0] > 1.0 ? rounds[0] : 1.0);
-  return wide ? 256 : what != 2 && rounds[0] <= 0.65 ? kGemm16Deep : 128;
+  return wide ? 256 : what != 2 && rounds[0] <= (M_total <= 160 * active ? 0.65 : 0.5) ? kGemm16Deep : 128;
 }
 
 // Few weights and many rows: enough parts to fill the chip with tiles of 128, each of 8

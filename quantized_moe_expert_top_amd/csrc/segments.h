@@ -7,13 +7,6 @@ namespace moe {
 
 // 16-bit operand type of a kernel: bf16 or fp16.
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
-template <bool F16>
-__device__ __forceinline__ f32x16 mfma32t(u32x4 a, u32x4 b, f32x16 c) {
-  if constexpr (F16)
-    return __builtin_amdgcn_mfma_f32_32x32x16_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
-  else
-    return mfma32(as_bf16x8(a), as_bf16x8(b), c);
-}
 // 16 x 16 x 32: lane l holds row l % 16 (of either operand), k = 8*(l / 16) .. + 7;
 // the accumulator's register r is row 4*(l / 16) + r of the first, column l % 16.
 template <bool F16>
@@ -78,11 +71,11 @@ __device__ __forceinline__ int lane_scan(int v) {
   return v;
 }
 
-// Row tile `idx` of all segments' tiles of TM rows, segment by segment; count:
-// all of them.  false: there are fewer.
+// The segment of row tile `idx` of all segments' tiles of TM rows, segment by segment;
+// count: all of them.  false: there are fewer.
 struct RowTile {
-  int e, r0, s1;   // segment, first row, the segment's end
-  int j, tiles;    // which of the segment's tiles this is, of how many
+  int e, r0, s1;  // segment, its first row and its end
+  int tiles;      // the segment's tiles
 };
 template <int TM>
 __device__ __forceinline__ int segment_tiles(const int32_t* seg, int E, int rows, int e, int& s0, int& s1) {
@@ -117,7 +110,6 @@ __device__ __forceinline__ bool find_tile(const int32_t* seg, int E, int rows, i
     t.r0 = __builtin_amdgcn_readlane(s0, src);
     t.s1 = __builtin_amdgcn_readlane(s1, src);
     idx -= (__builtin_amdgcn_readlane(end, src) - t.tiles) * weight;
-    t.j = 0;
     return true;
   }
   return false;
