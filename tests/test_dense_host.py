@@ -241,3 +241,8 @@ def test_dense_host_layer_under_sanitizers(tmp_path):
     r = subprocess.run([exe], capture_output=True, text=True, env=env, timeout=120)
     assert r.returncode == 0, r.stdout + r.stderr
     assert "dense host layer checks passed" in r.stdout
+
+
+def test_readme_shows_the_tested_calls():
+    from tests.test_gpu_dense import README_CALLS
+    assert "```\n" + README_CALLS + "```" in open(os.path.join(ROOT, "README.md")).read()

@@ -811,3 +811,47 @@ def test_largest_batch_of_the_small_kernels(lib):
     ref, mag = do.adapters(f64(y), f64(x), f64(A), f64(B), ids, f64(scale))
     got = q.moe_adapter_add(y, x, A, B, p.seg_offsets, p.sorted_pair, scale=scale)
     close(f64(got), ref, adapter_bound(ref, f64(y), mag, 40, 128, "bf16", "bf16"))
+
+
+def test_most_tokens(lib):
+    """2^24 - 1 tokens, of eight values each: the combine's gradient and an adapter, values that are exact."""
+    T = (1 << 24) - 1
+    t = torch.arange(T, dtype=torch.int32, device=DEV)
+    v = (t % 251 - 125).to(torch.bfloat16)  # exact in bf16
+    dout = v.view(T, 1).expand(T, 8).contiguous()
+    p = q.Permutation(counts=None, seg_offsets=i32([0, T]), sorted_pair=t, pair_pos=t, workspace=None)
+    g = q.moe_unpermute_combine_grad(dout, dout, p.pair_pos, torch.full((T, 1), 0.5, device=DEV), T, 1)
+    assert torch.equal(g.dy, dout * 0.5) and torch.equal(g.dw.view(-1), 8 * v.float() ** 2)
+    A, B = torch.ones(1, 8, 8, dtype=torch.bfloat16, device=DEV), torch.ones(1, 8, 8, dtype=torch.bfloat16, device=DEV)
+    got = q.moe_adapter_add(dout, dout, A, B, p.seg_offsets, p.sorted_pair)
+    assert torch.equal(got, (65 * v.float()).to(torch.bfloat16).view(T, 1).expand(T, 8))
+
+
+def test_layer_of_no_tokens(lib):
+    x, logits, gu, dn, dout = layer_case(9, 0, 4, 2, 64, 32, "bf16")
+    buf = q.moe_expert_layer_forward(x, logits, 2, gu, dn, keep=True)
+    g = q.moe_expert_layer_backward(dout, x, gu, dn, buf)
+    assert buf.out.shape == g.dx.shape == (0, 64) and g.dlogits.shape == (0, 4)
+    assert g.dgate_up.shape == gu.shape and (g.dgate_up == 0).all() and (g.ddown == 0).all()
+
+
+README_CALLS = """buf = q.moe_expert_layer_forward(x, logits, k, gate_up, down, keep=True)        # [E][2I][H], [E][H][I]; buf.out bf16 [T][H]
+grads = q.moe_expert_layer_backward(dout, x, gate_up, down, buf)                # .dx, .dlogits, .dgate_up, .ddown
+p = q.moe_permute(adapter_ids, n)                                               # int32 [T][1]; -1: no adapter
+q.moe_adapter_add(y, x, A, B, p.seg_offsets, p.sorted_pair, scale=scale, out=y)  # y[t] += scale[a] * B_a (A_a x[t])
+"""
+
+
+def test_calls_of_the_readme(lib):
+    T, E, k, H, I, n, r = 20, 4, 2, 64, 32, 3, 8
+    x, logits, gate_up, down, dout = layer_case(10, T, E, k, H, I, "bf16")
+    ids = [t % 4 - 1 for t in range(T)]
+    _, y, A, B, scale, _ = adapter_batch(3, ids, n, r, H, 40, "bf16", "bf16")
+    names = dict(q=q, x=x, logits=logits, k=k, gate_up=gate_up, down=down, dout=dout, n=n, A=A, B=B, scale=scale, y=y.clone(),
+                 adapter_ids=i32(ids).view(T, 1))
+    exec(README_CALLS, names)
+    (out, (dx, *_)) = layer_reference(x, logits, gate_up, down, k, dout)
+    rel = lambda got, ref: np.linalg.norm(f64(got) - ref) / np.linalg.norm(ref)  # noqa: E731
+    assert rel(names["buf"].out, out) <= 3 * HALF["bf16"] + HALF["fp16"] and rel(names["grads"].dx, dx) <= 6 * HALF["bf16"]
+    ref, mag = do.adapters(f64(y), f64(x), f64(A), f64(B), ids, f64(scale))
+    close(f64(names["y"]), ref, adapter_bound(ref, f64(y), mag, H, r, "bf16", "bf16"))
