@@ -11,11 +11,11 @@
 // and both added in fp32: one would round v to 8 bits (bf16), as much as the
 // output's own rounding.
 // Bytes bound long batches: y in, out, x and the adapters.  4096 tokens, 4096 to
-// 14336, rank 32, 16 adapters, y and out in bf16, us: 72 (288 MB, 4.0 TB/s; a copy of
+// 14336, rank 32, 16 adapters, y and out in bf16, us: 73 (288 MB, 3.9 TB/s; a copy of
 // them 55); with 32 tokens a workgroup 129, with single steps of the first product (a
-// line of x fetched by two wavefronts) and one chunk under way 78.  Latency bounds few
-// tokens: a chain of seven dependent accesses, 12 us for 32 tokens of 16 adapters of rank 16, 4096 to 4096, 6
-// of them the first product's.
+// line of x fetched by two wavefronts) and one chunk under way 78; rank 16 57, with one
+// chunk under way 82.  Latency bounds few tokens: a chain of dependent accesses, 10.4 us
+// for 32 tokens of 16 adapters of rank 16, 4096 to 4096, 6 of them the first product's.
 #include "segments.h"
 
 namespace moe {
@@ -94,7 +94,8 @@ __global__ __launch_bounds__(64 * waves(NR), NR <= 2 ? 4 : 2) void adapter_kerne
   constexpr int D = NR <= 4 ? 2 : 1;  // chunks under way, while the first product is worked out too
   Chunk ring[D];
 #pragma unroll
-  for (int u = 0; u < D; ++u) ring[u] = fetch(c0 + wv + W * u);
+  for (int u = 0; u < D; ++u)
+    if (u == 0 || c0 + wv + W * u < c1) ring[u] = fetch(c0 + wv + W * u);
 
   if (!none) {
     // First product: wavefront wv takes pairs wv, wv + W, ... of steps of 32 inputs, a
@@ -117,7 +118,11 @@ __global__ __launch_bounds__(64 * waves(NR), NR <= 2 ? 4 : 2) void adapter_kerne
     f32x4 acc[NR][NB] = {};
     Step s[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) s[u] = load(64 * (wv + W * (u >> 1)) + 32 * (u & 1));
+    for (int u = 0; u < U; ++u) {
+      // (in the order of their use, which the loop's waits count on: 77 us without, 73 so)
+      s[u] = load(64 * (wv + W * (u >> 1)) + 32 * (u & 1));
+      __builtin_amdgcn_sched_barrier(0);
+    }
     for (int k0 = 64 * wv; k0 < a.K; k0 += 32 * W * U) {
 #pragma unroll
       for (int u = 0; u < U; ++u) {
@@ -196,12 +201,13 @@ __global__ __launch_bounds__(64 * waves(NR), NR <= 2 ? 4 : 2) void adapter_kerne
             }
           }
         }
-        if (r0 + RI * i + lane / LR < t.s1 && ch < a.N && c < c1)
+        if (r0 + RI * i + lane / LR < t.s1 && ch < a.N)
           *reinterpret_cast<u32x4*>(static_cast<char*>(a.out) + ((size_t)row_tok[i] * a.N + ch) * ES) = o;
       }
     }
   };
-  for (int c = c0 + wv; c < c1; c += W * D) {
+  int c = c0 + wv;
+  for (; c + W * (2 * D - 1) < c1; c += W * D) {
 #pragma unroll
     for (int u = 0; u < D; ++u) {
       chunk(ring[u], c + W * u);
@@ -209,6 +215,14 @@ __global__ __launch_bounds__(64 * waves(NR), NR <= 2 ? 4 : 2) void adapter_kerne
       ring[u] = fetch(c + W * (D + u));
       __builtin_amdgcn_sched_barrier(0);
     }
+  }
+  // The last 2 D - 1 at most, apart: branches around the loop's loads would cost its waits
+  // their counts (4096 tokens: 4 %), loads of chunks that nobody uses 32 tokens 8 %.
+#pragma unroll
+  for (int u = 0; u < 2 * D - 1; ++u) {
+    if (c + W * u >= c1) return;
+    chunk(ring[u % D], c + W * u);
+    if (u + D < 2 * D - 1 && c + W * (u + D) < c1) ring[u] = fetch(c + W * (u + D));
   }
 }
 
