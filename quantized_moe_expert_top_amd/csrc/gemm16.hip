@@ -51,8 +51,11 @@ constexpr uint32_t kOut = ~0u;          // a buffer offset past any buffer: read
 constexpr uint32_t kLastGather = kGatherBytes;  // the same for a gathered row, also with a column added
 constexpr uint32_t kDrop = 0x80000000u;  // past any output tile, also with a row added: not stored
 
-// [256][64] of 16 bits in 16-byte chunks, 8 a row: chunk c of row r at place c ^ swz(r).
-__device__ __forceinline__ int swz(int row) { return (row & 7) ^ ((row >> 3) & 1); }
+// [256][64] of 16 bits in 16-byte chunks, 8 a row: chunk c of row r at place c ^ swz(r).  A read
+// of 16 rows' 4 chunks takes lanes 0-3, 12-15, 20-23 and 24-27 at a time, 4-11, 16-19 and 28-31,
+// and the same of the upper half: with this order each group covers all 64 banks (with bit 3 of
+// the row mixed in too, as 16 lanes in a row would want it, every bank came twice).
+__device__ __forceinline__ int swz(int row) { return row & 7; }
 
 // [64][256] of 16 bits in 32-byte units, 16 a row: unit u of row k at place u ^ tswz(k): the
 // four rows of a transposing read's 16 lanes and the eight of 32 lanes fall on different banks.
@@ -155,11 +158,12 @@ __device__ __forceinline__ void tile_loop(const GemmK& p, int epi, int n_ab, int
   };
 
   // The DMAs of a tile: a wavefront fetches 4 KB of P and QD of Q a step, 1 KB each;
-  // DMAs i and i + 2 differ by a fixed number of bytes (not where rows are gathered).
+  // DMAs i and i + 2 (direct operands: i and i + 1) differ by a fixed number of bytes (not
+  // where rows are gathered).
   // Rows past an operand's end lie past the descriptor's bytes and read zero.
-  constexpr int QO = GATHER && MODE == kForward ? QD : 2;
-  uint32_t po[2], qo[QO];                 // byte offsets of this lane's 16 bytes, or kOut
-  int pk = 0, qk = 0;                     // direct operands: first k of the lane's chunk in even DMAs (odd: ^ 8)
+  constexpr int QO = GATHER && MODE == kForward ? QD : QT ? 2 : 1;
+  uint32_t po[PT ? 2 : 1], qo[QO];        // byte offsets of this lane's 16 bytes, or kOut
+  int ck8 = 0;                            // direct operands: first k of the lane's chunk
   const uint16_t *pbase = p.w, *qbase = p.w;
   uint32_t pbytes = 0, qbytes = 0;
   int red = 0, ls0 = 0, ls1 = 0;
@@ -208,10 +212,8 @@ __device__ __forceinline__ void tile_loop(const GemmK& p, int epi, int n_ab, int
     } else {
       // SwiGLU: rows 64w .. 64w + 31 are gate channels of wavefront column w, 64w + 32 .. 64w + 63
       // their up channels (past the last gate channel: up ones, never stored)
-      pk = qk = 8 * ck;
       const int ch = GLU ? T / 2 * c.ab + 32 * (wv >> 1) + (lane >> 3) + (wv & 1 ? I : 0) : T * c.ab + br;
-#pragma unroll
-      for (int i = 0; i < 2; ++i) po[i] = ((uint32_t)(ch + 8 * i) * (uint32_t)p.K + 8 * (ck ^ i)) * 2;
+      po[0] = ((uint32_t)ch * (uint32_t)p.K + 8 * ck) * 2;
       pbase = p.w + (size_t)c.e * p.N * p.K;
       pbytes = (uint32_t)((size_t)p.N * p.K * 2);
     }
@@ -224,12 +226,12 @@ __device__ __forceinline__ void tile_loop(const GemmK& p, int epi, int n_ab, int
       qbase = p.dy + (size_t)c.s0 * p.N;
     } else {
       const int ld = MODE == kForward ? p.K : p.N;
-      qk = 8 * ck;
+      ck8 = 8 * ck;
 #pragma unroll
       for (int i = 0; i < QO; ++i) {
         const int r = bq + 8 * i;
         const uint32_t from = GATHER ? (uint32_t)__shfl((int)token(pair), 8 * i + (lane >> 3), 64) : r;
-        qo[i] = (from * (uint32_t)ld + 8 * (ck ^ (i & 1))) * 2;
+        qo[i] = (from * (uint32_t)ld + 8 * ck) * 2;
         if (GATHER && c.b0 + r >= c.s1) qo[i] = kOut;
       }
       qbase = MODE == kForward ? (GATHER ? p.a : p.a + (size_t)c.b0 * ld) : p.dy + (size_t)c.b0 * ld;
@@ -272,9 +274,9 @@ __device__ __forceinline__ void tile_loop(const GemmK& p, int epi, int n_ab, int
       for (int i = 0; i < 4; ++i) dma(pr, pd + 1024 * i, po[twin(i)], second(i) ? 8u * (uint32_t)na : 0u);
     } else {
       const rsrc_t pr = scalar_rsrc(pbase, pbytes);
-      const uint32_t even = pk < left ? po[0] : kOut, odd = (pk ^ 8) < left ? po[1] : kOut;
+      const uint32_t at = ck8 < left ? po[0] : kOut;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) dma(pr, pd + 1024 * i, i & 1 ? odd : even, i < 2 ? adv : adv + 32u * (uint32_t)p.K);
+      for (int i = 0; i < 4; ++i) dma(pr, pd + 1024 * i, at, adv + (uint32_t)i * 16u * (uint32_t)p.K);
     }
     if constexpr (QT) {
       const rsrc_t qr = scalar_rsrc(qbase + (size_t)(64 * st) * p.N, rows * (2u * (uint32_t)p.N));
@@ -285,8 +287,7 @@ __device__ __forceinline__ void tile_loop(const GemmK& p, int epi, int n_ab, int
       const int ld = MODE == kForward ? p.K : p.N;
 #pragma unroll
       for (int i = 0; i < QD; ++i)
-        dma(qr, qd + 1024 * i, (i & 1 ? qk ^ 8 : qk) < left ? qo[QO == QD ? i : i & 1] : kOut,
-            QO == QD ? adv : adv + (uint32_t)(i >> 1) * 32u * (uint32_t)ld);
+        dma(qr, qd + 1024 * i, ck8 < left ? qo[QO == QD ? i : 0] : kOut, QO == QD ? adv : adv + (uint32_t)i * 16u * (uint32_t)ld);
     }
   };
 
@@ -621,13 +622,13 @@ __device__ __forceinline__ void small_body(const GemmK& p, int epi, int n_cb, ch
 
   // this lane's part of a step's four DMAs, and its rows
   uint32_t po[4];
-  int ck[2] = {0, 0};
+  int ck = 0;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int r = 8 * i + (lane >> 3);
     if constexpr (MODE == kForward) {
       const int c = (lane & 7) ^ swz(r);
-      if (i < 2) ck[i] = 8 * c;
+      ck = 8 * c;  // (the same in every DMA)
       const int ch = GLU ? (i < 2 ? 16 * cb + r : I + 16 * cb + r - 16) : 32 * cb + r;
       po[i] = ((uint32_t)ch * (uint32_t)p.K + 8 * c) * 2;  // past the last channel: past the weights
     } else {
@@ -657,7 +658,7 @@ __device__ __forceinline__ void small_body(const GemmK& p, int epi, int n_cb, ch
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         __builtin_amdgcn_raw_ptr_buffer_load_lds(pr, (__attribute__((address_space(3))) void*)(ring[S] + 1024 * i), 16,
-                                                 ck[i & 1] < left ? po[i] : kOut, adv, 0, 0);
+                                                 ck < left ? po[i] : kOut, adv, 0, 0);
     } else {
       const rsrc_t pr = scalar_rsrc(w + (size_t)(left > 0 ? k0 : 0) * p.K, (uint32_t)max(min(left, 32), 0) * (2u * (uint32_t)p.K));
 #pragma unroll
