@@ -2,10 +2,10 @@
 // the rows and by the weights, on v_mfma_f32_16x16x32 (bf16 or fp16 operands,
 // fp32 sums): the matrix units run at the power limit, and random operands cost less
 // in this shape than in 32 x 32 x 16 (from registers alone 1978 and 1695 TFLOP/s; the
-// tiles below, 8192^3: 760 and 831 us).
-// Measured (bf16, random operands): 8192^3 759 us (1449 TFLOP/s), by the rows 769, by
-// the weights 767.  64 experts of 2048 x 2048, 65536 rows gathered, SwiGLU and what
-// enters it 534 us (1029); by the weights 535.  The rest goes to stores: all
+// tiles below at first, 8192^3: 760 and 831 us).
+// Measured (bf16, random operands): 8192^3 749 us (1468 TFLOP/s), by the rows 755, by
+// the weights 762.  64 experts of 2048 x 2048, 65536 rows gathered, SwiGLU and what
+// enters it 527 us (1044); by the weights 535.  The rest goes to stores: all
 // workgroups' tiles end at about the same time and wait for the memory (a quarter of
 // them storing costs nearly nothing), and to segments' partial last tiles.
 #include <type_traits>
@@ -54,7 +54,8 @@ constexpr uint32_t kDrop = 0x80000000u;  // past any output tile, also with a ro
 // [256][64] of 16 bits in 16-byte chunks, 8 a row: chunk c of row r at place c ^ swz(r).  A read
 // of 16 rows' 4 chunks takes lanes 0-3, 12-15, 20-23 and 24-27 at a time, 4-11, 16-19 and 28-31,
 // and the same of the upper half: with this order each group covers all 64 banks (with bit 3 of
-// the row mixed in too, as 16 lanes in a row would want it, every bank came twice).
+// the row mixed in too, as 16 lanes in a row would want it, every bank came twice: 8192^3 760 us
+// and not 749).
 __device__ __forceinline__ int swz(int row) { return row & 7; }
 
 // [64][256] of 16 bits in 32-byte units, 16 a row: unit u of row k at place u ^ tswz(k): the
