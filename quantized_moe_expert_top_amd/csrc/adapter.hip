@@ -7,9 +7,11 @@
 // neighbouring channels of one token.  A lane's register of tile i stands for
 // channel 16*(lane / 16) + 4*i + register of the chunk: 16 neighbouring channels
 // over the chunk's four tiles, 32 bytes in a row.
-// v goes to the second product as hi + lo, two 16-bit numbers, each multiplied
-// and both added in fp32: one would round v to 8 bits (bf16), as much as the
-// output's own rounding.
+// v keeps fp32's 24 bits and range: it goes to the second product as three bf16
+// numbers, B's fp16 numbers as two, all exact, and their products are added in fp32
+// (bf16 products for either type: fp16 parts of v would end at 65504 and at 2^-24).
+// Three parts cost bf16 nothing that shows, two of B cost fp16: 4096 tokens, 4096 to 14336,
+// ranks 16, 32, 64 and 128, us: 57, 74, 151, 246 in bf16, 64, 76, 161, 316 in fp16.
 // Bytes bound long batches: y in, out, x and the adapters.  4096 tokens, 4096 to
 // 14336, rank 32, 16 adapters, y and out in bf16, us: 73 (288 MB, 3.9 TB/s; a copy of
 // them 55); with 32 tokens a workgroup 129, with single steps of the first product (a
@@ -24,6 +26,50 @@ namespace {
 constexpr int kWorkgroups = 256;
 // Tiles of 16 tokens of a workgroup.
 constexpr int token_tiles(int nr) { return nr <= 2 ? 1 : 2; }
+// v = high + rest, high a bf16 number of v's sign that is nearer to zero.  Exact: rest has
+// 8 bits fewer than v (three parts hold fp32's 24 bits, two fp16's 11).  Neither part is zero
+// unless v is, so that an infinity which meets v meets numbers of v's sign; an infinite v has
+// the largest number for high and is itself the rest.
+struct Parts {
+  float high, rest;
+};
+__device__ __forceinline__ Parts cut_bf16(float v) {
+  // the next fp32 number towards zero (v - v * 2^-24, rounded), without its last 16 bits
+  const float below = __builtin_amdgcn_fmed3f(v, -0x1.fffffep127f, 0x1.fffffep127f) * 0x1.fffffep-1f;
+  const float high = __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, below) & 0xFFFF0000u);
+  return {high, v - high};
+}
+// Two floats that are bf16 numbers (their last 16 bits zero), as a pair.
+__device__ __forceinline__ uint32_t pair_bf16(float lo, float hi) {
+  return __builtin_amdgcn_perm(__builtin_bit_cast(uint32_t, hi), __builtin_bit_cast(uint32_t, lo), 0x07060302u);
+}
+// Eight of B's numbers as bf16 ones: themselves, or for fp16 high parts and rests of the numbers
+// times 2^-15, for which the sums make up.  Parts as of cut_bf16, in 8 instructions a pair where
+// that takes 12 (4096 tokens, 4096 to 14336, us: rank 16 66, rank 128 330): finite numbers are
+// below 2 then, the top bit of their exponent is 0, and an infinite one's is masked off.
+constexpr float kScaleB = 0x1p-15f;
+__device__ __forceinline__ Parts cut_f16(_Float16 v) {
+  const float below = __builtin_fmaf((float)v, kScaleB * 0x1.fffffep-1f, 0.0f);
+  const float high = __builtin_bit_cast(float, __builtin_bit_cast(uint32_t, below) & 0xBFFF0000u);
+  return {high, __builtin_fmaf((float)v, kScaleB, -high)};
+}
+template <bool F16>
+__device__ __forceinline__ void split_b(u32x4 b, u32x4 (&to)[F16 ? 2 : 1]) {
+  if constexpr (F16) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+      const uint32_t x = b[q];
+      const f16x2 v = __builtin_bit_cast(f16x2, x);
+      const Parts l = cut_f16(v[0]), h = cut_f16(v[1]);
+      to[0][q] = pair_bf16(l.high, h.high);
+      to[1][q] = pair_bf16(l.rest, h.rest);
+    }
+  } else {
+    to[0] = b;
+  }
+}
+
 // Wavefronts of a workgroup: the sums that they exchange take 2 KB of LDS each and tile of 16 ranks.
 constexpr int waves(int nr) { return nr <= 4 ? 8 : 4; }
 
@@ -43,7 +89,7 @@ __global__ __launch_bounds__(64 * waves(NR), NR <= 2 ? 4 : 2) void adapter_kerne
   constexpr int RED = W * NR * NB * 64 > W * 256 ? W * NR * NB * 64 : W * 256;
   __shared__ f32x4 lds[RED];
   auto red = [&](int w, int i, int b) { return lds + ((w * NR + i) * NB + b) * 64; };
-  __shared__ __attribute__((aligned(16))) uint16_t vh[kTM][RP + 8], vl[kTM][RP + 8];
+  __shared__ __attribute__((aligned(16))) uint16_t parts[3][kTM][RP + 8];  // of v
   const int lane = threadIdx.x & 63, wv = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
   const int col = lane & 15, quad = lane >> 4;
   int idx = blockIdx.x;
@@ -147,15 +193,17 @@ __global__ __launch_bounds__(64 * waves(NR), NR <= 2 ? 4 : 2) void adapter_kerne
       if (4 * c < a.r)  // (a padding rank: 0, also where x is infinite and 0 * x is not)
 #pragma unroll
         for (int w = 0; w < W; ++w) v += red(w, c >> 2, row >> 4)[16 * (c & 3) + (row & 15)];
-      uint16_t hi[4], lo[4];
+      f32x4 part[3];
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        hi[i] = round16<F16>(v[i]);
-        const float rest = v[i] - widen16<F16>(hi[i]);
-        lo[i] = fabsf(rest) < INFINITY ? round16<F16>(rest) : (uint16_t)0;  // (hi is then infinite or NaN and stays it)
+        const Parts first = cut_bf16(v[i]), second = cut_bf16(first.rest);
+        part[0][i] = first.high;
+        part[1][i] = second.high;
+        part[2][i] = second.rest;
       }
-      *reinterpret_cast<u32x2*>(&vh[row][4 * c]) = u32x2{hi[0] | (uint32_t)hi[1] << 16, hi[2] | (uint32_t)hi[3] << 16};
-      *reinterpret_cast<u32x2*>(&vl[row][4 * c]) = u32x2{lo[0] | (uint32_t)lo[1] << 16, lo[2] | (uint32_t)lo[3] << 16};
+#pragma unroll
+      for (int k = 0; k < 3; ++k)
+        *reinterpret_cast<u32x2*>(&parts[k][row][4 * c]) = u32x2{pair_bf16(part[k][0], part[k][1]), pair_bf16(part[k][2], part[k][3])};
     }
     __syncthreads();
   }
@@ -164,14 +212,25 @@ __global__ __launch_bounds__(64 * waves(NR), NR <= 2 ? 4 : 2) void adapter_kerne
     f32x4 d[4][NB] = {};
     if (!none) {
 #pragma unroll
-      for (int s = 0; s < RP / 32; ++s)
+      for (int s = 0; s < RP / 32; ++s) {
+        u32x4 v[3][NB];
 #pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          const u32x4 h = *reinterpret_cast<const u32x4*>(&vh[16 * b + col][32 * s + 8 * quad]);
-          const u32x4 l = *reinterpret_cast<const u32x4*>(&vl[16 * b + col][32 * s + 8 * quad]);
+        for (int q = 0; q < 3; ++q)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) d[i][b] = mfma16t<F16>(k.b[s][i], h, mfma16t<F16>(k.b[s][i], l, d[i][b]));
+          for (int b = 0; b < NB; ++b) v[q][b] = *reinterpret_cast<const u32x4*>(&parts[q][16 * b + col][32 * s + 8 * quad]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          constexpr int BP = F16 ? 2 : 1;
+          u32x4 w[BP];
+          split_b<F16>(k.b[s][i], w);
+#pragma unroll
+          for (int q = 2; q >= 0; --q)
+#pragma unroll
+            for (int x = BP - 1; x >= 0; --x)
+#pragma unroll
+              for (int b = 0; b < NB; ++b) d[i][b] = mfma16t<false>(w[x], v[q][b], d[i][b]);
         }
+      }
     }
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
@@ -184,7 +243,10 @@ __global__ __launch_bounds__(64 * waves(NR), NR <= 2 ? 4 : 2) void adapter_kerne
         const int r = RI * i - 16 * b + lane / LR, ch = 64 * c + V * (lane % LR);
         f32x4 v[V / 4];
 #pragma unroll
-        for (int q = 0; q < V / 4; ++q) v[q] = at[r * 16 + ((V / 4 * (lane % LR) + q) ^ r)];
+        for (int q = 0; q < V / 4; ++q) {
+          v[q] = at[r * 16 + ((V / 4 * (lane % LR) + q) ^ r)];
+          if constexpr (F16) v[q] *= 1.0f / kScaleB;
+        }
         u32x4 o = k.y[i];
         if (!none) {
           if constexpr (YT == 1) {
