@@ -11,6 +11,7 @@
 #include <type_traits>
 #include <utility>
 
+#include "offsets.h"
 #include "segments.h"
 
 namespace moe {
@@ -47,8 +48,7 @@ struct GemmK {  // kernel arguments
 // each other's ends of tiles, and short segments fill them.  The choice: gemm16_path.
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 constexpr int kCUs = 256;
-constexpr uint32_t kOut = ~0u;          // a buffer offset past any buffer: reads zero
-constexpr uint32_t kLastGather = kGatherBytes;  // the same for a gathered row, also with a column added
+constexpr uint32_t kLastGather = kGatherBytes;  // kOut's part for a gathered row, also with a column added
 constexpr uint32_t kDrop = 0x80000000u;  // past any output tile, also with a row added: not stored
 
 // [256][64] of 16 bits in 16-byte chunks, 8 a row: chunk c of row r at place c ^ swz(r).  A read
@@ -214,7 +214,7 @@ __device__ __forceinline__ void tile_loop(const GemmK& p, int epi, int n_ab, int
       // SwiGLU: rows 64w .. 64w + 31 are gate channels of wavefront column w, 64w + 32 .. 64w + 63
       // their up channels (past the last gate channel: up ones, never stored)
       const int ch = GLU ? T / 2 * c.ab + 32 * (wv >> 1) + (lane >> 3) + (wv & 1 ? I : 0) : T * c.ab + br;
-      po[0] = ((uint32_t)ch * (uint32_t)p.K + 8 * ck) * 2;
+      po[0] = row_offset(ch, p.N, p.K, 8 * ck);
       pbase = p.w + (size_t)c.e * p.N * p.K;
       pbytes = (uint32_t)((size_t)p.N * p.K * 2);
     }
@@ -267,7 +267,7 @@ __device__ __forceinline__ void tile_loop(const GemmK& p, int epi, int n_ab, int
         } else {
           at = (uint32_t)__shfl((int)from, 4 * i + (l >> 4), 64);
         }
-        dma(pr, pd + 1024 * i, po[twin(i)] == kOut ? kOut : at + po[twin(i)], 0);
+        dma(pr, pd + 1024 * i, offset_sum(po[twin(i)], at), 0);
       }
     } else if constexpr (PT) {
       const rsrc_t pr = scalar_rsrc(pbase + (size_t)(64 * st) * na, rows * (2u * (uint32_t)na));
@@ -631,19 +631,21 @@ __device__ __forceinline__ void small_body(const GemmK& p, int epi, int n_cb, ch
       const int c = (lane & 7) ^ swz(r);
       ck = 8 * c;  // (the same in every DMA)
       const int ch = GLU ? (i < 2 ? 16 * cb + r : I + 16 * cb + r - 16) : 32 * cb + r;
-      po[i] = ((uint32_t)ch * (uint32_t)p.K + 8 * c) * 2;  // past the last channel: past the weights
+      po[i] = row_offset(ch, p.N, p.K, 8 * c);
     } else {
       const int ch = 64 * cb + 8 * (((((lane >> 1) & 3) ^ tswz4(r)) << 1) + (lane & 1));
       po[i] = ch < p.K ? ((uint32_t)r * (uint32_t)p.K + ch) * 2 : kOut;
     }
   }
-  uint32_t qo[2];
+  uint32_t qo[2][SUB];
 #pragma unroll
   for (int x = 0; x < 2; ++x) {
     const int r = 16 * x + col;
     uint32_t from = r;
     if constexpr (GATHER) from = (uint32_t)min(max(p.div(p.gather[min(b0 + r, s1 - 1)]), 0), p.A_rows - 1);
-    qo[x] = b0 + r < s1 ? (from * (uint32_t)red + 8 * quad) * 2 : kOut;
+    const uint32_t first = b0 + r < s1 ? (from * (uint32_t)red + 8 * quad) * 2 : kOut;
+#pragma unroll
+    for (int u = 0; u < SUB; ++u) qo[x][u] = offset_sum(first, 64 * u);
   }
   const uint16_t* const rows = MODE == kForward ? p.a : p.dy;
   const rsrc_t qr = scalar_rsrc(GATHER ? rows : rows + (size_t)b0 * red,
@@ -669,7 +671,7 @@ __device__ __forceinline__ void small_body(const GemmK& p, int epi, int n_cb, ch
 #pragma unroll
     for (int x = 0; x < 2; ++x)
 #pragma unroll
-      for (int u = 0; u < SUB; ++u) q[S][x][u] = buf_x4(qr, 32 * u + 8 * quad < left ? qo[x] + 64 * u : kOut, adv);
+      for (int u = 0; u < SUB; ++u) q[S][x][u] = buf_x4(qr, 32 * u + 8 * quad < left ? qo[x][u] : kOut, adv);
   };
   f32x4 acc[AT][2] = {};
   auto multiply = [&](auto slot_tag) {
