@@ -281,7 +281,7 @@ def moe_expert_layer_backward(dout: torch.Tensor, x: torch.Tensor, gate_up: torc
                               buf: ExpertLayerBuffers, grad_dtype: torch.dtype = torch.float32, stream=None,
                               kernel: int = MOE_KERNEL_AUTO) -> ExpertLayerGrads:
     """Gradients of moe_expert_layer_forward from its output's (dout bf16 [T][H]), with the buffers that it kept: by x
-    (the k experts' shares added in fp32, bf16), the logits, and both weights (grad_dtype).  The routing's choice is
+    (the k experts' fp32 shares added in fp32, then bf16), the logits, and both weights (grad_dtype).  The routing's choice is
     taken as given, as everywhere; down's gradient sees the experts' outputs as the forward pass rounded them."""
     T, E, k, H, I = buf.sizes
     if _layer_sizes(x, E, k, gate_up, down) != buf.sizes:
@@ -302,7 +302,8 @@ def moe_expert_layer_backward(dout: torch.Tensor, x: torch.Tensor, gate_up: torc
     dpre = moe_grouped_gemm_grad_rows(down, c.dy, p.seg_offsets, P, MOE_EPI_SWIGLU_GRAD, pre=buf.pre, kernel=kernel)
     dgate_up = moe_grouped_gemm_grad_weights(dpre, x, p.seg_offsets, E, P, epi, gather_pair=p.sorted_pair, k=k,
                                              kernel=kernel)
-    dx = moe_grouped_gemm_grad_rows(gate_up, dpre, p.seg_offsets, P, _DTYPE_EPI[x.dtype], kernel=kernel)
+    # the shares stay in fp32 up to their sum: 16 bits would round each, and fp16 ends at 65504
+    dx = moe_grouped_gemm_grad_rows(gate_up, dpre, p.seg_offsets, P, MOE_EPI_NONE_F32, kernel=kernel)
     dx = moe_unpermute_combine(dx, p.pair_pos, None, T, k, n_valid=p.seg_offsets[-1:])
     return ExpertLayerGrads(dx, c.dlogits, dgate_up, ddown)
 

@@ -38,3 +38,52 @@ def test_weights_just_below_4_gib(lib, kernel):
     ref = f64(dy[:, at]).T @ f64(a[:, cols])
     mag = np.abs(f64(dy[:, at])).T @ np.abs(f64(a[:, cols]))
     close(f64(dw[0][at][:, cols]), ref, bound(ref, mag, M, "bf16"))
+
+
+def layer(seed, T, E, k, H, I, dt, size=1.0):
+    r = np.random.default_rng(seed)
+    mk = lambda *s: torch.from_numpy(r.standard_normal(s)).to(DEV)  # noqa: E731
+    return (mk(T, H).to(dt), mk(T, E).float(), (mk(E, 2 * I, H) / H ** 0.5 * size).to(dt),
+            (mk(E, H, I) / I ** 0.5).to(dt), mk(T, H).bfloat16())
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("T,E,k,H,I", [(3, 4, 3, 64, 32), (70, 12, 8, 136, 48)])
+def test_shares_of_dx_are_added_unrounded(lib, dt, T, E, k, H, I):
+    """dx rounds once: the k experts' fp32 shares, added in fp32 in the slots' order, to bf16."""
+    x, logits, gu, dn, dout = layer(1, T, E, k, H, I, dt)
+    buf = q.moe_expert_layer_forward(x, logits, k, gu, dn, keep=True)
+    g = q.moe_expert_layer_backward(dout, x, gu, dn, buf)
+    p, P = buf.perm, T * k
+    c = q.moe_unpermute_combine_grad(dout, buf.y_perm, p.pair_pos, buf.w, T, k, dtype=dt)
+    dpre = q.moe_grouped_gemm_grad_rows(dn, c.dy, p.seg_offsets, P, q.MOE_EPI_SWIGLU_GRAD, pre=buf.pre)
+    share = q.moe_grouped_gemm_grad_rows(gu, dpre, p.seg_offsets, P, q.MOE_EPI_NONE_F32)
+    ref = f64(share)[p.pair_pos.cpu().numpy().reshape(T, k)]
+    # an fp32 addition is off by 2^-24 of each partial sum; bf16 rounds once, to at most half a step
+    mag = np.abs(ref).sum(1)
+    close(f64(g.dx), ref.sum(1), 2.0 ** -8 * np.abs(ref.sum(1)) + (1 + 2.0 ** -8) * k * 2.0 ** -24 * mag)
+
+
+def test_shares_of_dx_past_fp16s_range(lib):
+    """Shares of dx above 65504, dx itself in bf16: finite, near the float64 gradient."""
+    T, E, k, H, I = 6, 2, 2, 64, 32
+    x, logits, gu, dn, dout = layer(2, T, E, k, H, I, torch.float16, size=64.0)
+    x = x / 64
+    dout = (dout.float() * 2048).bfloat16()
+    buf = q.moe_expert_layer_forward(x, logits, k, gu, dn, keep=True)
+    g = q.moe_expert_layer_backward(dout, x, gu, dn, buf)
+    v = x.double().cpu().requires_grad_()
+    gate = torch.softmax(logits.double().cpu().gather(1, buf.ids.long().cpu()), -1)
+    rows = []
+    for t in range(T):
+        s = 0.0
+        for j in range(k):
+            e = int(buf.ids[t, j])
+            y = gu[e].double().cpu() @ v[t]
+            s = s + gate[t, j] * (dn[e].double().cpu() @ (torch.nn.functional.silu(y[:I]) * y[I:]))
+        rows.append(s)
+    (torch.stack(rows) * dout.double().cpu()).sum().backward()
+    ref = v.grad.numpy()
+    assert np.abs(ref).max() > 2 * 65504
+    # roundings of h, y, dy, pre (its effect at most doubled) and dpre to fp16, of dx to bf16, in L2
+    assert np.linalg.norm(f64(g.dx) - ref) <= (6 * 2.0 ** -11 + 2.0 ** -8) * np.linalg.norm(ref)
