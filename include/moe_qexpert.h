@@ -404,7 +404,9 @@ moe_status moe_unpermute_combine(const void* y_perm, int32_t y_dtype, const int3
  *               not written (nor read, in the gradients)
  *   M_total     host upper bound of the rows, fewer than 2^30; out, dy and pre have M_total rows
  *               (without gather_pair A has at least as many)
- *   kernel      MOE_KERNEL_AUTO, or MOE_KERNEL_SMALL (not grad_weights), _TILE128 or _TILE256
+ *   kernel      MOE_KERNEL_AUTO, or MOE_KERNEL_SMALL (not grad_weights), _TILE128 or _TILE256;
+ *               MOE_KERNEL_SMALL with fewer than 2^24 tiles of 32 rows by 32 channels (grad_rows:
+ *               64 inputs), a partial one per segment counted in (else MOE_ERR_UNSUPPORTED)
  *   workspace   grad_weights: moe_grouped_gemm_grad_weights_workspace_size(...) bytes of
  *               device memory (fp32 partial sums where a few experts' rows are split
  *               over workgroups; 0, NULL allowed, for most sizes); nothing in it

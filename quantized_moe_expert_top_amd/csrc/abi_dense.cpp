@@ -41,6 +41,12 @@ moe_status check_sizes(int32_t dtype, int32_t E, int32_t N, int32_t K, int32_t M
   return check_kernel(kernel, small);
 }
 
+// The kernel for few rows is chosen for many only by the caller.
+moe_status check_small(int what, int32_t E, int32_t N, int32_t K, int32_t M_total, int32_t kernel) {
+  if (kernel != MOE_KERNEL_SMALL || moe::gemm16_small_workgroups(what, E, N, K, M_total) < moe::kGemm16MostSmall) return MOE_OK;
+  return fail(MOE_ERR_UNSUPPORTED, "M_total=%d: 2^24 or more tiles of 32 rows with MOE_KERNEL_SMALL", M_total);
+}
+
 moe_status check_rows(int32_t K, int32_t A_rows, const int32_t* gather_pair, int32_t k, int32_t M_total) {
   if (A_rows < 0) return fail(MOE_ERR_BAD_SHAPE, "A_rows=%d < 0", A_rows);
   if (gather_pair) {
@@ -68,6 +74,8 @@ moe_status moe_grouped_gemm(const void* w, int32_t dtype, int32_t E, int32_t N, 
     return fail(MOE_ERR_UNSUPPORTED, "N=%d must be a multiple of 16 with a SwiGLU epilogue", N);
   st = check_rows(K, A_rows, gather_pair, k, M_total);
   if (st != MOE_OK) return st;
+  st = check_small(0, E, N, K, M_total, kernel);
+  if (st != MOE_OK) return st;
   if (M_total == 0) return ok();
   if (!w || !A || !seg_offsets || !out) return fail(MOE_ERR_NULL_ARG, "w, A, seg_offsets and out are required");
   if (pre && epilogue != MOE_EPI_SWIGLU) return fail(MOE_ERR_BAD_FORMAT, "pre goes with the SwiGLU epilogue");
@@ -91,6 +99,8 @@ moe_status moe_grouped_gemm_grad_rows(const void* w, int32_t dtype, int32_t E, i
   if (st != MOE_OK) return st;
   if (!plain(epilogue) && epilogue != MOE_EPI_SWIGLU_GRAD)
     return fail(MOE_ERR_BAD_FORMAT, "epilogue %d of a gradient by the rows", epilogue);
+  st = check_small(1, E, N, K, M_total, kernel);
+  if (st != MOE_OK) return st;
   if (M_total == 0) return ok();
   if (!w || !dy || !seg_offsets || !out) return fail(MOE_ERR_NULL_ARG, "w, dy, seg_offsets and out are required");
   if ((epilogue == MOE_EPI_SWIGLU_GRAD) != (pre != nullptr))

@@ -852,8 +852,8 @@ int launch_deep(const Gemm16Args& a, hipStream_t s) {
 template <bool F16, int MODE, bool GATHER, bool GLU>
 int launch_small(const Gemm16Args& a, hipStream_t s) {
   const int n_cb = MODE == kRows ? (a.K + 63) / 64 : (a.N + 31) / 32;
-  const int64_t wgs = row_tiles(a.M_total, a.E, 32) * n_cb;
-  if (wgs >= ((int64_t)1 << 24)) return (int)hipErrorInvalidConfiguration;  // 2^32 threads
+  const int64_t wgs = gemm16_small_workgroups(MODE, a.E, a.N, a.K, a.M_total);
+  if (wgs >= kGemm16MostSmall) return (int)hipErrorInvalidConfiguration;  // (refused before)
   hipLaunchKernelGGL((small_kernel<F16, MODE, GATHER, GLU>), dim3((unsigned)wgs), dim3(256), 0, s, kernel_args(a), a.epilogue, n_cb);
   return (int)hipGetLastError();
 }

@@ -219,6 +219,10 @@ constexpr uint32_t kGatherBytes = 0xFFC00000u;
 // three stages.  what: 0 forward, 1 rows, 2 weights.
 constexpr int kGemm16Deep = 129;
 int gemm16_path(int what, int E, int N, int K, int M_total, int kernel);
+// Workgroups of the kernel for few rows (what 0 or 1): 32 rows, a partial tile per segment that has
+// rows, by 32 channels or 64 inputs.  Of 256 threads each: kGemm16MostSmall pass a launch's 2^32.
+constexpr int64_t kGemm16MostSmall = (int64_t)1 << 24;
+int64_t gemm16_small_workgroups(int what, int E, int N, int K, int M_total);
 // Parts that a weights' gradient splits the rows into (1: none; 128-row tiles only).
 int gemm16_splits(int E, int N, int K, int M_total, int kernel);
 int launch_gemm16(const Gemm16Args& a, void* stream);

@@ -234,6 +234,11 @@ int gemm16_path(int what, int E, int N, int K, int M_total, int kernel) {
   return wide ? 256 : what != 2 && rounds[0] <= (M_total <= 160 * active ? 0.65 : 0.5) ? kGemm16Deep : 128;
 }
 
+int64_t gemm16_small_workgroups(int what, int E, int N, int K, int M_total) {
+  const int64_t tiles = (int64_t)M_total / 32 + (E < M_total ? E : M_total);
+  return tiles * (what == 1 ? (K + 63) / 64 : (N + 31) / 32);
+}
+
 // Few weights and many rows: enough parts to fill the chip with tiles of 128, each of 8
 // steps of 64 rows or more.
 int gemm16_splits(int E, int N, int K, int M_total, int kernel) {
