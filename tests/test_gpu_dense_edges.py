@@ -5,7 +5,8 @@ import pytest
 import torch
 
 import quantized_moe_expert_top_amd as q
-from tests.test_gpu_dense import DEV, KERNELS, bound, close, f64, i32, tile
+from oracle import dense_oracle as do
+from tests.test_gpu_dense import DEV, DT, EPI, KERNELS, Batch, bound, close, f64, i32, tile
 
 pytestmark = pytest.mark.gpu
 
@@ -87,3 +88,23 @@ def test_shares_of_dx_past_fp16s_range(lib):
     assert np.abs(ref).max() > 2 * 65504
     # roundings of h, y, dy, pre (its effect at most doubled) and dpre to fp16, of dx to bf16, in L2
     assert np.linalg.norm(f64(g.dx) - ref) <= (6 * 2.0 ** -11 + 2.0 ** -8) * np.linalg.norm(ref)
+
+
+@pytest.mark.parametrize("counts,N,K", [([5000], 64, 40), ([0, 2100, 1030], 72, 136), ([2300, 1], 16, 264)])
+@pytest.mark.parametrize("out", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("dt", ["bf16", "fp16"])
+def test_split_rows_in_every_type(lib, dt, out, counts, N, K):
+    """The weights' gradient of long segments of few weights: fp32 parts in the workspace, added and rounded once by a
+    second kernel, for either operand type and every output type."""
+    n = np.array(counts).reshape(-1, 1, 1)
+    for gather in (False, True):
+        b = Batch(11, counts, N, K, dt, k=2 if gather else 1, gather=gather)
+        ref, mag = do.grad_weights(f64(b.dy), b.rows, b.offsets)
+        for kernel in (q.MOE_KERNEL_AUTO, q.MOE_KERNEL_TILE128):
+            need = q.moe_grouped_gemm_grad_weights_workspace_size(b.E, N, K, b.M, kernel)
+            assert need >= 2 * b.E * N * K * 4  # split
+            ws = torch.full((need,), 255, dtype=torch.uint8, device=DEV)  # NaNs
+            got = q.moe_grouped_gemm_grad_weights(b.dy, b.a, b.seg, b.E, b.M, EPI[out], gather_pair=b.pairs, k=b.k,
+                                                  kernel=kernel, workspace=ws)
+            assert got.dtype == DT[out]
+            close(f64(got), ref, bound(ref, mag, n, out), f"gather {gather}")
