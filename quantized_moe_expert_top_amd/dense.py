@@ -16,7 +16,7 @@ from typing import Optional
 import torch
 
 from . import (MOE_EPI_NONE, MOE_EPI_NONE_F16, MOE_EPI_NONE_F32, MOE_EPI_SWIGLU, MOE_EPI_SWIGLU_GRAD,
-               MOE_KERNEL_AUTO, Permutation, _DTYPE_EPI, lib, moe_route_permute, moe_unpermute_combine)
+               MOE_KERNEL_AUTO, MOE_KERNEL_SMALL, Permutation, _DTYPE_EPI, lib, moe_route_permute, moe_unpermute_combine)
 from .mx import _call, _device, _DTYPES, _elsewhere, _guard, _p, _want
 
 _PLAIN = {MOE_EPI_NONE: torch.bfloat16, MOE_EPI_NONE_F16: torch.float16, MOE_EPI_NONE_F32: torch.float32}
@@ -296,12 +296,13 @@ def moe_expert_layer_backward(dout: torch.Tensor, x: torch.Tensor, gate_up: torc
         with _guard(dev, stream):
             return moe_expert_layer_backward(dout, x, gate_up, down, buf, grad_dtype, None, kernel)
     p, P = buf.perm, T * k
+    weights_kernel = MOE_KERNEL_AUTO if kernel == MOE_KERNEL_SMALL else kernel  # (a choice of the gradient by the rows alone)
     c = moe_unpermute_combine_grad(dout, buf.y_perm, p.pair_pos, buf.w, T, k, dtype=x.dtype, ids=buf.ids, E=E,
                                    n_valid=p.seg_offsets[-1:])
-    ddown = moe_grouped_gemm_grad_weights(c.dy, buf.h, p.seg_offsets, E, P, epi, kernel=kernel)
+    ddown = moe_grouped_gemm_grad_weights(c.dy, buf.h, p.seg_offsets, E, P, epi, kernel=weights_kernel)
     dpre = moe_grouped_gemm_grad_rows(down, c.dy, p.seg_offsets, P, MOE_EPI_SWIGLU_GRAD, pre=buf.pre, kernel=kernel)
     dgate_up = moe_grouped_gemm_grad_weights(dpre, x, p.seg_offsets, E, P, epi, gather_pair=p.sorted_pair, k=k,
-                                             kernel=kernel)
+                                             kernel=weights_kernel)
     # the shares stay in fp32 up to their sum: 16 bits would round each, and fp16 ends at 65504
     dx = moe_grouped_gemm_grad_rows(gate_up, dpre, p.seg_offsets, P, MOE_EPI_NONE_F32, kernel=kernel)
     dx = moe_unpermute_combine(dx, p.pair_pos, None, T, k, n_valid=p.seg_offsets[-1:])

@@ -108,3 +108,17 @@ def test_split_rows_in_every_type(lib, dt, out, counts, N, K):
                                                   kernel=kernel, workspace=ws)
             assert got.dtype == DT[out]
             close(f64(got), ref, bound(ref, mag, n, out), f"gather {gather}")
+
+
+@pytest.mark.parametrize("kernel", KERNELS)
+def test_layer_with_every_kernel_choice(lib, kernel):
+    """Forward and backward by one choice each: the gradients of a choice differ from AUTO's by the sums' order alone."""
+    T, E, k, H, I = 40, 5, 2, 72, 40
+    x, logits, gu, dn, dout = layer(3, T, E, k, H, I, torch.bfloat16)
+    want = q.moe_expert_layer_forward(x, logits, k, gu, dn, keep=True)
+    ref = q.moe_expert_layer_backward(dout, x, gu, dn, want)
+    buf = q.moe_expert_layer_forward(x, logits, k, gu, dn, keep=True, kernel=KERNELS[kernel])
+    got = q.moe_expert_layer_backward(dout, x, gu, dn, buf, kernel=KERNELS[kernel])
+    # an fp32 sum of another order may round a 16-bit value the other way, a whole step (2^-7), at most
+    for a, b in ((buf.out, want.out), (got.dx, ref.dx), (got.dgate_up, ref.dgate_up), (got.ddown, ref.ddown)):
+        assert torch.linalg.vector_norm(a.double() - b.double()) <= 2.0 ** -7 * torch.linalg.vector_norm(b.double())
