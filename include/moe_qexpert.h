@@ -203,7 +203,8 @@ moe_status moe_route_permute(const float* logits, int32_t T, int32_t E, int32_t 
 #define MOE_KERNEL_TILE64_WIDE 3     /* INT4, MWQ: 64-row tiles, 128 SwiGLU / 256 plain channels */
 #define MOE_KERNEL_TILE64 4          /* INT4, MWQ: 64-row tiles, 64 SwiGLU / 128 plain channels */
 #define MOE_KERNEL_TILE128 5         /* INT4, MWQ: 128-row tiles fed through registers; 16-bit weights:
-                                        tiles of 128 output columns */
+                                        tiles of 128 output columns by 128 rows (few of them: by
+                                        128 or 256, as the segments' rows fall) */
 #define MOE_KERNEL_LDS_DMA 6         /* INT4, MWQ, DELTA2 with a base and a plain epilogue: 64- or
                                         128-row tiles fed by LDS-DMA (activation row sums in the
                                         workspace); nested MWQ: 16-row chunks of all widths */

@@ -13,8 +13,8 @@
 // Three parts cost bf16 nothing that shows, two of B cost fp16: 4096 tokens, 4096 to 14336,
 // ranks 16, 32, 64 and 128, us: 57, 74, 151, 246 in bf16, 64, 76, 161, 316 in fp16.
 // Bytes bound long batches: y in, out, x and the adapters.  4096 tokens, 4096 to
-// 14336, rank 32, 16 adapters, y and out in bf16, us: 73 (288 MB, 3.9 TB/s; a copy of
-// them 55); with 32 tokens a workgroup 129, with single steps of the first product (a
+// 14336, rank 32, 16 adapters, y and out in bf16, us: 74 (288 MB, 3.9 TB/s; a copy of
+// them 55), of which the first product, that all workgroups start with, 16; with 32 tokens a workgroup 129, with single steps of the first product (a
 // line of x fetched by two wavefronts) and one chunk under way 78; rank 16 57, with one
 // chunk under way 82.  Latency bounds few tokens: a chain of dependent accesses, 10.4 us
 // for 32 tokens of 16 adapters of rank 16, 4096 to 4096, 6 of them the first product's.

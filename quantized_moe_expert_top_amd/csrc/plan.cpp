@@ -217,6 +217,10 @@ int mxgemm_path(int M_total, int E, int N, int K, bool e2m1, int kernel) {
 // may be of 256 rows (deep_kernel).  Us so / with two workgroups a CU: 8 experts of 4096 x
 // 4096, 100 rows each 61 / 71, by the rows of 28672 x 4096, 128 rows each 435 / 586, forward
 // 4096 x 14336 221 / 312; but one expert of 4096 x 4096, 1200 rows (320 tiles) 68 / 49.
+// Other counts at 0.52 to 0.6 of the places: 16 of 2048 x 2048, 106 to 125 rows each 40 / 49,
+// 32 of 1024 x 8192 143 / 173, 4 of 8192 x 2048 38 / 45, by the rows 16 of 8192 x 2048 128 / 164;
+// but 4 of 4096 x 2048, 275 rows each 34 / 27, 2 of them, 550 rows 33 / 25, by the rows 2 of
+// 8192 x 4096, 550 rows 128 / 110 (segments of more than 192 rows take tiles of 128, in two rounds).
 int gemm16_path(int what, int E, int N, int K, int M_total, int kernel) {
   if (kernel == 1 && what != 2) return 0;
   if (kernel == 9) return 256;

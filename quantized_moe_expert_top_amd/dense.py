@@ -252,7 +252,7 @@ def moe_expert_layer_forward(x: torch.Tensor, logits: torch.Tensor, k: int, gate
                              buf: ExpertLayerBuffers = None, keep: bool = False, stream=None,
                              kernel: int = MOE_KERNEL_AUTO) -> ExpertLayerBuffers:
     """Route -> group -> gate_up (+SwiGLU) -> down -> combine with experts in 16 bits (gate_up [E][2I][H]: gate rows, then
-    up rows; down [E][H][I]), one stream.  keep (or buffers made with it): what moe_expert_layer_backward needs stays."""
+    up rows; down [E][H][I]), one stream.  The output is bf16 for either type of weights.  keep (or buffers made with it): what moe_expert_layer_backward needs stays."""
     if logits.dim() != 2:
         raise ValueError("logits must be float32 [T][E]")
     sizes = _layer_sizes(x, logits.shape[1], k, gate_up, down)
