@@ -461,8 +461,8 @@ moe_status moe_unpermute_combine_grad(const uint16_t* dout, const void* y_perm, 
  *               B [n][N][r] too
  *   scale       f32 [n], or NULL for 1
  *   seg_offsets i32 [n + 1], rows i32 [T]: moe_permute's seg_offsets and sorted_pair
- * Both products are accumulated in fp32, and A_a x keeps fp32's 24 bits and range between
- * them; scale multiplies the second one's sums, and out is rounded once.  Infinities and NaN
+ * Both products are accumulated in fp32, and A_a x keeps fp32's range and (from 2^-100 on) 24
+ * bits between them; scale multiplies the second one's sums, and out is rounded once.  Infinities and NaN
  * spread as in the formula.  A token stands in rows once.
  * 1 <= n <= 1024, T < 2^24, r a multiple of 8 up to 128 (pad others with zeros), K and N
  * multiples of 8; x, A and B less than 4 GiB each; 16-byte aligned buffers (scale, offsets

@@ -29,7 +29,8 @@ constexpr int token_tiles(int nr) { return nr <= 2 ? 1 : 2; }
 // v = high + rest, high a bf16 number of v's sign that is nearer to zero.  Exact: rest has
 // 8 bits fewer than v (three parts hold fp32's 24 bits, two fp16's 11).  Neither part is zero
 // unless v is, so that an infinity which meets v meets numbers of v's sign; an infinite v has
-// the largest number for high and is itself the rest.
+// the largest number for high and is itself the rest.  (Below 2^-100 a last part may be subnormal
+// and count for nothing: 2^-126 absolute.)
 struct Parts {
   float high, rest;
 };

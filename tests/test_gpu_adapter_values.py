@@ -208,3 +208,16 @@ def test_many_chunks_of_channels(lib, dt, y_dt, r, N):
     into = y.clone()
     assert q.moe_adapter_add(into, x, A, B, p.seg_offsets, p.sorted_pair, scale=scale, out=into) is into
     assert torch.equal(into, got)
+
+
+@pytest.mark.parametrize("r", [8, 32, 64, 128])
+@pytest.mark.parametrize("exponent", [60, 98])
+def test_first_products_near_the_least(lib, r, exponent):
+    """bf16: v of 2^-60 and 2^-98, brought back by the scale."""
+    g = np.random.default_rng(exponent + r)
+    T, K, N = 21, 40, 72
+    x, A = g.standard_normal((T, K)) * 2.0 ** -(exponent // 2), g.standard_normal((1, r, K)) * 2.0 ** -(exponent // 2)
+    x, A, B = dev(x, DT["bf16"]), dev(A, DT["bf16"]), dev(g.standard_normal((1, N, r)), DT["bf16"])
+    y, scale, p = torch.zeros(T, N, device=DEV), dev([2.0 ** exponent], torch.float32), group([0] * T, 1)
+    ref, mag = reference(y, x, A, B, [0] * T, f64(scale))
+    close(f64(q.moe_adapter_add(y, x, A, B, p.seg_offsets, p.sorted_pair, scale=scale)), ref, bound(ref, mag, K, r, "fp32"))
